@@ -74,7 +74,7 @@ def build_library(force: bool = False, verbose: bool = False, checked: bool = Fa
 
     with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-    tmp = lib_path.with_name(f".libmxq.{os.getpid()}.so")
+    tmp = lib_path.with_name(f".{lib_path.stem}.{os.getpid()}.so")
     subprocess.run([cc, *ARCH, "-shared", "-Xcompiler", "-fPIC", *map(str, objs), "-o", str(tmp)],
                    check=True)
     os.replace(tmp, lib_path)

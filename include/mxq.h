@@ -62,6 +62,7 @@ typedef struct CUstream_st *cudaStream_t;
 #define MXQ_DEV_BADOFFS 0x1u /* offs failed the device-side check: no output written */
 #define MXQ_DEV_TIMEOUT 0x2u /* an internal pipeline wait gave up: outputs incomplete */
 #define MXQ_DEV_OOB 0x4u     /* checked build only: a store out of its buffer was skipped */
+#define MXQ_DEV_BADINDEX 0x8u /* an expert, row or table index was out of range and left out */
 
 /*
  * Dual-axis MXFP8 quantization of one bf16 matrix, reading it once.
@@ -285,6 +286,109 @@ int mxq_quantize_2d_dual_3pass_noalloc(const void *x, int64_t M, int64_t N, cons
 int mxq_mxfp8_scaled_mm(const uint8_t *a, int64_t lda, const uint8_t *sa, const uint8_t *b,
                         int64_t ldb, const uint8_t *sb, float *d, int64_t Ma, int64_t Nb, int64_t K,
                         cudaStream_t stream);
+
+/* ======================================================================== *
+ * Operators of a mixture-of-experts training step around the cast.
+ *
+ * Types are MXQ_F32 or MXQ_BF16; sums, softmax statistics and norms are fp32
+ * and every result is rounded once.  Matrices are row-major with `ld`
+ * elements between their rows (ld >= the row's length, at most 2^31 - 1);
+ * pointers need the alignment of their elements only, and accesses widen to 16
+ * bytes where every pitch and address allows it.  `workspace` is device memory
+ * (16-byte aligned) that a call uses and leaves: at least the bytes that the
+ * matching _workspace() call returns (a host computation; negative: MXQ_E*).
+ * A too small one is refused with MXQ_EBADSHAPE.  Results have the same bits in
+ * every run: no sum depends on the order in which blocks run.
+ * ======================================================================== */
+
+/*
+ * Routing of `tokens` tokens to k of `experts` experts, with the balance loss.
+ *   logits   [tokens, experts], rows ld elements apart.
+ *   k        1 .. min(experts, 32); experts 1 .. MXQ_MAX_GROUPS.
+ *   mask     uint8 [tokens], 0 leaves the token out, or NULL.
+ *   ids      int32 [tokens, k]: the experts with the k largest logits, largest
+ *            first, ties to the lowest index.  A logit of -inf (or NaN) is never
+ *            chosen: where fewer than k are left the rest of the row is -1.
+ *   weights  fp32 [tokens, k]: p = softmax(logits) at the ids (renorm 0), or p
+ *            over the sum of the chosen (renorm 1); 0 beside an id of -1.
+ *   counts   int32 [experts]: tokens that chose each expert.
+ *   loss     fp32: E/(k n^2) * sum_e counts_e * sum_t p_te over the n = *routed
+ *            tokens that are not masked and have a logit other than -inf; 0 for
+ *            n == 0.  Tokens that are not counted have ids -1 and weights 0.
+ * A row with NaN or +inf has NaN probabilities (and makes the loss NaN).
+ *
+ * mxq_moe_route_backward: the logits' gradient from those of the weights and of
+ * the loss (each may be NULL: zero), with the choice held fixed; rows of tokens
+ * that are not counted are written as 0.  ids, counts and routed are the
+ * forward call's.  dlogits has the logits' type, rows ldd elements apart.
+ */
+int64_t mxq_moe_route_workspace(int32_t experts);
+int mxq_moe_route(const void *logits, int dtype, int64_t tokens, int32_t experts, int64_t ld,
+                  int32_t k, const uint8_t *mask, int renorm, float *weights, int32_t *ids,
+                  int32_t *counts, float *loss, int32_t *routed, uint8_t *workspace,
+                  int64_t workspace_bytes, cudaStream_t stream);
+int mxq_moe_route_backward(const void *logits, int dtype, int64_t tokens, int32_t experts,
+                           int64_t ld, int32_t k, const uint8_t *mask, int renorm,
+                           const int32_t *ids, const int32_t *counts, const int32_t *routed,
+                           const float *dweights, const float *dloss, void *dlogits, int64_t ldd,
+                           cudaStream_t stream);
+
+/*
+ * The exchange of rows between tokens and expert groups.  Assignment
+ * i = token*k + j takes row slots[i] of a matrix of M rows in which the groups
+ * follow one another, each in token order and filled up to a multiple of 128
+ * rows: the matrix and the offs that mxq_quantize_2d_dual takes.
+ *   mxq_moe_rows       the rows that hold every routing of these sizes, a
+ *                      multiple of 128 (a host computation; negative: MXQ_E*).
+ *   mxq_moe_plan       from ids int32 [tokens, k] (-1: not routed; an id outside
+ *                      [0, experts) also sets MXQ_DEV_BADINDEX): offs int32
+ *                      [experts] (cumulative ends), slots int32 [tokens, k] (-1:
+ *                      none), source int32 [M] (the assignment of each row, or -1).
+ *                      M >= mxq_moe_rows(), a multiple of 128.
+ *   mxq_moe_dispatch   rows[slots[i]] = x[i / k]; rows without an assignment 0.
+ *   mxq_moe_combine    y[t] = sum_j w[t, j] * rows[slots[t, j]], j ascending; w =
+ *                      1 for weights NULL, which is the gradient of dispatch.
+ *   mxq_moe_combine_backward   drows[slots[i]] = w_i * dy[i / k], other rows 0;
+ *                      dweights[i] = <dy[i / k], rows[slots[i]]>, 0 without a slot.
+ * x, y, dy are [tokens, D], rows and drows [M, D], all of one type; weights and
+ * dweights fp32 [tokens, k].  A slot outside [0, M) is left out and sets
+ * MXQ_DEV_BADINDEX.
+ */
+int64_t mxq_moe_rows(int64_t tokens, int32_t k, int32_t experts);
+int64_t mxq_moe_plan_workspace(int64_t tokens, int32_t k, int32_t experts);
+int mxq_moe_plan(const int32_t *ids, int64_t tokens, int32_t k, int32_t experts, int64_t M,
+                 int32_t *offs, int32_t *slots, int32_t *source, uint8_t *workspace,
+                 int64_t workspace_bytes, cudaStream_t stream);
+int mxq_moe_dispatch(const void *x, int dtype, int64_t tokens, int64_t D, int64_t ldx, int32_t k,
+                     const int32_t *slots, const int32_t *source, int64_t M, void *rows,
+                     int64_t ldr, cudaStream_t stream);
+int mxq_moe_combine(const void *rows, int dtype, int64_t M, int64_t D, int64_t ldr, int64_t tokens,
+                    int32_t k, const int32_t *slots, const float *weights, void *y, int64_t ldy,
+                    cudaStream_t stream);
+int mxq_moe_combine_backward(const void *dy, int dtype, int64_t tokens, int64_t D, int64_t ldy,
+                             const void *rows, int64_t ldr, int64_t M, int32_t k,
+                             const int32_t *slots, const int32_t *source, const float *weights,
+                             void *drows, int64_t ldd, float *dweights, cudaStream_t stream);
+
+/*
+ * Scaled lookup in a table [rows, D], and the table's gradient.
+ *   ids      int32 or int64 (ids_bytes 4 or 8) [tokens].  An id outside [0, rows)
+ *            gives a row of zeros, adds to no gradient and sets MXQ_DEV_BADINDEX.
+ *   mxq_embedding            y[t] = scale * table[ids[t]], types dtype -> out_dtype.
+ *   mxq_embedding_backward   dtable[v] = scale * sum of dy[t] over ids[t] == v, in
+ *            a fixed order; every row is written, 0 where no token has it.  Tokens
+ *            whose id is `padding` are left out (-1: none).  dy has type dtype,
+ *            dtable out_dtype.
+ * tokens at most 2^29 - 1.
+ */
+int mxq_embedding(const void *ids, int ids_bytes, int64_t tokens, const void *table, int dtype,
+                  int64_t rows, int64_t D, int64_t ldw, float scale, void *y, int out_dtype,
+                  int64_t ldy, cudaStream_t stream);
+int64_t mxq_embedding_backward_workspace(int64_t tokens, int64_t rows, int64_t D);
+int mxq_embedding_backward(const void *ids, int ids_bytes, int64_t tokens, const void *dy,
+                           int dtype, int64_t D, int64_t ldd, int64_t rows, int64_t padding,
+                           float scale, void *dtable, int out_dtype, int64_t ldw,
+                           uint8_t *workspace, int64_t workspace_bytes, cudaStream_t stream);
 
 /*
  * Device status word of the current device: a sticky OR of MXQ_DEV_* bits set

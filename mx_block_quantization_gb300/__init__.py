@@ -24,6 +24,9 @@ Operations (sources by page title):
 * :func:`mxfp8_scaled_mm` -- a block-scaled MXFP8 product on the tensor cores
   (tcgen05) that reads the cast's bytes as stored: the consumer check of the
   blocked scale layouts and the K-group slabs.
+* :func:`moe_route`, :func:`moe_plan`, :func:`moe_dispatch`, :func:`moe_combine`,
+  :func:`embedding` and their gradients (``training.py``) -- the operators of a
+  mixture-of-experts training step whose grouped rows the dual-axis cast takes.
 
 With MXQ_CHECKED=1 in the environment the binding loads libmxq_checked.so,
 the same kernels with every computed global access tested against its buffer.
@@ -58,6 +61,7 @@ RECORD_BYTES = {FMT_MX9: 18, FMT_MX6: 12}
 DEV_BADOFFS = 0x1
 DEV_TIMEOUT = 0x2
 DEV_OOB = 0x4  # checked library only: an out-of-buffer access was skipped
+DEV_BADINDEX = 0x8  # an expert, row or table index was out of range and left out
 
 _lib: Optional[ctypes.CDLL] = None
 
@@ -108,6 +112,22 @@ def lib() -> ctypes.CDLL:
                                        ctypes.c_int, vp]
         L.mxq_mxfp8_scaled_mm.restype = ctypes.c_int
         L.mxq_mxfp8_scaled_mm.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i64, i64, vp]
+        f32, ci = ctypes.c_float, ctypes.c_int
+        for name, restype, argtypes in (
+                ("mxq_moe_route_workspace", i64, [i32]),
+                ("mxq_moe_route", ci, [vp, ci, i64, i32, i64, i32, vp, ci, vp, vp, vp, vp, vp, vp, i64, vp]),
+                ("mxq_moe_route_backward", ci, [vp, ci, i64, i32, i64, i32, vp, ci, vp, vp, vp, vp, vp, vp, i64, vp]),
+                ("mxq_moe_rows", i64, [i64, i32, i32]),
+                ("mxq_moe_plan_workspace", i64, [i64, i32, i32]),
+                ("mxq_moe_plan", ci, [vp, i64, i32, i32, i64, vp, vp, vp, vp, i64, vp]),
+                ("mxq_moe_dispatch", ci, [vp, ci, i64, i64, i64, i32, vp, vp, i64, vp, i64, vp]),
+                ("mxq_moe_combine", ci, [vp, ci, i64, i64, i64, i64, i32, vp, vp, vp, i64, vp]),
+                ("mxq_moe_combine_backward", ci, [vp, ci, i64, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i64, vp, vp]),
+                ("mxq_embedding", ci, [vp, ci, i64, vp, ci, i64, i64, i64, f32, vp, ci, i64, vp]),
+                ("mxq_embedding_backward_workspace", i64, [i64, i64, i64]),
+                ("mxq_embedding_backward", ci, [vp, ci, i64, vp, ci, i64, i64, i64, i64, f32, vp, ci, i64, vp, i64, vp])):
+            fn = getattr(L, name)
+            fn.restype, fn.argtypes = restype, argtypes
         L.mxq_last_device_status.restype = ctypes.c_int
         L.mxq_last_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
         L.mxq_selftest_wait_timeout.restype = ctypes.c_int
@@ -560,3 +580,20 @@ def mxfp8_scaled_mm(a, sa, b, sb, *, out=None, stream=None):
         raise MxqError(rc, "mxq_mxfp8_scaled_mm")
     return out
 
+
+# ---------------------------------------------------------------------------
+# operators of a mixture-of-experts training step (training.py)
+# ---------------------------------------------------------------------------
+
+_TRAINING = ("Routing", "MoePlan", "moe_route", "moe_route_backward", "moe_rows", "moe_plan", "moe_dispatch",
+             "moe_combine", "moe_combine_backward", "embedding", "embedding_backward")
+
+
+def __getattr__(name):
+    # training.py imports torch, which this module leaves to the first call that needs it
+    if name in _TRAINING:
+        from . import training
+        for n in _TRAINING:
+            globals()[n] = getattr(training, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

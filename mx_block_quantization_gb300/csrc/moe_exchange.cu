@@ -1,0 +1,470 @@
+// moe_exchange.cu -- the rows that tokens and experts exchange: the plan of the
+// expert groups, dispatch, combine, and their gradients.
+//
+// Assignment i = token*k + j sends a token to its j-th expert.  The plan puts
+// the assignments of each expert one after another in token order (a stable
+// counting sort), each group starting at a multiple of 128 rows, which is what
+// the grouped MXFP8 cast takes: offs[e] is the cumulative end of group e,
+// slots[i] the row of assignment i, source[m] the assignment of row m or -1 for
+// the rows that only fill a group up or lie past the last one.
+//   dispatch           rows[slots[i]] = x[i / k], the other rows zero
+//   combine            y[t] = sum_j w_tj rows[slots[tk + j]]   (w = 1 without weights:
+//                      the gradient of dispatch)
+//   combine_backward   drows[slots[i]] = w_i dy[i / k], the other rows zero;
+//                      dweights[i] = <dy[i / k], rows[slots[i]]>
+// All of it is bound by HBM: a token's row is read once and its k rows written
+// or read by the same threads, with sums over j in ascending order in fp32.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "rank_tile.cuh"
+#include "train_common.cuh"
+
+namespace {
+
+using namespace mxq;
+
+__device__ unsigned int g_exchange_status = 0;
+
+constexpr int kGroupRows = 128;
+constexpr int kMaxK = 32;
+constexpr int kThreads = 256;
+constexpr int kFillRows = 8;  // rows looked at by a block that zeroes unused rows
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+struct ExpertKey {
+  const int32_t* ids;
+  int E;
+  __device__ int operator()(int64_t i) const {
+    const int32_t e = ids[i];
+    if (e >= 0 && e < E) return e;
+    if (e != -1) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
+    return -1;
+  }
+};
+
+__global__ void __launch_bounds__(kRankThreads)
+    plan_count_kernel(const int32_t* __restrict__ ids, RankSplit s, int E, int32_t* chunk_counts) {
+  extern __shared__ int32_t counts[];
+  pdl_wait();
+  rank_count(s, E, ExpertKey{ids, E}, counts);
+  for (int e = threadIdx.x; e < E; e += kRankThreads)
+    chunk_counts[static_cast<int64_t>(blockIdx.x) * E + e] = counts[e];
+}
+
+__global__ void __launch_bounds__(kRankThreads)
+    plan_kernel(const int32_t* __restrict__ ids, RankSplit s, int E, const int32_t* __restrict__ chunk_counts,
+                int32_t* __restrict__ offs, int32_t* __restrict__ slots, int32_t* __restrict__ source, int64_t M) {
+  extern __shared__ int32_t smem[];
+  int32_t* next = smem;         // [E]
+  int32_t* counts = smem + E;   // [warps, E]
+  __shared__ int32_t total[kRankMaxBins], begin[kRankMaxBins], work[kRankWarps];
+  pdl_wait();
+  const ExpertKey key{ids, E};
+  if (s.chunks == 1) {
+    rank_count(s, E, key, total);
+    for (int e = threadIdx.x; e < E; e += kRankThreads) next[e] = 0;
+  } else {
+    rank_totals(s, E, chunk_counts, total, next);
+  }
+  const int32_t end = rank_begins<kGroupRows>(E, total, begin, work);
+  const uint64_t m_bytes = static_cast<uint64_t>(M) * 4;
+  // rows that fill a group up: expert by expert over the blocks
+  for (int e = blockIdx.x; e < E; e += gridDim.x) {
+    const int64_t lo = begin[e] + total[e];
+    const int64_t hi = begin[e] + (total[e] + kGroupRows - 1) / kGroupRows * kGroupRows;
+    for (int64_t m = lo + threadIdx.x; m < hi; m += kRankThreads)
+      if (in_buf(source + m, 4, source, m_bytes, &g_exchange_status)) source[m] = -1;
+    if (threadIdx.x == 0) offs[e] = static_cast<int32_t>(hi);
+  }
+  for (int64_t m = end + static_cast<int64_t>(blockIdx.x) * kRankThreads + threadIdx.x; m < M;
+       m += static_cast<int64_t>(gridDim.x) * kRankThreads)
+    source[m] = -1;
+  for (int e = threadIdx.x; e < E; e += kRankThreads) next[e] += begin[e];
+  __syncthreads();
+  const uint64_t s_bytes = static_cast<uint64_t>(s.n) * 4;
+  rank_chunk(
+      s, E, key,
+      [&](int64_t i, int, int32_t place) {
+        if (in_buf(slots + i, 4, slots, s_bytes, &g_exchange_status)) slots[i] = place;
+        if (place >= 0 && in_buf(source + place, 4, source, m_bytes, &g_exchange_status))
+          source[place] = static_cast<int32_t>(i);
+      },
+      next, counts);
+}
+
+// ---------------------------------------------------------------------------
+// rows
+// ---------------------------------------------------------------------------
+struct ExchangeShape {
+  int64_t tokens, M, D;
+  int64_t ldt, ldm;  // elements between the rows of the token matrix and of the group matrix
+  int k, tx;         // tx: threads per token (a power of two)
+};
+
+__device__ __forceinline__ int64_t slot_of(const int32_t* slots, int64_t i, int64_t M) {
+  const int32_t s = slots[i];
+  if (s >= 0 && s < M) return s;
+  if (s != -1) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
+  return -1;
+}
+
+// Zeroes those of kFillRows rows that no assignment fills.
+template <typename T, int kV>
+__device__ void zero_unused(const ExchangeShape& s, const int32_t* source, T* rows, int64_t block) {
+  const int64_t nv = s.D / kV;
+  const uint64_t bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
+  for (int r = 0; r < kFillRows; ++r) {
+    const int64_t m = block * kFillRows + r;
+    if (m >= s.M) return;
+    if (source[m] >= 0) continue;
+    for (int64_t c = threadIdx.x; c < nv; c += kThreads)
+      if (in_buf(rows + m * s.ldm + c * kV, kV * sizeof(T), rows, bytes, &g_exchange_status))
+        *reinterpret_cast<Vec<T, kV>*>(rows + m * s.ldm + c * kV) = Vec<T, kV>{};
+  }
+}
+
+template <typename T, int kV>
+__global__ void __launch_bounds__(kThreads)
+    dispatch_kernel(const T* __restrict__ x, const ExchangeShape s, const int32_t* __restrict__ slots,
+                    const int32_t* __restrict__ source, T* __restrict__ rows, int64_t token_blocks) {
+  pdl_wait();
+  if (static_cast<int64_t>(blockIdx.x) >= token_blocks) {
+    zero_unused<T, kV>(s, source, rows, blockIdx.x - token_blocks);
+    return;
+  }
+  const int ty = kThreads / s.tx;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * ty + threadIdx.x / s.tx;
+  if (t >= s.tokens) return;
+  const int64_t nv = s.D / kV;
+  const uint64_t bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
+  for (int64_t c = threadIdx.x % s.tx; c < nv; c += s.tx) {
+    const Vec<T, kV> v = *reinterpret_cast<const Vec<T, kV>*>(x + t * s.ldt + c * kV);
+    for (int j = 0; j < s.k; ++j) {
+      const int64_t m = slot_of(slots, t * s.k + j, s.M);
+      if (m >= 0 && in_buf(rows + m * s.ldm + c * kV, kV * sizeof(T), rows, bytes, &g_exchange_status))
+        *reinterpret_cast<Vec<T, kV>*>(rows + m * s.ldm + c * kV) = v;
+    }
+  }
+}
+
+constexpr int kAtOnce = 8;  // rows of a token loaded before the first is used
+
+template <typename T, int kV>
+__global__ void __launch_bounds__(kThreads)
+    combine_kernel(const T* __restrict__ rows, const ExchangeShape s, const int32_t* __restrict__ slots,
+                   const float* __restrict__ weights, T* __restrict__ y) {
+  pdl_wait();
+  const int ty = kThreads / s.tx;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * ty + threadIdx.x / s.tx;
+  if (t >= s.tokens) return;
+  const int64_t nv = s.D / kV;
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
+  const uint64_t out_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldt + s.D) * sizeof(T);
+  for (int64_t c = threadIdx.x % s.tx; c < nv; c += s.tx) {
+    float acc[kV];
+#pragma unroll
+    for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < s.k; j0 += kAtOnce) {
+      Vec<T, kV> v[kAtOnce];
+      float w[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int64_t m = j0 + j < s.k ? slot_of(slots, t * s.k + j0 + j, s.M) : -1;
+        const bool live = m >= 0 && in_buf(rows + m * s.ldm + c * kV, kV * sizeof(T), rows, in_bytes, &g_exchange_status);
+        v[j] = live ? *reinterpret_cast<const Vec<T, kV>*>(rows + m * s.ldm + c * kV) : Vec<T, kV>{};
+        w[j] = live ? (weights != nullptr ? weights[t * s.k + j0 + j] : 1.0f) : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[i] = fmaf(w[j], widen(v[j].v[i]), acc[i]);
+    }
+    Vec<T, kV> out;
+#pragma unroll
+    for (int i = 0; i < kV; ++i) out.v[i] = narrow<T>(acc[i]);
+    if (in_buf(y + t * s.ldt + c * kV, kV * sizeof(T), y, out_bytes, &g_exchange_status))
+      *reinterpret_cast<Vec<T, kV>*>(y + t * s.ldt + c * kV) = out;
+  }
+}
+
+// kWarps warps per token (1 or all of the block's).
+template <typename T, int kV, int kWarps>
+__global__ void __launch_bounds__(kThreads)
+    combine_backward_kernel(const T* __restrict__ dy, const T* __restrict__ rows, const ExchangeShape s, int64_t ldr,
+                            const int32_t* __restrict__ slots, const int32_t* __restrict__ source,
+                            const float* __restrict__ weights, T* __restrict__ drows, float* __restrict__ dweights,
+                            int64_t token_blocks) {
+  __shared__ float red[kThreads / 32][kAtOnce];
+  pdl_wait();
+  if (static_cast<int64_t>(blockIdx.x) >= token_blocks) {
+    zero_unused<T, kV>(s, source, drows, blockIdx.x - token_blocks);
+    return;
+  }
+  constexpr int kGroup = kWarps * 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / kGroup) + threadIdx.x / kGroup;
+  const bool live_token = t < s.tokens;  // for kWarps > 1 the same for the whole block
+  if (kWarps == 1 && !live_token) return;
+  const int64_t nv = s.D / kV;
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.M - 1) * ldr + s.D) * sizeof(T);
+  const uint64_t out_bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
+  for (int j0 = 0; j0 < s.k; j0 += kAtOnce) {
+    float dot[kAtOnce], w[kAtOnce];
+    int64_t m[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      dot[j] = 0.0f;
+      m[j] = j0 + j < s.k ? slot_of(slots, t * s.k + j0 + j, s.M) : -1;
+      w[j] = m[j] >= 0 ? weights[t * s.k + j0 + j] : 0.0f;
+    }
+    for (int64_t c = threadIdx.x % kGroup; c < nv; c += kGroup) {
+      const Vec<T, kV> g = *reinterpret_cast<const Vec<T, kV>*>(dy + t * s.ldt + c * kV);
+      Vec<T, kV> v[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        v[j] = m[j] >= 0 && in_buf(rows + m[j] * ldr + c * kV, kV * sizeof(T), rows, in_bytes, &g_exchange_status)
+                   ? *reinterpret_cast<const Vec<T, kV>*>(rows + m[j] * ldr + c * kV)
+                   : Vec<T, kV>{};
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        Vec<T, kV> out;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) {
+          const float d = widen(g.v[i]);
+          dot[j] = fmaf(d, widen(v[j].v[i]), dot[j]);
+          out.v[i] = narrow<T>(w[j] * d);
+        }
+        if (m[j] >= 0 && in_buf(drows + m[j] * s.ldm + c * kV, kV * sizeof(T), drows, out_bytes, &g_exchange_status))
+          *reinterpret_cast<Vec<T, kV>*>(drows + m[j] * s.ldm + c * kV) = out;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) dot[j] = warp_sum(dot[j]);
+    if (kWarps > 1) {
+      if (lane == 0)
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) red[warp][j] = dot[j];
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        dot[j] = 0.0f;
+        for (int q = 0; q < kWarps; ++q) dot[j] += red[q][j];
+      }
+      __syncthreads();
+    }
+    if (threadIdx.x % kGroup == 0)
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (j0 + j < s.k) dweights[t * s.k + j0 + j] = m[j] >= 0 ? dot[j] : 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+struct RowsCall {
+  int dtype;
+  const void* in;        // x, or the group rows
+  const void* in2;       // dy of combine_backward
+  ExchangeShape s;
+  int64_t ldr;
+  const int32_t *slots, *source;
+  const float* weights;
+  void* out;
+  float* dweights;
+  cudaStream_t stream;
+};
+
+template <typename T, int kV>
+int launch_dispatch(const RowsCall& a) {
+  const int64_t token_blocks = ceil_div(a.s.tokens, kThreads / a.s.tx);
+  const int64_t blocks = token_blocks + ceil_div(a.s.M, kFillRows);
+  return launch_pdl(dispatch_kernel<T, kV>, static_cast<unsigned>(blocks), kThreads, 0, a.stream,
+                    static_cast<const T*>(a.in), a.s, a.slots, a.source, static_cast<T*>(a.out), token_blocks);
+}
+template <typename T, int kV>
+int launch_combine(const RowsCall& a) {
+  return launch_pdl(combine_kernel<T, kV>, static_cast<unsigned>(ceil_div(a.s.tokens, kThreads / a.s.tx)), kThreads, 0,
+                    a.stream, static_cast<const T*>(a.in), a.s, a.slots, a.weights, static_cast<T*>(a.out));
+}
+template <typename T, int kV>
+int launch_combine_backward(const RowsCall& a) {
+  const bool wide = a.s.D / kV >= kThreads;
+  const int64_t token_blocks = wide ? a.s.tokens : ceil_div(a.s.tokens, kThreads / 32);
+  const int64_t blocks = token_blocks + ceil_div(a.s.M, kFillRows);
+  return launch_pdl(wide ? combine_backward_kernel<T, kV, kThreads / 32> : combine_backward_kernel<T, kV, 1>,
+                    static_cast<unsigned>(blocks), kThreads, 0, a.stream, static_cast<const T*>(a.in2),
+                    static_cast<const T*>(a.in), a.s, a.ldr, a.slots, a.source, a.weights, static_cast<T*>(a.out),
+                    a.dweights, token_blocks);
+}
+
+enum class Rows { kDispatch, kCombine, kCombineBackward };
+template <Rows kWhat, typename T, int kV>
+int launch_rows(RowsCall a) {
+  const int64_t nv = a.s.D / kV;
+  int tx = 8;
+  while (tx < kThreads && tx < nv) tx *= 2;
+  a.s.tx = tx;
+  if constexpr (kWhat == Rows::kDispatch) return launch_dispatch<T, kV>(a);
+  if constexpr (kWhat == Rows::kCombine) return launch_combine<T, kV>(a);
+  return launch_combine_backward<T, kV>(a);
+}
+
+// The widest access, up to 16 bytes, that divides the row length, every row
+// pitch and every base address.
+template <Rows kWhat>
+int launch_by_alignment(const RowsCall& a) {
+  const uint64_t es = element_bytes(a.dtype);
+  const int align = common_alignment({a.s.D * es, a.s.ldt * es, a.s.ldm * es, a.ldr * es, address_of(a.in),
+                                      address_of(a.in2), address_of(a.out)});
+  if (a.dtype == MXQ_F32)
+    return align >= 16  ? launch_rows<kWhat, float, 4>(a)
+           : align >= 8 ? launch_rows<kWhat, float, 2>(a)
+                        : launch_rows<kWhat, float, 1>(a);
+  return align >= 16  ? launch_rows<kWhat, bf16_t, 8>(a)
+         : align >= 8 ? launch_rows<kWhat, bf16_t, 4>(a)
+         : align >= 4 ? launch_rows<kWhat, bf16_t, 2>(a)
+                      : launch_rows<kWhat, bf16_t, 1>(a);
+}
+
+constexpr int64_t kMaxLd = INT32_MAX;  // no byte range below can wrap
+
+int check_rows_shape(int dtype, int64_t tokens, int64_t D, int64_t ldt, int64_t ldm, int32_t k, int64_t M) {
+  if (dtype != MXQ_F32 && dtype != MXQ_BF16) return MXQ_EBADDTYPE;
+  if (tokens < 0 || D < 0 || M < 0 || k < 1 || k > kMaxK || M > INT32_MAX || tokens > INT32_MAX ||
+      tokens * k > INT32_MAX || D > INT32_MAX || ldt < D || ldm < D || ldt > kMaxLd || ldm > kMaxLd)
+    return MXQ_EBADSHAPE;
+  return MXQ_OK;
+}
+
+}  // namespace
+
+namespace mxq {
+int exchange_status_read(unsigned int* out, bool clear) { return read_status_word(g_exchange_status, out, clear); }
+}  // namespace mxq
+
+extern "C" int64_t mxq_moe_rows(int64_t tokens, int32_t k, int32_t experts) {
+  if (tokens < 0 || tokens > INT32_MAX || k < 1 || k > kMaxK || experts < 1 || experts > MXQ_MAX_GROUPS)
+    return MXQ_EBADSHAPE;
+  const int64_t n = tokens * k;
+  const int64_t m = (n + (kGroupRows - 1) * (n < experts ? n : experts)) / kGroupRows * kGroupRows;
+  return m > INT32_MAX ? MXQ_EBADSHAPE : m;
+}
+
+extern "C" int64_t mxq_moe_plan_workspace(int64_t tokens, int32_t k, int32_t experts) {
+  if (mxq_moe_rows(tokens, k, experts) < 0) return MXQ_EBADSHAPE;
+  const RankSplit s = rank_split(tokens * k);
+  return s.chunks == 1 ? 0 : static_cast<int64_t>(s.chunks) * experts * 4;
+}
+
+extern "C" int mxq_moe_plan(const int32_t* ids, int64_t tokens, int32_t k, int32_t experts, int64_t M, int32_t* offs,
+                            int32_t* slots, int32_t* source, uint8_t* workspace, int64_t workspace_bytes,
+                            cudaStream_t stream) {
+  const int64_t need_m = mxq_moe_rows(tokens, k, experts);
+  if (need_m < 0 || M < need_m || M > INT32_MAX || M % kGroupRows != 0) return MXQ_EBADSHAPE;
+  const int64_t need = mxq_moe_plan_workspace(tokens, k, experts);
+  if (workspace_bytes < need) return MXQ_EBADSHAPE;
+  if (!offs || (tokens > 0 && (!ids || !slots)) || (M > 0 && !source) || (need > 0 && !workspace)) return MXQ_ENULL;
+  if (!aligned_to(ids, 4) || !aligned_to(offs, 4) || !aligned_to(slots, 4) || !aligned_to(source, 4) ||
+      !aligned_to(workspace, 4))
+    return MXQ_EALIGN;
+  const uint64_t n4 = static_cast<uint64_t>(tokens) * k * 4;
+  const ByteRange out[4] = {range_of(offs, 4ull * experts), range_of(slots, n4), range_of(source, 4ull * M),
+                            range_of(workspace, need)};
+  const ByteRange in[1] = {range_of(ids, n4)};
+  if (outputs_overlap(out, 4, in, 1)) return MXQ_EOVERLAP;
+  const RankSplit s = rank_split(tokens * k);
+  int32_t* counts = reinterpret_cast<int32_t*>(workspace);
+  if (s.chunks > 1) {
+    const int rc = launch_pdl(plan_count_kernel, s.chunks, kRankThreads, experts * 4, stream, ids, s, experts, counts);
+    if (rc != MXQ_OK) return rc;
+  }
+  return launch_pdl(plan_kernel, s.chunks, kRankThreads, rank_smem(experts), stream, ids, s, experts, counts, offs,
+                    slots, source, M);
+}
+
+extern "C" int mxq_moe_dispatch(const void* x, int dtype, int64_t tokens, int64_t D, int64_t ldx, int32_t k,
+                                const int32_t* slots, const int32_t* source, int64_t M, void* rows, int64_t ldr,
+                                cudaStream_t stream) {
+  const int rc = check_rows_shape(dtype, tokens, D, ldx, ldr, k, M);
+  if (rc != MXQ_OK) return rc;
+  if (M == 0 || D == 0) return MXQ_OK;
+  if ((tokens > 0 && (!x || !slots)) || !source || !rows) return MXQ_ENULL;
+  const int es = element_bytes(dtype);
+  if (!aligned_to(x, es) || !aligned_to(rows, es) || !aligned_to(slots, 4) || !aligned_to(source, 4)) return MXQ_EALIGN;
+  const ByteRange out[1] = {range_of(rows, pitched_bytes(M, D, ldr, es))};
+  const ByteRange in[3] = {range_of(x, pitched_bytes(tokens, D, ldx, es)),
+                           range_of(slots, static_cast<uint64_t>(tokens) * k * 4), range_of(source, 4ull * M)};
+  if (outputs_overlap(out, 1, in, 3)) return MXQ_EOVERLAP;
+  RowsCall a = {};
+  a.dtype = dtype;
+  a.in = x;
+  a.s = {tokens, M, D, ldx, ldr, k, 0};
+  a.slots = slots;
+  a.source = source;
+  a.out = rows;
+  a.stream = stream;
+  return launch_by_alignment<Rows::kDispatch>(a);
+}
+
+extern "C" int mxq_moe_combine(const void* rows, int dtype, int64_t M, int64_t D, int64_t ldr, int64_t tokens,
+                               int32_t k, const int32_t* slots, const float* weights, void* y, int64_t ldy,
+                               cudaStream_t stream) {
+  const int rc = check_rows_shape(dtype, tokens, D, ldy, ldr, k, M);
+  if (rc != MXQ_OK) return rc;
+  if (tokens == 0 || D == 0) return MXQ_OK;
+  if ((M > 0 && !rows) || !slots || !y) return MXQ_ENULL;
+  const int es = element_bytes(dtype);
+  if (!aligned_to(rows, es) || !aligned_to(y, es) || !aligned_to(slots, 4) || !aligned_to(weights, 4)) return MXQ_EALIGN;
+  const uint64_t n4 = static_cast<uint64_t>(tokens) * k * 4;
+  const ByteRange out[1] = {range_of(y, pitched_bytes(tokens, D, ldy, es))};
+  const ByteRange in[3] = {range_of(rows, pitched_bytes(M, D, ldr, es)), range_of(slots, n4), range_of(weights, n4)};
+  if (outputs_overlap(out, 1, in, 3)) return MXQ_EOVERLAP;
+  RowsCall a = {};
+  a.dtype = dtype;
+  a.in = rows;
+  a.s = {tokens, M, D, ldy, ldr, k, 0};
+  a.slots = slots;
+  a.weights = weights;
+  a.out = y;
+  a.stream = stream;
+  return launch_by_alignment<Rows::kCombine>(a);
+}
+
+extern "C" int mxq_moe_combine_backward(const void* dy, int dtype, int64_t tokens, int64_t D, int64_t ldy,
+                                        const void* rows, int64_t ldr, int64_t M, int32_t k, const int32_t* slots,
+                                        const int32_t* source, const float* weights, void* drows, int64_t ldd,
+                                        float* dweights, cudaStream_t stream) {
+  const int rc = check_rows_shape(dtype, tokens, D, ldy, ldd, k, M);
+  if (rc != MXQ_OK) return rc;
+  if (ldr < D || ldr > kMaxLd) return MXQ_EBADSHAPE;
+  if (tokens == 0 && (M == 0 || D == 0)) return MXQ_OK;
+  const bool has_rows = M > 0 && D > 0;
+  if ((tokens > 0 && ((D > 0 && !dy) || !slots || !weights || !dweights)) || (M > 0 && !source) || (has_rows && (!rows || !drows)))
+    return MXQ_ENULL;
+  const int es = element_bytes(dtype);
+  if (!aligned_to(dy, es) || !aligned_to(rows, es) || !aligned_to(drows, es) || !aligned_to(slots, 4) ||
+      !aligned_to(source, 4) || !aligned_to(weights, 4) || !aligned_to(dweights, 4))
+    return MXQ_EALIGN;
+  const uint64_t n4 = static_cast<uint64_t>(tokens) * k * 4;
+  const ByteRange out[2] = {range_of(drows, pitched_bytes(M, D, ldd, es)), range_of(dweights, n4)};
+  const ByteRange in[5] = {range_of(dy, pitched_bytes(tokens, D, ldy, es)), range_of(rows, pitched_bytes(M, D, ldr, es)),
+                           range_of(slots, n4), range_of(source, 4ull * M), range_of(weights, n4)};
+  if (outputs_overlap(out, 2, in, 5)) return MXQ_EOVERLAP;
+  RowsCall a = {};
+  a.dtype = dtype;
+  a.in = rows;
+  a.in2 = dy;
+  a.s = {tokens, M, D, ldy, ldd, k, 0};
+  a.ldr = ldr;
+  a.slots = slots;
+  a.source = source;
+  a.weights = weights;
+  a.out = drows;
+  a.dweights = dweights;
+  a.stream = stream;
+  return launch_by_alignment<Rows::kCombineBackward>(a);
+}

@@ -1,0 +1,497 @@
+// moe_route.cu -- routing of tokens to experts with the balance loss, and the
+// gradient of the logits.
+//
+// For a token's logits l over E experts:  p = softmax(l);  the k experts with
+// the largest logits, ties to the lowest index;  weights p (or p over the
+// chosen ones' sum);  counts_e = tokens that chose e;  and over the n routed
+// tokens the balance loss  E/(k n^2) sum_e counts_e sum_t p_te.  With
+// c_e = dloss E counts_e/(k n^2), the logits' gradient is
+//   p_e (c_e - sum p c)  +  the chosen weights' part, which is
+//   w_j (dw_j - sum w dw) at the chosen experts for weights over their sum, and
+//   p_e ([e chosen] dw_e - sum_chosen p dw) otherwise.
+//
+// One warp owns a token; a lane keeps kPer of its logits in registers, so the
+// logits are read once each way.  Choosing is by an order-preserving integer
+// key: one warp-wide integer maximum gives the value and one warp-wide minimum
+// over the lanes that hold it gives the lowest index.  A lane also keeps the
+// sums over its tokens of the probabilities of its experts; they are added up
+// per block and then over the blocks in a fixed order, so the loss has the
+// same bits in every run.
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "train_common.cuh"
+
+namespace {
+
+using namespace mxq;
+
+__device__ unsigned int g_route_status = 0;
+
+constexpr int kMaxK = 32;  // a chosen expert per lane
+
+// Unsigned key in the order of the values: 0 for -inf and NaN (never chosen),
+// the same for both zeros.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  const uint32_t k = (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+  return x > -CUDART_INF_F ? k : 0u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
+}
+
+// Expert of register i of a lane: vectors of kV consecutive experts per lane.
+template <int kV>
+__device__ __forceinline__ int expert_of(int i, int lane) {
+  return (i / kV) * (32 * kV) + lane * kV + i % kV;
+}
+
+// The lane's logits of one row; experts past E read as -inf.
+template <typename T, int kPer, int kV>
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&x)[kPer]) {
+#pragma unroll
+  for (int c = 0; c < kPer / kV; ++c) {
+    const int e0 = expert_of<kV>(c * kV, lane);
+    if (e0 + kV <= E) {
+      const Vec<T, kV> v = *reinterpret_cast<const Vec<T, kV>*>(row + e0);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) x[c * kV + j] = widen(v.v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kV; ++j) x[c * kV + j] = e0 + j < E ? widen(row[e0 + j]) : -CUDART_INF_F;
+    }
+  }
+}
+
+struct RouteShape {
+  int64_t tokens, ld;
+  int E, k, renorm;
+};
+
+// Sums over the blocks in block order: counts, routed tokens and loss.
+// part_p/part_c are [blocks, E], part_n [blocks].
+__device__ void join_blocks(const RouteShape s, int blocks, const float* part_p, const int32_t* part_c,
+                            const int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out,
+                            float* red) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  int n = 0;
+  for (int b = 0; b < blocks; ++b) n += part_n[b];
+  float local = 0.0f;
+  for (int e = tid; e < s.E; e += nt) {
+    float p = 0.0f;
+    int c = 0;
+#pragma unroll 8
+    for (int b = 0; b < blocks; ++b) {
+      p += part_p[static_cast<int64_t>(b) * s.E + e];
+      c += part_c[static_cast<int64_t>(b) * s.E + e];
+    }
+    counts[e] = c;
+    local += static_cast<float>(c) * p;
+  }
+  local = warp_sum(local);
+  if ((tid & 31) == 0) red[tid >> 5] = local;
+  __syncthreads();
+  if (tid == 0) {
+    float sum = 0.0f;
+    for (int w = 0; w < nt / 32; ++w) sum += red[w];
+    const float fn = static_cast<float>(n);
+    *loss = n > 0 ? sum * (static_cast<float>(s.E) / (static_cast<float>(s.k) * fn * fn)) : 0.0f;
+    *n_out = n;
+  }
+}
+
+template <typename T, int kPer, int kV, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1)
+    route_kernel(const T* __restrict__ logits, const RouteShape s, const uint8_t* __restrict__ mask,
+                 float* __restrict__ weights, int32_t* __restrict__ ids, float* part_p,
+                 int32_t* part_c, int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kWarps = kThreads / 32;
+  int32_t* hist = reinterpret_cast<int32_t*>(smem);         // [E]
+  float* sums = reinterpret_cast<float*>(hist + s.E);       // [E]
+  __shared__ int32_t routed_tokens;
+  __shared__ float red[kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  for (int e = tid; e < s.E; e += kThreads) hist[e] = 0, sums[e] = 0.0f;
+  if (tid == 0) routed_tokens = 0;
+  __syncthreads();
+  pdl_wait();
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
+  const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
+  float acc[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
+  int routed_here = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < s.tokens; t += step) {
+    const T* row = logits + t * s.ld;
+    float x[kPer];
+    if (in_buf(row, s.E * sizeof(T), logits, in_bytes, &g_route_status)) load_row<T, kPer, kV>(row, s.E, lane, x);
+    uint32_t key[kPer], best = 0;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      key[i] = order_key(x[i]);
+      best = max(best, key[i]);
+      nan |= x[i] != x[i];
+    }
+    best = __reduce_max_sync(0xFFFFFFFFu, best);
+    const bool routed = (mask == nullptr || mask[t] != 0) && (best != 0u || __any_sync(0xFFFFFFFFu, nan));
+    int my_id = -1;
+    float my_w = 0.0f;
+    if (routed) {
+      ++routed_here;
+      const float top = best != 0u ? key_value(best) : -CUDART_INF_F;
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        x[i] = exp2_ftz((x[i] - top) * kLog2E);
+        if (expert_of<kV>(i, lane) >= s.E) x[i] = 0.0f;
+        sum += x[i];
+      }
+      const float inv = 1.0f / warp_sum(sum);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
+      for (int j = 0; j < s.k; ++j) {
+        uint32_t local = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (key[i] > local) local = key[i], at = expert_of<kV>(i, lane);
+        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, local);
+        if (m == 0u) break;
+        const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, local == m ? static_cast<uint32_t>(at) : ~0u));
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if (expert_of<kV>(i, lane) == e) key[i] = 0u;
+        if (lane == j) {
+          my_id = e;
+          my_w = exp2_ftz((key_value(m) - top) * kLog2E);
+        }
+      }
+      my_w *= inv;  // NaN for a row with NaN or +inf, over the chosen ones' sum too
+      if (s.renorm) my_w /= warp_sum(my_w);
+      if (my_id < 0) my_w = 0.0f;
+      if (my_id >= 0) atomicAdd(&hist[my_id], 1);
+    }
+    if (lane < s.k && in_buf(weights + t * s.k + lane, 4, weights, out_bytes, &g_route_status) &&
+        in_buf(ids + t * s.k + lane, 4, ids, out_bytes, &g_route_status)) {
+      weights[t * s.k + lane] = my_w;
+      ids[t * s.k + lane] = my_id;
+    }
+  }
+  if (lane == 0 && routed_here) atomicAdd(&routed_tokens, routed_here);
+  // the warps' sums, one warp after the other
+  for (int w = 0; w < kWarps; ++w) {
+    if (warp == w) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = expert_of<kV>(i, lane);
+        if (e < s.E) sums[e] += acc[i];
+      }
+    }
+    __syncthreads();
+  }
+  if (gridDim.x == 1) {
+    join_blocks(s, 1, sums, hist, &routed_tokens, counts, loss, n_out, red);
+    return;
+  }
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * s.E;
+  for (int e = tid; e < s.E; e += kThreads) {
+    part_p[base + e] = sums[e];
+    part_c[base + e] = hist[e];
+  }
+  if (tid == 0) part_n[blockIdx.x] = routed_tokens;
+}
+
+constexpr int kJoinThreads = 1024;
+__global__ void __launch_bounds__(kJoinThreads)
+    route_join_kernel(const RouteShape s, int blocks, const float* part_p, const int32_t* part_c,
+                      const int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out) {
+  __shared__ float red[kJoinThreads / 32];
+  pdl_wait();
+  join_blocks(s, blocks, part_p, part_c, part_n, counts, loss, n_out, red);
+}
+
+template <typename T, int kPer, int kV, int kThreads>
+__global__ void __launch_bounds__(kThreads)
+    route_backward_kernel(const T* __restrict__ logits, const RouteShape s, const uint8_t* __restrict__ mask,
+                          const int32_t* __restrict__ ids, const int32_t* __restrict__ counts,
+                          const int32_t* __restrict__ n_in, const float* __restrict__ dweights,
+                          const float* __restrict__ dloss, T* __restrict__ dlogits, int64_t ldd) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the chosen experts' part of a row, zero between rows
+  constexpr int kRow = kPer * 32;
+  float* chosen = reinterpret_cast<float*>(smem) + warp * kRow;
+  for (int e = lane; e < kRow; e += 32) chosen[e] = 0.0f;
+  __syncwarp();
+  pdl_wait();
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
+  const uint64_t out_bytes = (static_cast<uint64_t>(s.tokens - 1) * ldd + s.E) * sizeof(T);
+  float c[kPer];
+  {
+    const float n = static_cast<float>(*n_in);
+    const float f = dloss != nullptr && n > 0.0f ? *dloss * (static_cast<float>(s.E) / (static_cast<float>(s.k) * n * n)) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = expert_of<kV>(i, lane);
+      c[i] = dloss != nullptr && e < s.E ? f * static_cast<float>(counts[e]) : 0.0f;
+    }
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < s.tokens; t += step) {
+    const T* row = logits + t * s.ld;
+    float x[kPer];
+    if (in_buf(row, s.E * sizeof(T), logits, in_bytes, &g_route_status)) load_row<T, kPer, kV>(row, s.E, lane, x);
+    float top = -CUDART_INF_F;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      top = fmaxf(top, x[i]);  // skips NaN
+      nan |= x[i] != x[i];
+    }
+    top = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(top)));
+    const bool some = top > -CUDART_INF_F;  // false for NaN, the value of key 0
+    const bool routed = (mask == nullptr || mask[t] != 0) && (some || __any_sync(0xFFFFFFFFu, nan));
+    T* out = dlogits + t * ldd;
+    if (routed) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        x[i] = exp2_ftz((x[i] - top) * kLog2E);
+        if (expert_of<kV>(i, lane) >= s.E) x[i] = 0.0f;
+        sum += x[i];
+      }
+      const float inv = 1.0f / warp_sum(sum);
+      float pc = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        x[i] *= inv;
+        pc = fmaf(x[i], c[i], pc);
+      }
+      int e = -1;
+      float w = 0.0f, dw = 0.0f;
+      if (dweights != nullptr && lane < s.k) {
+        e = ids[t * s.k + lane];
+        if (e < 0 || e >= s.E) e = -1;
+        if (e >= 0) {
+          dw = dweights[t * s.k + lane];
+          w = exp2_ftz((widen(row[e]) - top) * kLog2E);
+        }
+      }
+      float part = 0.0f;
+      w *= inv;
+      if (s.renorm) {
+        const float all = warp_sum(w);
+        if (e >= 0) w /= all;
+        const float dot = warp_sum(w * dw);
+        part = w * (dw - dot);
+      } else {
+        part = w * dw;
+        pc += part;
+      }
+      if (e >= 0) chosen[e] = part;
+      __syncwarp();
+      const float total = warp_sum(pc);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = fmaf(x[i], c[i] - total, chosen[expert_of<kV>(i, lane)]);
+      __syncwarp();
+      if (e >= 0) chosen[e] = 0.0f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = 0.0f;
+    }
+    if (!in_buf(out, s.E * sizeof(T), dlogits, out_bytes, &g_route_status)) continue;
+#pragma unroll
+    for (int q = 0; q < kPer / kV; ++q) {
+      const int e0 = expert_of<kV>(q * kV, lane);
+      if (e0 + kV <= s.E) {
+        Vec<T, kV> v;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) v.v[j] = narrow<T>(x[q * kV + j]);
+        *reinterpret_cast<Vec<T, kV>*>(out + e0) = v;
+      } else {
+#pragma unroll
+        for (int j = 0; j < kV; ++j)
+          if (e0 + j < s.E) out[e0 + j] = narrow<T>(x[q * kV + j]);
+      }
+    }
+  }
+}
+
+// kPer registers of logits per lane hold up to 32 * kPer experts; the block is
+// as large as the registers allow, so that there are few partial sums.
+template <int kPer>
+constexpr int route_threads() {
+  return kPer <= 8 ? 1024 : kPer == 16 ? 512 : 256;
+}
+constexpr int kBackThreads = 256;
+
+struct RouteCall {
+  const void* logits;
+  RouteShape s;
+  const uint8_t* mask;
+  float* weights;
+  int32_t *ids, *counts;
+  float* loss;
+  int32_t* n;
+  uint8_t* workspace;
+  // backward
+  const float *dweights, *dloss;
+  void* dlogits;
+  int64_t ldd;
+  int sms;
+  cudaStream_t stream;
+};
+
+int route_blocks(int64_t tokens, int warps, int sms) {
+  const int64_t want = ceil_div(tokens, warps);
+  return static_cast<int>(want < 1 ? 1 : want < sms ? want : sms);
+}
+
+template <typename T, int kPer, int kV>
+int launch_route(const RouteCall& a) {
+  constexpr int kThreads = route_threads<kPer>();
+  const int blocks = route_blocks(a.s.tokens, kThreads / 32, a.sms);
+  float* part_p = reinterpret_cast<float*>(a.workspace);
+  int32_t* part_c = reinterpret_cast<int32_t*>(part_p + static_cast<int64_t>(blocks) * a.s.E);
+  int32_t* part_n = part_c + static_cast<int64_t>(blocks) * a.s.E;
+  int rc = launch_pdl(route_kernel<T, kPer, kV, kThreads>, blocks, kThreads, a.s.E * 8, a.stream,
+                      static_cast<const T*>(a.logits), a.s, a.mask, a.weights, a.ids, part_p, part_c, part_n,
+                      a.counts, a.loss, a.n);
+  if (rc != MXQ_OK || blocks == 1) return rc;
+  return launch_pdl(route_join_kernel, 1, kJoinThreads, 0, a.stream, a.s, blocks, part_p, part_c, part_n,
+                    a.counts, a.loss, a.n);
+}
+
+template <typename T, int kPer, int kV>
+int launch_route_backward(const RouteCall& a) {
+  const int64_t want = ceil_div(a.s.tokens, kBackThreads / 32);
+  const int64_t cap = static_cast<int64_t>(a.sms) * (2048 / kBackThreads);
+  return launch_pdl(route_backward_kernel<T, kPer, kV, kBackThreads>, static_cast<unsigned>(want < cap ? want : cap),
+                    kBackThreads, kPer * 32 * 4 * (kBackThreads / 32), a.stream, static_cast<const T*>(a.logits), a.s,
+                    a.mask, a.ids, a.counts, a.n, a.dweights, a.dloss, static_cast<T*>(a.dlogits), a.ldd);
+}
+
+template <typename T, int kPer, int kV, bool kBack>
+int launch_one(const RouteCall& a) {
+  if constexpr (kBack)
+    return launch_route_backward<T, kPer, kV>(a);
+  else
+    return launch_route<T, kPer, kV>(a);
+}
+
+// Vectors of 4 elements (2 for up to 64 experts) where base and row pitch are
+// aligned to them, else single elements.
+template <typename T, bool kBack>
+int launch_typed(const RouteCall& a) {
+  const uint64_t pitch = static_cast<uint64_t>(a.s.ld) * sizeof(T);
+  const uint64_t dpitch = kBack ? static_cast<uint64_t>(a.ldd) * sizeof(T) : 0;
+  const int align = common_alignment({address_of(a.logits), pitch, kBack ? address_of(a.dlogits) : 0, dpitch});
+  const bool v4 = align >= static_cast<int>(4 * sizeof(T)), v2 = align >= static_cast<int>(2 * sizeof(T));
+  const int E = a.s.E;
+  if (E <= 64) return v2 ? launch_one<T, 2, 2, kBack>(a) : launch_one<T, 2, 1, kBack>(a);
+  if (E <= 128) return v4 ? launch_one<T, 4, 4, kBack>(a) : launch_one<T, 4, 1, kBack>(a);
+  if (E <= 256) return v4 ? launch_one<T, 8, 4, kBack>(a) : launch_one<T, 8, 1, kBack>(a);
+  if (E <= 512) return v4 ? launch_one<T, 16, 4, kBack>(a) : launch_one<T, 16, 1, kBack>(a);
+  return v4 ? launch_one<T, 32, 4, kBack>(a) : launch_one<T, 32, 1, kBack>(a);
+}
+
+int check_route_shape(int dtype, int64_t tokens, int32_t experts, int32_t k, int64_t ld) {
+  if (dtype != MXQ_F32 && dtype != MXQ_BF16) return MXQ_EBADDTYPE;
+  if (tokens < 0 || tokens > INT32_MAX || experts < 1 || experts > MXQ_MAX_GROUPS || k < 1 || k > experts ||
+      k > kMaxK || ld < experts || ld > INT32_MAX)
+    return MXQ_EBADSHAPE;
+  return MXQ_OK;
+}
+
+constexpr int kMaxBlocks = 256;  // partial sums held in the workspace
+
+}  // namespace
+
+namespace mxq {
+int route_status_read(unsigned int* out, bool clear) {
+  return read_status_word(g_route_status, out, clear);
+}
+}  // namespace mxq
+
+extern "C" int64_t mxq_moe_route_workspace(int32_t experts) {
+  if (experts < 1 || experts > MXQ_MAX_GROUPS) return MXQ_EBADSHAPE;
+  return (static_cast<int64_t>(experts) * 8 + 4) * kMaxBlocks;
+}
+
+extern "C" int mxq_moe_route(const void* logits, int dtype, int64_t tokens, int32_t experts, int64_t ld, int32_t k,
+                             const uint8_t* mask, int renorm, float* weights, int32_t* ids, int32_t* counts,
+                             float* loss, int32_t* routed, uint8_t* workspace, int64_t workspace_bytes,
+                             cudaStream_t stream) {
+  int rc = check_route_shape(dtype, tokens, experts, k, ld);
+  if (rc != MXQ_OK) return rc;
+  const int64_t need = mxq_moe_route_workspace(experts);
+  if (workspace_bytes < need) return MXQ_EBADSHAPE;
+  if (!counts || !loss || !routed || !workspace || (tokens > 0 && (!logits || !weights || !ids))) return MXQ_ENULL;
+  const int es = element_bytes(dtype);
+  if (!aligned_to(logits, es) || !aligned_to(weights, 4) || !aligned_to(ids, 4) || !aligned_to(counts, 4) ||
+      !aligned_to(loss, 4) || !aligned_to(routed, 4) || !aligned_to(workspace, 16))
+    return MXQ_EALIGN;
+  const uint64_t chosen = static_cast<uint64_t>(tokens) * k * 4;
+  const ByteRange out[6] = {range_of(weights, chosen), range_of(ids, chosen), range_of(counts, 4ull * experts),
+                            range_of(loss, 4), range_of(routed, 4), range_of(workspace, need)};
+  const ByteRange in[2] = {range_of(logits, pitched_bytes(tokens, experts, ld, es)), range_of(mask, tokens)};
+  if (outputs_overlap(out, 6, in, 2)) return MXQ_EOVERLAP;
+  const int sms = sm_count_current_device(nullptr);
+  if (sms <= 0) return MXQ_ECUDA;
+  RouteCall a = {};
+  a.logits = logits;
+  a.s = {tokens, ld, experts, k, renorm != 0};
+  a.mask = mask;
+  a.weights = weights;
+  a.ids = ids;
+  a.counts = counts;
+  a.loss = loss;
+  a.n = routed;
+  a.workspace = workspace;
+  a.sms = sms < kMaxBlocks ? sms : kMaxBlocks;
+  a.stream = stream;
+  return dtype == MXQ_F32 ? launch_typed<float, false>(a) : launch_typed<bf16_t, false>(a);
+}
+
+extern "C" int mxq_moe_route_backward(const void* logits, int dtype, int64_t tokens, int32_t experts, int64_t ld,
+                                      int32_t k, const uint8_t* mask, int renorm, const int32_t* ids,
+                                      const int32_t* counts, const int32_t* routed, const float* dweights,
+                                      const float* dloss, void* dlogits, int64_t ldd, cudaStream_t stream) {
+  int rc = check_route_shape(dtype, tokens, experts, k, ld);
+  if (rc != MXQ_OK) return rc;
+  if (ldd < experts || ldd > INT32_MAX) return MXQ_EBADSHAPE;
+  if (tokens == 0) return MXQ_OK;
+  if (!logits || !ids || !counts || !routed || !dlogits) return MXQ_ENULL;
+  const int es = element_bytes(dtype);
+  if (!aligned_to(logits, es) || !aligned_to(dlogits, es) || !aligned_to(ids, 4) || !aligned_to(counts, 4) ||
+      !aligned_to(routed, 4) || !aligned_to(dweights, 4) || !aligned_to(dloss, 4))
+    return MXQ_EALIGN;
+  const uint64_t chosen = static_cast<uint64_t>(tokens) * k * 4;
+  const ByteRange out[1] = {range_of(dlogits, pitched_bytes(tokens, experts, ldd, es))};
+  const ByteRange in[7] = {range_of(logits, pitched_bytes(tokens, experts, ld, es)), range_of(mask, tokens),
+                           range_of(ids, chosen), range_of(counts, 4ull * experts), range_of(routed, 4),
+                           range_of(dweights, chosen), range_of(dloss, 4)};
+  if (outputs_overlap(out, 1, in, 7)) return MXQ_EOVERLAP;
+  const int sms = sm_count_current_device(nullptr);
+  if (sms <= 0) return MXQ_ECUDA;
+  RouteCall a = {};
+  a.logits = logits;
+  a.s = {tokens, ld, experts, k, renorm != 0};
+  a.mask = mask;
+  a.ids = const_cast<int32_t*>(ids);
+  a.counts = const_cast<int32_t*>(counts);
+  a.n = const_cast<int32_t*>(routed);
+  a.dweights = dweights;
+  a.dloss = dloss;
+  a.dlogits = dlogits;
+  a.ldd = ldd;
+  a.sms = sms;
+  a.stream = stream;
+  return dtype == MXQ_F32 ? launch_typed<float, true>(a) : launch_typed<bf16_t, true>(a);
+}

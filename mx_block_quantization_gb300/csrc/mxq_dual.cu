@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "mxq.h"
@@ -764,6 +765,9 @@ int compose_status_read(unsigned int* out, bool clear);  // mxq_compose.cu
 int cols_status_read(unsigned int* out, bool clear);     // mx_cols_tma.cu
 int packed_status_read(unsigned int* out, bool clear);   // mx_packed.cu
 int mma_status_read(unsigned int* out, bool clear);      // mxq_mma_check.cu
+int route_status_read(unsigned int* out, bool clear);      // moe_route.cu
+int exchange_status_read(unsigned int* out, bool clear);   // moe_exchange.cu
+int embedding_status_read(unsigned int* out, bool clear);  // embedding.cu
 }
 
 // The device status word is the OR of the per-file words of the kernels.
@@ -788,7 +792,13 @@ extern "C" int mxq_device_status(uint32_t* out, int clear) {
   unsigned int g = 0;
   rc = mxq::mma_status_read(&g, clear != 0);
   if (rc != MXQ_OK) return rc;
-  *out = v | w | c | t | k | g;
+  v |= w | c | t | k | g;
+  for (auto* read : {mxq::route_status_read, mxq::exchange_status_read, mxq::embedding_status_read}) {
+    rc = read(&g, clear != 0);
+    if (rc != MXQ_OK) return rc;
+    v |= g;
+  }
+  *out = v;
   return MXQ_OK;
 }
 

@@ -1,0 +1,109 @@
+// train_common.cuh -- element types, vector access and warp sums shared by the
+// training kernels (routing, exchange, embedding table, orthogonalisation).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <initializer_list>
+
+#include "mxq.h"
+#include "mxq_check.cuh"
+#include "mxq_device.cuh"
+#include "mxq_host.h"
+
+namespace mxq {
+
+// bf16 values are handled as their bits; widening is exact, rounding is to
+// nearest even.
+using bf16_t = uint16_t;
+
+__device__ __forceinline__ float widen(float v) { return v; }
+__device__ __forceinline__ float widen(bf16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) {
+  return v;
+}
+template <>
+__device__ __forceinline__ bf16_t narrow<bf16_t>(float v) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// kN elements of T as one access of kN * sizeof(T) bytes (at most 16).
+template <typename T, int kN>
+struct alignas(sizeof(T) * kN) Vec {
+  T v[kN];
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+  return v;
+}
+
+// 2^x, subnormal results flushed to zero.
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2E = 1.4426950408889634f;
+
+// The widest power of two of bytes, up to 16, that divides every value.
+inline int common_alignment(std::initializer_list<uint64_t> values) {
+  uint64_t all = 16;
+  for (uint64_t v : values) all |= v;
+  return static_cast<int>(all & (~all + 1));
+}
+inline uint64_t address_of(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Bytes of a [rows, cols] matrix with `ld` elements between its rows.
+inline uint64_t pitched_bytes(int64_t rows, int64_t cols, int64_t ld, int esize) {
+  return rows > 0 ? (static_cast<uint64_t>(rows - 1) * ld + cols) * esize : 0;
+}
+
+inline int element_bytes(int dtype) { return dtype == MXQ_F32 ? 4 : 2; }
+
+// Launch with programmatic stream serialization (see allow_programmatic_launch).
+template <typename... Params, typename... Args>
+inline int launch_pdl(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                      cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  allow_programmatic_launch(&cfg, &attr);
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) == cudaSuccess ? MXQ_OK : MXQ_ECUDA;
+}
+
+// The output ranges must overlap neither one another nor an input; inputs may
+// share storage.
+inline bool outputs_overlap(const ByteRange* out, int n_out, const ByteRange* in, int n_in) {
+  if (ranges_overlap(out, n_out)) return true;
+  for (int i = 0; i < n_in; ++i)
+    for (int o = 0; o < n_out; ++o) {
+      const ByteRange two[2] = {out[o], in[i]};
+      if (ranges_overlap(two, 2)) return true;
+    }
+  return false;
+}
+
+inline ByteRange range_of(const void* p, uint64_t bytes) { return {address_of(p), p ? bytes : 0}; }
+
+// Reads (and with `clear` zeroes) a kernel file's status word.
+inline int read_status_word(const unsigned int& symbol, unsigned int* out, bool clear) {
+  if (cudaMemcpyFromSymbol(out, symbol, sizeof *out) != cudaSuccess) return MXQ_ECUDA;
+  const unsigned int zero = 0;
+  if (clear && cudaMemcpyToSymbol(symbol, &zero, sizeof zero) != cudaSuccess) return MXQ_ECUDA;
+  return MXQ_OK;
+}
+
+}  // namespace mxq

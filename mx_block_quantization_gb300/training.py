@@ -1,0 +1,352 @@
+"""Operators of a mixture-of-experts training step around the MXFP8 cast.
+
+Routing with its balance loss (:func:`moe_route`), the exchange of rows with the
+128-row expert groups that :func:`quantize_2d_dual` takes (:func:`moe_plan`,
+:func:`moe_dispatch`, :func:`moe_combine`), the embedding table
+(:func:`embedding`) and their gradients, each a call of its own.  The functions
+marshal torch CUDA tensors into the C ABI of ``include/mxq.h``, which states
+each operation; there is no CPU path.
+
+Matrices may have strided rows (unit column stride).  With ``stream`` a call runs
+on that stream, and the outputs and workspaces that it allocates belong to it;
+otherwise it runs on the current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import contextlib
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import BF16, F32, OK, MxqError, lib
+
+_CODES = {torch.float32: F32, torch.bfloat16: BF16}
+_NOTHING = contextlib.nullcontext()
+
+
+class Routing(NamedTuple):
+    weights: torch.Tensor  # float32 [T, k]
+    ids: torch.Tensor      # int32 [T, k], -1 where there is no expert
+    counts: torch.Tensor   # int32 [E]
+    loss: torch.Tensor     # float32 []
+    routed: torch.Tensor   # int32 []: tokens that take part
+
+
+class MoePlan(NamedTuple):
+    offs: torch.Tensor    # int32 [E]: cumulative group ends, multiples of 128
+    slots: torch.Tensor   # int32 [T, k]: row of each assignment, -1 for none
+    source: torch.Tensor  # int32 [M]: assignment of each row, -1 for none
+
+
+def _code(t, name):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    return code
+
+
+def _matrix(t, name, rows=None, cols=None, device=None):
+    """Row pitch of a 2-D CUDA tensor with unit column stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    m, n = t.shape
+    if (rows is not None and m != rows) or (cols is not None and n != cols):
+        raise ValueError(f"{name} must be [{m if rows is None else rows}, {n if cols is None else cols}]")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if m <= 1 or n == 0:
+        if n > 1 and t.stride(1) != 1:
+            raise ValueError(f"{name} must have unit column stride")
+        return max(n, 1)
+    ld = t.stride(0)
+    if (n > 1 and t.stride(1) != 1) or ld < n:
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return ld
+
+
+def _flat(t, name, dtype, shape, device):
+    """A contiguous CUDA tensor of one type and shape."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _mask_pointer(mask, tokens, device):
+    if mask is None:
+        return None
+    return _flat(mask, "mask", torch.uint8 if mask.dtype == torch.uint8 else torch.bool, (tokens,), device)
+
+
+def _on(device, stream):
+    """Context in which a call's allocations and launches belong to its stream."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return _NOTHING
+
+
+def _stream(device, stream):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _check(rc, what):
+    if rc != OK:
+        raise MxqError(rc, what)
+
+
+def _workspace(size, what, device):
+    """(tensor, pointer, bytes) of a call's workspace from the size the library asks for."""
+    if size < 0:
+        raise MxqError(int(size), what)
+    t = torch.empty(size, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), size
+
+
+# ---------------------------------------------------------------------------
+# routing
+# ---------------------------------------------------------------------------
+
+def moe_route(logits, k: int, *, mask=None, renorm: bool = True, out: Optional[Routing] = None,
+              stream=None) -> Routing:
+    """The k experts of each token from its logits [T, E] (fp32 or bf16), with
+    softmax weights (over the chosen experts' sum with ``renorm``), the tokens of
+    each expert and the balance loss.  ``mask``: bool or uint8 [T], false leaves
+    the token out.  A logit of -inf marks an expert that must not be chosen."""
+    ld = _matrix(logits, "logits")
+    code = _code(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    mask_p = _mask_pointer(mask, T, dev)
+    L = lib()
+    with _on(dev, stream):
+        if out is None:
+            # one allocation for the small results: counts, loss, routed
+            small = torch.empty(E + 2, dtype=torch.int32, device=dev)
+            out = Routing(torch.empty((T, k), dtype=torch.float32, device=dev),
+                          torch.empty((T, k), dtype=torch.int32, device=dev), small[:E],
+                          small[E].view(torch.float32), small[E + 1])
+        w = _flat(out.weights, "weights", torch.float32, (T, k), dev)
+        i = _flat(out.ids, "ids", torch.int32, (T, k), dev)
+        c = _flat(out.counts, "counts", torch.int32, (E,), dev)
+        l = _flat(out.loss, "loss", torch.float32, (), dev)
+        n = _flat(out.routed, "routed", torch.int32, (), dev)
+        ws, wp, wb = _workspace(L.mxq_moe_route_workspace(E), "mxq_moe_route", dev)
+        _check(L.mxq_moe_route(logits.data_ptr(), code, T, E, ld, k, mask_p, int(renorm), w, i, c, l, n, wp, wb,
+                               _stream(dev, stream)), "mxq_moe_route")
+    return out
+
+
+def moe_route_backward(logits, routing: Routing, dweights=None, dloss=None, *, mask=None,
+                       renorm: bool = True, out=None, stream=None):
+    """Gradient of the logits from those of the weights [T, k] and of the loss []
+    (fp32; None for zero); logits, mask and renorm as in :func:`moe_route`."""
+    ld = _matrix(logits, "logits")
+    code = _code(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    k = routing.ids.shape[-1]
+    i = _flat(routing.ids, "ids", torch.int32, (T, k), dev)
+    c = _flat(routing.counts, "counts", torch.int32, (E,), dev)
+    n = _flat(routing.routed, "routed", torch.int32, (), dev)
+    dw = None if dweights is None else _flat(dweights, "dweights", torch.float32, (T, k), dev)
+    dl = None if dloss is None else _flat(dloss, "dloss", torch.float32, (), dev)
+    mask_p = _mask_pointer(mask, T, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+        ldd = _matrix(out, "out", T, E, dev)
+        if out.dtype != logits.dtype:
+            raise ValueError("out must have the logits' type")
+        _check(lib().mxq_moe_route_backward(logits.data_ptr(), code, T, E, ld, k, mask_p, int(renorm), i, c, n, dw, dl,
+                                            out.data_ptr(), ldd, _stream(dev, stream)), "mxq_moe_route_backward")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# exchange
+# ---------------------------------------------------------------------------
+
+def moe_rows(tokens: int, k: int, experts: int) -> int:
+    """Rows that hold every routing of these sizes in groups of whole 128 rows."""
+    m = lib().mxq_moe_rows(tokens, k, experts)
+    if m < 0:
+        raise MxqError(int(m), "mxq_moe_rows")
+    return int(m)
+
+
+def moe_plan(ids, experts: int, *, rows: Optional[int] = None, out: Optional[MoePlan] = None,
+             stream=None) -> MoePlan:
+    """Expert groups of the assignments ids (int32 [T, k], -1: not routed), each
+    in token order and filled up to a multiple of 128 rows.  ``rows`` (at least
+    :func:`moe_rows`, a multiple of 128) sets M."""
+    if ids.dim() != 2:
+        raise ValueError("ids must be 2-D")
+    T, k = ids.shape
+    dev = ids.device
+    p = _flat(ids, "ids", torch.int32, (T, k), dev)
+    L = lib()
+    M = out.source.numel() if out is not None else moe_rows(T, k, experts) if rows is None else int(rows)
+    with _on(dev, stream):
+        if out is None:
+            out = MoePlan(torch.empty((experts,), dtype=torch.int32, device=dev),
+                          torch.empty((T, k), dtype=torch.int32, device=dev),
+                          torch.empty((max(M, 0),), dtype=torch.int32, device=dev))
+        o = _flat(out.offs, "offs", torch.int32, (experts,), dev)
+        s = _flat(out.slots, "slots", torch.int32, (T, k), dev)
+        m = _flat(out.source, "source", torch.int32, (M,), dev)
+        ws, wp, wb = _workspace(L.mxq_moe_plan_workspace(T, k, experts), "mxq_moe_plan", dev)
+        _check(L.mxq_moe_plan(p, T, k, experts, M, o, s, m, wp, wb, _stream(dev, stream)), "mxq_moe_plan")
+    return out
+
+
+def _plan_pointers(plan, device):
+    if plan.slots.dim() != 2:
+        raise ValueError("slots must be 2-D")
+    T, k = plan.slots.shape
+    M = plan.source.numel()
+    return T, k, M, _flat(plan.slots, "slots", torch.int32, (T, k), device), \
+        _flat(plan.source, "source", torch.int32, (M,), device)
+
+
+def moe_dispatch(x, plan: MoePlan, *, out=None, stream=None):
+    """Rows [M, D] of the expert groups from the tokens' rows x [T, D] (fp32 or
+    bf16); rows without an assignment are zero."""
+    dev = x.device
+    code = _code(x, "x")
+    T, k, M, slots, source = _plan_pointers(plan, dev)
+    ldx = _matrix(x, "x", T)
+    D = x.shape[1]
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, D), dtype=x.dtype, device=dev)
+        ldr = _matrix(out, "out", M, D, dev)
+        if out.dtype != x.dtype:
+            raise ValueError("out must have x's type")
+        _check(lib().mxq_moe_dispatch(x.data_ptr(), code, T, D, ldx, k, slots, source, M, out.data_ptr(), ldr,
+                                      _stream(dev, stream)), "mxq_moe_dispatch")
+    return out
+
+
+def moe_combine(rows, plan: MoePlan, weights=None, *, out=None, stream=None):
+    """Each token's sum over its experts of weight times row: y [T, D] from rows
+    [M, D] and weights fp32 [T, k].  Without weights the plain sum, which is the
+    gradient of :func:`moe_dispatch`."""
+    dev = rows.device
+    code = _code(rows, "rows")
+    T, k, M, slots, _ = _plan_pointers(plan, dev)
+    ldr = _matrix(rows, "rows", M)
+    D = rows.shape[1]
+    w = None if weights is None else _flat(weights, "weights", torch.float32, (T, k), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, D), dtype=rows.dtype, device=dev)
+        ldy = _matrix(out, "out", T, D, dev)
+        if out.dtype != rows.dtype:
+            raise ValueError("out must have the rows' type")
+        _check(lib().mxq_moe_combine(rows.data_ptr(), code, M, D, ldr, T, k, slots, w, out.data_ptr(), ldy,
+                                     _stream(dev, stream)), "mxq_moe_combine")
+    return out
+
+
+def moe_combine_backward(dy, rows, plan: MoePlan, weights, *, out=None, stream=None):
+    """Gradients (drows [M, D], dweights fp32 [T, k]) of :func:`moe_combine` from
+    dy [T, D]."""
+    dev = rows.device
+    code = _code(rows, "rows")
+    T, k, M, slots, source = _plan_pointers(plan, dev)
+    ldr = _matrix(rows, "rows", M)
+    D = rows.shape[1]
+    ldy = _matrix(dy, "dy", T, D, dev)
+    if dy.dtype != rows.dtype:
+        raise ValueError("dy must have the rows' type")
+    w = _flat(weights, "weights", torch.float32, (T, k), dev)
+    with _on(dev, stream):
+        if out is None:
+            out = (torch.empty((M, D), dtype=rows.dtype, device=dev),
+                   torch.empty((T, k), dtype=torch.float32, device=dev))
+        drows, dweights = out
+        ldd = _matrix(drows, "drows", M, D, dev)
+        if drows.dtype != rows.dtype:
+            raise ValueError("drows must have the rows' type")
+        dw = _flat(dweights, "dweights", torch.float32, (T, k), dev)
+        _check(lib().mxq_moe_combine_backward(dy.data_ptr(), code, T, D, ldy, rows.data_ptr(), ldr, M, k, slots, source,
+                                              w, drows.data_ptr(), ldd, dw, _stream(dev, stream)),
+               "mxq_moe_combine_backward")
+    return drows, dweights
+
+
+# ---------------------------------------------------------------------------
+# embedding table
+# ---------------------------------------------------------------------------
+
+def _ids_pointer(ids):
+    if not ids.is_cuda:
+        raise ValueError("ids must be a CUDA tensor (no CPU path)")
+    if ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 or int64 tensor")
+    return ids.data_ptr(), ids.element_size()
+
+
+def embedding(ids, table, *, scale: float = 1.0, dtype=None, out=None, stream=None):
+    """scale * table[ids] for a table [V, D] (fp32 or bf16) and ids of any shape:
+    [*ids.shape, D] of type ``dtype`` (the table's unless given).  An id outside
+    the table gives zeros and sets DEV_BADINDEX in :func:`device_status`."""
+    p, ib = _ids_pointer(ids)
+    dev = table.device
+    if ids.device != dev:
+        raise ValueError(f"ids must be on {dev}")
+    code = _code(table, "table")
+    ldw = _matrix(table, "table")
+    V, D = table.shape
+    T = ids.numel()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((*ids.shape, D), dtype=table.dtype if dtype is None else dtype, device=dev)
+            ldy = max(D, 1)
+        else:
+            if dtype is not None and out.dtype != dtype:
+                raise ValueError(f"out must be {dtype}")
+            if out.shape != (*ids.shape, D):
+                raise ValueError(f"out must be {[*ids.shape, D]}")
+            ldy = _matrix(out if out.dim() == 2 else out.view(-1, D), "out", T, D, dev)
+        _check(lib().mxq_embedding(p, ib, T, table.data_ptr(), code, V, D, ldw, scale, out.data_ptr(), _code(out, "out"),
+                                   ldy, _stream(dev, stream)), "mxq_embedding")
+    return out
+
+
+def embedding_backward(ids, dy, rows: int, *, scale: float = 1.0, padding_idx: Optional[int] = None,
+                       dtype=None, out=None, stream=None):
+    """Gradient [rows, D] of the table of :func:`embedding` from dy [*ids.shape, D]:
+    scale times the sum of dy over the tokens of each id, in fp32 and in a fixed
+    order, of type ``dtype`` (dy's unless given).  Tokens with ``padding_idx`` are
+    left out."""
+    p, ib = _ids_pointer(ids)
+    dev = dy.device
+    if ids.device != dev:
+        raise ValueError(f"ids must be on {dev}")
+    if tuple(dy.shape[:-1]) != tuple(ids.shape):
+        raise ValueError(f"dy must be {[*ids.shape]} x D")
+    code = _code(dy, "dy")
+    D = dy.shape[-1]
+    T = ids.numel()
+    ldd = _matrix(dy if dy.dim() == 2 else dy.view(-1, D) if T and D else dy.reshape(T, D), "dy", T, D)
+    if padding_idx is not None and not 0 <= padding_idx < rows:
+        raise ValueError(f"padding_idx must be in [0, {rows})")
+    L = lib()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((rows, D), dtype=dy.dtype if dtype is None else dtype, device=dev)
+        elif dtype is not None and out.dtype != dtype:
+            raise ValueError(f"out must be {dtype}")
+        ldw = _matrix(out, "out", rows, D, dev)
+        ws, wp, wb = _workspace(L.mxq_embedding_backward_workspace(T, rows, D), "mxq_embedding_backward", dev)
+        _check(L.mxq_embedding_backward(p, ib, T, dy.data_ptr(), code, D, ldd, rows,
+                                        -1 if padding_idx is None else padding_idx, scale, out.data_ptr(),
+                                        _code(out, "out"), ldw, wp, wb, _stream(dev, stream)),
+               "mxq_embedding_backward")
+    return out

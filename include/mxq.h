@@ -391,6 +391,27 @@ int mxq_embedding_backward(const void *ids, int ids_bytes, int64_t tokens, const
                            uint8_t *workspace, int64_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * Newton-Schulz orthogonalisation of a momentum matrix, or of a stack of them:
+ *   X = g / (|g|_F + eps);  `steps` times  X <- (aI + bA + cA^2) X, A = X X^T
+ *   (X (aI + bA + cA^2), A = X^T X, for m > n: the same matrix);  out = scale * X.
+ *   g        [batch, m, n], rows ld and matrices `stride` elements apart.
+ *   out      bf16 [batch, m, n], rows ldo and matrices stride_o elements apart.
+ *   steps    1 .. 64; a, b, c finite; eps >= 0.  m, n at most 2^20, batch at
+ *            most 65535.
+ * The products take fp16 operands and accumulate in fp32 (tcgen05); the norm is
+ * fp32.  The iterates are taken to stay within |X| <= 1.5 in the spectral norm,
+ * as they do for the usual coefficients (3.4445, -4.775, 2.0315); beyond eight
+ * times that fp16 overflows.  Directions in which g is zero, or below 2^-12 of
+ * its norm, carry rounding noise that the iteration magnifies up to a^steps.
+ * Every internal wait is bounded (MXQ_DEV_TIMEOUT in the status word).
+ */
+int64_t mxq_orthogonalize_workspace(int64_t batch, int64_t m, int64_t n);
+int mxq_orthogonalize(const void *g, int dtype, int64_t batch, int64_t m, int64_t n, int64_t ld,
+                      int64_t stride, int32_t steps, float a, float b, float c, float eps,
+                      float scale, void *out, int64_t ldo, int64_t stride_o, uint8_t *workspace,
+                      int64_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Device status word of the current device: a sticky OR of MXQ_DEV_* bits set
  * by kernels since the last clear.  Writes it to *out and clears it when
  * `clear` is non-zero.  This call synchronizes the device (it reads device

@@ -25,8 +25,9 @@ Operations (sources by page title):
   (tcgen05) that reads the cast's bytes as stored: the consumer check of the
   blocked scale layouts and the K-group slabs.
 * :func:`moe_route`, :func:`moe_plan`, :func:`moe_dispatch`, :func:`moe_combine`,
-  :func:`embedding` and their gradients (``training.py``) -- the operators of a
-  mixture-of-experts training step whose grouped rows the dual-axis cast takes.
+  :func:`embedding` and their gradients, :func:`orthogonalize` (``training.py``) --
+  the operators of a mixture-of-experts training step whose grouped rows the
+  dual-axis cast takes.
 
 With MXQ_CHECKED=1 in the environment the binding loads libmxq_checked.so,
 the same kernels with every computed global access tested against its buffer.
@@ -125,7 +126,10 @@ def lib() -> ctypes.CDLL:
                 ("mxq_moe_combine_backward", ci, [vp, ci, i64, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i64, vp, vp]),
                 ("mxq_embedding", ci, [vp, ci, i64, vp, ci, i64, i64, i64, f32, vp, ci, i64, vp]),
                 ("mxq_embedding_backward_workspace", i64, [i64, i64, i64]),
-                ("mxq_embedding_backward", ci, [vp, ci, i64, vp, ci, i64, i64, i64, i64, f32, vp, ci, i64, vp, i64, vp])):
+                ("mxq_embedding_backward", ci, [vp, ci, i64, vp, ci, i64, i64, i64, i64, f32, vp, ci, i64, vp, i64, vp]),
+                ("mxq_orthogonalize_workspace", i64, [i64, i64, i64]),
+                ("mxq_orthogonalize", ci, [vp, ci, i64, i64, i64, i64, i64, i32, f32, f32, f32, f32, f32, vp, i64, i64,
+                                           vp, i64, vp])):
             fn = getattr(L, name)
             fn.restype, fn.argtypes = restype, argtypes
         L.mxq_last_device_status.restype = ctypes.c_int
@@ -586,7 +590,7 @@ def mxfp8_scaled_mm(a, sa, b, sb, *, out=None, stream=None):
 # ---------------------------------------------------------------------------
 
 _TRAINING = ("Routing", "MoePlan", "moe_route", "moe_route_backward", "moe_rows", "moe_plan", "moe_dispatch",
-             "moe_combine", "moe_combine_backward", "embedding", "embedding_backward")
+             "moe_combine", "moe_combine_backward", "embedding", "embedding_backward", "orthogonalize")
 
 
 def __getattr__(name):

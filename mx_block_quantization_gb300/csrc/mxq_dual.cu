@@ -768,6 +768,7 @@ int mma_status_read(unsigned int* out, bool clear);      // mxq_mma_check.cu
 int route_status_read(unsigned int* out, bool clear);      // moe_route.cu
 int exchange_status_read(unsigned int* out, bool clear);   // moe_exchange.cu
 int embedding_status_read(unsigned int* out, bool clear);  // embedding.cu
+int ortho_status_read(unsigned int* out, bool clear);      // orthogonalize.cu
 }
 
 // The device status word is the OR of the per-file words of the kernels.
@@ -793,7 +794,8 @@ extern "C" int mxq_device_status(uint32_t* out, int clear) {
   rc = mxq::mma_status_read(&g, clear != 0);
   if (rc != MXQ_OK) return rc;
   v |= w | c | t | k | g;
-  for (auto* read : {mxq::route_status_read, mxq::exchange_status_read, mxq::embedding_status_read}) {
+  for (auto* read : {mxq::route_status_read, mxq::exchange_status_read, mxq::embedding_status_read,
+                     mxq::ortho_status_read}) {
     rc = read(&g, clear != 0);
     if (rc != MXQ_OK) return rc;
     v |= g;

@@ -61,7 +61,7 @@ inline int common_alignment(std::initializer_list<uint64_t> values) {
 }
 inline uint64_t address_of(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Bytes of a [rows, cols] matrix with `ld` elements between its rows.
 inline uint64_t pitched_bytes(int64_t rows, int64_t cols, int64_t ld, int esize) {

@@ -350,3 +350,48 @@ def embedding_backward(ids, dy, rows: int, *, scale: float = 1.0, padding_idx: O
                                         _code(out, "out"), ldw, wp, wb, _stream(dev, stream)),
                "mxq_embedding_backward")
     return out
+
+
+# ---------------------------------------------------------------------------
+# orthogonalised updates
+# ---------------------------------------------------------------------------
+
+def _stacked(t, name):
+    """(batch, m, n, ld, stride) of a matrix or a stack of them, rows and matrices strided."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must be 2-D or 3-D")
+    if t.dim() == 2:
+        return 1, *t.shape, _matrix(t, name), 0
+    batch, m, n = t.shape
+    if t.numel() == 0:
+        return batch, m, n, max(n, 1), max(m * n, 1)
+    ld = _matrix(t[0], name)
+    stride = t.stride(0)
+    if batch > 1 and stride < (m - 1) * ld + n:
+        raise ValueError(f"{name} must have matrices that do not overlap")
+    return batch, m, n, ld, stride if batch > 1 else 0
+
+
+def orthogonalize(g, *, steps: int = 5, coefficients=(3.4445, -4.775, 2.0315), eps: float = 1e-7,
+                  scale: float = 1.0, out=None, stream=None):
+    """Newton-Schulz orthogonalisation of a momentum g [m, n], or of each matrix of
+    a stack [batch, m, n] (fp32 or bf16): ``steps`` times X <- (aI + bA + cA^2) X
+    with A = X X^T from X = g / (|g| + eps), as the Muon optimiser does.  Returns
+    scale * X in bf16."""
+    code = _code(g, "g")
+    batch, m, n, ld, stride = _stacked(g, "g")
+    a, b, c = coefficients
+    dev = g.device
+    L = lib()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
+        elif out.dtype != torch.bfloat16 or out.shape != g.shape or out.device != dev:
+            raise ValueError(f"out must be a bfloat16 tensor {list(g.shape)} on {dev}")
+        _, _, _, ldo, stride_o = _stacked(out, "out")
+        ws, wp, wb = _workspace(L.mxq_orthogonalize_workspace(batch, m, n), "mxq_orthogonalize", dev)
+        _check(L.mxq_orthogonalize(g.data_ptr(), code, batch, m, n, ld, stride, steps, a, b, c, eps, scale,
+                                   out.data_ptr(), ldo, stride_o, wp, wb, _stream(dev, stream)), "mxq_orthogonalize")
+    return out

@@ -6,20 +6,25 @@
 //
 // which drives the singular values towards 1.  A step is three products:
 //   gram     A = X X^T, symmetric: the tiles of one triangle are computed and
-//            stored twice, the second time transposed.  Its epilogue also stores
-//            A' = bI + cA, so that
-//   square   P = A' A + aI needs no second input; symmetric again, and
+//            stored twice, the second time transposed;
+//   square   P = aI + bA + cA A, symmetric again; and
 //   update   X <- P X (X P for a tall X).
 // All operands are fp16 with fp32 accumulation in tensor memory.  fp16 and not
 // bf16: both run at the same rate, the values are bounded (a spectral norm of
 // about 1.2 for the usual coefficients, so no element is larger), and the three
-// more mantissa bits make the rounding of an operand 2^-12 instead of 2^-9; with
-// bf16 the error of the result was of the size of its own rounding to bf16.
+// more mantissa bits make the rounding of an operand 2^-12 instead of 2^-9.
 // Powers of two keep small elements out of fp16's subnormal range: X is stored
-// times 2^13, A, A' and P times powers taken from the coefficients' bounds.
+// times 2^13, A and P times powers taken from the coefficients' bounds.
+//
+// The rounding that matters is that of the diagonals of A and P, which hold most
+// of their weight once the singular values draw together: what fp16 leaves of
+// them is kept in fp32 vectors, d_A and d_P, and put back in the epilogues of
+// the products that read them (A A = A'A' + d A' + A'd + d d with the rounded
+// A'; P X = P'X + d X).  The error of the result before its own rounding to bf16
+// (1.7e-3) is then 0.8e-3, instead of 1.7e-3 to 2.7e-3 without.
 // The iteration's map of a singular value has slopes of up to 1.6 around 1, and
 // the value of a small matrix hangs on few roundings, so its error can reach 1%
-// (sides of 1 to 24 in a simulation; 0.25% from a side of 48 on).  Sides of at
+// (sides up to 16 in a simulation; 0.14% from a side of 48 on).  Sides of at
 // most kSplitSide therefore carry every matrix as a pair, its rounding to fp16
 // and the rounding of what that leaves (22 bits in all), and every product is
 // the sum of three: high times high, high times low and low times high.
@@ -50,30 +55,37 @@ __device__ unsigned int g_ortho_status = 0;
 // norm and conversion
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 256;
-constexpr int kMaxParts = 256;  // partial sums of squares per matrix
+constexpr int kMaxParts = 2048;  // partial sums of squares per matrix
 constexpr float kXScale = 8192.0f;
 
 struct Matrix {
   int64_t batch, m, n, ld, stride;  // rows ld, matrices stride elements apart
 };
 
+// Blocks of a matrix take rows in turn; tx threads (a power of two) share a row.
 template <typename T, int kV>
 __global__ void __launch_bounds__(kThreads)
-    norm_kernel(const T* __restrict__ g, const Matrix a, int parts, float* __restrict__ sums) {
+    norm_kernel(const T* __restrict__ g, const Matrix a, int parts, int tx, float* __restrict__ sums) {
   __shared__ float red[kThreads / 32];
   pdl_wait();
-  const int64_t b = blockIdx.x / parts;
-  const int part = static_cast<int>(blockIdx.x % parts);
-  const int64_t nv = a.n / kV, items = a.m * nv;
-  const int64_t per = ceil_div(items, parts), lo = part * per, hi = min(items, lo + per);
+  const int64_t b = blockIdx.x / parts, part = blockIdx.x % parts, nv = a.n / kV;
+  const int ty = kThreads / tx;
   const uint64_t bytes = ((a.batch - 1) * a.stride + (a.m - 1) * a.ld + a.n) * sizeof(T);
+  constexpr int kAhead = 4;
   float sum = 0.0f;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-    const T* p = g + b * a.stride + (i / nv) * a.ld + (i % nv) * kV;
-    if (!in_buf(p, kV * sizeof(T), g, bytes, &g_ortho_status)) continue;
-    const Vec<T, kV> v = *reinterpret_cast<const Vec<T, kV>*>(p);
+  for (int64_t r = part * ty + threadIdx.x / tx; r < a.m; r += static_cast<int64_t>(parts) * ty) {
+    const T* row = g + b * a.stride + r * a.ld;
+    if (!in_buf(row, a.n * sizeof(T), g, bytes, &g_ortho_status)) continue;
+    for (int64_t c = threadIdx.x % tx; c < nv; c += kAhead * tx) {
+      Vec<T, kV> v[kAhead];
 #pragma unroll
-    for (int j = 0; j < kV; ++j) sum = fmaf(widen(v.v[j]), widen(v.v[j]), sum);
+      for (int q = 0; q < kAhead; ++q)
+        v[q] = c + q * tx < nv ? *reinterpret_cast<const Vec<T, kV>*>(row + (c + q * tx) * kV) : Vec<T, kV>{};
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int j = 0; j < kV; ++j) sum = fmaf(widen(v[q].v[j]), widen(v[q].v[j]), sum);
+    }
   }
   sum = warp_sum(sum);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
@@ -87,12 +99,12 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, int kV>
 __global__ void __launch_bounds__(kThreads)
-    scale_kernel(const T* __restrict__ g, const Matrix a, int parts, const float* __restrict__ sums, float eps,
+    scale_kernel(const T* __restrict__ g, const Matrix a, int parts, int tx, const float* __restrict__ sums, float eps,
                  __half* __restrict__ x, __half* __restrict__ x_low, int64_t ldx) {
   __shared__ float factor;
   pdl_wait();
-  const int64_t nv = a.n / kV, items = a.m * nv;
-  const int64_t blocks = gridDim.x / a.batch, b = blockIdx.x / blocks, q = blockIdx.x % blocks;
+  const int64_t b = blockIdx.x / parts, part = blockIdx.x % parts, nv = a.n / kV;
+  const int ty = kThreads / tx;
   if (threadIdx.x < 32) {
     float s = 0.0f;
     for (int i = threadIdx.x; i < parts; i += 32) s += sums[b * parts + i];
@@ -103,22 +115,25 @@ __global__ void __launch_bounds__(kThreads)
   const float f = factor;
   const uint64_t in_bytes = ((a.batch - 1) * a.stride + (a.m - 1) * a.ld + a.n) * sizeof(T);
   const uint64_t out_bytes = static_cast<uint64_t>(a.batch) * a.m * ldx * 2;
-  for (int64_t i = q * kThreads + threadIdx.x; i < items; i += blocks * kThreads) {
-    const int64_t r = i / nv, c = (i % nv) * kV;
-    const T* p = g + b * a.stride + r * a.ld + c;
-    if (!in_buf(p, kV * sizeof(T), g, in_bytes, &g_ortho_status)) continue;
-    const Vec<T, kV> v = *reinterpret_cast<const Vec<T, kV>*>(p);
-    Vec<uint16_t, kV> o;
+  for (int64_t r = part * ty + threadIdx.x / tx; r < a.m; r += static_cast<int64_t>(parts) * ty) {
+    const T* row = g + b * a.stride + r * a.ld;
+    __half* to = x + (b * a.m + r) * ldx;
+    if (!in_buf(row, a.n * sizeof(T), g, in_bytes, &g_ortho_status) ||
+        !in_buf(to, a.n * 2, x, out_bytes, &g_ortho_status))
+      continue;
+#pragma unroll 4
+    for (int64_t c = threadIdx.x % tx; c < nv; c += tx) {
+      const Vec<T, kV> v = *reinterpret_cast<const Vec<T, kV>*>(row + c * kV);
+      Vec<uint16_t, kV> o;
 #pragma unroll
-    for (int j = 0; j < kV; ++j) o.v[j] = __half_as_ushort(__float2half_rn(widen(v.v[j]) * f));
-    __half* to = x + (b * a.m + r) * ldx + c;
-    if (!in_buf(to, sizeof o, x, out_bytes, &g_ortho_status)) continue;
-    *reinterpret_cast<Vec<uint16_t, kV>*>(to) = o;
-    if (x_low == nullptr) continue;
+      for (int j = 0; j < kV; ++j) o.v[j] = __half_as_ushort(__float2half_rn(widen(v.v[j]) * f));
+      *reinterpret_cast<Vec<uint16_t, kV>*>(to + c * kV) = o;
+      if (x_low == nullptr) continue;
 #pragma unroll
-    for (int j = 0; j < kV; ++j)
-      o.v[j] = __half_as_ushort(__float2half_rn(widen(v.v[j]) * f - __half2float(__ushort_as_half(o.v[j]))));
-    *reinterpret_cast<Vec<uint16_t, kV>*>(x_low + (to - x)) = o;
+      for (int j = 0; j < kV; ++j)
+        o.v[j] = __half_as_ushort(__float2half_rn(widen(v.v[j]) * f - __half2float(__ushort_as_half(o.v[j]))));
+      *reinterpret_cast<Vec<uint16_t, kV>*>(x_low + (to - x) + c * kV) = o;
+    }
   }
 }
 
@@ -130,29 +145,34 @@ constexpr int kHalf = 128;                      // rows of A and of B that one C
 constexpr int kStepK = 64;                      // elements of K per stage: one 128-byte swizzle row
 constexpr int kOperandBytes = kHalf * kStepK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kAccCols = 256;                   // tensor memory columns of one accumulator
 constexpr int kChunkCols = 64;                  // columns an epilogue warp stages at a time
 constexpr int kStagingBytes = 32 * kChunkCols * 2;
-constexpr int kStagings = 2;                    // staging buffers per epilogue warp
-constexpr int kGemmThreads = 256;               // producer, MMA, alloc, idle, 4 epilogue warps
-constexpr int kGemmSmem = 1024 + kStages * kStageBytes + 4 * kStagings * kStagingBytes;
+constexpr int kEpilogueWarps = 8;               // two for each 32 rows, each half of the columns
+constexpr int kWarpChunks = kTile / kChunkCols / 2;  // and as many staging buffers per warp
+constexpr int kGemmThreads = 128 + 32 * kEpilogueWarps;  // producer, MMA, allocation, idle; epilogue
+constexpr int kGemmSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kWarpChunks * kStagingBytes;
+static_assert(kWarpChunks == 2, "the epilogue pairs its two buffers");
 
 struct Maps {
   CUtensorMap a[2], b[2];  // operands, high and low parts
-  CUtensorMap d[2][2];     // up to two outputs, high and low parts: boxes of 64 columns x 32 rows
-  CUtensorMap dt[2];       // the high parts' transposes: boxes of 32 columns x 64 rows
+  CUtensorMap d[2];        // output, high and low parts: boxes of 64 columns x 32 rows
+  CUtensorMap add[2];      // addend, the same
+  CUtensorMap dt;          // the high part's transpose: boxes of 32 columns x 64 rows
 };
 
 struct Product {
   int64_t rows, cols;      // of the output
   int32_t ksteps;          // stages along K of one product
-  int32_t split;           // operands and outputs are pairs: three products
   int32_t tiles_m, tiles_n, tiles;  // tiles: all of the batch
-  int32_t symmetric;       // one triangle of tiles, stored twice
   int32_t a_mn, b_mn;      // operand lies with K along its rows
-  int32_t outputs;         // 1 or 2
-  float scale[2], diagonal[2];  // d = scale * acc, + diagonal where row == column
+  // output = scale * acc + (add_scale + scale * (d[row] + d[column])) * addend
+  //          and where row == column, + diagonal + add_scale * d + scale * d * d
+  float scale, add_scale, diagonal;
+  const float *d_row, *d_col;       // [batch, d_ld]: what the rounding left of a diagonal; NULL: zero
+  float* d_out;                     // the same of this output's diagonal, or NULL
+  int64_t d_ld;
   // the last update writes bf16 to the caller's matrix
   bf16_t* out;             // NULL: fp16 through map d
   int64_t ldo, stride_o;
@@ -173,13 +193,23 @@ __device__ __forceinline__ uint32_t at_leader(uint32_t addr) {
   return r;
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  // relaxed: what it orders are tensor memory reads, by their own fence; a release
+  // at cluster scope would wait for the stores before it (2 us a tile, measured)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Load of a box whose bytes are counted by a barrier of the pair's leader.
 __device__ __forceinline__ void load_3d_pair(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
                                              uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
@@ -237,8 +267,9 @@ __device__ __forceinline__ uint32_t instruction_desc(bool a_mn, bool b_mn) {
 struct TileAt {
   int32_t batch, i, j;  // matrix, tile row, tile column
 };
+template <bool kSymmetric>
 __device__ __forceinline__ TileAt tile_at(const Product& p, int t) {
-  if (!p.symmetric) {
+  if (!kSymmetric) {
     const int per = p.tiles_m * p.tiles_n;
     const int r = t % per;
     return {t / per, r % p.tiles_m, r / p.tiles_m};
@@ -255,6 +286,9 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ float2 half2_values(uint32_t bits) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&bits));
+}
 __device__ __forceinline__ uint32_t bf162_bits(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -262,32 +296,22 @@ __device__ __forceinline__ uint32_t bf162_bits(float lo, float hi) {
 
 struct alignas(8) Barriers {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+  uint64_t addend[kEpilogueWarps][kWarpChunks];
   uint32_t tmem, abort_flag;
 };
 
-// One 64-column chunk of a warp's 32 rows, staged and stored; v holds the
-// finished values of this lane's row.
 __device__ __forceinline__ float half_rounded(float v) { return __half2float(__float2half_rn(v)); }
 
-template <bool kBf16>
-__device__ __forceinline__ void stage_rows(uint32_t buf, int lane, const float (&v)[64]) {
-#pragma unroll
-  for (int q = 0; q < 8; ++q) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = kBf16 ? bf162_bits(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]) : half2_bits(v[8 * q + 2 * j], v[8 * q + 2 * j + 1]);
-    // the 128-byte swizzle: 16-byte piece q of row r lies at piece q ^ (r % 8)
-    sts128(buf + lane * 128 + ((q ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-  }
-}
-__device__ __forceinline__ void stage_columns(uint32_t buf, int lane, const float (&v)[64]) {
-#pragma unroll
-  for (int j = 0; j < 64; ++j)
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + j * 64 + lane * 2), "h"(__half_as_ushort(__float2half_rn(v[j])))
-                 : "memory");
+__device__ __forceinline__ void unpack8(const uint4 w, float (&v)[8]) {
+  const float2 a = half2_values(w.x), b = half2_values(w.y), c = half2_values(w.z), d = half2_values(w.w);
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
 }
 
+// kSymmetric: one triangle of tiles, stored twice.  kAddends: parts of the
+// addend.  kColumns: the columns' d_col multiplies it (d_row, where given, always
+// does).  kBf16: the last update, to the caller's matrix.  kSplit: operands and
+// results are pairs, three products.
+template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit>
 __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p) {
   extern __shared__ uint8_t raw[];
@@ -305,8 +329,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&bars.acc_full[s]), 1);
-      mbar_init(smem_u32(&bars.acc_empty[s]), 8);  // four epilogue warps of both CTAs
+      mbar_init(smem_u32(&bars.acc_empty[s]), 2 * kEpilogueWarps);  // of both CTAs
     }
+    for (int w = 0; w < kEpilogueWarps; ++w)
+      for (int c = 0; c < kWarpChunks; ++c) mbar_init(smem_u32(&bars.addend[w][c]), 1);
     bars.abort_flag = 0u;
     mbar_init_fence();
     tma_prefetch_desc(&maps.a[0]);
@@ -326,13 +352,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  const int ksteps = p.split ? 3 * p.ksteps : p.ksteps;
+  const int ksteps = kSplit ? 3 * p.ksteps : p.ksteps;
   int issued = 0;  // stages loaded so far (the producer's; its pair takes the same number)
   if (warp == 0 && lane == 0) {
     // ---- producer: this CTA's half of A and of B -------------------------
     bool ok = true;
     for (int t = first; ok && t < p.tiles; t += step) {
-      const TileAt at = tile_at(p, t);
+      const TileAt at = tile_at<kSymmetric>(p, t);
       const int32_t ra = at.i * kTile + static_cast<int32_t>(rank) * kHalf;
       const int32_t rb = at.j * kTile + static_cast<int32_t>(rank) * kHalf;
       for (int kk = 0; kk < ksteps; ++kk, ++issued) {
@@ -387,93 +413,210 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       if (ok) commit_pair(smem_u32(&bars.acc_full[acc]));
     }
   } else if (warp >= 4) {
-    // ---- epilogue: this CTA's 128 rows, 32 per warp -----------------------
-    const int w = warp - 4;
-    const uint32_t mine = staging + w * kStagings * kStagingBytes;
-    int done = 0, used = 0;
-    for (int t = first; t < p.tiles; t += step, ++done) {
-      const TileAt at = tile_at(p, t);
+    // ---- epilogue: 32 of this CTA's 128 rows and half of the columns per warp --
+    // The addend is loaded into the buffers that the results are staged in and
+    // replaced piece by piece.  Without a second result the two chunks of a warp
+    // have a buffer each, and the next tile's addend is loaded while this one's
+    // results leave; with one (the transposed block or the low parts) a chunk
+    // takes both.
+    const int e = warp - 4, quarter = e & 3;
+    const uint32_t buf0 = staging + (2 * e) * kStagingBytes, buf1 = buf0 + kStagingBytes;
+    const uint32_t bar0 = smem_u32(&bars.addend[e][0]);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    constexpr bool low = kSplit && !kBf16;  // a split side has one tile: never mirrored
+    constexpr bool both = kSymmetric || low;
+    uint32_t phases = 0u, flying = 0u;             // a bit per buffer: parity to wait for, addend in flight
+    const auto load_addend = [&](int b, int part, const TileAt& at, int c) {  // lane 0 issues; all lanes keep count
+      const int32_t row0 = at.i * kTile + static_cast<int32_t>(rank) * kHalf + quarter * 32;
+      const int32_t col0 = at.j * kTile + (2 * (e >> 2) + c) * kChunkCols;
+      if (row0 >= p.rows || col0 >= p.cols) return;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar0 + 8 * b, kStagingBytes);
+        load_3d(buf0 + b * kStagingBytes, &maps.add[part], col0, row0, at.batch, bar0 + 8 * b);
+      }
+      flying |= 1u << b;
+    };
+    const auto wait_addend = [&](int b) {
+      const bool got = mbar_wait_bounded(bar0 + 8 * b, (phases >> b) & 1, abort_flag, &g_ortho_status, MXQ_DEV_TIMEOUT);
+      if (!__all_sync(0xFFFFFFFFu, got)) return false;
+      flying &= ~(1u << b);
+      phases ^= 1u << b;
+      return true;
+    };
+    int done = 0;
+    bool ok = true;
+    if (kAddends == 1 && !both && first < p.tiles) {
+      const TileAt at = tile_at<kSymmetric>(p, first);
+      load_addend(0, 0, at, 0);
+      load_addend(1, 0, at, 1);
+    }
+    for (int t = first; ok && t < p.tiles; t += step, ++done) {
+      const TileAt at = tile_at<kSymmetric>(p, t);
       const int acc = done & 1;
-      const bool ready = mbar_wait_bounded(smem_u32(&bars.acc_full[acc]), (done >> 1) & 1, abort_flag, &g_ortho_status, MXQ_DEV_TIMEOUT);
-      if (!__all_sync(0xFFFFFFFFu, ready)) break;
-      fence_after();
-      const int64_t row0 = static_cast<int64_t>(at.i) * kTile + rank * kHalf + w * 32;
+      const int64_t row0 = static_cast<int64_t>(at.i) * kTile + rank * kHalf + quarter * 32;
       const int64_t row = row0 + lane;
-      const bool mirror = p.symmetric && at.i != at.j;
+      const bool mirror = kSymmetric && at.i != at.j;
+      const float dr = p.d_row != nullptr && row < p.rows ? p.d_row[at.batch * p.d_ld + row] : 0.0f;
+      if (kColumns && lane < 4) {  // this warp's 128 columns, four lines
+        const int64_t col = static_cast<int64_t>(at.j) * kTile + 2 * (e >> 2) * kChunkCols + 32 * lane;
+        if (col < p.cols) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.d_col + at.batch * p.d_ld + col));
+      }
+      if (both && kAddends) {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        for (int q = 0; q < kAddends; ++q) load_addend(q, q, at, 0);
+      }
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(&bars.acc_full[acc]), (done >> 1) & 1, abort_flag,
+                                                     &g_ortho_status, MXQ_DEV_TIMEOUT));
+      if (!ok) break;
+      fence_after();
 #pragma unroll 1
-      for (int c = 0; c < kTile / kChunkCols; ++c) {
-        const int64_t col0 = static_cast<int64_t>(at.j) * kTile + c * kChunkCols;
-        uint32_t raw0[32], raw1[32];
-        const uint32_t addr = tmem + (static_cast<uint32_t>(w * 32) << 16) + acc * kAccCols + c * kChunkCols;
-        tmem_load_32(addr, raw0);
-        tmem_load_32(addr + 32, raw1);
+      for (int c = 0; c < kWarpChunks; ++c) {
+        const int tile_col = (2 * (e >> 2) + c) * kChunkCols;
+        const int64_t col0 = static_cast<int64_t>(at.j) * kTile + tile_col;
+        const bool inside = row0 < p.rows && col0 < p.cols;
+        const uint32_t buf = both || c == 0 ? buf0 : buf1;
+        if (inside) {
+          if (both && kAddends > 0) {
+            if (c > 0) {
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
+              for (int q = 0; q < kAddends; ++q) load_addend(q, q, at, c);
+            }
+          } else if (kAddends == 0) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+          }
+          for (int q = 0; ok && q < kAddends; ++q) ok = wait_addend(both ? q : c);
+          if (!ok) break;
+        }
+        // everything of the chunk is read before anything is written: the
+        // accesses are volatile and keep their order
+        uint32_t raw[2][32];
+        tmem_load_32(lanes + acc * kAccCols + tile_col, raw[0]);
+        tmem_load_32(lanes + acc * kAccCols + tile_col + 32, raw[1]);
+        uint4 a4[8], l4[8];
+        const auto piece = [&](int q) { return lane * 128 + ((q ^ (lane & 7)) << 4); };  // the 128-byte swizzle
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          if (kAddends > 0) a4[q] = lds128(buf + piece(q));
+          if (kAddends == 2) l4[q] = lds128(buf1 + piece(q));
+        }
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        if (c == kTile / kChunkCols - 1) {  // the accumulator is free again
+        if (c == kWarpChunks - 1) {  // this warp is done with the accumulator
           fence_before();
           __syncwarp();
           if (lane == 0) arrive_cluster(at_leader(smem_u32(&bars.acc_empty[acc])));
         }
-        if (row0 >= p.rows || col0 >= p.cols) continue;
-        for (int o = 0; o < p.outputs; ++o) {
-          const float f = p.scale[o], dg = p.diagonal[o];
-          float v[64];
+        if (!inside) continue;
+        const float k0 = fmaf(p.scale, dr, p.add_scale);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            v[j] = __uint_as_float(raw0[j]) * f;
-            v[32 + j] = __uint_as_float(raw1[j]) * f;
+        for (int h = 0; h < 2; ++h) {  // 32 columns at a time
+          const int64_t col = col0 + 32 * h;
+          float4 dc[8];
+          if (kColumns) {
+            const float4* d = reinterpret_cast<const float4*>(p.d_col + at.batch * p.d_ld + col);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)  // d_ld is a multiple of 8
+              dc[q] = col + 4 * q < p.cols ? d[q] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           }
-          if (dg != 0.0f && row >= col0 && row < col0 + kChunkCols) {
+          float v[32];
 #pragma unroll
-            for (int j = 0; j < 64; ++j)
-              if (col0 + j == row) v[j] += dg;
-          }
-          // the row's values; then the transposed block, or the low parts (a split side has one tile)
-          const int again = mirror || (p.split && p.out == nullptr) ? 1 : 0;
-          for (int flip = 0; flip <= again; ++flip) {
-            if (flip && !mirror) {
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[h][i]) * p.scale;
+          if (kAddends > 0) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) v[j] -= half_rounded(v[j]);
+            for (int q = 0; q < 4; ++q) {
+              float a[8];
+              unpack8(a4[4 * h + q], a);
+              if (kAddends == 2) {
+                float l[8];
+                unpack8(l4[4 * h + q], l);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) a[i] += l[i];
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float4 d = dc[2 * q + i / 4];
+                const float k = kColumns ? fmaf(p.scale, i % 4 == 0 ? d.x : i % 4 == 1 ? d.y : i % 4 == 2 ? d.z : d.w, k0) : k0;
+                v[8 * q + i] = fmaf(k, a[i], v[8 * q + i]);
+              }
             }
-            const uint32_t buf = mine + (used % kStagings) * kStagingBytes;
-            ++used;
-            if (lane == 0) bulk_wait_read<kStagings - 1>();
-            __syncwarp();
-            if (flip && mirror)
-              stage_columns(buf, lane, v);
-            else if (p.out != nullptr)
-              stage_rows<true>(buf, lane, v);
+          }
+          if (kSymmetric && row >= col && row < col + 32 && row < p.rows) {
+            const float on = p.diagonal + p.add_scale * dr + p.scale * dr * dr;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (col + i == row) {
+                v[i] += on;
+                if (!kSplit) p.d_out[at.batch * p.d_ld + row] = v[i] - half_rounded(v[i]);
+              }
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = kBf16 ? bf162_bits(v[2 * i], v[2 * i + 1]) : half2_bits(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sts128(buf + piece(4 * h + q), w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          if (mirror) {  // transposed: 64 rows of this warp's 32 rows
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf1 + (32 * h + i) * 64 + lane * 2),
+                           "h"(static_cast<uint16_t>(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu))
+                           : "memory");
+          }
+          if (low) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = half2_bits(v[2 * i] - half_rounded(v[2 * i]), v[2 * i + 1] - half_rounded(v[2 * i + 1]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sts128(buf1 + piece(4 * h + q), w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          }
+        }
+        if (kBf16 && !p.out_map) {
+          // a matrix whose pitch or address no tensor map takes
+          __syncwarp();
+          bf16_t* out = p.out + at.batch * p.stride_o;
+          const uint64_t bytes = ((p.rows - 1) * p.ldo + p.cols) * 2;
+          for (int r = 0; r < 32 && row0 + r < p.rows; ++r)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int i = 32 * half + lane;
+              uint16_t value;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(value) : "r"(buf + r * 128 + ((((i >> 3) ^ (r & 7)) << 4) | ((i & 7) * 2))));
+              bf16_t* to = out + (row0 + r) * p.ldo + col0 + i;
+              if (col0 + i < p.cols && in_buf(to, 2, out, bytes, &g_ortho_status)) *to = value;
+            }
+          fence_proxy_async_smem();  // read before the next addend comes in
+          __syncwarp();
+          continue;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          const int32_t r0 = static_cast<int32_t>(row0), c0 = static_cast<int32_t>(col0);
+          store_3d(&maps.d[0], c0, r0, at.batch, buf);
+          if (mirror) store_3d(&maps.dt, r0, c0, at.batch, buf1);
+          if (low) store_3d(&maps.d[1], c0, r0, at.batch, buf1);
+          bulk_commit();
+        }
+      }
+      if (ok && kAddends == 1 && !both && t + step < p.tiles) {
+        const TileAt next = tile_at<kSymmetric>(p, t + step);
+#pragma unroll
+        for (int c = 0; c < kWarpChunks; ++c) {
+          // the first chunk's store has been read once at most the second's is left
+          const bool second = (static_cast<int64_t>(at.j) * kTile + (2 * (e >> 2) + 1) * kChunkCols) < p.cols;
+          if (lane == 0) {
+            if (c == 0 && second)
+              bulk_wait_read<1>();
             else
-              stage_rows<false>(buf, lane, v);
-            if (p.out != nullptr && !p.out_map) {
-              // a matrix whose pitch or address no tensor map takes
-              __syncwarp();
-              bf16_t* out = p.out + at.batch * p.stride_o;
-              const uint64_t bytes = ((p.rows - 1) * p.ldo + p.cols) * 2;
-              for (int r = 0; r < 32 && row0 + r < p.rows; ++r)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int j = 32 * h + lane;
-                  uint16_t e;
-                  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e) : "r"(buf + r * 128 + ((((j >> 3) ^ (r & 7)) << 4) | ((j & 7) * 2))));
-                  bf16_t* to = out + (row0 + r) * p.ldo + col0 + j;
-                  if (col0 + j < p.cols && in_buf(to, 2, out, bytes, &g_ortho_status)) *to = e;
-                }
-              __syncwarp();
-              continue;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (flip && mirror)
-                store_3d(&maps.dt[o], static_cast<int32_t>(row0), static_cast<int32_t>(col0), at.batch, buf);
-              else
-                store_3d(&maps.d[o][flip], static_cast<int32_t>(col0), static_cast<int32_t>(row0), at.batch, buf);
-              bulk_commit();
-            }
+              bulk_wait_read<0>();
           }
+          __syncwarp();
+          load_addend(c, 0, next, c);
         }
       }
     }
+    for (int b = 0; b < 2; ++b)  // after a wait that ran out
+      if (flying >> b & 1u) mbar_wait_drain(bar0 + 8 * b, (phases >> b) & 1);
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
   }
@@ -502,8 +645,8 @@ struct Layout {
   int64_t side, ldx, lds;            // pitches of X and of the square matrices
   int parts;                         // 2 with low parts
   int64_t x[2][2];                   // X of the even and of the odd steps: high, low
-  int64_t gram[2], gram2[2], poly[2];
-  int64_t sums, bytes;
+  int64_t gram[2], poly[2];
+  int64_t d_gram, d_poly, sums, bytes;
 };
 Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   Layout l;
@@ -520,9 +663,10 @@ Layout layout_of(int64_t batch, int64_t m, int64_t n) {
     l.x[0][q] = take(there ? xb : 0);
     l.x[1][q] = take(there ? xb : 0);
     l.gram[q] = take(there ? sb : 0);
-    l.gram2[q] = take(there ? sb : 0);
     l.poly[q] = take(there ? sb : 0);
   }
+  l.d_gram = take(up(batch * l.lds * 4, 256));
+  l.d_poly = take(up(batch * l.lds * 4, 256));
   l.sums = take(up(batch * kMaxParts * 4, 256));
   l.bytes = at;
   return l;
@@ -547,14 +691,24 @@ bool encode_half(CUtensorMap* map, const Stack& t, uint32_t box_cols, uint32_t b
   return encode(map, t, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, box_cols, box_rows, swizzle);
 }
 
+template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit>
 int launch_product(const Maps& maps, Product p, int64_t batch, int sms, cudaStream_t stream) {
   p.tiles_m = static_cast<int32_t>(ceil_div(p.rows, kTile));
   p.tiles_n = static_cast<int32_t>(ceil_div(p.cols, kTile));
-  const int64_t per = p.symmetric ? static_cast<int64_t>(p.tiles_m) * (p.tiles_m + 1) / 2
-                                  : static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  const int64_t per = kSymmetric ? static_cast<int64_t>(p.tiles_m) * (p.tiles_m + 1) / 2
+                                 : static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   p.tiles = static_cast<int32_t>(per * batch);
+  const auto kernel = product_kernel<kSymmetric, kAddends, kColumns, kBf16, kSplit>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ECUDA;
+  static bool attr_done[64] = {};  // benign race: the same attribute set twice
+  if (!attr_done[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem) != cudaSuccess)
+      return MXQ_ECUDA;
+    attr_done[dev] = true;
+  }
   const int pairs = sms / 2 < p.tiles ? sms / 2 : p.tiles;
-  return launch_pdl(product_kernel, 2 * pairs, kGemmThreads, kGemmSmem, stream, maps, p);
+  return launch_pdl(kernel, 2 * pairs, kGemmThreads, kGemmSmem, stream, maps, p);
 }
 
 // The largest power of two that keeps values up to `bound` within half of fp16's range.
@@ -567,25 +721,28 @@ float scale_for(double bound) {
 
 template <typename T, int kV>
 int launch_scale(const void* g, const Matrix& a, float eps, uint8_t* ws, const Layout& l, int sms, cudaStream_t stream) {
-  const int64_t items = a.m * (a.n / kV);
-  int64_t parts = ceil_div(items, kThreads * 8);
+  const int64_t nv = a.n / kV;
+  int tx = 8;
+  while (tx < kThreads && tx < nv) tx *= 2;
+  int64_t parts = ceil_div(a.m, kThreads / tx);
+  const int64_t most = ceil_div(static_cast<int64_t>(sms) * (2048 / kThreads), a.batch);
+  if (parts > most) parts = most;
   if (parts > kMaxParts) parts = kMaxParts;
+  const unsigned blocks = static_cast<unsigned>(a.batch * parts);
   float* sums = reinterpret_cast<float*>(ws + l.sums);
-  int rc = launch_pdl(norm_kernel<T, kV>, static_cast<unsigned>(a.batch * parts), kThreads, 0, stream,
-                      static_cast<const T*>(g), a, static_cast<int>(parts), sums);
+  const int rc = launch_pdl(norm_kernel<T, kV>, blocks, kThreads, 0, stream, static_cast<const T*>(g), a,
+                            static_cast<int>(parts), tx, sums);
   if (rc != MXQ_OK) return rc;
-  int64_t blocks = ceil_div(items, kThreads * 2);
-  const int64_t most = ceil_div(static_cast<int64_t>(sms) * 8, a.batch);
-  if (blocks > most) blocks = most;
-  return launch_pdl(scale_kernel<T, kV>, static_cast<unsigned>(a.batch * blocks), kThreads, 0, stream,
-                    static_cast<const T*>(g), a, static_cast<int>(parts), sums, eps,
-                    reinterpret_cast<__half*>(ws + l.x[0][0]),
+  return launch_pdl(scale_kernel<T, kV>, blocks, kThreads, 0, stream, static_cast<const T*>(g), a,
+                    static_cast<int>(parts), tx, sums, eps, reinterpret_cast<__half*>(ws + l.x[0][0]),
                     l.parts == 2 ? reinterpret_cast<__half*>(ws + l.x[0][1]) : nullptr, l.ldx);
 }
 template <typename T>
 int scale_vector(const void* g, const Matrix& a, float eps, uint8_t* ws, const Layout& l, int sms, cudaStream_t stream) {
   const uint64_t es = sizeof(T);
   const int v = common_alignment({address_of(g), a.n * es, a.ld * es, a.stride * es}) / static_cast<int>(es);
+  if constexpr (sizeof(T) == 2)
+    if (v >= 8) return launch_scale<T, 8>(g, a, eps, ws, l, sms, stream);
   return v >= 4   ? launch_scale<T, 4>(g, a, eps, ws, l, sms, stream)
          : v >= 2 ? launch_scale<T, 2>(g, a, eps, ws, l, sms, stream)
                   : launch_scale<T, 1>(g, a, eps, ws, l, sms, stream);
@@ -635,15 +792,8 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
                           range_of(workspace, l.bytes)};
   const ByteRange in[1] = {range_of(g, static_cast<uint64_t>((batch - 1) * stride + (m - 1) * ld + n) * es)};
   if (outputs_overlap(o, 2, in, 1)) return MXQ_EOVERLAP;
-  int dev = 0;
-  const int sms = sm_count_current_device(&dev);
-  if (sms <= 0 || dev < 0 || dev >= 64) return MXQ_ECUDA;
-  static bool attr_done[64] = {};  // benign race: the same attribute set twice
-  if (!attr_done[dev]) {
-    if (cudaFuncSetAttribute(product_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem) != cudaSuccess)
-      return MXQ_ECUDA;
-    attr_done[dev] = true;
-  }
+  const int sms = sm_count_current_device(nullptr);
+  if (sms <= 0) return MXQ_ECUDA;
 
   const Matrix a = {batch, m, n, ld, batch > 1 ? stride : 0};
   int rc = dtype == MXQ_F32 ? scale_vector<float>(g, a, eps, workspace, l, sms, stream)
@@ -657,7 +807,7 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
   // boxes: K-major operand 64 x 128, MN-major operand 64 x 64, stores 64 x 32 and 32 x 64
   struct Set {
     CUtensorMap k, mn, rows, columns;
-  } x[2][2], gram[2], gram2[2], poly[2];
+  } x[2][2], gram[2], poly[2];
   CUtensorMap final_rows;
   bool ok = true;
   const auto set = [&](Set* to, const Stack& t) {
@@ -667,7 +817,6 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
   for (int q = 0; q < l.parts; ++q) {
     for (int i = 0; i < 2; ++i) set(&x[i][q], matrix(l.x[i][q]));
     set(&gram[q], square(l.gram[q]));
-    set(&gram2[q], square(l.gram2[q]));
     set(&poly[q], square(l.poly[q]));
   }
   if (!ok) return MXQ_ECUDA;
@@ -677,70 +826,87 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
       encode(&final_rows, Stack{out, batch, m, n, ldo, so}, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, 32, true);
 
   // |X| <= 1.5 and so |A| <= 2 are taken as bounds of the iterates
-  const double ba = fabs(ca), bb = fabs(cb), bc = fabs(cc);
-  const float sa = scale_for(2.0), sa2 = scale_for(bb + 2 * bc), sp = scale_for(ba + 2 * bb + 4 * bc);
+  const float sa = scale_for(2.0), sp = scale_for(fabs(ca) + 2 * fabs(cb) + 4 * fabs(cc));
   const int parts = l.parts;
+  const bool split = parts == 2;
+  float* d_gram = reinterpret_cast<float*>(workspace + l.d_gram);
+  float* d_poly = reinterpret_cast<float*>(workspace + l.d_poly);
   for (int s = 0; s < steps; ++s) {
     const int from = s & 1, to = from ^ 1;
     Maps maps = {};
     Product p = {};
-    // A and A'
+    // A
     for (int q = 0; q < parts; ++q) {
       maps.a[q] = maps.b[q] = wide ? x[from][q].k : x[from][q].mn;
-      maps.d[0][q] = gram[q].rows;
-      maps.d[1][q] = gram2[q].rows;
+      maps.d[q] = gram[q].rows;
     }
-    maps.dt[0] = gram[0].columns;
-    maps.dt[1] = gram2[0].columns;
+    maps.dt = gram[0].columns;
     p.rows = p.cols = side;
     p.ksteps = static_cast<int32_t>(ceil_div(length, kStepK));
-    p.split = parts == 2;
-    p.symmetric = 1;
     p.a_mn = p.b_mn = !wide;
-    p.outputs = 2;
-    p.scale[0] = sa / (kXScale * kXScale);
-    p.scale[1] = cc * sa2 / (kXScale * kXScale);
-    p.diagonal[1] = cb * sa2;
-    if ((rc = launch_product(maps, p, batch, sms, stream)) != MXQ_OK) return rc;
-    // P = A' A + aI
+    p.scale = sa / (kXScale * kXScale);
+    p.d_ld = l.lds;
+    p.d_out = d_gram;
+    rc = split ? launch_product<true, 0, false, false, true>(maps, p, batch, sms, stream)
+               : launch_product<true, 0, false, false, false>(maps, p, batch, sms, stream);
+    if (rc != MXQ_OK) return rc;
+    // P = aI + bA + cAA
     p = {};
     for (int q = 0; q < parts; ++q) {
-      maps.a[q] = gram2[q].k;
-      maps.b[q] = gram[q].k;
-      maps.d[0][q] = poly[q].rows;
+      maps.a[q] = maps.b[q] = gram[q].k;
+      maps.add[q] = gram[q].rows;
+      maps.d[q] = poly[q].rows;
     }
-    maps.dt[0] = poly[0].columns;
+    maps.dt = poly[0].columns;
     p.rows = p.cols = side;
     p.ksteps = static_cast<int32_t>(ceil_div(side, kStepK));
-    p.split = parts == 2;
-    p.symmetric = 1;
-    p.outputs = 1;
-    p.scale[0] = sp / (sa * sa2);
-    p.diagonal[0] = ca * sp;
-    if ((rc = launch_product(maps, p, batch, sms, stream)) != MXQ_OK) return rc;
+    p.scale = cc * sp / (sa * sa);
+    p.add_scale = cb * sp / sa;
+    p.diagonal = ca * sp;
+    p.d_ld = l.lds;
+    if (!split) {
+      p.d_row = p.d_col = d_gram;
+      p.d_out = d_poly;
+    }
+    rc = split ? launch_product<true, 2, false, false, true>(maps, p, batch, sms, stream)
+               : launch_product<true, 1, true, false, false>(maps, p, batch, sms, stream);
+    if (rc != MXQ_OK) return rc;
     // X <- P X, or X P
     p = {};
     for (int q = 0; q < parts; ++q) {
       maps.a[q] = wide ? poly[q].k : x[from][q].k;
       maps.b[q] = wide ? x[from][q].mn : poly[q].k;
-      maps.d[0][q] = x[to][q].rows;
+      maps.d[q] = x[to][q].rows;
     }
     p.b_mn = wide;
     p.rows = m;
     p.cols = n;
     p.ksteps = static_cast<int32_t>(ceil_div(side, kStepK));
-    p.split = parts == 2;
-    p.outputs = 1;
-    p.scale[0] = 1.0f / sp;
-    if (s + 1 == steps) {
-      if (out_map) maps.d[0][0] = final_rows;
+    p.scale = 1.0f / sp;
+    if (!split) {
+      maps.add[0] = x[from][0].rows;
+      p.d_ld = l.lds;
+      (wide ? p.d_row : p.d_col) = d_poly;
+    }
+    const bool last = s + 1 == steps;
+    if (last) {
+      if (out_map) maps.d[0] = final_rows;
       p.out = static_cast<bf16_t*>(out);
       p.ldo = ldo;
       p.stride_o = so;
       p.out_map = out_map;
-      p.scale[0] = scale / (sp * kXScale);
+      p.scale = scale / (sp * kXScale);
     }
-    if ((rc = launch_product(maps, p, batch, sms, stream)) != MXQ_OK) return rc;
+    if (split)
+      rc = last ? launch_product<false, 0, false, true, true>(maps, p, batch, sms, stream)
+                : launch_product<false, 0, false, false, true>(maps, p, batch, sms, stream);
+    else if (wide)
+      rc = last ? launch_product<false, 1, false, true, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 1, false, false, false>(maps, p, batch, sms, stream);
+    else
+      rc = last ? launch_product<false, 1, true, true, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 1, true, false, false>(maps, p, batch, sms, stream);
+    if (rc != MXQ_OK) return rc;
   }
   return MXQ_OK;
 }

@@ -296,7 +296,8 @@ int mxq_mxfp8_scaled_mm(const uint8_t *a, int64_t lda, const uint8_t *sa, const 
  * pointers need the alignment of their elements only, and accesses widen to 16
  * bytes where every pitch and address allows it.  `workspace` is device memory
  * (16-byte aligned) that a call uses and leaves: at least the bytes that the
- * matching _workspace() call returns (a host computation; negative: MXQ_E*).
+ * matching _workspace() call returns (a host computation; negative: MXQ_E*;
+ * 0: none, the pointer may be NULL).
  * A too small one is refused with MXQ_EBADSHAPE.  Results have the same bits in
  * every run: no sum depends on the order in which blocks run.
  * ======================================================================== */
@@ -322,7 +323,7 @@ int mxq_mxfp8_scaled_mm(const uint8_t *a, int64_t lda, const uint8_t *sa, const 
  * that are not counted are written as 0.  ids, counts and routed are the
  * forward call's.  dlogits has the logits' type, rows ldd elements apart.
  */
-int64_t mxq_moe_route_workspace(int32_t experts);
+int64_t mxq_moe_route_workspace(int64_t tokens, int32_t experts);
 int mxq_moe_route(const void *logits, int dtype, int64_t tokens, int32_t experts, int64_t ld,
                   int32_t k, const uint8_t *mask, int renorm, float *weights, int32_t *ids,
                   int32_t *counts, float *loss, int32_t *routed, uint8_t *workspace,

@@ -115,7 +115,7 @@ def lib() -> ctypes.CDLL:
         L.mxq_mxfp8_scaled_mm.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i64, i64, vp]
         f32, ci = ctypes.c_float, ctypes.c_int
         for name, restype, argtypes in (
-                ("mxq_moe_route_workspace", i64, [i32]),
+                ("mxq_moe_route_workspace", i64, [i64, i32]),
                 ("mxq_moe_route", ci, [vp, ci, i64, i32, i64, i32, vp, ci, vp, vp, vp, vp, vp, vp, i64, vp]),
                 ("mxq_moe_route_backward", ci, [vp, ci, i64, i32, i64, i32, vp, ci, vp, vp, vp, vp, vp, vp, i64, vp]),
                 ("mxq_moe_rows", i64, [i64, i32, i32]),

@@ -329,6 +329,10 @@ template <int kPer>
 constexpr int route_threads() {
   return kPer <= 8 ? 1024 : kPer == 16 ? 512 : 256;
 }
+// warps of a block for that many experts
+int warps_for(int experts) {
+  return (experts <= 256 ? route_threads<8>() : experts <= 512 ? route_threads<16>() : route_threads<32>()) / 32;
+}
 constexpr int kBackThreads = 256;
 
 struct RouteCall {
@@ -419,9 +423,10 @@ int route_status_read(unsigned int* out, bool clear) {
 }
 }  // namespace mxq
 
-extern "C" int64_t mxq_moe_route_workspace(int32_t experts) {
-  if (experts < 1 || experts > MXQ_MAX_GROUPS) return MXQ_EBADSHAPE;
-  return (static_cast<int64_t>(experts) * 8 + 4) * kMaxBlocks;
+extern "C" int64_t mxq_moe_route_workspace(int64_t tokens, int32_t experts) {
+  if (tokens < 0 || tokens > INT32_MAX || experts < 1 || experts > MXQ_MAX_GROUPS) return MXQ_EBADSHAPE;
+  const int64_t blocks = ceil_div(tokens, warps_for(experts));
+  return blocks <= 1 ? 0 : (static_cast<int64_t>(experts) * 8 + 4) * (blocks < kMaxBlocks ? blocks : kMaxBlocks);
 }
 
 extern "C" int mxq_moe_route(const void* logits, int dtype, int64_t tokens, int32_t experts, int64_t ld, int32_t k,
@@ -430,9 +435,9 @@ extern "C" int mxq_moe_route(const void* logits, int dtype, int64_t tokens, int3
                              cudaStream_t stream) {
   int rc = check_route_shape(dtype, tokens, experts, k, ld);
   if (rc != MXQ_OK) return rc;
-  const int64_t need = mxq_moe_route_workspace(experts);
+  const int64_t need = mxq_moe_route_workspace(tokens, experts);
   if (workspace_bytes < need) return MXQ_EBADSHAPE;
-  if (!counts || !loss || !routed || !workspace || (tokens > 0 && (!logits || !weights || !ids))) return MXQ_ENULL;
+  if (!counts || !loss || !routed || (need > 0 && !workspace) || (tokens > 0 && (!logits || !weights || !ids))) return MXQ_ENULL;
   const int es = element_bytes(dtype);
   if (!aligned_to(logits, es) || !aligned_to(weights, 4) || !aligned_to(ids, 4) || !aligned_to(counts, 4) ||
       !aligned_to(loss, 4) || !aligned_to(routed, 4) || !aligned_to(workspace, 16))

@@ -13,7 +13,6 @@ otherwise it runs on the current stream of the tensors' device.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import NamedTuple, Optional
 
 import torch
@@ -21,7 +20,6 @@ import torch
 from . import BF16, F32, OK, MxqError, lib
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
-_NOTHING = contextlib.nullcontext()
 
 
 class Routing(NamedTuple):
@@ -76,35 +74,31 @@ def _flat(t, name, dtype, shape, device):
 
 
 def _mask_pointer(mask, tokens, device):
-    if mask is None:
-        return None
     return _flat(mask, "mask", torch.uint8 if mask.dtype == torch.uint8 else torch.bool, (tokens,), device)
 
 
-def _on(device, stream):
-    """Context in which a call's allocations and launches belong to its stream."""
+def _elsewhere(device, stream):
+    """None when a call on `device` may run as things are, else the context in
+    which its allocations and launches belong to its device and stream."""
     if stream is not None:
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
-    return _NOTHING
+    return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
-def _stream(device, stream):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-
-def _check(rc, what):
-    if rc != OK:
-        raise MxqError(rc, what)
+# the handle of a device's current stream; the public call builds a Stream object
+# around it, which takes as long as a launch
+_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _workspace(size, what, device):
-    """(tensor, pointer, bytes) of a call's workspace from the size the library asks for."""
-    if size < 0:
-        raise MxqError(int(size), what)
+    """(tensor, pointer) of a call's workspace of the size the library asks for."""
+    if size <= 0:
+        if size < 0:
+            raise MxqError(int(size), what)
+        return None, None
     t = torch.empty(size, dtype=torch.uint8, device=device)
-    return t, t.data_ptr(), size
+    return t, t.data_ptr()
 
 
 # ---------------------------------------------------------------------------
@@ -117,27 +111,34 @@ def moe_route(logits, k: int, *, mask=None, renorm: bool = True, out: Optional[R
     softmax weights (over the chosen experts' sum with ``renorm``), the tokens of
     each expert and the balance loss.  ``mask``: bool or uint8 [T], false leaves
     the token out.  A logit of -inf marks an expert that must not be chosen."""
+    dev = logits.device
     ld = _matrix(logits, "logits")
     code = _code(logits, "logits")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_route(logits, k, mask=mask, renorm=renorm, out=out)
     T, E = logits.shape
-    dev = logits.device
-    mask_p = _mask_pointer(mask, T, dev)
+    mask_p = None if mask is None else _mask_pointer(mask, T, dev)
     L = lib()
-    with _on(dev, stream):
-        if out is None:
-            # one allocation for the small results: counts, loss, routed
-            small = torch.empty(E + 2, dtype=torch.int32, device=dev)
-            out = Routing(torch.empty((T, k), dtype=torch.float32, device=dev),
-                          torch.empty((T, k), dtype=torch.int32, device=dev), small[:E],
-                          small[E].view(torch.float32), small[E + 1])
-        w = _flat(out.weights, "weights", torch.float32, (T, k), dev)
-        i = _flat(out.ids, "ids", torch.int32, (T, k), dev)
-        c = _flat(out.counts, "counts", torch.int32, (E,), dev)
-        l = _flat(out.loss, "loss", torch.float32, (), dev)
-        n = _flat(out.routed, "routed", torch.int32, (), dev)
-        ws, wp, wb = _workspace(L.mxq_moe_route_workspace(E), "mxq_moe_route", dev)
-        _check(L.mxq_moe_route(logits.data_ptr(), code, T, E, ld, k, mask_p, int(renorm), w, i, c, l, n, wp, wb,
-                               _stream(dev, stream)), "mxq_moe_route")
+    size = L.mxq_moe_route_workspace(T, E)
+    ws, wp = _workspace(size, "mxq_moe_route", dev)
+    if out is None:
+        out = Routing(torch.empty((T, k), dtype=torch.float32, device=dev),
+                      torch.empty((T, k), dtype=torch.int32, device=dev),
+                      torch.empty(E, dtype=torch.int32, device=dev),
+                      torch.empty((), dtype=torch.float32, device=dev),
+                      torch.empty((), dtype=torch.int32, device=dev))
+    else:
+        for t, name, dtype, shape in zip(out, Routing._fields,
+                                         (torch.float32, torch.int32, torch.int32, torch.float32, torch.int32),
+                                         ((T, k), (T, k), (E,), (), ())):
+            _flat(t, name, dtype, shape, dev)
+    rc = L.mxq_moe_route(logits.data_ptr(), code, T, E, ld, k, mask_p, bool(renorm), out[0].data_ptr(),
+                         out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), wp, size,
+                         _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_route")
     return out
 
 
@@ -145,25 +146,31 @@ def moe_route_backward(logits, routing: Routing, dweights=None, dloss=None, *, m
                        renorm: bool = True, out=None, stream=None):
     """Gradient of the logits from those of the weights [T, k] and of the loss []
     (fp32; None for zero); logits, mask and renorm as in :func:`moe_route`."""
+    dev = logits.device
     ld = _matrix(logits, "logits")
     code = _code(logits, "logits")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_route_backward(logits, routing, dweights, dloss, mask=mask, renorm=renorm, out=out)
     T, E = logits.shape
-    dev = logits.device
     k = routing.ids.shape[-1]
     i = _flat(routing.ids, "ids", torch.int32, (T, k), dev)
     c = _flat(routing.counts, "counts", torch.int32, (E,), dev)
     n = _flat(routing.routed, "routed", torch.int32, (), dev)
     dw = None if dweights is None else _flat(dweights, "dweights", torch.float32, (T, k), dev)
     dl = None if dloss is None else _flat(dloss, "dloss", torch.float32, (), dev)
-    mask_p = _mask_pointer(mask, T, dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    mask_p = None if mask is None else _mask_pointer(mask, T, dev)
+    if out is None:
+        out, ldd = torch.empty((T, E), dtype=logits.dtype, device=dev), E
+    else:
         ldd = _matrix(out, "out", T, E, dev)
         if out.dtype != logits.dtype:
             raise ValueError("out must have the logits' type")
-        _check(lib().mxq_moe_route_backward(logits.data_ptr(), code, T, E, ld, k, mask_p, int(renorm), i, c, n, dw, dl,
-                                            out.data_ptr(), ldd, _stream(dev, stream)), "mxq_moe_route_backward")
+    rc = lib().mxq_moe_route_backward(logits.data_ptr(), code, T, E, ld, k, mask_p, bool(renorm), i, c, n, dw, dl,
+                                      out.data_ptr(), ldd, _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_route_backward")
     return out
 
 
@@ -189,18 +196,26 @@ def moe_plan(ids, experts: int, *, rows: Optional[int] = None, out: Optional[Moe
     T, k = ids.shape
     dev = ids.device
     p = _flat(ids, "ids", torch.int32, (T, k), dev)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_plan(ids, experts, rows=rows, out=out)
     L = lib()
-    M = out.source.numel() if out is not None else moe_rows(T, k, experts) if rows is None else int(rows)
-    with _on(dev, stream):
-        if out is None:
-            out = MoePlan(torch.empty((experts,), dtype=torch.int32, device=dev),
-                          torch.empty((T, k), dtype=torch.int32, device=dev),
-                          torch.empty((max(M, 0),), dtype=torch.int32, device=dev))
-        o = _flat(out.offs, "offs", torch.int32, (experts,), dev)
-        s = _flat(out.slots, "slots", torch.int32, (T, k), dev)
-        m = _flat(out.source, "source", torch.int32, (M,), dev)
-        ws, wp, wb = _workspace(L.mxq_moe_plan_workspace(T, k, experts), "mxq_moe_plan", dev)
-        _check(L.mxq_moe_plan(p, T, k, experts, M, o, s, m, wp, wb, _stream(dev, stream)), "mxq_moe_plan")
+    size = L.mxq_moe_plan_workspace(T, k, experts)
+    ws, wp = _workspace(size, "mxq_moe_plan", dev)
+    if out is None:
+        M = L.mxq_moe_rows(T, k, experts) if rows is None else int(rows)
+        out = MoePlan(torch.empty(experts, dtype=torch.int32, device=dev),
+                      torch.empty((T, k), dtype=torch.int32, device=dev),
+                      torch.empty(max(M, 0), dtype=torch.int32, device=dev))
+    else:
+        M = out.source.numel()
+        for t, name, shape in zip(out, MoePlan._fields, ((experts,), (T, k), (M,))):
+            _flat(t, name, torch.int32, shape, dev)
+    rc = L.mxq_moe_plan(p, T, k, experts, M, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), wp, size,
+                        _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_plan")
     return out
 
 
@@ -220,15 +235,21 @@ def moe_dispatch(x, plan: MoePlan, *, out=None, stream=None):
     code = _code(x, "x")
     T, k, M, slots, source = _plan_pointers(plan, dev)
     ldx = _matrix(x, "x", T)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_dispatch(x, plan, out=out)
     D = x.shape[1]
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((M, D), dtype=x.dtype, device=dev)
+    if out is None:
+        out, ldr = torch.empty((M, D), dtype=x.dtype, device=dev), max(D, 1)
+    else:
         ldr = _matrix(out, "out", M, D, dev)
         if out.dtype != x.dtype:
             raise ValueError("out must have x's type")
-        _check(lib().mxq_moe_dispatch(x.data_ptr(), code, T, D, ldx, k, slots, source, M, out.data_ptr(), ldr,
-                                      _stream(dev, stream)), "mxq_moe_dispatch")
+    rc = lib().mxq_moe_dispatch(x.data_ptr(), code, T, D, ldx, k, slots, source, M, out.data_ptr(), ldr,
+                                _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_dispatch")
     return out
 
 
@@ -240,16 +261,22 @@ def moe_combine(rows, plan: MoePlan, weights=None, *, out=None, stream=None):
     code = _code(rows, "rows")
     T, k, M, slots, _ = _plan_pointers(plan, dev)
     ldr = _matrix(rows, "rows", M)
-    D = rows.shape[1]
     w = None if weights is None else _flat(weights, "weights", torch.float32, (T, k), dev)
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((T, D), dtype=rows.dtype, device=dev)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_combine(rows, plan, weights, out=out)
+    D = rows.shape[1]
+    if out is None:
+        out, ldy = torch.empty((T, D), dtype=rows.dtype, device=dev), max(D, 1)
+    else:
         ldy = _matrix(out, "out", T, D, dev)
         if out.dtype != rows.dtype:
             raise ValueError("out must have the rows' type")
-        _check(lib().mxq_moe_combine(rows.data_ptr(), code, M, D, ldr, T, k, slots, w, out.data_ptr(), ldy,
-                                     _stream(dev, stream)), "mxq_moe_combine")
+    rc = lib().mxq_moe_combine(rows.data_ptr(), code, M, D, ldr, T, k, slots, w, out.data_ptr(), ldy,
+                               _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_combine")
     return out
 
 
@@ -265,18 +292,24 @@ def moe_combine_backward(dy, rows, plan: MoePlan, weights, *, out=None, stream=N
     if dy.dtype != rows.dtype:
         raise ValueError("dy must have the rows' type")
     w = _flat(weights, "weights", torch.float32, (T, k), dev)
-    with _on(dev, stream):
-        if out is None:
-            out = (torch.empty((M, D), dtype=rows.dtype, device=dev),
-                   torch.empty((T, k), dtype=torch.float32, device=dev))
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_combine_backward(dy, rows, plan, weights, out=out)
+    if out is None:
+        drows, ldd = torch.empty((M, D), dtype=rows.dtype, device=dev), max(D, 1)
+        dweights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        dw = dweights.data_ptr()
+    else:
         drows, dweights = out
         ldd = _matrix(drows, "drows", M, D, dev)
         if drows.dtype != rows.dtype:
             raise ValueError("drows must have the rows' type")
         dw = _flat(dweights, "dweights", torch.float32, (T, k), dev)
-        _check(lib().mxq_moe_combine_backward(dy.data_ptr(), code, T, D, ldy, rows.data_ptr(), ldr, M, k, slots, source,
-                                              w, drows.data_ptr(), ldd, dw, _stream(dev, stream)),
-               "mxq_moe_combine_backward")
+    rc = lib().mxq_moe_combine_backward(dy.data_ptr(), code, T, D, ldy, rows.data_ptr(), ldr, M, k, slots, source, w,
+                                        drows.data_ptr(), ldd, dw, _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_combine_backward")
     return drows, dweights
 
 
@@ -302,20 +335,25 @@ def embedding(ids, table, *, scale: float = 1.0, dtype=None, out=None, stream=No
         raise ValueError(f"ids must be on {dev}")
     code = _code(table, "table")
     ldw = _matrix(table, "table")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return embedding(ids, table, scale=scale, dtype=dtype, out=out)
     V, D = table.shape
     T = ids.numel()
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((*ids.shape, D), dtype=table.dtype if dtype is None else dtype, device=dev)
-            ldy = max(D, 1)
-        else:
-            if dtype is not None and out.dtype != dtype:
-                raise ValueError(f"out must be {dtype}")
-            if out.shape != (*ids.shape, D):
-                raise ValueError(f"out must be {[*ids.shape, D]}")
-            ldy = _matrix(out if out.dim() == 2 else out.view(-1, D), "out", T, D, dev)
-        _check(lib().mxq_embedding(p, ib, T, table.data_ptr(), code, V, D, ldw, scale, out.data_ptr(), _code(out, "out"),
-                                   ldy, _stream(dev, stream)), "mxq_embedding")
+    if out is None:
+        out = torch.empty((*ids.shape, D), dtype=table.dtype if dtype is None else dtype, device=dev)
+        ldy = max(D, 1)
+    else:
+        if dtype is not None and out.dtype != dtype:
+            raise ValueError(f"out must be {dtype}")
+        if out.shape != (*ids.shape, D):
+            raise ValueError(f"out must be {[*ids.shape, D]}")
+        ldy = _matrix(out if out.dim() == 2 else out.view(-1, D), "out", T, D, dev)
+    rc = lib().mxq_embedding(p, ib, T, table.data_ptr(), code, V, D, ldw, scale, out.data_ptr(), _code(out, "out"), ldy,
+                             _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_embedding")
     return out
 
 
@@ -337,18 +375,23 @@ def embedding_backward(ids, dy, rows: int, *, scale: float = 1.0, padding_idx: O
     ldd = _matrix(dy if dy.dim() == 2 else dy.view(-1, D) if T and D else dy.reshape(T, D), "dy", T, D)
     if padding_idx is not None and not 0 <= padding_idx < rows:
         raise ValueError(f"padding_idx must be in [0, {rows})")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return embedding_backward(ids, dy, rows, scale=scale, padding_idx=padding_idx, dtype=dtype, out=out)
     L = lib()
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty((rows, D), dtype=dy.dtype if dtype is None else dtype, device=dev)
-        elif dtype is not None and out.dtype != dtype:
+    size = L.mxq_embedding_backward_workspace(T, rows, D)
+    ws, wp = _workspace(size, "mxq_embedding_backward", dev)
+    if out is None:
+        out, ldw = torch.empty((rows, D), dtype=dy.dtype if dtype is None else dtype, device=dev), max(D, 1)
+    else:
+        if dtype is not None and out.dtype != dtype:
             raise ValueError(f"out must be {dtype}")
         ldw = _matrix(out, "out", rows, D, dev)
-        ws, wp, wb = _workspace(L.mxq_embedding_backward_workspace(T, rows, D), "mxq_embedding_backward", dev)
-        _check(L.mxq_embedding_backward(p, ib, T, dy.data_ptr(), code, D, ldd, rows,
-                                        -1 if padding_idx is None else padding_idx, scale, out.data_ptr(),
-                                        _code(out, "out"), ldw, wp, wb, _stream(dev, stream)),
-               "mxq_embedding_backward")
+    rc = L.mxq_embedding_backward(p, ib, T, dy.data_ptr(), code, D, ldd, rows, -1 if padding_idx is None else padding_idx,
+                                  scale, out.data_ptr(), _code(out, "out"), ldw, wp, size, _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_embedding_backward")
     return out
 
 
@@ -384,14 +427,20 @@ def orthogonalize(g, *, steps: int = 5, coefficients=(3.4445, -4.775, 2.0315), e
     batch, m, n, ld, stride = _stacked(g, "g")
     a, b, c = coefficients
     dev = g.device
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return orthogonalize(g, steps=steps, coefficients=coefficients, eps=eps, scale=scale, out=out)
+    if out is None:
+        out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
+    elif out.dtype != torch.bfloat16 or out.shape != g.shape or out.device != dev:
+        raise ValueError(f"out must be a bfloat16 tensor {list(g.shape)} on {dev}")
+    _, _, _, ldo, stride_o = _stacked(out, "out")
     L = lib()
-    with _on(dev, stream):
-        if out is None:
-            out = torch.empty(g.shape, dtype=torch.bfloat16, device=dev)
-        elif out.dtype != torch.bfloat16 or out.shape != g.shape or out.device != dev:
-            raise ValueError(f"out must be a bfloat16 tensor {list(g.shape)} on {dev}")
-        _, _, _, ldo, stride_o = _stacked(out, "out")
-        ws, wp, wb = _workspace(L.mxq_orthogonalize_workspace(batch, m, n), "mxq_orthogonalize", dev)
-        _check(L.mxq_orthogonalize(g.data_ptr(), code, batch, m, n, ld, stride, steps, a, b, c, eps, scale,
-                                   out.data_ptr(), ldo, stride_o, wp, wb, _stream(dev, stream)), "mxq_orthogonalize")
+    size = L.mxq_orthogonalize_workspace(batch, m, n)
+    ws, wp = _workspace(size, "mxq_orthogonalize", dev)
+    rc = L.mxq_orthogonalize(g.data_ptr(), code, batch, m, n, ld, stride, steps, a, b, c, eps, scale, out.data_ptr(), ldo,
+                             stride_o, wp, size, _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_orthogonalize")
     return out

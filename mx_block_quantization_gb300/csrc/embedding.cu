@@ -23,7 +23,7 @@ using namespace mxq;
 __device__ unsigned int g_embedding_status = 0;
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerBlock = 32;  // table rows a block of the gradient writes
+constexpr int kRowsPerBlock = 16;  // table rows a block of the gradient writes
 constexpr int kChunk = 32;         // sorted places per piece of a long run
 constexpr int kDigitBits = 10;     // at most kRankMaxBins bins
 
@@ -135,82 +135,107 @@ struct GradShape {
   int tx;
 };
 
-// First place whose key is >= v.
-__device__ __forceinline__ int64_t lower_bound(const int32_t* __restrict__ keys, int64_t n, int64_t v) {
-  int64_t lo = 0, hi = n;
+// First place whose key is >= v, by a whole warp: each step splits the range in
+// 33 with 32 probes at once (3 dependent loads for 32768 keys, where a binary
+// search has 15).
+__device__ __forceinline__ int64_t warp_lower_bound(const int32_t* __restrict__ keys, int64_t n, int64_t v) {
+  const int lane = threadIdx.x & 31;
+  int64_t lo = 0, hi = n;  // the answer lies in [lo, hi]
   while (lo < hi) {
-    const int64_t mid = (lo + hi) >> 1;
-    if (keys[mid] < v)
-      lo = mid + 1;
-    else
-      hi = mid;
+    const int64_t step = (hi - lo) / 33 + 1;
+    const int64_t at = lo + step * (lane + 1) - 1;  // probes lo + step - 1, lo + 2 step - 1, ...
+    const bool below = at < hi && keys[at] < v;
+    const int k = __popc(__ballot_sync(0xFFFFFFFFu, below));  // the first k probes lie below v
+    const int64_t next = lo + step * k;
+    hi = min(hi, next + step - 1);
+    lo = next;
   }
   return lo;
 }
 
-// acc += dy[tokens[p]] over the places [lo, hi), in order.
-template <typename T, int kV>
+// acc[u] += dy[tokens[p]] over the places [lo, hi), in order, for the kU column
+// vectors c, c + tx, ...: kU * kAhead loads before the first is used.
+template <typename T, int kV, int kU>
 __device__ __forceinline__ void add_tokens(const T* __restrict__ dy, const GradShape& s,
-                                           const int32_t* __restrict__ tokens, int64_t lo, int64_t hi, int64_t col,
-                                           float (&acc)[kV]) {
+                                           const int32_t* __restrict__ tokens, int64_t lo, int64_t hi, int64_t c,
+                                           int tx, int64_t nv, float (&acc)[kU][kV]) {
   const uint64_t bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldd + s.D) * sizeof(T);
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 8 / kU;
   for (int64_t p = lo; p < hi; p += kAhead) {
-    Vec<T, kV> v[kAhead];
+    Vec<T, kV> v[kAhead][kU];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      v[a] = Vec<T, kV>{};
-      if (p + a < hi) {
-        const T* src = dy + static_cast<int64_t>(tokens[p + a]) * s.ldd + col;
-        if (in_buf(src, sizeof v[a], dy, bytes, &g_embedding_status)) v[a] = *reinterpret_cast<const Vec<T, kV>*>(src);
+      const T* row = dy + (p + a < hi ? static_cast<int64_t>(tokens[p + a]) * s.ldd : 0);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        v[a][u] = Vec<T, kV>{};
+        const T* src = row + (c + u * tx) * kV;
+        if (p + a < hi && c + u * tx < nv && in_buf(src, sizeof v[a][u], dy, bytes, &g_embedding_status))
+          v[a][u] = load_once<T, kV>(src);
       }
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a)
-      if (p + a < hi) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) acc[i] += widen(v[a].v[i]);
-      }
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int i = 0; i < kV; ++i) acc[u][i] += widen(v[a][u].v[i]);
   }
+}
+
+// Column vectors a thread holds at once: more of them where each is narrow.
+template <typename T, int kV>
+__host__ __device__ constexpr int columns_at_once() {
+  return sizeof(T) * kV >= 16 ? 2 : 4;
 }
 
 // Pieces of the runs longer than kChunk places: pieces[2c] is the part of the
 // run that holds the first place of chunk c, pieces[2c + 1] that of the run
-// that holds its last place where this is another one.
+// that holds its last place where this is another one.  Blocks of a chunk share
+// its columns.
+constexpr int kPieceThreads = 128;
 template <typename T, int kV>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kPieceThreads)
     pieces_kernel(const int32_t* __restrict__ keys, const int32_t* __restrict__ tokens, const T* __restrict__ dy,
-                  const GradShape s, float* __restrict__ pieces) {
-  __shared__ int64_t part_lo[2], part_hi[2];
+                  const GradShape s, int column_blocks, float* __restrict__ pieces) {
+  __shared__ int part_lo[2], part_hi[2];  // from the chunk's first place
   pdl_wait();
-  const int64_t c = blockIdx.x, lo = c * kChunk, hi = min(lo + kChunk, s.tokens);
-  if (threadIdx.x < 2) {
-    const int q = threadIdx.x;
-    const int32_t key = keys[q == 0 ? lo : hi - 1];
-    int64_t a = lo, b = lo;  // empty: not a long run, or a row outside the table
-    if (key < s.rows && (q == 0 || key != keys[lo])) {
-      const int64_t begin = lower_bound(keys, s.tokens, key);
-      if (begin + kChunk < s.tokens && keys[begin + kChunk] == key) {
-        a = max(begin, lo);
-        b = a + 1;
-        while (b < hi && keys[b] == key) ++b;
-      }
+  static_assert(kChunk == 32, "a lane per place");
+  constexpr int kU = columns_at_once<T, kV>();
+  const int64_t chunk = blockIdx.x / column_blocks;
+  const int64_t lo = chunk * kChunk, hi = min(lo + kChunk, s.tokens);
+  if (threadIdx.x < 64) {
+    // warp 0: the run of the chunk's first place; warp 1: that of its last one
+    const int q = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t at = q == 0 ? lo : hi - 1;
+    const int32_t key = keys[at], first = keys[lo];
+    // equal keys side by side, up to kChunk of them before the place and from it on
+    const bool before = at - 1 - lane >= 0 && keys[at - 1 - lane] == key;
+    const bool after = at + lane < s.tokens && keys[at + lane] == key;
+    const int left = __ffs(~__ballot_sync(0xFFFFFFFFu, before)) - 1, right = __ffs(~__ballot_sync(0xFFFFFFFFu, after)) - 1;
+    const bool next = at + kChunk < s.tokens && keys[at + kChunk] == key;  // one more than a whole chunk
+    const int n_left = left < 0 ? 32 : left, n_right = right < 0 ? 32 + next : right;
+    if (lane == 0) {
+      const bool used = key < s.rows && n_left + n_right > kChunk && (q == 0 || key != first);
+      const int n = static_cast<int>(hi - lo), place = static_cast<int>(at - lo);
+      part_lo[q] = used ? max(0, place - n_left) : 0;
+      part_hi[q] = used ? min(n, place + n_right) : 0;
     }
-    part_lo[q] = a;
-    part_hi[q] = b;
   }
   __syncthreads();
   const int64_t nv = s.D / kV;
+  const int tx = column_blocks * kPieceThreads;
   for (int q = 0; q < 2; ++q) {
     if (part_lo[q] == part_hi[q]) continue;
-    float* out = pieces + (2 * c + q) * s.D;
-    for (int64_t v = threadIdx.x; v < nv; v += kThreads) {
-      float acc[kV];
+    float* out = pieces + (2 * chunk + q) * s.D;
+    for (int64_t c = (blockIdx.x % column_blocks) * kPieceThreads + threadIdx.x; c < nv; c += kU * tx) {
+      float acc[kU][kV] = {};
+      add_tokens<T, kV, kU>(dy, s, tokens, lo + part_lo[q], lo + part_hi[q], c, tx, nv, acc);
 #pragma unroll
-      for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
-      add_tokens<T, kV>(dy, s, tokens, part_lo[q], part_hi[q], v * kV, acc);
+      for (int u = 0; u < kU; ++u)
+        if (c + u * tx < nv)
 #pragma unroll
-      for (int i = 0; i < kV; ++i) out[v * kV + i] = acc[i];
+          for (int i = 0; i < kV; ++i) out[(c + u * tx) * kV + i] = acc[u][i];
     }
   }
 }
@@ -219,36 +244,54 @@ template <typename T, typename U, int kV>
 __global__ void __launch_bounds__(kThreads)
     table_kernel(const int32_t* __restrict__ keys, const int32_t* __restrict__ tokens, const T* __restrict__ dy,
                  const GradShape s, const float* __restrict__ pieces, float scale, U* __restrict__ dtable) {
-  __shared__ int64_t bound[kRowsPerBlock + 1];
+  __shared__ int64_t range[2];
+  __shared__ int64_t run_lo[kRowsPerBlock], run_hi[kRowsPerBlock];
   pdl_wait();
+  constexpr int kU = columns_at_once<T, kV>();
   const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock;
   const int n = static_cast<int>(min(static_cast<int64_t>(kRowsPerBlock), s.rows - v0));
-  if (threadIdx.x <= n) bound[threadIdx.x] = lower_bound(keys, s.tokens, v0 + threadIdx.x);
+  if (threadIdx.x < 64) {
+    const int64_t at = warp_lower_bound(keys, s.tokens, threadIdx.x < 32 ? v0 : v0 + n);
+    if ((threadIdx.x & 31) == 0) range[threadIdx.x >> 5] = at;
+  } else if (threadIdx.x - 64 < kRowsPerBlock) {
+    run_lo[threadIdx.x - 64] = run_hi[threadIdx.x - 64] = 0;
+  }
+  __syncthreads();
+  for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += kThreads) {
+    const int32_t key = keys[i];
+    if (i == range[0] || keys[i - 1] != key) run_lo[key - v0] = i;
+    if (i == range[1] - 1 || keys[i + 1] != key) run_hi[key - v0] = i + 1;
+  }
   __syncthreads();
   const int ty = kThreads / s.tx;
   const int64_t nv = s.D / kV;
   const uint64_t out_bytes = (static_cast<uint64_t>(s.rows - 1) * s.ldw + s.D) * sizeof(U);
   for (int r = threadIdx.x / s.tx; r < n; r += ty) {
-    const int64_t lo = bound[r], hi = bound[r + 1];
+    const int64_t lo = run_lo[r], hi = run_hi[r];
     U* row = dtable + (v0 + r) * s.ldw;
-    for (int64_t c = threadIdx.x % s.tx; c < nv; c += s.tx) {
-      float acc[kV];
-#pragma unroll
-      for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
+    for (int64_t c = threadIdx.x % s.tx; c < nv; c += kU * s.tx) {
+      float acc[kU][kV] = {};
       if (hi - lo > kChunk) {
         for (int64_t q = lo / kChunk; q * kChunk < hi; ++q) {
-          const float* piece = pieces + (2 * q + (q * kChunk < lo ? 1 : 0)) * s.D + c * kV;
+          const float* piece = pieces + (2 * q + (q * kChunk < lo ? 1 : 0)) * s.D;
 #pragma unroll
-          for (int i = 0; i < kV; ++i) acc[i] += piece[i];
+          for (int u = 0; u < kU; ++u)
+            if (c + u * s.tx < nv)
+#pragma unroll
+              for (int i = 0; i < kV; ++i) acc[u][i] += piece[(c + u * s.tx) * kV + i];
         }
       } else if (hi > lo) {
-        add_tokens<T, kV>(dy, s, tokens, lo, hi, c * kV, acc);
+        add_tokens<T, kV, kU>(dy, s, tokens, lo, hi, c, s.tx, nv, acc);
       }
-      Vec<U, kV> out;
 #pragma unroll
-      for (int i = 0; i < kV; ++i) out.v[i] = narrow<U>(scale * acc[i]);
-      if (in_buf(row + c * kV, sizeof out, dtable, out_bytes, &g_embedding_status))
-        *reinterpret_cast<Vec<U, kV>*>(row + c * kV) = out;
+      for (int u = 0; u < kU; ++u) {
+        Vec<U, kV> out;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) out.v[i] = narrow<U>(scale * acc[u][i]);
+        U* to = row + (c + u * s.tx) * kV;
+        if (c + u * s.tx < nv && in_buf(to, sizeof out, dtable, out_bytes, &g_embedding_status))
+          *reinterpret_cast<Vec<U, kV>*>(to) = out;
+      }
     }
   }
 }
@@ -310,12 +353,17 @@ struct GradCall {
 };
 template <typename T, typename U, int kV>
 int launch_table(GradCall a) {
+  const int64_t nv = a.s.D / kV;
   if (a.s.tokens > kChunk) {
-    const int rc = launch_pdl(pieces_kernel<T, kV>, static_cast<unsigned>(ceil_div(a.s.tokens, kChunk)), kThreads, 0,
-                              a.stream, a.keys, a.tokens, static_cast<const T*>(a.dy), a.s, a.pieces);
+    const int64_t blocks = ceil_div(nv, kPieceThreads * columns_at_once<T, kV>());
+    const int column_blocks = static_cast<int>(blocks < 8 ? blocks : 8);
+    const int rc = launch_pdl(pieces_kernel<T, kV>, static_cast<unsigned>(ceil_div(a.s.tokens, kChunk) * column_blocks),
+                              kPieceThreads, 0, a.stream, a.keys, a.tokens, static_cast<const T*>(a.dy), a.s,
+                              column_blocks, a.pieces);
     if (rc != MXQ_OK) return rc;
   }
-  a.s.tx = threads_per_row(a.s.D / kV);
+  // a thread of a row holds several column vectors at once
+  a.s.tx = threads_per_row(ceil_div(nv, columns_at_once<T, kV>()));
   return launch_pdl(table_kernel<T, U, kV>, static_cast<unsigned>(ceil_div(a.s.rows, kRowsPerBlock)), kThreads, 0,
                     a.stream, a.keys, a.tokens, static_cast<const T*>(a.dy), a.s, a.pieces, a.scale,
                     static_cast<U*>(a.dtable));

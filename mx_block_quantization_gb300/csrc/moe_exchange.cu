@@ -71,13 +71,13 @@ __global__ void __launch_bounds__(kRankThreads)
   }
   const int32_t end = rank_begins<kGroupRows>(E, total, begin, work);
   const uint64_t m_bytes = static_cast<uint64_t>(M) * 4;
-  // rows that fill a group up: expert by expert over the blocks
-  for (int e = blockIdx.x; e < E; e += gridDim.x) {
+  // rows that fill a group up: a warp per expert
+  for (int e = blockIdx.x * kRankWarps + (threadIdx.x >> 5); e < E; e += gridDim.x * kRankWarps) {
     const int64_t lo = begin[e] + total[e];
     const int64_t hi = begin[e] + (total[e] + kGroupRows - 1) / kGroupRows * kGroupRows;
-    for (int64_t m = lo + threadIdx.x; m < hi; m += kRankThreads)
+    for (int64_t m = lo + (threadIdx.x & 31); m < hi; m += 32)
       if (in_buf(source + m, 4, source, m_bytes, &g_exchange_status)) source[m] = -1;
-    if (threadIdx.x == 0) offs[e] = static_cast<int32_t>(hi);
+    if ((threadIdx.x & 31) == 0) offs[e] = static_cast<int32_t>(hi);
   }
   for (int64_t m = end + static_cast<int64_t>(blockIdx.x) * kRankThreads + threadIdx.x; m < M;
        m += static_cast<int64_t>(gridDim.x) * kRankThreads)
@@ -103,13 +103,6 @@ struct ExchangeShape {
   int64_t ldt, ldm;  // elements between the rows of the token matrix and of the group matrix
   int k, tx;         // tx: threads per token (a power of two)
 };
-
-__device__ __forceinline__ int64_t slot_of(const int32_t* slots, int64_t i, int64_t M) {
-  const int32_t s = slots[i];
-  if (s >= 0 && s < M) return s;
-  if (s != -1) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
-  return -1;
-}
 
 // Zeroes those of kFillRows rows that no assignment fills.
 template <typename T, int kV>
@@ -140,116 +133,168 @@ __global__ void __launch_bounds__(kThreads)
   if (t >= s.tokens) return;
   const int64_t nv = s.D / kV;
   const uint64_t bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
+  bool bad = false;
   for (int64_t c = threadIdx.x % s.tx; c < nv; c += s.tx) {
-    const Vec<T, kV> v = *reinterpret_cast<const Vec<T, kV>*>(x + t * s.ldt + c * kV);
+    const Vec<T, kV> v = load_once<T, kV>(x + t * s.ldt + c * kV);
     for (int j = 0; j < s.k; ++j) {
-      const int64_t m = slot_of(slots, t * s.k + j, s.M);
-      if (m >= 0 && in_buf(rows + m * s.ldm + c * kV, kV * sizeof(T), rows, bytes, &g_exchange_status))
+      const int64_t m = slots[t * s.k + j];
+      const bool live = m >= 0 && m < s.M;
+      bad |= !live && m != -1;
+      if (live && in_buf(rows + m * s.ldm + c * kV, kV * sizeof(T), rows, bytes, &g_exchange_status))
         *reinterpret_cast<Vec<T, kV>*>(rows + m * s.ldm + c * kV) = v;
     }
   }
+  if (bad) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
 }
 
-constexpr int kAtOnce = 8;  // rows of a token loaded before the first is used
+// The rows and weights of kJ choices of a token, from choice j0 on: loaded once,
+// before the columns, so that the rows' loads depend on nothing but registers.
+template <int kJ>
+struct Choices {
+  int64_t row[kJ];  // -1: none
+  float w[kJ];
+  __device__ __forceinline__ Choices(const int32_t* slots, const float* weights, const ExchangeShape& s, int64_t t,
+                                     int j0, int64_t ld) {
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const int32_t m = j0 + j < s.k ? slots[t * s.k + j0 + j] : -1;
+      const bool live = m >= 0 && m < s.M;
+      bad |= !live && m != -1;
+      row[j] = live ? m * ld : -1;
+      w[j] = live ? (weights != nullptr ? weights[t * s.k + j0 + j] : 1.0f) : 0.0f;
+    }
+    if (bad) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
+  }
+};
 
-template <typename T, int kV>
+// kJ choices and kU columns (kJ * kU = kAtOnce row pieces) are loaded before the
+// first is used: enough in flight for HBM with few choices as with many.  With
+// the choices read inside the column loop the loads went one by one (57344 rows
+// of 7168 bf16: 462 us).
+constexpr int kAtOnce = 8;
+
+template <typename T, int kV, int kJ>
 __global__ void __launch_bounds__(kThreads)
     combine_kernel(const T* __restrict__ rows, const ExchangeShape s, const int32_t* __restrict__ slots,
                    const float* __restrict__ weights, T* __restrict__ y) {
   pdl_wait();
+  constexpr int kU = kAtOnce / kJ;
   const int ty = kThreads / s.tx;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * ty + threadIdx.x / s.tx;
   if (t >= s.tokens) return;
   const int64_t nv = s.D / kV;
   const uint64_t in_bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
   const uint64_t out_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldt + s.D) * sizeof(T);
-  for (int64_t c = threadIdx.x % s.tx; c < nv; c += s.tx) {
-    float acc[kV];
+  const Choices<kJ> first(slots, weights, s, t, 0, s.ldm);
+  for (int64_t c = threadIdx.x % s.tx; c < nv; c += kU * s.tx) {
+    float acc[kU][kV];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < s.k; j0 += kAtOnce) {
-      Vec<T, kV> v[kAtOnce];
-      float w[kAtOnce];
+    for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        const int64_t m = j0 + j < s.k ? slot_of(slots, t * s.k + j0 + j, s.M) : -1;
-        const bool live = m >= 0 && in_buf(rows + m * s.ldm + c * kV, kV * sizeof(T), rows, in_bytes, &g_exchange_status);
-        v[j] = live ? *reinterpret_cast<const Vec<T, kV>*>(rows + m * s.ldm + c * kV) : Vec<T, kV>{};
-        w[j] = live ? (weights != nullptr ? weights[t * s.k + j0 + j] : 1.0f) : 0.0f;
-      }
+      for (int i = 0; i < kV; ++i) acc[u][i] = 0.0f;
+    const auto add = [&](const Choices<kJ>& from) {
+      Vec<T, kV> v[kJ][kU];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
+      for (int j = 0; j < kJ; ++j)
 #pragma unroll
-        for (int i = 0; i < kV; ++i) acc[i] = fmaf(w[j], widen(v[j].v[i]), acc[i]);
+        for (int u = 0; u < kU; ++u) {
+          const T* p = rows + from.row[j] + (c + u * s.tx) * kV;
+          v[j][u] = Vec<T, kV>{};
+          if (from.row[j] >= 0 && c + u * s.tx < nv && in_buf(p, sizeof v[j][u], rows, in_bytes, &g_exchange_status))
+            v[j][u] = load_once<T, kV>(p);
+        }
+#pragma unroll
+      for (int j = 0; j < kJ; ++j)
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int i = 0; i < kV; ++i) acc[u][i] = fmaf(from.w[j], widen(v[j][u].v[i]), acc[u][i]);
+    };
+    add(first);
+    if (kJ == kAtOnce)
+      for (int j0 = kJ; j0 < s.k; j0 += kJ) add(Choices<kJ>(slots, weights, s, t, j0, s.ldm));
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      Vec<T, kV> out;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) out.v[i] = narrow<T>(acc[u][i]);
+      T* to = y + t * s.ldt + (c + u * s.tx) * kV;
+      if (c + u * s.tx < nv && in_buf(to, sizeof out, y, out_bytes, &g_exchange_status)) *reinterpret_cast<Vec<T, kV>*>(to) = out;
     }
-    Vec<T, kV> out;
-#pragma unroll
-    for (int i = 0; i < kV; ++i) out.v[i] = narrow<T>(acc[i]);
-    if (in_buf(y + t * s.ldt + c * kV, kV * sizeof(T), y, out_bytes, &g_exchange_status))
-      *reinterpret_cast<Vec<T, kV>*>(y + t * s.ldt + c * kV) = out;
   }
 }
 
 // kWarps warps per token (1 or all of the block's).
-template <typename T, int kV, int kWarps>
+template <typename T, int kV, int kJ, int kWarps>
 __global__ void __launch_bounds__(kThreads)
     combine_backward_kernel(const T* __restrict__ dy, const T* __restrict__ rows, const ExchangeShape s, int64_t ldr,
                             const int32_t* __restrict__ slots, const int32_t* __restrict__ source,
                             const float* __restrict__ weights, T* __restrict__ drows, float* __restrict__ dweights,
                             int64_t token_blocks) {
-  __shared__ float red[kThreads / 32][kAtOnce];
+  __shared__ float red[kThreads / 32][kJ];
   pdl_wait();
   if (static_cast<int64_t>(blockIdx.x) >= token_blocks) {
     zero_unused<T, kV>(s, source, drows, blockIdx.x - token_blocks);
     return;
   }
+  constexpr int kU = kAtOnce / kJ;
   constexpr int kGroup = kWarps * 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / kGroup) + threadIdx.x / kGroup;
-  const bool live_token = t < s.tokens;  // for kWarps > 1 the same for the whole block
-  if (kWarps == 1 && !live_token) return;
+  if (t >= s.tokens) return;  // a whole warp, and for kWarps > 1 a whole block
   const int64_t nv = s.D / kV;
   const uint64_t in_bytes = (static_cast<uint64_t>(s.M - 1) * ldr + s.D) * sizeof(T);
   const uint64_t out_bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
-  for (int j0 = 0; j0 < s.k; j0 += kAtOnce) {
-    float dot[kAtOnce], w[kAtOnce];
-    int64_t m[kAtOnce];
+  for (int j0 = 0; j0 < s.k; j0 += kJ) {
+    const Choices<kJ> from(slots, weights, s, t, j0, ldr);
+    int64_t to[kJ];
+    float dot[kJ];
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
+    for (int j = 0; j < kJ; ++j) {
+      to[j] = from.row[j] >= 0 ? static_cast<int64_t>(slots[t * s.k + j0 + j]) * s.ldm : -1;
       dot[j] = 0.0f;
-      m[j] = j0 + j < s.k ? slot_of(slots, t * s.k + j0 + j, s.M) : -1;
-      w[j] = m[j] >= 0 ? weights[t * s.k + j0 + j] : 0.0f;
     }
-    for (int64_t c = threadIdx.x % kGroup; c < nv; c += kGroup) {
-      const Vec<T, kV> g = *reinterpret_cast<const Vec<T, kV>*>(dy + t * s.ldt + c * kV);
-      Vec<T, kV> v[kAtOnce];
+    for (int64_t c = threadIdx.x % kGroup; c < nv; c += kU * kGroup) {
+      Vec<T, kV> g[kU], v[kJ][kU];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
-        v[j] = m[j] >= 0 && in_buf(rows + m[j] * ldr + c * kV, kV * sizeof(T), rows, in_bytes, &g_exchange_status)
-                   ? *reinterpret_cast<const Vec<T, kV>*>(rows + m[j] * ldr + c * kV)
-                   : Vec<T, kV>{};
+      for (int u = 0; u < kU; ++u) {
+        const int64_t col = (c + u * kGroup) * kV;
+        g[u] = Vec<T, kV>{};
+        if (c + u * kGroup < nv) g[u] = *reinterpret_cast<const Vec<T, kV>*>(dy + t * s.ldt + col);
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
-        Vec<T, kV> out;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) {
-          const float d = widen(g.v[i]);
-          dot[j] = fmaf(d, widen(v[j].v[i]), dot[j]);
-          out.v[i] = narrow<T>(w[j] * d);
+        for (int j = 0; j < kJ; ++j) {
+          v[j][u] = Vec<T, kV>{};
+          if (from.row[j] >= 0 && c + u * kGroup < nv &&
+              in_buf(rows + from.row[j] + col, sizeof v[j][u], rows, in_bytes, &g_exchange_status))
+            v[j][u] = load_once<T, kV>(rows + from.row[j] + col);
         }
-        if (m[j] >= 0 && in_buf(drows + m[j] * s.ldm + c * kV, kV * sizeof(T), drows, out_bytes, &g_exchange_status))
-          *reinterpret_cast<Vec<T, kV>*>(drows + m[j] * s.ldm + c * kV) = out;
       }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          Vec<T, kV> out;
+#pragma unroll
+          for (int i = 0; i < kV; ++i) {
+            const float d = widen(g[u].v[i]);
+            dot[j] = fmaf(d, widen(v[j][u].v[i]), dot[j]);
+            out.v[i] = narrow<T>(from.w[j] * d);
+          }
+          T* p = drows + to[j] + (c + u * kGroup) * kV;
+          if (to[j] >= 0 && c + u * kGroup < nv && in_buf(p, sizeof out, drows, out_bytes, &g_exchange_status))
+            *reinterpret_cast<Vec<T, kV>*>(p) = out;
+        }
     }
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) dot[j] = warp_sum(dot[j]);
+    for (int j = 0; j < kJ; ++j) dot[j] = warp_sum(dot[j]);
     if (kWarps > 1) {
       if (lane == 0)
 #pragma unroll
-        for (int j = 0; j < kAtOnce; ++j) red[warp][j] = dot[j];
+        for (int j = 0; j < kJ; ++j) red[warp][j] = dot[j];
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) {
+      for (int j = 0; j < kJ; ++j) {
         dot[j] = 0.0f;
         for (int q = 0; q < kWarps; ++q) dot[j] += red[q][j];
       }
@@ -257,8 +302,8 @@ __global__ void __launch_bounds__(kThreads)
     }
     if (threadIdx.x % kGroup == 0)
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
-        if (j0 + j < s.k) dweights[t * s.k + j0 + j] = m[j] >= 0 ? dot[j] : 0.0f;
+      for (int j = 0; j < kJ; ++j)
+        if (j0 + j < s.k) dweights[t * s.k + j0 + j] = from.row[j] >= 0 ? dot[j] : 0.0f;
   }
 }
 
@@ -285,20 +330,28 @@ int launch_dispatch(const RowsCall& a) {
   return launch_pdl(dispatch_kernel<T, kV>, static_cast<unsigned>(blocks), kThreads, 0, a.stream,
                     static_cast<const T*>(a.in), a.s, a.slots, a.source, static_cast<T*>(a.out), token_blocks);
 }
+// Choices handled at once: 2, 4 or 8, the smallest that holds k.
 template <typename T, int kV>
 int launch_combine(const RowsCall& a) {
-  return launch_pdl(combine_kernel<T, kV>, static_cast<unsigned>(ceil_div(a.s.tokens, kThreads / a.s.tx)), kThreads, 0,
-                    a.stream, static_cast<const T*>(a.in), a.s, a.slots, a.weights, static_cast<T*>(a.out));
+  const auto kernel = a.s.k <= 2 ? combine_kernel<T, kV, 2> : a.s.k <= 4 ? combine_kernel<T, kV, 4> : combine_kernel<T, kV, 8>;
+  return launch_pdl(kernel, static_cast<unsigned>(ceil_div(a.s.tokens, kThreads / a.s.tx)), kThreads, 0, a.stream,
+                    static_cast<const T*>(a.in), a.s, a.slots, a.weights, static_cast<T*>(a.out));
 }
-template <typename T, int kV>
+template <typename T, int kV, int kJ>
 int launch_combine_backward(const RowsCall& a) {
   const bool wide = a.s.D / kV >= kThreads;
   const int64_t token_blocks = wide ? a.s.tokens : ceil_div(a.s.tokens, kThreads / 32);
   const int64_t blocks = token_blocks + ceil_div(a.s.M, kFillRows);
-  return launch_pdl(wide ? combine_backward_kernel<T, kV, kThreads / 32> : combine_backward_kernel<T, kV, 1>,
+  return launch_pdl(wide ? combine_backward_kernel<T, kV, kJ, kThreads / 32> : combine_backward_kernel<T, kV, kJ, 1>,
                     static_cast<unsigned>(blocks), kThreads, 0, a.stream, static_cast<const T*>(a.in2),
                     static_cast<const T*>(a.in), a.s, a.ldr, a.slots, a.source, a.weights, static_cast<T*>(a.out),
                     a.dweights, token_blocks);
+}
+template <typename T, int kV>
+int launch_combine_backward(const RowsCall& a) {
+  return a.s.k <= 2   ? launch_combine_backward<T, kV, 2>(a)
+         : a.s.k <= 4 ? launch_combine_backward<T, kV, 4>(a)
+                      : launch_combine_backward<T, kV, 8>(a);
 }
 
 enum class Rows { kDispatch, kCombine, kCombineBackward };

@@ -11,13 +11,18 @@
 //   p_e ([e chosen] dw_e - sum_chosen p dw) otherwise.
 //
 // One warp owns a token; a lane keeps kPer of its logits in registers, so the
-// logits are read once each way.  Choosing is by an order-preserving integer
-// key: one warp-wide integer maximum gives the value and one warp-wide minimum
-// over the lanes that hold it gives the lowest index.  A lane also keeps the
+// logits are read once each way, the next token's while this one is worked on.
+// Choosing works on an order-preserving integer key, with the warp-wide integer
+// maximum.  The k-th largest of the lanes' own maxima is at most the k-th largest
+// logit, so only the few logits from there on (k to a dozen of random ones) are
+// gathered, one per lane, and the k largest taken from them, ties by one more
+// warp-wide minimum over the indices.  With more than 32 such logits (many equal
+// ones) every logit takes part in each of the k rounds.  A lane also keeps the
 // sums over its tokens of the probabilities of its experts; they are added up
 // per block and then over the blocks in a fixed order, so the loss has the
 // same bits in every run.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math_constants.h>
 #include <stdint.h>
 
@@ -48,57 +53,91 @@ __device__ __forceinline__ int expert_of(int i, int lane) {
   return (i / kV) * (32 * kV) + lane * kV + i % kV;
 }
 
-// The lane's logits of one row; experts past E read as -inf.
+// A lane's logits of one row as they are stored; and as values, experts past E
+// as -inf.
 template <typename T, int kPer, int kV>
-__device__ __forceinline__ void load_row(const T* row, int E, int lane, float (&x)[kPer]) {
+struct Row {
+  Vec<T, kV> v[kPer / kV];
+  __device__ __forceinline__ void load(const T* row, int E, int lane) {
 #pragma unroll
-  for (int c = 0; c < kPer / kV; ++c) {
-    const int e0 = expert_of<kV>(c * kV, lane);
-    if (e0 + kV <= E) {
-      const Vec<T, kV> v = *reinterpret_cast<const Vec<T, kV>*>(row + e0);
+    for (int c = 0; c < kPer / kV; ++c) {
+      const int e0 = expert_of<kV>(c * kV, lane);
+      if (e0 + kV <= E) {
+        v[c] = load_once<T, kV>(row + e0);
+      } else {
 #pragma unroll
-      for (int j = 0; j < kV; ++j) x[c * kV + j] = widen(v.v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kV; ++j) x[c * kV + j] = e0 + j < E ? widen(row[e0 + j]) : -CUDART_INF_F;
+        for (int j = 0; j < kV; ++j)
+          if (e0 + j < E) v[c].v[j] = row[e0 + j];
+      }
     }
   }
-}
+  __device__ __forceinline__ void values(int E, int lane, float (&x)[kPer]) const {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = expert_of<kV>(i, lane) < E ? widen(v[i / kV].v[i % kV]) : -CUDART_INF_F;
+  }
+};
 
 struct RouteShape {
   int64_t tokens, ld;
   int E, k, renorm;
 };
 
-// Sums over the blocks in block order: counts, routed tokens and loss.
-// part_p/part_c are [blocks, E], part_n [blocks].
+// Sums over the blocks: counts, routed tokens and loss.  part_p/part_c are
+// [blocks, E], part_n [blocks].  The threads form `groups` teams with a thread
+// per expert; a team adds up every groups-th block and the teams' sums are
+// added in order.  `red` holds 2 * blockDim.x words.
 __device__ void join_blocks(const RouteShape s, int blocks, const float* part_p, const int32_t* part_c,
                             const int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out,
                             float* red) {
   const int tid = threadIdx.x, nt = blockDim.x;
-  int n = 0;
-  for (int b = 0; b < blocks; ++b) n += part_n[b];
+  int team = 32;
+  while (team < s.E && team < nt) team *= 2;
+  const int groups = nt / team, group = tid / team;
+  float* sum_p = red;
+  int32_t* sum_c = reinterpret_cast<int32_t*>(red + nt);
+  __shared__ float warp_loss[32];
+  __shared__ int32_t all_n;
+  if (tid < 32) {
+    int n = 0;
+    for (int b = tid; b < blocks; b += 32) n += part_n[b];
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+    if (tid == 0) all_n = n;
+  }
   float local = 0.0f;
-  for (int e = tid; e < s.E; e += nt) {
+  for (int e0 = 0; e0 < s.E; e0 += team) {
+    const int e = e0 + tid % team;
     float p = 0.0f;
     int c = 0;
+    if (e < s.E) {
 #pragma unroll 8
-    for (int b = 0; b < blocks; ++b) {
-      p += part_p[static_cast<int64_t>(b) * s.E + e];
-      c += part_c[static_cast<int64_t>(b) * s.E + e];
+      for (int b = group; b < blocks; b += groups) {
+        p += part_p[static_cast<int64_t>(b) * s.E + e];
+        c += part_c[static_cast<int64_t>(b) * s.E + e];
+      }
     }
-    counts[e] = c;
-    local += static_cast<float>(c) * p;
+    sum_p[tid] = p;
+    sum_c[tid] = c;
+    __syncthreads();
+    if (group == 0 && e < s.E) {
+      for (int g = 1; g < groups; ++g) {
+        p += sum_p[g * team + tid];
+        c += sum_c[g * team + tid];
+      }
+      counts[e] = c;
+      local += static_cast<float>(c) * p;
+    }
+    __syncthreads();
   }
   local = warp_sum(local);
-  if ((tid & 31) == 0) red[tid >> 5] = local;
+  if ((tid & 31) == 0) warp_loss[tid >> 5] = local;
   __syncthreads();
-  if (tid == 0) {
-    float sum = 0.0f;
-    for (int w = 0; w < nt / 32; ++w) sum += red[w];
-    const float fn = static_cast<float>(n);
-    *loss = n > 0 ? sum * (static_cast<float>(s.E) / (static_cast<float>(s.k) * fn * fn)) : 0.0f;
-    *n_out = n;
+  if (tid < 32) {
+    local = warp_sum(tid < nt / 32 ? warp_loss[tid] : 0.0f);
+    if (tid == 0) {
+      const float n = static_cast<float>(all_n);
+      *loss = all_n > 0 ? local * (static_cast<float>(s.E) / (static_cast<float>(s.k) * n * n)) : 0.0f;
+      *n_out = all_n;
+    }
   }
 }
 
@@ -109,10 +148,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                  int32_t* part_c, int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kWarps = kThreads / 32;
-  int32_t* hist = reinterpret_cast<int32_t*>(smem);         // [E]
+  float* red = reinterpret_cast<float*>(smem);              // [2 * threads], for the join
+  int32_t* hist = reinterpret_cast<int32_t*>(red + 2 * kThreads);  // [E]
   float* sums = reinterpret_cast<float*>(hist + s.E);       // [E]
   __shared__ int32_t routed_tokens;
-  __shared__ float red[kWarps];
+  __shared__ uint2 few[kWarps][32];                         // key and expert of the logits gathered
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int e = tid; e < s.E; e += kThreads) hist[e] = 0, sums[e] = 0.0f;
   if (tid == 0) routed_tokens = 0;
@@ -125,53 +165,102 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
   int routed_here = 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < s.tokens; t += step) {
-    const T* row = logits + t * s.ld;
+  Row<T, kPer, kV> ahead;
+  const auto fetch = [&](int64_t t) {
+    if (t < s.tokens && in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status))
+      ahead.load(logits + t * s.ld, s.E, lane);
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  fetch(t);
+  for (; t < s.tokens; t += step) {
     float x[kPer];
-    if (in_buf(row, s.E * sizeof(T), logits, in_bytes, &g_route_status)) load_row<T, kPer, kV>(row, s.E, lane, x);
-    uint32_t key[kPer], best = 0;
-    bool nan = false;
+    ahead.values(s.E, lane, x);
+    fetch(t + step);
+    float best = -CUDART_INF_F;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      key[i] = order_key(x[i]);
-      best = max(best, key[i]);
-      nan |= x[i] != x[i];
+    for (int i = 0; i < kPer; ++i) best = fmaxf(best, x[i]);  // skips NaN
+    // the k-th largest lane maximum, equal ones counted once; 0 when there are fewer
+    uint32_t mine = order_key(best), bar = 0, top_key = 0;
+    for (int j = 0; j < s.k; ++j) {
+      bar = __reduce_max_sync(0xFFFFFFFFu, mine);
+      if (j == 0) top_key = bar;
+      if (bar == 0u) break;
+      if (mine == bar) mine = 0u;
     }
-    best = __reduce_max_sync(0xFFFFFFFFu, best);
-    const bool routed = (mask == nullptr || mask[t] != 0) && (best != 0u || __any_sync(0xFFFFFFFFu, nan));
+    bool routed = mask == nullptr || mask[t] != 0;
+    if (routed && top_key == 0u) {  // no logit to choose: counted only if one is NaN
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) nan |= x[i] != x[i];
+      routed = __any_sync(0xFFFFFFFFu, nan);
+    }
     int my_id = -1;
     float my_w = 0.0f;
     if (routed) {
       ++routed_here;
-      const float top = best != 0u ? key_value(best) : -CUDART_INF_F;
+      const float top = top_key != 0u ? key_value(top_key) : -CUDART_INF_F;
+      const float from = bar != 0u ? key_value(bar) : -FLT_MAX;
+      uint32_t my_key = 0;
+      if (top_key != 0u) {
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const bool in = x[i] >= from;  // false for NaN and -inf
+          const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
+          if (who != 0u) {
+            const int at = n + __popc(who & ((1u << lane) - 1u));
+            if (in && at < 32) few[warp][at] = make_uint2(order_key(x[i]), expert_of<kV>(i, lane));
+            n += __popc(who);
+          }
+        }
+        __syncwarp();
+        if (n <= 32) {
+          const uint2 mine2 = lane < n ? few[warp][lane] : make_uint2(0u, 0u);
+          uint32_t key = mine2.x;
+          for (int j = 0; j < s.k; ++j) {
+            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, key);
+            if (m == 0u) break;
+            const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, key == m ? mine2.y : ~0u);
+            if (key == m && mine2.y == e) key = 0u;
+            if (lane == j) {
+              my_id = static_cast<int>(e);
+              my_key = m;
+            }
+          }
+        } else {
+          uint32_t key[kPer];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) key[i] = order_key(x[i]);
+          for (int j = 0; j < s.k; ++j) {
+            uint32_t local = 0;
+            int at = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (key[i] > local) local = key[i], at = expert_of<kV>(i, lane);
+            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, local);
+            if (m == 0u) break;
+            const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, local == m ? static_cast<uint32_t>(at) : ~0u));
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+              if (expert_of<kV>(i, lane) == e) key[i] = 0u;
+            if (lane == j) {
+              my_id = e;
+              my_key = m;
+            }
+          }
+        }
+        __syncwarp();
+      }
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        x[i] = exp2_ftz((x[i] - top) * kLog2E);
-        if (expert_of<kV>(i, lane) >= s.E) x[i] = 0.0f;
+        x[i] = exp2_ftz((x[i] - top) * kLog2E);  // 0 past E: those are -inf
         sum += x[i];
       }
       const float inv = 1.0f / warp_sum(sum);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
-      for (int j = 0; j < s.k; ++j) {
-        uint32_t local = 0;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (key[i] > local) local = key[i], at = expert_of<kV>(i, lane);
-        const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, local);
-        if (m == 0u) break;
-        const int e = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, local == m ? static_cast<uint32_t>(at) : ~0u));
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (expert_of<kV>(i, lane) == e) key[i] = 0u;
-        if (lane == j) {
-          my_id = e;
-          my_w = exp2_ftz((key_value(m) - top) * kLog2E);
-        }
-      }
-      my_w *= inv;  // NaN for a row with NaN or +inf, over the chosen ones' sum too
+      if (my_id >= 0) my_w = exp2_ftz((key_value(my_key) - top) * kLog2E) * inv;  // NaN in a row with NaN or +inf
       if (s.renorm) my_w /= warp_sum(my_w);
       if (my_id < 0) my_w = 0.0f;
       if (my_id >= 0) atomicAdd(&hist[my_id], 1);
@@ -210,7 +299,7 @@ constexpr int kJoinThreads = 1024;
 __global__ void __launch_bounds__(kJoinThreads)
     route_join_kernel(const RouteShape s, int blocks, const float* part_p, const int32_t* part_c,
                       const int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out) {
-  __shared__ float red[kJoinThreads / 32];
+  __shared__ float red[2 * kJoinThreads];
   pdl_wait();
   join_blocks(s, blocks, part_p, part_c, part_n, counts, loss, n_out, red);
 }
@@ -243,10 +332,26 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp; t < s.tokens; t += step) {
+  Row<T, kPer, kV> ahead;
+  const auto fetch = [&](int64_t t) {
+    if (t < s.tokens && in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status))
+      ahead.load(logits + t * s.ld, s.E, lane);
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  fetch(t);
+  for (; t < s.tokens; t += step) {
     const T* row = logits + t * s.ld;
+    int e = -1;
+    float dw = 0.0f;
+    if (dweights != nullptr && lane < s.k) {
+      e = ids[t * s.k + lane];
+      dw = dweights[t * s.k + lane];
+      if (e < 0 || e >= s.E) e = -1;
+    }
+    const float chosen_logit = e >= 0 ? widen(row[e]) : 0.0f;
     float x[kPer];
-    if (in_buf(row, s.E * sizeof(T), logits, in_bytes, &g_route_status)) load_row<T, kPer, kV>(row, s.E, lane, x);
+    ahead.values(s.E, lane, x);
+    fetch(t + step);
     float top = -CUDART_INF_F;
     bool nan = false;
 #pragma unroll
@@ -262,8 +367,7 @@ __global__ void __launch_bounds__(kThreads)
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        x[i] = exp2_ftz((x[i] - top) * kLog2E);
-        if (expert_of<kV>(i, lane) >= s.E) x[i] = 0.0f;
+        x[i] = exp2_ftz((x[i] - top) * kLog2E);  // 0 past E: those are -inf
         sum += x[i];
       }
       const float inv = 1.0f / warp_sum(sum);
@@ -273,16 +377,8 @@ __global__ void __launch_bounds__(kThreads)
         x[i] *= inv;
         pc = fmaf(x[i], c[i], pc);
       }
-      int e = -1;
-      float w = 0.0f, dw = 0.0f;
-      if (dweights != nullptr && lane < s.k) {
-        e = ids[t * s.k + lane];
-        if (e < 0 || e >= s.E) e = -1;
-        if (e >= 0) {
-          dw = dweights[t * s.k + lane];
-          w = exp2_ftz((widen(row[e]) - top) * kLog2E);
-        }
-      }
+      float w = e >= 0 ? exp2_ftz((chosen_logit - top) * kLog2E) : 0.0f;
+      if (e < 0) dw = 0.0f;
       float part = 0.0f;
       w *= inv;
       if (s.renorm) {
@@ -298,7 +394,11 @@ __global__ void __launch_bounds__(kThreads)
       __syncwarp();
       const float total = warp_sum(pc);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) x[i] = fmaf(x[i], c[i] - total, chosen[expert_of<kV>(i, lane)]);
+      for (int q = 0; q < kPer / kV; ++q) {
+        const Vec<float, kV> add = *reinterpret_cast<const Vec<float, kV>*>(chosen + expert_of<kV>(q * kV, lane));
+#pragma unroll
+        for (int i = 0; i < kV; ++i) x[q * kV + i] = fmaf(x[q * kV + i], c[q * kV + i] - total, add.v[i]);
+      }
       __syncwarp();
       if (e >= 0) chosen[e] = 0.0f;
     } else {
@@ -364,7 +464,7 @@ int launch_route(const RouteCall& a) {
   float* part_p = reinterpret_cast<float*>(a.workspace);
   int32_t* part_c = reinterpret_cast<int32_t*>(part_p + static_cast<int64_t>(blocks) * a.s.E);
   int32_t* part_n = part_c + static_cast<int64_t>(blocks) * a.s.E;
-  int rc = launch_pdl(route_kernel<T, kPer, kV, kThreads>, blocks, kThreads, a.s.E * 8, a.stream,
+  int rc = launch_pdl(route_kernel<T, kPer, kV, kThreads>, blocks, kThreads, a.s.E * 8 + kThreads * 8, a.stream,
                       static_cast<const T*>(a.logits), a.s, a.mask, a.weights, a.ids, part_p, part_c, part_n,
                       a.counts, a.loss, a.n);
   if (rc != MXQ_OK || blocks == 1) return rc;

@@ -39,6 +39,21 @@ struct alignas(sizeof(T) * kN) Vec {
   T v[kN];
 };
 
+// Load of data that is read once: not kept in L1, first to leave L2.
+template <typename T, int kN>
+__device__ __forceinline__ Vec<T, kN> load_once(const T* p) {
+  Vec<T, kN> v;
+  if constexpr (sizeof v == 16)
+    *reinterpret_cast<uint4*>(&v) = __ldcs(reinterpret_cast<const uint4*>(p));
+  else if constexpr (sizeof v == 8)
+    *reinterpret_cast<uint2*>(&v) = __ldcs(reinterpret_cast<const uint2*>(p));
+  else if constexpr (sizeof v == 4)
+    *reinterpret_cast<uint32_t*>(&v) = __ldcs(reinterpret_cast<const uint32_t*>(p));
+  else
+    *reinterpret_cast<uint16_t*>(&v) = __ldcs(reinterpret_cast<const uint16_t*>(p));
+  return v;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(kRankThreads)
     digit_count_kernel(const Source src, const RankSplit s, int shift, int bins, int32_t* chunk_counts) {
   extern __shared__ int32_t counts[];
   pdl_wait();
+  pdl_launch_dependents();  // as few blocks follow
   rank_count(s, bins, [&](int64_t i) { return (src.full(i) >> shift) & (bins - 1); }, counts);
   for (int b = threadIdx.x; b < bins; b += kRankThreads)
     chunk_counts[static_cast<int64_t>(blockIdx.x) * bins + b] = counts[b];

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kRankThreads)
     plan_count_kernel(const int32_t* __restrict__ ids, RankSplit s, int E, int32_t* chunk_counts) {
   extern __shared__ int32_t counts[];
   pdl_wait();
+  pdl_launch_dependents();  // as few blocks follow
   rank_count(s, E, ExpertKey{ids, E}, counts);
   for (int e = threadIdx.x; e < E; e += kRankThreads)
     chunk_counts[static_cast<int64_t>(blockIdx.x) * E + e] = counts[e];

@@ -12,12 +12,11 @@
 //
 // One warp owns a token; a lane keeps kPer of its logits in registers, so the
 // logits are read once each way, the next token's while this one is worked on.
-// Choosing works on an order-preserving integer key, with the warp-wide integer
-// maximum.  The k-th largest of the lanes' own maxima is at most the k-th largest
-// logit, so only the few logits from there on (k to a dozen of random ones) are
-// gathered, one per lane, and the k largest taken from them, ties by one more
-// warp-wide minimum over the indices.  With more than 32 such logits (many equal
-// ones) every logit takes part in each of the k rounds.  A lane also keeps the
+// The k-th largest of the lanes' own maxima is at most the k-th largest logit, so
+// only the few logits from there on (k to a dozen of random ones) are gathered,
+// one per lane, and each counts those before it: larger, or equal with a lower
+// index.  With more than 32 such logits (many equal ones) every logit takes part
+// in each of k rounds of a warp-wide maximum.  A lane also keeps the
 // sums over its tokens of the probabilities of its experts; they are added up
 // per block and then over the blocks in a fixed order, so the loss has the
 // same bits in every run.
@@ -53,11 +52,25 @@ __device__ __forceinline__ int expert_of(int i, int lane) {
   return (i / kV) * (32 * kV) + lane * kV + i % kV;
 }
 
-// A lane's logits of one row as they are stored; and as values, experts past E
-// as -inf.
+// A lane's logits of one row as they are stored; experts past E are -inf and
+// stay so.
+template <typename T>
+__device__ __forceinline__ T minus_infinity();
+template <>
+__device__ __forceinline__ float minus_infinity<float>() {
+  return -CUDART_INF_F;
+}
+template <>
+__device__ __forceinline__ bf16_t minus_infinity<bf16_t>() {
+  return 0xFF80u;
+}
 template <typename T, int kPer, int kV>
 struct Row {
   Vec<T, kV> v[kPer / kV];
+  __device__ __forceinline__ Row() {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i / kV].v[i % kV] = minus_infinity<T>();
+  }
   __device__ __forceinline__ void load(const T* row, int E, int lane) {
 #pragma unroll
     for (int c = 0; c < kPer / kV; ++c) {
@@ -71,11 +84,18 @@ struct Row {
       }
     }
   }
-  __device__ __forceinline__ void values(int E, int lane, float (&x)[kPer]) const {
+  __device__ __forceinline__ void values(float (&x)[kPer]) const {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) x[i] = expert_of<kV>(i, lane) < E ? widen(v[i / kV].v[i % kV]) : -CUDART_INF_F;
+    for (int i = 0; i < kPer; ++i) x[i] = widen(v[i / kV].v[i % kV]);
   }
 };
+
+// 1/x to one unit in the last place, without the exact division's branches.
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 struct RouteShape {
   int64_t tokens, ld;
@@ -148,18 +168,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                  int32_t* part_c, int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kWarps = kThreads / 32;
-  float* red = reinterpret_cast<float*>(smem);              // [2 * threads], for the join
-  int32_t* hist = reinterpret_cast<int32_t*>(red + 2 * kThreads);  // [E]
+  float* by_warp = reinterpret_cast<float*>(smem);          // [warps, 32 * kPer]; then
+  float* red = by_warp;                                     // [2 * threads] for the join
+  int32_t* hist = reinterpret_cast<int32_t*>(by_warp + (kPer > 2 ? kPer : 2) * kThreads);  // [E]
   float* sums = reinterpret_cast<float*>(hist + s.E);       // [E]
   __shared__ int32_t routed_tokens;
-  __shared__ uint2 few[kWarps][32];                         // key and expert of the logits gathered
+  __shared__ float2 few[kWarps][32];                        // the logits gathered, with their experts
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int e = tid; e < s.E; e += kThreads) hist[e] = 0, sums[e] = 0.0f;
+  for (int e = tid; e < s.E; e += kThreads) hist[e] = 0;
   if (tid == 0) routed_tokens = 0;
   __syncthreads();
   pdl_wait();
   const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
   const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
+  if (gridDim.x > 1) pdl_launch_dependents();  // the join that follows has one block
   float acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
@@ -174,18 +196,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   fetch(t);
   for (; t < s.tokens; t += step) {
     float x[kPer];
-    ahead.values(s.E, lane, x);
+    ahead.values(x);
     fetch(t + step);
     float best = -CUDART_INF_F;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) best = fmaxf(best, x[i]);  // skips NaN
     // the k-th largest lane maximum, equal ones counted once; 0 when there are fewer
-    uint32_t mine = order_key(best), bar = 0, top_key = 0;
-    for (int j = 0; j < s.k; ++j) {
-      bar = __reduce_max_sync(0xFFFFFFFFu, mine);
-      if (j == 0) top_key = bar;
-      if (bar == 0u) break;
+    uint32_t mine = order_key(best);
+    const uint32_t top_key = __reduce_max_sync(0xFFFFFFFFu, mine);
+    uint32_t bar = top_key;
+#pragma unroll 4
+    for (int j = 1; j < s.k; ++j) {
       if (mine == bar) mine = 0u;
+      bar = __reduce_max_sync(0xFFFFFFFFu, mine);
     }
     bool routed = mask == nullptr || mask[t] != 0;
     if (routed && top_key == 0u) {  // no logit to choose: counted only if one is NaN
@@ -194,38 +217,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < kPer; ++i) nan |= x[i] != x[i];
       routed = __any_sync(0xFFFFFFFFu, nan);
     }
-    int my_id = -1;
-    float my_w = 0.0f;
+    // a lane with a chosen expert: its place among the chosen, its expert and its logit
+    int rank = kMaxK, my_id = -1;
+    float my_x = 0.0f, my_w = 0.0f;
     if (routed) {
       ++routed_here;
       const float top = top_key != 0u ? key_value(top_key) : -CUDART_INF_F;
       const float from = bar != 0u ? key_value(bar) : -FLT_MAX;
-      uint32_t my_key = 0;
       if (top_key != 0u) {
         int n = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const bool in = x[i] >= from;  // false for NaN and -inf
           const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-          if (who != 0u) {
-            const int at = n + __popc(who & ((1u << lane) - 1u));
-            if (in && at < 32) few[warp][at] = make_uint2(order_key(x[i]), expert_of<kV>(i, lane));
-            n += __popc(who);
-          }
+          // past 32 they overwrite one another and are not used
+          if (in)
+            few[warp][(n + __popc(who & ((1u << lane) - 1u))) & 31] =
+                make_float2(x[i], __int_as_float(expert_of<kV>(i, lane)));
+          n += __popc(who);
         }
         __syncwarp();
         if (n <= 32) {
-          const uint2 mine2 = lane < n ? few[warp][lane] : make_uint2(0u, 0u);
-          uint32_t key = mine2.x;
-          for (int j = 0; j < s.k; ++j) {
-            const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, key);
-            if (m == 0u) break;
-            const uint32_t e = __reduce_min_sync(0xFFFFFFFFu, key == m ? mine2.y : ~0u);
-            if (key == m && mine2.y == e) key = 0u;
-            if (lane == j) {
-              my_id = static_cast<int>(e);
-              my_key = m;
-            }
+          const float2 own = few[warp][lane];
+          const int e = __float_as_int(own.y);
+          int before = 0;
+#pragma unroll 4
+          for (int i = 0; i < n; ++i) {
+            const float2 other = few[warp][i];
+            before += other.x > own.x || (other.x == own.x && __float_as_int(other.y) < e) ? 1 : 0;
+          }
+          if (lane < n && before < s.k) {
+            rank = before;
+            my_id = e;
+            my_x = own.x;
           }
         } else {
           uint32_t key[kPer];
@@ -244,8 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kPer; ++i)
               if (expert_of<kV>(i, lane) == e) key[i] = 0u;
             if (lane == j) {
+              rank = j;
               my_id = e;
-              my_key = m;
+              my_x = key_value(m);
             }
           }
         }
@@ -257,32 +282,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         x[i] = exp2_ftz((x[i] - top) * kLog2E);  // 0 past E: those are -inf
         sum += x[i];
       }
-      const float inv = 1.0f / warp_sum(sum);
+      const float inv = reciprocal(warp_sum(sum));
 #pragma unroll
       for (int i = 0; i < kPer; ++i) acc[i] = fmaf(x[i], inv, acc[i]);
-      if (my_id >= 0) my_w = exp2_ftz((key_value(my_key) - top) * kLog2E) * inv;  // NaN in a row with NaN or +inf
+      if (my_id >= 0) {
+        my_w = exp2_ftz((my_x - top) * kLog2E) * inv;  // NaN in a row with NaN or +inf
+        atomicAdd(&hist[my_id], 1);
+      }
       if (s.renorm) my_w /= warp_sum(my_w);
       if (my_id < 0) my_w = 0.0f;
-      if (my_id >= 0) atomicAdd(&hist[my_id], 1);
     }
-    if (lane < s.k && in_buf(weights + t * s.k + lane, 4, weights, out_bytes, &g_route_status) &&
-        in_buf(ids + t * s.k + lane, 4, ids, out_bytes, &g_route_status)) {
-      weights[t * s.k + lane] = my_w;
-      ids[t * s.k + lane] = my_id;
+    // the chosen ones' lanes write their places, and as many others the places left
+    const uint32_t chosen = __ballot_sync(0xFFFFFFFFu, my_id >= 0);
+    if (my_id < 0) rank = __popc(chosen) + __popc(~chosen & ((1u << lane) - 1u));
+    if (rank < s.k && in_buf(weights + t * s.k + rank, 4, weights, out_bytes, &g_route_status) &&
+        in_buf(ids + t * s.k + rank, 4, ids, out_bytes, &g_route_status)) {
+      weights[t * s.k + rank] = my_w;
+      ids[t * s.k + rank] = my_id;
     }
   }
   if (lane == 0 && routed_here) atomicAdd(&routed_tokens, routed_here);
-  // the warps' sums, one warp after the other
-  for (int w = 0; w < kWarps; ++w) {
-    if (warp == w) {
+  // the warps' sums side by side, then added up in warp order
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int e = expert_of<kV>(i, lane);
-        if (e < s.E) sums[e] += acc[i];
-      }
-    }
-    __syncthreads();
+  for (int i = 0; i < kPer; ++i) by_warp[warp * (32 * kPer) + expert_of<kV>(i, lane)] = acc[i];
+  __syncthreads();
+  for (int e = tid; e < s.E; e += kThreads) {
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int w = 0; w < kWarps; ++w) sum += by_warp[w * (32 * kPer) + e];
+    sums[e] = sum;
   }
+  __syncthreads();
   if (gridDim.x == 1) {
     join_blocks(s, 1, sums, hist, &routed_tokens, counts, loss, n_out, red);
     return;
@@ -315,7 +345,8 @@ __global__ void __launch_bounds__(kThreads)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the chosen experts' part of a row, zero between rows
   constexpr int kRow = kPer * 32;
-  float* chosen = reinterpret_cast<float*>(smem) + warp * kRow;
+  float* chosen = reinterpret_cast<float*>(smem) + warp * 2 * kRow;
+  float* probs = chosen + kRow;
   for (int e = lane; e < kRow; e += 32) chosen[e] = 0.0f;
   __syncwarp();
   pdl_wait();
@@ -332,25 +363,26 @@ __global__ void __launch_bounds__(kThreads)
     }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  // the next token's logits, chosen experts and their gradients
   Row<T, kPer, kV> ahead;
+  int32_t e_ahead = -1;
+  float dw_ahead = 0.0f;
   const auto fetch = [&](int64_t t) {
-    if (t < s.tokens && in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status))
+    if (t >= s.tokens) return;
+    if (in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status))
       ahead.load(logits + t * s.ld, s.E, lane);
+    if (dweights != nullptr && lane < s.k) {
+      e_ahead = ids[t * s.k + lane];
+      dw_ahead = dweights[t * s.k + lane];
+    }
   };
   int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   fetch(t);
   for (; t < s.tokens; t += step) {
-    const T* row = logits + t * s.ld;
-    int e = -1;
-    float dw = 0.0f;
-    if (dweights != nullptr && lane < s.k) {
-      e = ids[t * s.k + lane];
-      dw = dweights[t * s.k + lane];
-      if (e < 0 || e >= s.E) e = -1;
-    }
-    const float chosen_logit = e >= 0 ? widen(row[e]) : 0.0f;
+    const int e = e_ahead >= 0 && e_ahead < s.E ? e_ahead : -1;
+    float dw = dw_ahead;
     float x[kPer];
-    ahead.values(s.E, lane, x);
+    ahead.values(x);
     fetch(t + step);
     float top = -CUDART_INF_F;
     bool nan = false;
@@ -370,17 +402,25 @@ __global__ void __launch_bounds__(kThreads)
         x[i] = exp2_ftz((x[i] - top) * kLog2E);  // 0 past E: those are -inf
         sum += x[i];
       }
-      const float inv = 1.0f / warp_sum(sum);
+      const float inv = reciprocal(warp_sum(sum));
       float pc = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         x[i] *= inv;
         pc = fmaf(x[i], c[i], pc);
       }
-      float w = e >= 0 ? exp2_ftz((chosen_logit - top) * kLog2E) : 0.0f;
+      // the probabilities of the chosen experts, from the lanes that hold them
+#pragma unroll
+      for (int q = 0; q < kPer / kV; ++q) {
+        Vec<float, kV> p;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) p.v[i] = x[q * kV + i];
+        *reinterpret_cast<Vec<float, kV>*>(probs + expert_of<kV>(q * kV, lane)) = p;
+      }
+      __syncwarp();
+      float w = e >= 0 ? probs[e] : 0.0f;
       if (e < 0) dw = 0.0f;
       float part = 0.0f;
-      w *= inv;
       if (s.renorm) {
         const float all = warp_sum(w);
         if (e >= 0) w /= all;
@@ -433,7 +473,11 @@ constexpr int route_threads() {
 int warps_for(int experts) {
   return (experts <= 256 ? route_threads<8>() : experts <= 512 ? route_threads<16>() : route_threads<32>()) / 32;
 }
-constexpr int kBackThreads = 256;
+// threads of a block of the backward pass: its shared rows stay within 32 KB
+template <int kPer>
+constexpr int back_threads() {
+  return kPer <= 16 ? 256 : 128;
+}
 
 struct RouteCall {
   const void* logits;
@@ -464,7 +508,7 @@ int launch_route(const RouteCall& a) {
   float* part_p = reinterpret_cast<float*>(a.workspace);
   int32_t* part_c = reinterpret_cast<int32_t*>(part_p + static_cast<int64_t>(blocks) * a.s.E);
   int32_t* part_n = part_c + static_cast<int64_t>(blocks) * a.s.E;
-  int rc = launch_pdl(route_kernel<T, kPer, kV, kThreads>, blocks, kThreads, a.s.E * 8 + kThreads * 8, a.stream,
+  int rc = launch_pdl(route_kernel<T, kPer, kV, kThreads>, blocks, kThreads, a.s.E * 8 + (kPer > 2 ? kPer : 2) * kThreads * 4, a.stream,
                       static_cast<const T*>(a.logits), a.s, a.mask, a.weights, a.ids, part_p, part_c, part_n,
                       a.counts, a.loss, a.n);
   if (rc != MXQ_OK || blocks == 1) return rc;
@@ -474,10 +518,11 @@ int launch_route(const RouteCall& a) {
 
 template <typename T, int kPer, int kV>
 int launch_route_backward(const RouteCall& a) {
+  constexpr int kBackThreads = back_threads<kPer>();
   const int64_t want = ceil_div(a.s.tokens, kBackThreads / 32);
   const int64_t cap = static_cast<int64_t>(a.sms) * (2048 / kBackThreads);
   return launch_pdl(route_backward_kernel<T, kPer, kV, kBackThreads>, static_cast<unsigned>(want < cap ? want : cap),
-                    kBackThreads, kPer * 32 * 4 * (kBackThreads / 32), a.stream, static_cast<const T*>(a.logits), a.s,
+                    kBackThreads, 2 * kPer * 32 * 4 * (kBackThreads / 32), a.stream, static_cast<const T*>(a.logits), a.s,
                     a.mask, a.ids, a.counts, a.n, a.dweights, a.dloss, static_cast<T*>(a.dlogits), a.ldd);
 }
 

@@ -175,8 +175,20 @@ struct Choices {
 // of 7168 bf16: 462 us).
 constexpr int kAtOnce = 8;
 
-template <typename T, int kV, int kJ>
-__global__ void __launch_bounds__(kThreads)
+//
+// Six blocks of 256 threads on a multiprocessor (40 registers) and 64 threads a
+// token read fastest: 155 us for 57344 rows of 7168 bf16 (6.0 TB/s), against 169
+// with 256 threads a token, 193 with three blocks of those, and 265 with a warp
+// a token and the next columns loaded ahead.
+// With fewer choices the columns at once take registers for their sums too.
+template <int kJ>
+__host__ __device__ constexpr int combine_blocks() {
+  return kJ == kAtOnce ? 6 : 4;
+}
+
+// kMore: there may be more than kJ choices.
+template <typename T, int kV, int kJ, bool kMore>
+__global__ void __launch_bounds__(kThreads, combine_blocks<kJ>())
     combine_kernel(const T* __restrict__ rows, const ExchangeShape s, const int32_t* __restrict__ slots,
                    const float* __restrict__ weights, T* __restrict__ y) {
   pdl_wait();
@@ -203,7 +215,7 @@ __global__ void __launch_bounds__(kThreads)
           const T* p = rows + from.row[j] + (c + u * s.tx) * kV;
           v[j][u] = Vec<T, kV>{};
           if (from.row[j] >= 0 && c + u * s.tx < nv && in_buf(p, sizeof v[j][u], rows, in_bytes, &g_exchange_status))
-            v[j][u] = load_once<T, kV>(p);
+            v[j][u] = *reinterpret_cast<const Vec<T, kV>*>(p);
         }
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
@@ -213,7 +225,7 @@ __global__ void __launch_bounds__(kThreads)
           for (int i = 0; i < kV; ++i) acc[u][i] = fmaf(from.w[j], widen(v[j][u].v[i]), acc[u][i]);
     };
     add(first);
-    if (kJ == kAtOnce)
+    if (kMore)
       for (int j0 = kJ; j0 < s.k; j0 += kJ) add(Choices<kJ>(slots, weights, s, t, j0, s.ldm));
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
@@ -226,9 +238,21 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// kWarps warps per token (1 or all of the block's).
+// Row pieces a thread of the gradient holds at once.  It also keeps the token's
+// own piece and writes as much as it reads, so with 16-byte pieces four are
+// faster than eight (64 groups, 57344 rows of 7168 bf16: 299 us against 437;
+// 32768 rows of 2048: 66 against 113); with 8-byte ones eight (30021 rows of
+// 2050 fp32: 119 against 134); with 2-byte ones four (36000 rows of 1001 bf16: 65
+// against 79).
+template <typename T, int kV>
+__host__ __device__ constexpr int back_at_once() {
+  return sizeof(T) * kV == 8 || sizeof(T) * kV == 4 ? 8 : 4;
+}
+constexpr int kBackBlocks = 4;
+
+// kWarps warps per token: 1, 2 or all of the block's.
 template <typename T, int kV, int kJ, int kWarps>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kBackBlocks)
     combine_backward_kernel(const T* __restrict__ dy, const T* __restrict__ rows, const ExchangeShape s, int64_t ldr,
                             const int32_t* __restrict__ slots, const int32_t* __restrict__ source,
                             const float* __restrict__ weights, T* __restrict__ drows, float* __restrict__ dweights,
@@ -239,24 +263,25 @@ __global__ void __launch_bounds__(kThreads)
     zero_unused<T, kV>(s, source, drows, blockIdx.x - token_blocks);
     return;
   }
-  constexpr int kU = kAtOnce / kJ;
+  constexpr int kU = back_at_once<T, kV>() / kJ;
   constexpr int kGroup = kWarps * 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / kGroup) + threadIdx.x / kGroup;
-  if (t >= s.tokens) return;  // a whole warp, and for kWarps > 1 a whole block
+  const bool live = t < s.tokens;
+  if (kWarps == 1 && !live) return;  // others stay for the block's barriers
   const int64_t nv = s.D / kV;
   const uint64_t in_bytes = (static_cast<uint64_t>(s.M - 1) * ldr + s.D) * sizeof(T);
   const uint64_t out_bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
   for (int j0 = 0; j0 < s.k; j0 += kJ) {
-    const Choices<kJ> from(slots, weights, s, t, j0, ldr);
+    const Choices<kJ> from(slots, weights, s, live ? t : 0, j0, ldr);
     int64_t to[kJ];
     float dot[kJ];
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
-      to[j] = from.row[j] >= 0 ? static_cast<int64_t>(slots[t * s.k + j0 + j]) * s.ldm : -1;
+      to[j] = from.row[j] >= 0 && live ? static_cast<int64_t>(slots[t * s.k + j0 + j]) * s.ldm : -1;
       dot[j] = 0.0f;
     }
-    for (int64_t c = threadIdx.x % kGroup; c < nv; c += kU * kGroup) {
+    for (int64_t c = threadIdx.x % kGroup; live && c < nv; c += kU * kGroup) {
       Vec<T, kV> g[kU], v[kJ][kU];
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -297,11 +322,11 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int j = 0; j < kJ; ++j) {
         dot[j] = 0.0f;
-        for (int q = 0; q < kWarps; ++q) dot[j] += red[q][j];
+        for (int q = 0; q < kWarps; ++q) dot[j] += red[warp / kWarps * kWarps + q][j];
       }
       __syncthreads();
     }
-    if (threadIdx.x % kGroup == 0)
+    if (live && threadIdx.x % kGroup == 0)
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
         if (j0 + j < s.k) dweights[t * s.k + j0 + j] = from.row[j] >= 0 ? dot[j] : 0.0f;
@@ -321,6 +346,7 @@ struct RowsCall {
   const float* weights;
   void* out;
   float* dweights;
+  int sms;
   cudaStream_t stream;
 };
 
@@ -332,27 +358,43 @@ int launch_dispatch(const RowsCall& a) {
                     static_cast<const T*>(a.in), a.s, a.slots, a.source, static_cast<T*>(a.out), token_blocks);
 }
 // Choices handled at once: 2, 4 or 8, the smallest that holds k.
+template <typename T, int kV, int kJ, bool kMore>
+int launch_combine(RowsCall a) {
+  // 64 threads a token, more where the tokens are too few to fill the GPU
+  const int64_t fill = static_cast<int64_t>(a.sms) * combine_blocks<kJ>() * kThreads;
+  int tx = 8;
+  while (tx < a.s.tx && (tx < 64 || tx * a.s.tokens < fill)) tx *= 2;
+  a.s.tx = tx;
+  return launch_pdl(combine_kernel<T, kV, kJ, kMore>, static_cast<unsigned>(ceil_div(a.s.tokens, kThreads / tx)), kThreads,
+                    0, a.stream, static_cast<const T*>(a.in), a.s, a.slots, a.weights, static_cast<T*>(a.out));
+}
 template <typename T, int kV>
 int launch_combine(const RowsCall& a) {
-  const auto kernel = a.s.k <= 2 ? combine_kernel<T, kV, 2> : a.s.k <= 4 ? combine_kernel<T, kV, 4> : combine_kernel<T, kV, 8>;
-  return launch_pdl(kernel, static_cast<unsigned>(ceil_div(a.s.tokens, kThreads / a.s.tx)), kThreads, 0, a.stream,
-                    static_cast<const T*>(a.in), a.s, a.slots, a.weights, static_cast<T*>(a.out));
+  return a.s.k <= 2   ? launch_combine<T, kV, 2, false>(a)
+         : a.s.k <= 4 ? launch_combine<T, kV, 4, false>(a)
+         : a.s.k <= 8 ? launch_combine<T, kV, 8, false>(a)
+                      : launch_combine<T, kV, 8, true>(a);
 }
+template <typename T, int kV, int kJ, int kWarps>
+int launch_combine_backward(const RowsCall& a) {
+  const int64_t token_blocks = ceil_div(a.s.tokens, kThreads / 32 / kWarps);
+  const int64_t blocks = token_blocks + ceil_div(a.s.M, kFillRows);
+  return launch_pdl(combine_backward_kernel<T, kV, kJ, kWarps>, static_cast<unsigned>(blocks), kThreads, 0, a.stream,
+                    static_cast<const T*>(a.in2), static_cast<const T*>(a.in), a.s, a.ldr, a.slots, a.source, a.weights,
+                    static_cast<T*>(a.out), a.dweights, token_blocks);
+}
+// A warp a token for narrow rows; for wide ones two, or all of a block's where
+// the tokens are too few to fill the GPU.
 template <typename T, int kV, int kJ>
 int launch_combine_backward(const RowsCall& a) {
-  const bool wide = a.s.D / kV >= kThreads;
-  const int64_t token_blocks = wide ? a.s.tokens : ceil_div(a.s.tokens, kThreads / 32);
-  const int64_t blocks = token_blocks + ceil_div(a.s.M, kFillRows);
-  return launch_pdl(wide ? combine_backward_kernel<T, kV, kJ, kThreads / 32> : combine_backward_kernel<T, kV, kJ, 1>,
-                    static_cast<unsigned>(blocks), kThreads, 0, a.stream, static_cast<const T*>(a.in2),
-                    static_cast<const T*>(a.in), a.s, a.ldr, a.slots, a.source, a.weights, static_cast<T*>(a.out),
-                    a.dweights, token_blocks);
+  const int64_t nv = a.s.D / kV, fill = static_cast<int64_t>(a.sms) * kBackBlocks * kThreads;
+  if (nv < 64) return launch_combine_backward<T, kV, kJ, 1>(a);
+  return nv >= kThreads && a.s.tokens * 64 < fill ? launch_combine_backward<T, kV, kJ, kThreads / 32>(a)
+                                                  : launch_combine_backward<T, kV, kJ, 2>(a);
 }
 template <typename T, int kV>
 int launch_combine_backward(const RowsCall& a) {
-  return a.s.k <= 2   ? launch_combine_backward<T, kV, 2>(a)
-         : a.s.k <= 4 ? launch_combine_backward<T, kV, 4>(a)
-                      : launch_combine_backward<T, kV, 8>(a);
+  return a.s.k <= 2 ? launch_combine_backward<T, kV, 2>(a) : launch_combine_backward<T, kV, 4>(a);
 }
 
 enum class Rows { kDispatch, kCombine, kCombineBackward };
@@ -484,6 +526,8 @@ extern "C" int mxq_moe_combine(const void* rows, int dtype, int64_t M, int64_t D
   a.slots = slots;
   a.weights = weights;
   a.out = y;
+  a.sms = sm_count_current_device(nullptr);
+  if (a.sms <= 0) return MXQ_ECUDA;
   a.stream = stream;
   return launch_by_alignment<Rows::kCombine>(a);
 }
@@ -519,6 +563,8 @@ extern "C" int mxq_moe_combine_backward(const void* dy, int dtype, int64_t token
   a.weights = weights;
   a.out = drows;
   a.dweights = dweights;
+  a.sms = sm_count_current_device(nullptr);
+  if (a.sms <= 0) return MXQ_ECUDA;
   a.stream = stream;
   return launch_by_alignment<Rows::kCombineBackward>(a);
 }

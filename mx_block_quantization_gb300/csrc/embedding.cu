@@ -3,13 +3,17 @@
 //   lookup     y[t] = scale * table[ids[t]]
 //   gradient   dtable[v] = scale * sum over the tokens t with ids[t] = v of dy[t]
 //
-// The gradient sorts the tokens by id (rank_tile.cuh: stable, one launch pair
-// per digit of at most 10 bits), so that the tokens of a row lie side by side,
-// and then writes every row of the table once: zero where no token has it, the
-// sum in token order otherwise.  A frequent id would keep one block busy for
-// long, so a run of more than kChunk tokens is first summed in pieces, one per
-// chunk of kChunk sorted places, by a launch of its own; the row then adds the
-// pieces in order.  Sums are in fp32 and their order depends on the ids alone.
+// The gradient sorts the tokens by id, stably, so that the tokens of a row lie side
+// by side.  Most of its time is writing the table, most rows of which no token has:
+// the launches of the sort, which keep few blocks busy, zero the whole table with
+// the others (6.2 TB/s), and the last launch writes the rows that have tokens,
+// found from the places where a run of equal ids begins.  (Writing every row once,
+// by its number, needs the runs before any of it and a search for each block of
+// rows: 259 us at 131072x4096 bf16 with 16384 tokens, now 213.)
+// A frequent id would keep one block busy for long, so a run of more than kChunk
+// tokens is first summed in pieces, one per chunk of kChunk sorted places, by a
+// launch of its own; the row then adds the pieces in order.  Sums are in fp32 and
+// their order depends on the ids alone.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -23,7 +27,7 @@ using namespace mxq;
 __device__ unsigned int g_embedding_status = 0;
 
 constexpr int kThreads = 256;
-constexpr int kRowsPerBlock = 16;  // table rows a block of the gradient writes
+constexpr int kStarts = 8;         // sorted places whose runs a block of the last launch writes
 constexpr int kChunk = 32;         // sorted places per piece of a long run
 constexpr int kDigitBits = 10;     // at most kRankMaxBins bins
 
@@ -62,6 +66,43 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ---------------------------------------------------------------------------
+// gradient: zeroing the table
+// ---------------------------------------------------------------------------
+// A launch's share of the table: `rows` rows of row_bytes, pitch bytes apart.
+struct Fill {
+  uint8_t* base;
+  int64_t rows, row_bytes, pitch;
+  const uint8_t* table;  // the whole table and its bytes, for the checked build
+  uint64_t table_bytes;
+};
+
+__device__ __forceinline__ void zero_bytes(uint8_t* p, int64_t n, int64_t first, int64_t step, const Fill& f) {
+  // 2-byte pieces up to the first 16-byte boundary and after the last one
+  int64_t head = static_cast<int64_t>(-reinterpret_cast<intptr_t>(p) & 15);
+  if (head > n) head = n;
+  const int64_t body = (n - head) / 16, tail = (n - head) % 16;
+  uint4* q = reinterpret_cast<uint4*>(p + head);
+  for (int64_t i = first; i < body; i += step)
+    if (in_buf(q + i, 16, f.table, f.table_bytes, &g_embedding_status)) q[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (first < head / 2) reinterpret_cast<uint16_t*>(p)[first] = 0;
+  if (first < tail / 2) reinterpret_cast<uint16_t*>(p + head + 16 * body)[first] = 0;
+}
+
+// Blocks past the launch's own zero the fill; true for those.
+template <int kBlockThreads>
+__device__ __forceinline__ bool fill_block(const Fill& f, int own_blocks) {
+  const int64_t block = static_cast<int64_t>(blockIdx.x) - own_blocks, blocks = gridDim.x - own_blocks;
+  if (block < 0) return false;
+  if (f.rows == 1) {
+    zero_bytes(f.base, f.row_bytes, block * kBlockThreads + threadIdx.x, blocks * kBlockThreads, f);
+  } else {
+    for (int64_t r = block; r < f.rows; r += blocks)
+      zero_bytes(f.base + r * f.pitch, f.row_bytes, threadIdx.x, kBlockThreads, f);
+  }
+  return true;
+}
+
+// ---------------------------------------------------------------------------
 // gradient: sort
 // ---------------------------------------------------------------------------
 // Ids as keys: an id out of range, or the padding id, takes the key `rows`,
@@ -88,10 +129,11 @@ struct SortedKey {
 
 template <typename Source>
 __global__ void __launch_bounds__(kRankThreads)
-    digit_count_kernel(const Source src, const RankSplit s, int shift, int bins, int32_t* chunk_counts) {
+    digit_count_kernel(const Source src, const RankSplit s, int shift, int bins, int32_t* chunk_counts, const Fill fill) {
   extern __shared__ int32_t counts[];
   pdl_wait();
-  pdl_launch_dependents();  // as few blocks follow
+  pdl_launch_dependents();  // the sort's blocks wait beside the zeroing ones
+  if (fill_block<kRankThreads>(fill, s.chunks)) return;
   rank_count(s, bins, [&](int64_t i) { return (src.full(i) >> shift) & (bins - 1); }, counts);
   for (int b = threadIdx.x; b < bins; b += kRankThreads)
     chunk_counts[static_cast<int64_t>(blockIdx.x) * bins + b] = counts[b];
@@ -101,12 +143,14 @@ template <typename Source>
 __global__ void __launch_bounds__(kRankThreads)
     digit_sort_kernel(const Source src, const RankSplit s, int shift, int bins,
                       const int32_t* __restrict__ chunk_counts, int32_t* __restrict__ keys,
-                      int32_t* __restrict__ tokens) {
+                      int32_t* __restrict__ tokens, const Fill fill) {
   extern __shared__ int32_t smem[];
   int32_t* next = smem;
   int32_t* counts = smem + bins;
   __shared__ int32_t total[kRankMaxBins], begin[kRankMaxBins], work[kRankWarps];
   pdl_wait();
+  pdl_launch_dependents();
+  if (fill_block<kRankThreads>(fill, s.chunks)) return;
   const auto key = [&](int64_t i) { return (src.full(i) >> shift) & (bins - 1); };
   if (s.chunks == 1) {
     rank_count(s, bins, key, total);
@@ -128,12 +172,115 @@ __global__ void __launch_bounds__(kRankThreads)
       next, counts);
 }
 
+// Up to kSmallTokens tokens: all digits in one launch by one block, the items in
+// its registers and, between the digits, in its shared memory.  A warp holds
+// 32 * rounds consecutive items, so the order stays that of the tokens.
+// Against the launches above: 16384 tokens 33 us, about as long, but 4096 13 us instead of 27.
+constexpr int kSmallThreads = 1024;
+constexpr int kSmallWarps = kSmallThreads / 32;
+constexpr int kSmallRounds = 16;
+constexpr int64_t kSmallTokens = kSmallThreads * kSmallRounds;
+
+inline size_t small_sort_smem(int64_t n, int bins) {
+  return static_cast<size_t>(n) * 8 + static_cast<size_t>(kSmallWarps) * bins * 2 + static_cast<size_t>(bins) * 4;
+}
+
+template <int kRounds, typename Source>
+__global__ void __launch_bounds__(kSmallThreads)
+    small_sort_kernel(const Source src, int n, int passes, int bits, int32_t* __restrict__ keys,
+                      int32_t* __restrict__ tokens, const Fill fill) {
+  extern __shared__ int32_t smem[];
+  __shared__ int32_t warp_sums[kSmallWarps];
+  const int holders = (n + 32 * kRounds - 1) / (32 * kRounds);  // warps with items
+  pdl_wait();
+  pdl_launch_dependents();
+  if (fill_block<kSmallThreads>(fill, 1)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bins = 1 << bits;
+  int32_t* sorted_keys = smem;                                      // [n]
+  int32_t* sorted_tokens = smem + n;                                // [n]
+  int32_t* begin = smem + 2 * n;                                    // [bins]
+  uint16_t* counts = reinterpret_cast<uint16_t*>(begin + bins);     // [warps, bins]
+  uint16_t* mine = counts + warp * bins;
+  const int first = warp * (32 * kRounds) + lane;
+  int32_t key[kRounds], token[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int i = first + 32 * r;
+    key[r] = i < n ? src.full(i) : -1;
+    token[r] = i;
+  }
+  for (int q = 0; q < passes; ++q) {
+    for (int i = tid; i < holders * bins / 2; i += kSmallThreads) reinterpret_cast<uint32_t*>(counts)[i] = 0u;
+    __syncthreads();
+    const int shift = q * bits;
+    uint16_t at[kRounds];
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const int d = key[r] >= 0 ? (key[r] >> shift) & (bins - 1) : -1;
+      const uint32_t same = same_key(d, bits);
+      const int before = d >= 0 ? mine[d] : 0;
+      at[r] = static_cast<uint16_t>(before + __popc(same & ((1u << lane) - 1u)));
+      __syncwarp();
+      if (d >= 0 && lane == 31 - __clz(same)) mine[d] = static_cast<uint16_t>(at[r] + 1);
+      __syncwarp();
+    }
+    __syncthreads();
+    // per digit: the items of the warps before, and of the digits before
+    int32_t total = 0;
+    if (tid < bins) {
+#pragma unroll 8
+      for (int w = 0; w < holders; ++w) {
+        const int c = counts[w * bins + tid];
+        counts[w * bins + tid] = static_cast<uint16_t>(total);
+        total += c;
+      }
+    }
+    int32_t sum = total;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t y = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += y;
+    }
+    if (lane == 31) warp_sums[warp] = sum;
+    __syncthreads();
+    int32_t before = lane < warp ? warp_sums[lane] : 0;
+    before = __reduce_add_sync(0xFFFFFFFFu, before);
+    if (tid < bins) begin[tid] = before + sum - total;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r)
+      if (key[r] >= 0) {
+        const int d = (key[r] >> shift) & (bins - 1);
+        const int place = begin[d] + mine[d] + at[r];
+        sorted_keys[place] = key[r];
+        sorted_tokens[place] = token[r];
+      }
+    __syncthreads();
+    if (q + 1 < passes) {
+#pragma unroll
+      for (int r = 0; r < kRounds; ++r) {
+        const int i = first + 32 * r;
+        if (i < n) {
+          key[r] = sorted_keys[i];
+          token[r] = sorted_tokens[i];
+        }
+      }
+      __syncthreads();
+    }
+  }
+  const uint64_t bytes = static_cast<uint64_t>(n) * 4;
+  for (int i = tid; i < n; i += kSmallThreads) {
+    if (!in_buf(keys + i, 4, keys, bytes, &g_embedding_status)) continue;
+    keys[i] = sorted_keys[i];
+    tokens[i] = sorted_tokens[i];
+  }
+}
+
 // ---------------------------------------------------------------------------
 // gradient: sums
 // ---------------------------------------------------------------------------
 struct GradShape {
   int64_t tokens, rows, D, ldd, ldw;
-  int tx;
 };
 
 // First place whose key is >= v, by a whole warp: each step splits the range in
@@ -154,14 +301,25 @@ __device__ __forceinline__ int64_t warp_lower_bound(const int32_t* __restrict__ 
   return lo;
 }
 
+// Column vectors and tokens that a thread holds at once: 64 bytes of wide pieces,
+// more of narrow ones.
+template <typename T, int kV>
+__host__ __device__ constexpr int columns_at_once() {
+  return sizeof(T) * kV >= 16 ? 1 : 4;
+}
+template <typename T, int kV>
+__host__ __device__ constexpr int tokens_at_once() {
+  return sizeof(T) * kV >= 16 ? 8 : sizeof(T) * kV >= 8 ? 2 : 4;
+}
+
 // acc[u] += dy[tokens[p]] over the places [lo, hi), in order, for the kU column
 // vectors c, c + tx, ...: kU * kAhead loads before the first is used.
 template <typename T, int kV, int kU>
 __device__ __forceinline__ void add_tokens(const T* __restrict__ dy, const GradShape& s,
-                                           const int32_t* __restrict__ tokens, int64_t lo, int64_t hi, int64_t c,
+                                           const int32_t* tokens, int64_t lo, int64_t hi, int64_t c,
                                            int tx, int64_t nv, float (&acc)[kU][kV]) {
   const uint64_t bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldd + s.D) * sizeof(T);
-  constexpr int kAhead = 8 / kU;
+  constexpr int kAhead = tokens_at_once<T, kV>();
   for (int64_t p = lo; p < hi; p += kAhead) {
     Vec<T, kV> v[kAhead][kU];
 #pragma unroll
@@ -169,10 +327,9 @@ __device__ __forceinline__ void add_tokens(const T* __restrict__ dy, const GradS
       const T* row = dy + (p + a < hi ? static_cast<int64_t>(tokens[p + a]) * s.ldd : 0);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        v[a][u] = Vec<T, kV>{};
         const T* src = row + (c + u * tx) * kV;
-        if (p + a < hi && c + u * tx < nv && in_buf(src, sizeof v[a][u], dy, bytes, &g_embedding_status))
-          v[a][u] = load_once<T, kV>(src);
+        const bool in = p + a < hi && c + u * tx < nv;
+        v[a][u] = load_if<T, kV>(src, in && in_buf(src, sizeof v[a][u], dy, bytes, &g_embedding_status));
       }
     }
 #pragma unroll
@@ -182,12 +339,6 @@ __device__ __forceinline__ void add_tokens(const T* __restrict__ dy, const GradS
 #pragma unroll
         for (int i = 0; i < kV; ++i) acc[u][i] += widen(v[a][u].v[i]);
   }
-}
-
-// Column vectors a thread holds at once: more of them where each is narrow.
-template <typename T, int kV>
-__host__ __device__ constexpr int columns_at_once() {
-  return sizeof(T) * kV >= 16 ? 2 : 4;
 }
 
 // Pieces of the runs longer than kChunk places: pieces[2c] is the part of the
@@ -241,58 +392,148 @@ __global__ void __launch_bounds__(kPieceThreads)
   }
 }
 
-template <typename T, typename U, int kV>
-__global__ void __launch_bounds__(kThreads)
-    table_kernel(const int32_t* __restrict__ keys, const int32_t* __restrict__ tokens, const T* __restrict__ dy,
-                 const GradShape s, const float* __restrict__ pieces, float scale, U* __restrict__ dtable) {
-  __shared__ int64_t range[2];
-  __shared__ int64_t run_lo[kRowsPerBlock], run_hi[kRowsPerBlock];
-  pdl_wait();
-  constexpr int kU = columns_at_once<T, kV>();
-  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock;
-  const int n = static_cast<int>(min(static_cast<int64_t>(kRowsPerBlock), s.rows - v0));
-  if (threadIdx.x < 64) {
-    const int64_t at = warp_lower_bound(keys, s.tokens, threadIdx.x < 32 ? v0 : v0 + n);
-    if ((threadIdx.x & 31) == 0) range[threadIdx.x >> 5] = at;
-  } else if (threadIdx.x - 64 < kRowsPerBlock) {
-    run_lo[threadIdx.x - 64] = run_hi[threadIdx.x - 64] = 0;
-  }
-  __syncthreads();
-  for (int64_t i = range[0] + threadIdx.x; i < range[1]; i += kThreads) {
-    const int32_t key = keys[i];
-    if (i == range[0] || keys[i - 1] != key) run_lo[key - v0] = i;
-    if (i == range[1] - 1 || keys[i + 1] != key) run_hi[key - v0] = i + 1;
-  }
-  __syncthreads();
-  const int ty = kThreads / s.tx;
-  const int64_t nv = s.D / kV;
-  const uint64_t out_bytes = (static_cast<uint64_t>(s.rows - 1) * s.ldw + s.D) * sizeof(U);
-  for (int r = threadIdx.x / s.tx; r < n; r += ty) {
-    const int64_t lo = run_lo[r], hi = run_hi[r];
-    U* row = dtable + (v0 + r) * s.ldw;
-    for (int64_t c = threadIdx.x % s.tx; c < nv; c += kU * s.tx) {
-      float acc[kU][kV] = {};
-      if (hi - lo > kChunk) {
-        for (int64_t q = lo / kChunk; q * kChunk < hi; ++q) {
-          const float* piece = pieces + (2 * q + (q * kChunk < lo ? 1 : 0)) * s.D;
+// acc[u] += the pieces of the run [lo, hi) in order, several loaded at once.
+template <int kV, int kU>
+__device__ __forceinline__ void add_pieces(const float* __restrict__ pieces, const GradShape& s, int64_t lo, int64_t hi,
+                                           int64_t c, int tx, int64_t nv, float (&acc)[kU][kV]) {
+  constexpr int kF = kV < 4 ? kV : 4, kAhead = kV * kU >= 16 ? 2 : 4;
+  const int64_t last = (hi - 1) / kChunk;
+  for (int64_t q = lo / kChunk; q <= last; q += kAhead) {
+    Vec<float, kF> v[kAhead][kU][kV / kF];
 #pragma unroll
-          for (int u = 0; u < kU; ++u)
-            if (c + u * s.tx < nv)
+    for (int a = 0; a < kAhead; ++a) {
+      const float* piece = pieces + (2 * (q + a) + ((q + a) * kChunk < lo ? 1 : 0)) * s.D;
 #pragma unroll
-              for (int i = 0; i < kV; ++i) acc[u][i] += piece[(c + u * s.tx) * kV + i];
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int f = 0; f < kV / kF; ++f) {
+          v[a][u][f] = Vec<float, kF>{};
+          if (q + a <= last && c + u * tx < nv)
+            v[a][u][f] = *reinterpret_cast<const Vec<float, kF>*>(piece + (c + u * tx) * kV + f * kF);
         }
-      } else if (hi > lo) {
-        add_tokens<T, kV, kU>(dy, s, tokens, lo, hi, c, s.tx, nv, acc);
-      }
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int k = 0; k < kV; ++k) acc[u][k] += v[a][u][k / kF].v[k % kF];
+  }
+}
+
+template <typename T, int kV>
+__host__ __device__ constexpr int row_columns() {
+  return sizeof(T) * kV >= 16 ? 1 : sizeof(T) * kV >= 8 ? 2 : 4;
+}
+
+// The rows of the runs that begin at one of the block's kStarts places.  A thread
+// loads its columns of all those places' tokens before it adds any up: which run
+// a place belongs to only decides where the sums are cut.  The last run is
+// followed past the block's places; the first places may belong to a run that
+// began before and are left out.
+template <typename T, typename U, int kV>
+__global__ void __launch_bounds__(kThreads, 4)
+    rows_kernel(const int32_t* __restrict__ keys, const int32_t* __restrict__ tokens, const T* __restrict__ dy,
+                const GradShape s, const float* __restrict__ pieces, float scale, U* __restrict__ dtable) {
+  __shared__ int32_t near_key[64], near_token[64];
+  __shared__ uint64_t starts_of;
+  pdl_wait();
+  static_assert(kStarts + kChunk < 64, "the ends of short runs lie within the places looked at");
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kStarts;
+  if (threadIdx.x < 64) {
+    const int64_t at = first + threadIdx.x;
+    near_key[threadIdx.x] = at < s.tokens ? keys[at] : -1;
+    near_token[threadIdx.x] = at < s.tokens ? tokens[at] : 0;
+  }
+  const int32_t before = first > 0 ? keys[first - 1] : -1;
+  __syncthreads();
+  if (threadIdx.x < 32) {  // a bit for each place where another id than before begins, or past the end
+    const int i = threadIdx.x;
+    const uint32_t lo = __ballot_sync(0xFFFFFFFFu, near_key[i] < 0 || near_key[i] != (i > 0 ? near_key[i - 1] : before));
+    const uint32_t hi = __ballot_sync(0xFFFFFFFFu, near_key[32 + i] < 0 || near_key[32 + i] != near_key[31 + i]);
+    if (i == 0) starts_of = static_cast<uint64_t>(hi) << 32 | lo;
+  }
+  __syncthreads();
+  const uint64_t starts = starts_of;
+  // places to add up, and those after which a row is written
+  uint32_t live = 0, ends = 0;
+  int last = -1, last_end = 0;  // a run that goes on past the block's places: its beginning and end
+  bool long_run = false;
+#pragma unroll
+  for (int p = 0; p < kStarts; ++p) {
+    if ((starts >> p & 1u) == 0u || near_key[p] < 0 || near_key[p] >= s.rows) continue;
+    const int length = __ffsll(static_cast<long long>(starts >> (p + 1)));  // 0: past the places looked at
+    if (length > 0 && p + length <= kStarts) {
+      live |= ((1u << length) - 1u) << p;
+      ends |= 1u << (p + length - 1);
+    } else {
+      last = p;
+      long_run = length == 0 || length > kChunk;
+      last_end = p + length;
+      if (!long_run) live |= ((1u << kStarts) - 1u) & ~((1u << p) - 1u);
+    }
+  }
+  if (live == 0u && last < 0) return;
+  int64_t long_end = 0;
+  if (long_run) long_end = warp_lower_bound(keys, s.tokens, static_cast<int64_t>(near_key[last]) + 1);
+  const int64_t nv = s.D / kV;
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldd + s.D) * sizeof(T);
+  const uint64_t out_bytes = (static_cast<uint64_t>(s.rows - 1) * s.ldw + s.D) * sizeof(U);
+  constexpr int kU = row_columns<T, kV>();
+  const int tx = blockDim.x;
+  for (int64_t c = threadIdx.x; c < nv; c += kU * tx) {
+    Vec<T, kV> v[kStarts][kU];
+    float acc[kU][kV] = {};
+    const auto load = [&](int place, bool wanted, Vec<T, kV> (&to)[kU]) {
+      const T* src = dy + static_cast<int64_t>(near_token[place]) * s.ldd + c * kV;
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        to[u] = load_if<T, kV>(src + u * tx * kV, wanted && c + u * tx < nv &&
+                                                      in_buf(src + u * tx * kV, sizeof to[u], dy, in_bytes, &g_embedding_status));
+    };
+    const auto add = [&](const Vec<T, kV> (&from)[kU]) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int k = 0; k < kV; ++k) acc[u][k] += widen(from[u].v[k]);
+    };
+    const auto write = [&](int32_t key) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         Vec<U, kV> out;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) out.v[i] = narrow<U>(scale * acc[u][i]);
-        U* to = row + (c + u * s.tx) * kV;
-        if (c + u * s.tx < nv && in_buf(to, sizeof out, dtable, out_bytes, &g_embedding_status))
+        for (int k = 0; k < kV; ++k) {
+          out.v[k] = narrow<U>(scale * acc[u][k]);
+          acc[u][k] = 0.0f;
+        }
+        U* to = dtable + key * s.ldw + (c + u * tx) * kV;
+        if (c + u * tx < nv && in_buf(to, sizeof out, dtable, out_bytes, &g_embedding_status))
           *reinterpret_cast<Vec<U, kV>*>(to) = out;
       }
+    };
+#pragma unroll
+    for (int p = 0; p < kStarts; ++p)
+      load(p, (live >> p & 1u) != 0u, v[p]);
+#pragma unroll
+    for (int p = 0; p < kStarts; ++p)
+      {
+        add(v[p]);  // zero where not wanted
+        if (ends >> p & 1u) write(near_key[p]);
+      }
+    if (last >= 0) {
+      if (long_run) {
+        add_pieces<kV, kU>(pieces, s, first + last, long_end, c, tx, nv, acc);
+      } else {
+        for (int p = kStarts; p < last_end; p += kStarts) {
+#pragma unroll
+          for (int q = 0; q < kStarts; ++q)
+            load(p + q < last_end ? p + q : 0, p + q < last_end, v[q]);
+#pragma unroll
+          for (int q = 0; q < kStarts; ++q)
+            add(v[q]);
+        }
+      }
+      write(near_key[last]);
     }
   }
 }
@@ -352,22 +593,46 @@ struct GradCall {
   void* dtable;
   cudaStream_t stream;
 };
+
+// The table in `parts` shares for zeroing; share q.  A table without gaps is one
+// row, cut at 16-byte pieces.
+Fill fill_share(void* dtable, const GradShape& s, int esize, int q, int parts) {
+  Fill f = {};
+  f.table = static_cast<const uint8_t*>(dtable);
+  f.table_bytes = pitched_bytes(s.rows, s.D, s.ldw, esize);
+  if (s.ldw == s.D) {
+    const int64_t bytes = s.rows * s.D * esize, share = ceil_div(ceil_div(bytes, parts), 16) * 16;
+    const int64_t lo = share * q < bytes ? share * q : bytes, hi = share * (q + 1) < bytes ? share * (q + 1) : bytes;
+    f.base = static_cast<uint8_t*>(dtable) + lo;
+    f.rows = 1;
+    f.row_bytes = hi - lo;
+  } else {
+    const int64_t lo = s.rows * q / parts, hi = s.rows * (q + 1) / parts;
+    f.base = static_cast<uint8_t*>(dtable) + lo * s.ldw * esize;
+    f.rows = hi - lo;
+    f.row_bytes = s.D * esize;
+  }
+  f.pitch = s.ldw * esize;
+  return f;
+}
+
 template <typename T, typename U, int kV>
 int launch_table(GradCall a) {
   const int64_t nv = a.s.D / kV;
   if (a.s.tokens > kChunk) {
     const int64_t blocks = ceil_div(nv, kPieceThreads * columns_at_once<T, kV>());
     const int column_blocks = static_cast<int>(blocks < 8 ? blocks : 8);
-    const int rc = launch_pdl(pieces_kernel<T, kV>, static_cast<unsigned>(ceil_div(a.s.tokens, kChunk) * column_blocks),
-                              kPieceThreads, 0, a.stream, a.keys, a.tokens, static_cast<const T*>(a.dy), a.s,
-                              column_blocks, a.pieces);
+    const int64_t own = ceil_div(a.s.tokens, kChunk) * column_blocks;
+    const int rc = launch_pdl(pieces_kernel<T, kV>, static_cast<unsigned>(own), kPieceThreads, 0, a.stream, a.keys,
+                              a.tokens, static_cast<const T*>(a.dy), a.s, column_blocks, a.pieces);
     if (rc != MXQ_OK) return rc;
   }
-  // a thread of a row holds several column vectors at once
-  a.s.tx = threads_per_row(ceil_div(nv, columns_at_once<T, kV>()));
-  return launch_pdl(table_kernel<T, U, kV>, static_cast<unsigned>(ceil_div(a.s.rows, kRowsPerBlock)), kThreads, 0,
-                    a.stream, a.keys, a.tokens, static_cast<const T*>(a.dy), a.s, a.pieces, a.scale,
-                    static_cast<U*>(a.dtable));
+  if (a.s.tokens == 0) return MXQ_OK;
+  // as many threads as a row has columns for them, 64 to 256
+  int threads = 64;
+  while (threads < kThreads && threads * row_columns<T, kV>() < nv) threads *= 2;
+  return launch_pdl(rows_kernel<T, U, kV>, static_cast<unsigned>(ceil_div(a.s.tokens, kStarts)), threads, 0, a.stream,
+                    a.keys, a.tokens, static_cast<const T*>(a.dy), a.s, a.pieces, a.scale, static_cast<U*>(a.dtable));
 }
 template <typename T, typename U>
 int table_vector(const GradCall& a) {
@@ -407,36 +672,76 @@ GradPlan grad_plan(int64_t tokens, int64_t rows, int64_t D) {
 
 template <typename Source>
 int launch_digit(const Source& src, const GradPlan& p, int shift, int32_t* counts, int32_t* keys, int32_t* tokens,
-                 cudaStream_t stream) {
+                 const Fill* fills, int fill_blocks, cudaStream_t stream) {
   const int bins = 1 << p.d.bits;
   if (p.s.chunks > 1) {
-    const int rc = launch_pdl(digit_count_kernel<Source>, p.s.chunks, kRankThreads, bins * 4, stream, src, p.s, shift,
-                              bins, counts);
+    const int rc = launch_pdl(digit_count_kernel<Source>, p.s.chunks + fill_blocks, kRankThreads, bins * 4, stream, src, p.s,
+                              shift, bins, counts, *fills++);
     if (rc != MXQ_OK) return rc;
   }
-  return launch_pdl(digit_sort_kernel<Source>, p.s.chunks, kRankThreads, rank_smem(bins), stream, src, p.s, shift, bins,
-                    counts, keys, tokens);
+  return launch_pdl(digit_sort_kernel<Source>, p.s.chunks + fill_blocks, kRankThreads, rank_smem(bins), stream, src, p.s,
+                    shift, bins, counts, keys, tokens, *fills);
 }
+
+template <int kRounds, typename Source>
+int launch_small_sort(const Source& src, const GradPlan& p, int32_t* keys, int32_t* tokens, const Fill& fill,
+                      int fill_blocks, cudaStream_t stream) {
+  const auto kernel = small_sort_kernel<kRounds, Source>;
+  const size_t most = small_sort_smem(static_cast<int64_t>(kRounds) * kSmallThreads, kRankMaxBins);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ECUDA;
+  static bool attr_done[64] = {};  // benign race: the same attribute set twice
+  if (!attr_done[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most)) != cudaSuccess)
+      return MXQ_ECUDA;
+    attr_done[dev] = true;
+  }
+  return launch_pdl(kernel, 1 + fill_blocks, kSmallThreads, small_sort_smem(p.s.n, 1 << p.d.bits), stream, src,
+                    static_cast<int>(p.s.n), p.d.passes, p.d.bits, keys, tokens, fill);
+}
+
+constexpr int kMaxLaunches = 2 * 4;  // four digits of 8 bits at most
 
 template <typename I>
 int launch_gradient(const void* ids, const GradPlan& p, int64_t padding, uint8_t* workspace, GradCall a, int dtype,
-                    int out_dtype) {
+                    int out_dtype, int sms) {
   int32_t* counts = reinterpret_cast<int32_t*>(workspace + p.counts);
   int32_t* buf = reinterpret_cast<int32_t*>(workspace + p.keys);
   const int64_t n = p.s.n;
   int32_t* keys[2] = {buf, buf + 2 * n};
   int32_t* tokens[2] = {buf + n, buf + 3 * n};
-  for (int q = 0; q < p.d.passes; ++q) {
-    const int shift = q * p.d.bits, to = q & 1;
-    const int rc = q == 0 ? launch_digit(IdKey<I>{static_cast<const I*>(ids), a.s.rows, padding}, p, shift, counts,
-                                         keys[to], tokens[to], a.stream)
-                          : launch_digit(SortedKey{keys[to ^ 1], tokens[to ^ 1]}, p, shift, counts, keys[to],
-                                         tokens[to], a.stream);
+  // every launch of the sort zeroes an equal share of the table
+  const bool small = n <= kSmallTokens;
+  const int per_digit = p.s.chunks > 1 ? 2 : 1;
+  const int launches = small ? 1 : p.d.passes * per_digit;
+  Fill fills[kMaxLaunches];
+  for (int q = 0; q < launches; ++q) fills[q] = fill_share(a.dtable, a.s, element_bytes(out_dtype), q, launches);
+  const int64_t want = ceil_div(fills[0].rows * fills[0].row_bytes, 16 * kThreads * 4);
+  const int fill_blocks = static_cast<int>(want < 8 * sms ? want : 8 * sms);
+  const IdKey<I> source{static_cast<const I*>(ids), a.s.rows, padding};
+  if (small) {
+    const int blocks = static_cast<int>(ceil_div(fill_blocks, kSmallThreads / kThreads));
+    const int rc = n <= kSmallThreads
+                       ? launch_small_sort<1>(source, p, keys[0], tokens[0], fills[0], blocks, a.stream)
+                   : n <= 4 * kSmallThreads
+                       ? launch_small_sort<4>(source, p, keys[0], tokens[0], fills[0], blocks, a.stream)
+                       : launch_small_sort<kSmallRounds>(source, p, keys[0], tokens[0], fills[0], blocks, a.stream);
     if (rc != MXQ_OK) return rc;
+    a.keys = keys[0];
+    a.tokens = tokens[0];
+  } else {
+    for (int q = 0; q < p.d.passes; ++q) {
+      const int shift = q * p.d.bits, to = q & 1;
+      const Fill* f = fills + q * per_digit;
+      const int rc = q == 0 ? launch_digit(source, p, shift, counts, keys[to], tokens[to], f, fill_blocks, a.stream)
+                            : launch_digit(SortedKey{keys[to ^ 1], tokens[to ^ 1]}, p, shift, counts, keys[to],
+                                           tokens[to], f, fill_blocks, a.stream);
+      if (rc != MXQ_OK) return rc;
+    }
+    const int last = (p.d.passes - 1) & 1;
+    a.keys = keys[last];
+    a.tokens = tokens[last];
   }
-  const int last = (p.d.passes - 1) & 1;
-  a.keys = keys[last];
-  a.tokens = tokens[last];
   a.pieces = reinterpret_cast<float*>(workspace + p.pieces);
   if (dtype == MXQ_F32) return out_dtype == MXQ_F32 ? table_vector<float, float>(a) : table_vector<float, bf16_t>(a);
   return out_dtype == MXQ_F32 ? table_vector<bf16_t, float>(a) : table_vector<bf16_t, bf16_t>(a);
@@ -501,10 +806,12 @@ extern "C" int mxq_embedding_backward(const void* ids, int ids_bytes, int64_t to
   if (outputs_overlap(out, 2, in, 2)) return MXQ_EOVERLAP;
   GradCall a = {};
   a.dy = dy;
-  a.s = {tokens, rows, D, ldd, ldw, 0};
+  a.s = {tokens, rows, D, ldd, ldw};
   a.scale = scale;
   a.dtable = dtable;
   a.stream = stream;
-  return ids_bytes == 4 ? launch_gradient<int32_t>(ids, p, padding, workspace, a, dtype, out_dtype)
-                        : launch_gradient<int64_t>(ids, p, padding, workspace, a, dtype, out_dtype);
+  const int sms = sm_count_current_device(nullptr);
+  if (sms <= 0) return MXQ_ECUDA;
+  return ids_bytes == 4 ? launch_gradient<int32_t>(ids, p, padding, workspace, a, dtype, out_dtype, sms)
+                        : launch_gradient<int64_t>(ids, p, padding, workspace, a, dtype, out_dtype, sms);
 }

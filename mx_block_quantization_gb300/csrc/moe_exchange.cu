@@ -170,25 +170,18 @@ struct Choices {
 };
 
 // kJ choices and kU columns (kJ * kU = kAtOnce row pieces) are loaded before the
-// first is used: enough in flight for HBM with few choices as with many.  With
-// the choices read inside the column loop the loads went one by one (57344 rows
-// of 7168 bf16: 462 us).
+// first is used: enough in flight for HBM with few choices as with many.  Four
+// blocks of 256 threads on a multiprocessor (64 registers) and 64 threads a token
+// read fastest: 57344 rows of 7168 bf16 in 140 us (6.6 TB/s); 157 with six blocks,
+// 234 with 32 threads a token, and 52 us against 28 with 256 threads a token at
+// 32768 rows of 2048.  With the choices read inside the column loop the loads
+// went one by one (462 us).
 constexpr int kAtOnce = 8;
-
-//
-// Six blocks of 256 threads on a multiprocessor (40 registers) and 64 threads a
-// token read fastest: 155 us for 57344 rows of 7168 bf16 (6.0 TB/s), against 169
-// with 256 threads a token, 193 with three blocks of those, and 265 with a warp
-// a token and the next columns loaded ahead.
-// With fewer choices the columns at once take registers for their sums too.
-template <int kJ>
-__host__ __device__ constexpr int combine_blocks() {
-  return kJ == kAtOnce ? 6 : 4;
-}
+constexpr int kCombineBlocks = 4;
 
 // kMore: there may be more than kJ choices.
 template <typename T, int kV, int kJ, bool kMore>
-__global__ void __launch_bounds__(kThreads, combine_blocks<kJ>())
+__global__ void __launch_bounds__(kThreads, kCombineBlocks)
     combine_kernel(const T* __restrict__ rows, const ExchangeShape s, const int32_t* __restrict__ slots,
                    const float* __restrict__ weights, T* __restrict__ y) {
   pdl_wait();
@@ -213,9 +206,8 @@ __global__ void __launch_bounds__(kThreads, combine_blocks<kJ>())
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const T* p = rows + from.row[j] + (c + u * s.tx) * kV;
-          v[j][u] = Vec<T, kV>{};
-          if (from.row[j] >= 0 && c + u * s.tx < nv && in_buf(p, sizeof v[j][u], rows, in_bytes, &g_exchange_status))
-            v[j][u] = *reinterpret_cast<const Vec<T, kV>*>(p);
+          v[j][u] = load_if<T, kV>(p, from.row[j] >= 0 && c + u * s.tx < nv &&
+                                          in_buf(p, sizeof v[j][u], rows, in_bytes, &g_exchange_status));
         }
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
@@ -240,13 +232,12 @@ __global__ void __launch_bounds__(kThreads, combine_blocks<kJ>())
 
 // Row pieces a thread of the gradient holds at once.  It also keeps the token's
 // own piece and writes as much as it reads, so with 16-byte pieces four are
-// faster than eight (64 groups, 57344 rows of 7168 bf16: 299 us against 437;
-// 32768 rows of 2048: 66 against 113); with 8-byte ones eight (30021 rows of
-// 2050 fp32: 119 against 134); with 2-byte ones four (36000 rows of 1001 bf16: 65
-// against 79).
+// faster than eight (64 groups, 57344 rows of 7168 bf16: 299 us against 322;
+// 32768 rows of 2048: 62 against 72); with narrower ones eight (30021 rows of 2050
+// fp32: 121 against 134; 36000 rows of 1001 bf16: 55 against 65).
 template <typename T, int kV>
 __host__ __device__ constexpr int back_at_once() {
-  return sizeof(T) * kV == 8 || sizeof(T) * kV == 4 ? 8 : 4;
+  return sizeof(T) * kV == 16 ? 4 : 8;
 }
 constexpr int kBackBlocks = 4;
 
@@ -286,14 +277,12 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks)
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int64_t col = (c + u * kGroup) * kV;
-        g[u] = Vec<T, kV>{};
-        if (c + u * kGroup < nv) g[u] = *reinterpret_cast<const Vec<T, kV>*>(dy + t * s.ldt + col);
+        g[u] = load_if<T, kV>(dy + t * s.ldt + col, c + u * kGroup < nv);
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
-          v[j][u] = Vec<T, kV>{};
-          if (from.row[j] >= 0 && c + u * kGroup < nv &&
-              in_buf(rows + from.row[j] + col, sizeof v[j][u], rows, in_bytes, &g_exchange_status))
-            v[j][u] = load_once<T, kV>(rows + from.row[j] + col);
+          const T* p = rows + from.row[j] + col;
+          v[j][u] = load_if<T, kV>(p, from.row[j] >= 0 && c + u * kGroup < nv &&
+                                          in_buf(p, sizeof v[j][u], rows, in_bytes, &g_exchange_status));
         }
       }
 #pragma unroll
@@ -361,7 +350,7 @@ int launch_dispatch(const RowsCall& a) {
 template <typename T, int kV, int kJ, bool kMore>
 int launch_combine(RowsCall a) {
   // 64 threads a token, more where the tokens are too few to fill the GPU
-  const int64_t fill = static_cast<int64_t>(a.sms) * combine_blocks<kJ>() * kThreads;
+  const int64_t fill = static_cast<int64_t>(a.sms) * kCombineBlocks * kThreads;
   int tx = 8;
   while (tx < a.s.tx && (tx < 64 || tx * a.s.tokens < fill)) tx *= 2;
   a.s.tx = tx;

@@ -39,19 +39,52 @@ struct alignas(sizeof(T) * kN) Vec {
   T v[kN];
 };
 
-// Load of data that is read once: not kept in L1, first to leave L2.
+// Load of data that this launch does not write, not kept in L1; zero where `wanted`
+// is false.  The condition is the load's own predicate: as a branch around each
+// load it makes the loads wait for one another.
+template <typename T, int kN>
+__device__ __forceinline__ Vec<T, kN> load_if(const T* p, bool wanted) {
+  Vec<T, kN> v;
+  const uint32_t w = wanted ? 1u : 0u;
+  if constexpr (sizeof v == 16) {
+    uint4 q;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)
+        : "l"(p), "r"(w));
+    *reinterpret_cast<uint4*>(&v) = q;
+  } else if constexpr (sizeof v == 8) {
+    uint2 q;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];\n\t}"
+        : "=&r"(q.x), "=&r"(q.y)
+        : "l"(p), "r"(w));
+    *reinterpret_cast<uint2*>(&v) = q;
+  } else if constexpr (sizeof v == 4) {
+    uint32_t q;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.b32 %0, [%1];\n\t}"
+        : "=&r"(q)
+        : "l"(p), "r"(w));
+    *reinterpret_cast<uint32_t*>(&v) = q;
+  } else {
+    uint16_t q;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t"
+        "@p ld.global.nc.L1::no_allocate.b16 %0, [%1];\n\t}"
+        : "=&h"(q)
+        : "l"(p), "r"(w));
+    *reinterpret_cast<uint16_t*>(&v) = q;
+  }
+  return v;
+}
 template <typename T, int kN>
 __device__ __forceinline__ Vec<T, kN> load_once(const T* p) {
-  Vec<T, kN> v;
-  if constexpr (sizeof v == 16)
-    *reinterpret_cast<uint4*>(&v) = __ldcs(reinterpret_cast<const uint4*>(p));
-  else if constexpr (sizeof v == 8)
-    *reinterpret_cast<uint2*>(&v) = __ldcs(reinterpret_cast<const uint2*>(p));
-  else if constexpr (sizeof v == 4)
-    *reinterpret_cast<uint32_t*>(&v) = __ldcs(reinterpret_cast<const uint32_t*>(p));
-  else
-    *reinterpret_cast<uint16_t*>(&v) = __ldcs(reinterpret_cast<const uint16_t*>(p));
-  return v;
+  return load_if<T, kN>(p, true);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {

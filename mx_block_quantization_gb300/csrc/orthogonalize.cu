@@ -165,7 +165,10 @@ struct Maps {
 struct Product {
   int64_t rows, cols;      // of the output
   int32_t ksteps;          // stages along K of one product
-  int32_t tiles_m, tiles_n, tiles;  // tiles: all of the batch
+  int32_t tiles_m, tiles_n, tiles;  // tiles: all of the batch and of the slices
+  int32_t slices, per_slice;        // K in slices of that many stages, each summed by itself
+  float* partial;                   // [slices, batch, rows, d_ld] sums of the slices, or NULL
+  int64_t partial_stride;           // elements between the slices
   int32_t a_mn, b_mn;      // operand lies with K along its rows
   // output = scale * acc + (add_scale + scale * (d[row] + d[column])) * addend
   //          and where row == column, + diagonal + add_scale * d + scale * d * d
@@ -259,27 +262,36 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
          (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: fp32 accumulator, fp16 operands, 256 x 256.
-__device__ __forceinline__ uint32_t instruction_desc(bool a_mn, bool b_mn) {
-  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((kTile / 8u) << 17) | ((kTile / 16u) << 24);
+// Instruction descriptor: fp32 accumulator, fp16 operands, 256 rows, n columns.
+__device__ __forceinline__ uint32_t instruction_desc(bool a_mn, bool b_mn, uint32_t n) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | ((n / 8u) << 17) | ((kTile / 16u) << 24);
+}
+// Columns that a tile's MMAs compute, half of them from each CTA's B: a multiple of
+// 128 (64 a CTA, the width of an MN-major box), as few as the matrix has left.
+__device__ __forceinline__ int32_t tile_width(const Product& p, int32_t j) {
+  const int64_t left = p.cols - static_cast<int64_t>(j) * kTile;
+  return left > kTile / 2 ? kTile : kTile / 2;
 }
 
 struct TileAt {
   int32_t batch, i, j;  // matrix, tile row, tile column
+  int32_t slice;
 };
 template <bool kSymmetric>
 __device__ __forceinline__ TileAt tile_at(const Product& p, int t) {
+  const int all = p.tiles / p.slices, slice = t / all;
+  t -= slice * all;
   if (!kSymmetric) {
     const int per = p.tiles_m * p.tiles_n;
     const int r = t % per;
-    return {t / per, r % p.tiles_m, r / p.tiles_m};
+    return {t / per, r % p.tiles_m, r / p.tiles_m, slice};
   }
   const int per = p.tiles_m * (p.tiles_m + 1) / 2;
   const int r = t % per;
   int i = static_cast<int>((sqrtf(8.0f * r + 1.0f) - 1.0f) * 0.5f);
   while (i * (i + 1) / 2 > r) --i;
   while ((i + 1) * (i + 2) / 2 <= r) ++i;
-  return {t / per, i, r - i * (i + 1) / 2};
+  return {t / per, i, r - i * (i + 1) / 2, slice};
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -310,8 +322,8 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&v)[8]) {
 // kSymmetric: one triangle of tiles, stored twice.  kAddends: parts of the
 // addend.  kColumns: the columns' d_col multiplies it (d_row, where given, always
 // does).  kBf16: the last update, to the caller's matrix.  kSplit: operands and
-// results are pairs, three products.
-template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit>
+// results are pairs, three products.  kPartial: the sums of a slice of K, in fp32.
+template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit, bool kPartial>
 __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p) {
   extern __shared__ uint8_t raw[];
@@ -360,8 +372,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     for (int t = first; ok && t < p.tiles; t += step) {
       const TileAt at = tile_at<kSymmetric>(p, t);
       const int32_t ra = at.i * kTile + static_cast<int32_t>(rank) * kHalf;
-      const int32_t rb = at.j * kTile + static_cast<int32_t>(rank) * kHalf;
-      for (int kk = 0; kk < ksteps; ++kk, ++issued) {
+      const int32_t rb = at.j * kTile + static_cast<int32_t>(rank) * (tile_width(p, at.j) / 2);
+      const int k_end = min(ksteps, (at.slice + 1) * p.per_slice);
+      for (int kk = at.slice * p.per_slice; kk < k_end; ++kk, ++issued) {
         const int part = kk / p.ksteps, k = (kk - part * p.ksteps) * kStepK;  // high*high, high*low, low*high
         const CUtensorMap* map_a = &maps.a[part == 2];
         const CUtensorMap* map_b = &maps.b[part == 1];
@@ -390,15 +403,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     }
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- MMA issue for the pair -------------------------------------------
-    const uint32_t idesc = instruction_desc(p.a_mn, p.b_mn);
     const uint64_t step_a = (p.a_mn ? 16 * 128 : 32) >> 4, step_b = (p.b_mn ? 16 * 128 : 32) >> 4;  // 16 of K
     int n = 0, done = 0;
     bool ok = true;
     for (int t = first; ok && t < p.tiles; t += step, ++done) {
       const int acc = done & 1;
+      const TileAt at = tile_at<kSymmetric>(p, t);
+      const uint32_t idesc = instruction_desc(p.a_mn, p.b_mn, static_cast<uint32_t>(tile_width(p, at.j)));
+      const int count = min(ksteps, (at.slice + 1) * p.per_slice) - at.slice * p.per_slice;
       ok = mbar_wait_bounded(smem_u32(&bars.acc_empty[acc]), ((done >> 1) & 1) ^ 1, abort_flag, &g_ortho_status, MXQ_DEV_TIMEOUT);
       fence_after();
-      for (int k = 0; ok && k < ksteps; ++k, ++n) {
+      for (int k = 0; ok && k < count; ++k, ++n) {
         const int s = n % kStages;
         ok = mbar_wait_bounded(smem_u32(&bars.full[s]), (n / kStages) & 1, abort_flag, &g_ortho_status, MXQ_DEV_TIMEOUT);
         if (!ok) break;
@@ -415,16 +430,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
   } else if (warp >= 4) {
     // ---- epilogue: 32 of this CTA's 128 rows and half of the columns per warp --
     // The addend is loaded into the buffers that the results are staged in and
-    // replaced piece by piece.  Without a second result the two chunks of a warp
-    // have a buffer each, and the next tile's addend is loaded while this one's
-    // results leave; with one (the transposed block or the low parts) a chunk
-    // takes both.
+    // replaced piece by piece; the next tile's is loaded while this one's results
+    // leave.  Without a second result the two chunks of a warp have a buffer each;
+    // with one (the transposed block or the low parts) a chunk takes both.
     const int e = warp - 4, quarter = e & 3;
     const uint32_t buf0 = staging + (2 * e) * kStagingBytes, buf1 = buf0 + kStagingBytes;
     const uint32_t bar0 = smem_u32(&bars.addend[e][0]);
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    constexpr bool low = kSplit && !kBf16;  // a split side has one tile: never mirrored
-    constexpr bool both = kSymmetric || low;
+    constexpr bool low = kSplit && !kBf16 && !kPartial;  // a split side has one tile: never mirrored
+    // a tile of the diagonal has no transposed block to store, and uses both
+    // buffers like one of an ordinary product
+    const auto needs_both = [&](const TileAt& at) { return low || (kSymmetric && at.i != at.j); };
     uint32_t phases = 0u, flying = 0u;             // a bit per buffer: parity to wait for, addend in flight
     const auto load_addend = [&](int b, int part, const TileAt& at, int c) {  // lane 0 issues; all lanes keep count
       const int32_t row0 = at.i * kTile + static_cast<int32_t>(rank) * kHalf + quarter * 32;
@@ -445,26 +461,28 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     };
     int done = 0;
     bool ok = true;
-    if (kAddends == 1 && !both && first < p.tiles) {
-      const TileAt at = tile_at<kSymmetric>(p, first);
-      load_addend(0, 0, at, 0);
-      load_addend(1, 0, at, 1);
-    }
+    // a tile's addend, as far as there are buffers for it
+    const auto load_addends = [&](const TileAt& at) {
+      if (kAddends == 1) {
+        load_addend(0, 0, at, 0);
+        if (!needs_both(at)) load_addend(1, 0, at, 1);
+      }
+      if (kAddends == 2) {
+        load_addend(0, 0, at, 0);
+        load_addend(1, 1, at, 0);
+      }
+    };
+    if (first < p.tiles) load_addends(tile_at<kSymmetric>(p, first));
     for (int t = first; ok && t < p.tiles; t += step, ++done) {
       const TileAt at = tile_at<kSymmetric>(p, t);
       const int acc = done & 1;
       const int64_t row0 = static_cast<int64_t>(at.i) * kTile + rank * kHalf + quarter * 32;
       const int64_t row = row0 + lane;
-      const bool mirror = kSymmetric && at.i != at.j;
+      const bool mirror = kSymmetric && at.i != at.j, both = needs_both(at) || kAddends == 2;
       const float dr = p.d_row != nullptr && row < p.rows ? p.d_row[at.batch * p.d_ld + row] : 0.0f;
       if (kColumns && lane < 4) {  // this warp's 128 columns, four lines
         const int64_t col = static_cast<int64_t>(at.j) * kTile + 2 * (e >> 2) * kChunkCols + 32 * lane;
         if (col < p.cols) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.d_col + at.batch * p.d_ld + col));
-      }
-      if (both && kAddends) {
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-        for (int q = 0; q < kAddends; ++q) load_addend(q, q, at, 0);
       }
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(&bars.acc_full[acc]), (done >> 1) & 1, abort_flag,
                                                      &g_ortho_status, MXQ_DEV_TIMEOUT));
@@ -483,13 +501,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
               __syncwarp();
               for (int q = 0; q < kAddends; ++q) load_addend(q, q, at, c);
             }
-          } else if (kAddends == 0) {
-            if (lane == 0) bulk_wait_read<0>();
+          } else if (kAddends == 0 && !kPartial) {
+            if (lane == 0) {
+              if (both || c == 0)
+                bulk_wait_read<0>();
+              else
+                bulk_wait_read<1>();  // the first chunk's store may still read the other buffer
+            }
             __syncwarp();
           }
-          for (int q = 0; ok && q < kAddends; ++q) ok = wait_addend(both ? q : c);
+          for (int q = 0; ok && q < kAddends; ++q) ok = wait_addend(kAddends == 2 ? q : both ? 0 : c);
           if (!ok) break;
         }
+        if (!inside && c < kWarpChunks - 1) continue;
         // everything of the chunk is read before anything is written: the
         // accesses are volatile and keep their order
         uint32_t raw[2][32];
@@ -509,6 +533,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           if (lane == 0) arrive_cluster(at_leader(smem_u32(&bars.acc_empty[acc])));
         }
         if (!inside) continue;
+        if (kPartial) {
+          float* to = p.partial + at.slice * p.partial_stride + (static_cast<int64_t>(at.batch) * p.rows + row) * p.d_ld + col0;
+          if (row < p.rows)
+#pragma unroll
+            for (int i = 0; i < 64; i += 4)
+              if (col0 + i < p.d_ld)  // a multiple of 8
+                *reinterpret_cast<uint4*>(to + i) =
+                    make_uint4(raw[i / 32][i % 32], raw[i / 32][i % 32 + 1], raw[i / 32][i % 32 + 2], raw[i / 32][i % 32 + 3]);
+          continue;
+        }
         const float k0 = fmaf(p.scale, dr, p.add_scale);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // 32 columns at a time
@@ -542,14 +576,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
               }
             }
           }
-          if (kSymmetric && row >= col && row < col + 32 && row < p.rows) {
+          if (kSymmetric && row0 < col + 32 && col < row0 + 32) {  // the warp's rows meet these columns
+            const int own_column = static_cast<int>(row - col);
             const float on = p.diagonal + p.add_scale * dr + p.scale * dr * dr;
+            float own = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (col + i == row) {
-                v[i] += on;
-                if (!kSplit) p.d_out[at.batch * p.d_ld + row] = v[i] - half_rounded(v[i]);
-              }
+            for (int i = 0; i < 32; ++i) {
+              v[i] += i == own_column ? on : 0.0f;
+              own = i == own_column ? v[i] : own;
+            }
+            if (!kSplit && own_column >= 0 && own_column < 32 && row < p.rows)
+              p.d_out[at.batch * p.d_ld + row] = own - half_rounded(own);
           }
           uint32_t w[16];
 #pragma unroll
@@ -598,20 +635,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           bulk_commit();
         }
       }
-      if (ok && kAddends == 1 && !both && t + step < p.tiles) {
+      if (ok && kAddends > 0 && t + step < p.tiles) {
         const TileAt next = tile_at<kSymmetric>(p, t + step);
-#pragma unroll
-        for (int c = 0; c < kWarpChunks; ++c) {
-          // the first chunk's store has been read once at most the second's is left
-          const bool second = (static_cast<int64_t>(at.j) * kTile + (2 * (e >> 2) + 1) * kChunkCols) < p.cols;
-          if (lane == 0) {
-            if (c == 0 && second)
-              bulk_wait_read<1>();
-            else
-              bulk_wait_read<0>();
-          }
+        // the first chunk's store has been read once at most the second's is left
+        const bool second = (static_cast<int64_t>(at.j) * kTile + (2 * (e >> 2) + 1) * kChunkCols) < p.cols;
+        if (kSymmetric || kAddends == 2 || !second) {
+          if (lane == 0) bulk_wait_read<0>();
           __syncwarp();
-          load_addend(c, 0, next, c);
+          load_addends(next);
+        } else {
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+          load_addend(0, 0, next, 0);
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          load_addend(1, 0, next, 1);
         }
       }
     }
@@ -632,7 +670,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
   __syncthreads();
   fence_after();
   if (warp == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
-  cluster_sync_all();
+}
+
+// The slices' sums added up in order: A (fp16, its low part or its diagonal's
+// remainder) from the lower triangle of tiles.
+struct Join {
+  const float* partial;
+  int64_t batch, side, ld, stride;
+  int slices;
+  float scale;
+  __half *high, *low;
+  float* d_out;
+};
+__global__ void __launch_bounds__(kThreads) join_kernel(const Join a) {
+  pdl_wait();
+  const int64_t n = a.batch * a.side * a.ld;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (at >= n) return;
+  const int64_t j = at % a.ld, row = at / a.ld, i = row % a.side;
+  if (j >= a.side) return;
+  const float* p = a.partial + (i / kTile >= j / kTile ? at : (row - i + j) * a.ld + i);
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int s = 0; s < a.slices; ++s) sum += p[s * a.stride];
+  const float v = sum * a.scale, h = half_rounded(v);
+  const uint64_t bytes = static_cast<uint64_t>(n) * 2;
+  if (!in_buf(a.high + at, 2, a.high, bytes, &g_ortho_status)) return;
+  a.high[at] = __float2half_rn(v);
+  if (a.low != nullptr)
+    a.low[at] = __float2half_rn(v - h);
+  else if (i == j)
+    a.d_out[row / a.side * a.ld + i] = v - h;
 }
 
 // ---------------------------------------------------------------------------
@@ -641,12 +709,36 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
 // Sides up to this carry pairs of fp16 (see the head of the file).
 constexpr int64_t kSplitSide = 64;
 
+// Slices of K for the gram matrix: where its tiles are few and K is long, the CTA
+// pairs left over take slices of K, and a further launch adds the slices up.
+// A stage takes a pair 0.3 us, a slice's sums pass through L2 twice at 4 TB/s, and
+// the further launch costs 5 us (64x8192: 671 us with one slice, 140 with 64;
+// 512x8192: a few slices; 1000x2000: 224 us with one, 282 with five).  Returns 0
+// for one slice.  Sized for the pairs of the whole GPU, whatever it has.
+constexpr int64_t kPairs = 76, kSliceStages = 6;
+int64_t gram_slices(int64_t batch, int64_t side, int64_t length) {
+  const int64_t tiles_m = ceil_div(side, kTile), tiles = batch * tiles_m * (tiles_m + 1) / 2;
+  if (tiles == 0) return 0;
+  const int64_t stages = ceil_div(length, kStepK) * (side <= kSplitSide ? 3 : 1);
+  const double product_us = 0.3 * static_cast<double>(stages);
+  const double slice_us = 8.0 * static_cast<double>(batch * side * side) / 4.0e6;
+  int64_t most = kPairs / tiles;
+  if (most > stages / kSliceStages) most = stages / kSliceStages;
+  int64_t best = 0;
+  double best_us = product_us;
+  for (int64_t n = 2; n <= most; ++n) {
+    const double us = product_us / static_cast<double>(n) + slice_us * static_cast<double>(n) + 5.0;
+    if (us < best_us) best = n, best_us = us;
+  }
+  return best;
+}
+
 struct Layout {
   int64_t side, ldx, lds;            // pitches of X and of the square matrices
   int parts;                         // 2 with low parts
   int64_t x[2][2];                   // X of the even and of the odd steps: high, low
   int64_t gram[2], poly[2];
-  int64_t d_gram, d_poly, sums, bytes;
+  int64_t d_gram, d_poly, sums, partial, bytes;
 };
 Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   Layout l;
@@ -668,6 +760,7 @@ Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   l.d_gram = take(up(batch * l.lds * 4, 256));
   l.d_poly = take(up(batch * l.lds * 4, 256));
   l.sums = take(up(batch * kMaxParts * 4, 256));
+  l.partial = take(up(gram_slices(batch, l.side, l.side == m ? n : m) * batch * l.side * l.lds * 4, 256));
   l.bytes = at;
   return l;
 }
@@ -691,14 +784,18 @@ bool encode_half(CUtensorMap* map, const Stack& t, uint32_t box_cols, uint32_t b
   return encode(map, t, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, box_cols, box_rows, swizzle);
 }
 
-template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit>
+template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit, bool kPartial>
 int launch_product(const Maps& maps, Product p, int64_t batch, int sms, cudaStream_t stream) {
   p.tiles_m = static_cast<int32_t>(ceil_div(p.rows, kTile));
   p.tiles_n = static_cast<int32_t>(ceil_div(p.cols, kTile));
   const int64_t per = kSymmetric ? static_cast<int64_t>(p.tiles_m) * (p.tiles_m + 1) / 2
                                  : static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-  p.tiles = static_cast<int32_t>(per * batch);
-  const auto kernel = product_kernel<kSymmetric, kAddends, kColumns, kBf16, kSplit>;
+  if (p.slices == 0) {
+    p.slices = 1;
+    p.per_slice = INT32_MAX / 2;
+  }
+  p.tiles = static_cast<int32_t>(per * batch * p.slices);
+  const auto kernel = product_kernel<kSymmetric, kAddends, kColumns, kBf16, kSplit, kPartial>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ECUDA;
   static bool attr_done[64] = {};  // benign race: the same attribute set twice
@@ -847,8 +944,23 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.scale = sa / (kXScale * kXScale);
     p.d_ld = l.lds;
     p.d_out = d_gram;
-    rc = split ? launch_product<true, 0, false, false, true>(maps, p, batch, sms, stream)
-               : launch_product<true, 0, false, false, false>(maps, p, batch, sms, stream);
+    if (const int64_t slices = gram_slices(batch, side, length); slices > 0) {
+      p.partial = reinterpret_cast<float*>(workspace + l.partial);
+      p.partial_stride = batch * side * l.lds;
+      const int64_t stages = p.ksteps * (split ? 3 : 1);
+      p.per_slice = static_cast<int32_t>(ceil_div(stages, slices));
+      p.slices = static_cast<int32_t>(ceil_div(stages, p.per_slice));
+      rc = split ? launch_product<true, 0, false, false, true, true>(maps, p, batch, sms, stream)
+                 : launch_product<true, 0, false, false, false, true>(maps, p, batch, sms, stream);
+      if (rc != MXQ_OK) return rc;
+      const Join join = {p.partial, batch, side, l.lds, p.partial_stride, p.slices, p.scale,
+                         reinterpret_cast<__half*>(workspace + l.gram[0]),
+                         split ? reinterpret_cast<__half*>(workspace + l.gram[1]) : nullptr, d_gram};
+      rc = launch_pdl(join_kernel, static_cast<unsigned>(ceil_div(p.partial_stride, kThreads)), kThreads, 0, stream, join);
+    } else {
+      rc = split ? launch_product<true, 0, false, false, true, false>(maps, p, batch, sms, stream)
+                 : launch_product<true, 0, false, false, false, false>(maps, p, batch, sms, stream);
+    }
     if (rc != MXQ_OK) return rc;
     // P = aI + bA + cAA
     p = {};
@@ -868,8 +980,8 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
       p.d_row = p.d_col = d_gram;
       p.d_out = d_poly;
     }
-    rc = split ? launch_product<true, 2, false, false, true>(maps, p, batch, sms, stream)
-               : launch_product<true, 1, true, false, false>(maps, p, batch, sms, stream);
+    rc = split ? launch_product<true, 2, false, false, true, false>(maps, p, batch, sms, stream)
+               : launch_product<true, 1, true, false, false, false>(maps, p, batch, sms, stream);
     if (rc != MXQ_OK) return rc;
     // X <- P X, or X P
     p = {};
@@ -898,14 +1010,14 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
       p.scale = scale / (sp * kXScale);
     }
     if (split)
-      rc = last ? launch_product<false, 0, false, true, true>(maps, p, batch, sms, stream)
-                : launch_product<false, 0, false, false, true>(maps, p, batch, sms, stream);
+      rc = last ? launch_product<false, 0, false, true, true, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 0, false, false, true, false>(maps, p, batch, sms, stream);
     else if (wide)
-      rc = last ? launch_product<false, 1, false, true, false>(maps, p, batch, sms, stream)
-                : launch_product<false, 1, false, false, false>(maps, p, batch, sms, stream);
+      rc = last ? launch_product<false, 1, false, true, false, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 1, false, false, false, false>(maps, p, batch, sms, stream);
     else
-      rc = last ? launch_product<false, 1, true, true, false>(maps, p, batch, sms, stream)
-                : launch_product<false, 1, true, false, false>(maps, p, batch, sms, stream);
+      rc = last ? launch_product<false, 1, true, true, false, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 1, true, false, false, false>(maps, p, batch, sms, stream);
     if (rc != MXQ_OK) return rc;
   }
   return MXQ_OK;

@@ -55,27 +55,32 @@ __device__ unsigned int g_ortho_status = 0;
 // norm and conversion
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 256;
+constexpr int kAhead = 4;        // loads a thread has in flight
 constexpr int kMaxParts = 2048;  // partial sums of squares per matrix
 constexpr float kXScale = 8192.0f;
 
 struct Matrix {
   int64_t batch, m, n, ld, stride;  // rows ld, matrices stride elements apart
+  int64_t last;                     // elements of the last row
 };
 
 // Blocks of a matrix take rows in turn; tx threads (a power of two) share a row.
+// Where the matrix and X have no gaps between their rows, the rows are pieces of
+// kThreads * kAhead loads instead (launch_scale).  Both kernels are bound by DRAM;
+// what they need is loads in flight: with rows of 512 floats a thread had one.
 template <typename T, int kV>
 __global__ void __launch_bounds__(kThreads)
     norm_kernel(const T* __restrict__ g, const Matrix a, int parts, int tx, float* __restrict__ sums) {
   __shared__ float red[kThreads / 32];
   pdl_wait();
-  const int64_t b = blockIdx.x / parts, part = blockIdx.x % parts, nv = a.n / kV;
+  const int64_t b = blockIdx.x / parts, part = blockIdx.x % parts;
   const int ty = kThreads / tx;
-  const uint64_t bytes = ((a.batch - 1) * a.stride + (a.m - 1) * a.ld + a.n) * sizeof(T);
-  constexpr int kAhead = 4;
+  const uint64_t bytes = ((a.batch - 1) * a.stride + (a.m - 1) * a.ld + a.last) * sizeof(T);
   float sum = 0.0f;
   for (int64_t r = part * ty + threadIdx.x / tx; r < a.m; r += static_cast<int64_t>(parts) * ty) {
     const T* row = g + b * a.stride + r * a.ld;
-    if (!in_buf(row, a.n * sizeof(T), g, bytes, &g_ortho_status)) continue;
+    const int64_t nv = (r == a.m - 1 ? a.last : a.n) / kV;
+    if (!in_buf(row, nv * kV * sizeof(T), g, bytes, &g_ortho_status)) continue;
     for (int64_t c = threadIdx.x % tx; c < nv; c += kAhead * tx) {
       Vec<T, kV> v[kAhead];
 #pragma unroll
@@ -100,10 +105,10 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, int kV>
 __global__ void __launch_bounds__(kThreads)
     scale_kernel(const T* __restrict__ g, const Matrix a, int parts, int tx, const float* __restrict__ sums, float eps,
-                 __half* __restrict__ x, __half* __restrict__ x_low, int64_t ldx) {
+                 __half* __restrict__ x, __half* __restrict__ x_low, int64_t ldx, int64_t stride_x) {
   __shared__ float factor;
   pdl_wait();
-  const int64_t b = blockIdx.x / parts, part = blockIdx.x % parts, nv = a.n / kV;
+  const int64_t b = blockIdx.x / parts, part = blockIdx.x % parts;
   const int ty = kThreads / tx;
   if (threadIdx.x < 32) {
     float s = 0.0f;
@@ -113,26 +118,34 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   const float f = factor;
-  const uint64_t in_bytes = ((a.batch - 1) * a.stride + (a.m - 1) * a.ld + a.n) * sizeof(T);
-  const uint64_t out_bytes = static_cast<uint64_t>(a.batch) * a.m * ldx * 2;
+  const uint64_t in_bytes = ((a.batch - 1) * a.stride + (a.m - 1) * a.ld + a.last) * sizeof(T);
+  const uint64_t out_bytes = static_cast<uint64_t>((a.batch - 1) * stride_x + (a.m - 1) * ldx + a.last) * 2;
   for (int64_t r = part * ty + threadIdx.x / tx; r < a.m; r += static_cast<int64_t>(parts) * ty) {
     const T* row = g + b * a.stride + r * a.ld;
-    __half* to = x + (b * a.m + r) * ldx;
-    if (!in_buf(row, a.n * sizeof(T), g, in_bytes, &g_ortho_status) ||
-        !in_buf(to, a.n * 2, x, out_bytes, &g_ortho_status))
+    __half* to = x + b * stride_x + r * ldx;
+    const int64_t nv = (r == a.m - 1 ? a.last : a.n) / kV;
+    if (!in_buf(row, nv * kV * sizeof(T), g, in_bytes, &g_ortho_status) ||
+        !in_buf(to, nv * kV * 2, x, out_bytes, &g_ortho_status))
       continue;
-#pragma unroll 4
-    for (int64_t c = threadIdx.x % tx; c < nv; c += tx) {
-      const Vec<T, kV> v = *reinterpret_cast<const Vec<T, kV>*>(row + c * kV);
-      Vec<uint16_t, kV> o;
+    for (int64_t c = threadIdx.x % tx; c < nv; c += kAhead * tx) {
+      Vec<T, kV> v[kAhead];
 #pragma unroll
-      for (int j = 0; j < kV; ++j) o.v[j] = __half_as_ushort(__float2half_rn(widen(v.v[j]) * f));
-      *reinterpret_cast<Vec<uint16_t, kV>*>(to + c * kV) = o;
-      if (x_low == nullptr) continue;
+      for (int q = 0; q < kAhead; ++q)
+        v[q] = c + q * tx < nv ? *reinterpret_cast<const Vec<T, kV>*>(row + (c + q * tx) * kV) : Vec<T, kV>{};
 #pragma unroll
-      for (int j = 0; j < kV; ++j)
-        o.v[j] = __half_as_ushort(__float2half_rn(widen(v.v[j]) * f - __half2float(__ushort_as_half(o.v[j]))));
-      *reinterpret_cast<Vec<uint16_t, kV>*>(x_low + (to - x) + c * kV) = o;
+      for (int q = 0; q < kAhead; ++q) {
+        if (c + q * tx >= nv) continue;
+        __half* at = to + (c + q * tx) * kV;
+        Vec<uint16_t, kV> o;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) o.v[j] = __half_as_ushort(__float2half_rn(widen(v[q].v[j]) * f));
+        *reinterpret_cast<Vec<uint16_t, kV>*>(at) = o;
+        if (x_low == nullptr) continue;
+#pragma unroll
+        for (int j = 0; j < kV; ++j)
+          o.v[j] = __half_as_ushort(__float2half_rn(widen(v[q].v[j]) * f - __half2float(__ushort_as_half(o.v[j]))));
+        *reinterpret_cast<Vec<uint16_t, kV>*>(x_low + (at - x)) = o;
+      }
     }
   }
 }
@@ -817,8 +830,16 @@ float scale_for(double bound) {
 }
 
 template <typename T, int kV>
-int launch_scale(const void* g, const Matrix& a, float eps, uint8_t* ws, const Layout& l, int sms, cudaStream_t stream) {
-  const int64_t nv = a.n / kV;
+int launch_scale(const void* g, Matrix a, float eps, uint8_t* ws, const Layout& l, int sms, cudaStream_t stream) {
+  int64_t ldx = l.ldx;
+  const int64_t stride_x = a.m * ldx;
+  if (a.ld == a.n && ldx == a.n) {  // one run of elements, in pieces
+    const int64_t total = a.m * a.n;
+    a.n = a.ld = ldx = kThreads * kAhead * kV;
+    a.m = ceil_div(total, a.n);
+    a.last = total - (a.m - 1) * a.n;
+  }
+  const int64_t nv = (a.m > 1 ? a.n : a.last) / kV;
   int tx = 8;
   while (tx < kThreads && tx < nv) tx *= 2;
   int64_t parts = ceil_div(a.m, kThreads / tx);
@@ -832,7 +853,7 @@ int launch_scale(const void* g, const Matrix& a, float eps, uint8_t* ws, const L
   if (rc != MXQ_OK) return rc;
   return launch_pdl(scale_kernel<T, kV>, blocks, kThreads, 0, stream, static_cast<const T*>(g), a,
                     static_cast<int>(parts), tx, sums, eps, reinterpret_cast<__half*>(ws + l.x[0][0]),
-                    l.parts == 2 ? reinterpret_cast<__half*>(ws + l.x[0][1]) : nullptr, l.ldx);
+                    l.parts == 2 ? reinterpret_cast<__half*>(ws + l.x[0][1]) : nullptr, ldx, stride_x);
 }
 template <typename T>
 int scale_vector(const void* g, const Matrix& a, float eps, uint8_t* ws, const Layout& l, int sms, cudaStream_t stream) {
@@ -892,7 +913,7 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
   const int sms = sm_count_current_device(nullptr);
   if (sms <= 0) return MXQ_ECUDA;
 
-  const Matrix a = {batch, m, n, ld, batch > 1 ? stride : 0};
+  const Matrix a = {batch, m, n, ld, batch > 1 ? stride : 0, n};
   int rc = dtype == MXQ_F32 ? scale_vector<float>(g, a, eps, workspace, l, sms, stream)
                             : scale_vector<bf16_t>(g, a, eps, workspace, l, sms, stream);
   if (rc != MXQ_OK) return rc;

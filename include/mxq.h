@@ -373,8 +373,8 @@ int mxq_moe_combine_backward(const void *dy, int dtype, int64_t tokens, int64_t 
 
 /*
  * Scaled lookup in a table [rows, D], and the table's gradient.
- *   ids      int32 or int64 (ids_bytes 4 or 8) [tokens].  An id outside [0, rows)
- *            gives a row of zeros, adds to no gradient and sets MXQ_DEV_BADINDEX.
+ *   ids      int32 or int64 (ids_bytes 4 or 8, else MXQ_EBADDTYPE) [tokens].  An id
+ *            outside [0, rows) gives a row of zeros, adds to no gradient and sets MXQ_DEV_BADINDEX.
  *   mxq_embedding            y[t] = scale * table[ids[t]], types dtype -> out_dtype.
  *   mxq_embedding_backward   dtable[v] = scale * sum of dy[t] over ids[t] == v, in
  *            a fixed order; every row is written, 0 where no token has it.  Tokens

@@ -14,12 +14,20 @@
 // logits are read once each way, the next token's while this one is worked on.
 // The k-th largest of the lanes' own maxima is at most the k-th largest logit, so
 // only the few logits from there on (k to a dozen of random ones) are gathered,
-// one per lane, and each counts those before it: larger, or equal with a lower
-// index.  With more than 32 such logits (many equal ones) every logit takes part
-// in each of k rounds of a warp-wide maximum.  A lane also keeps the
-// sums over its tokens of the probabilities of its experts; they are added up
-// per block and then over the blocks in a fixed order, so the loss has the
-// same bits in every run.
+// one per lane, and each counts those before it by keys that no two share.  With
+// more than 32 such logits (many equal ones) every logit takes part in each of k
+// rounds of a warp-wide maximum.  A lane also keeps the sums over its tokens of
+// the probabilities of its experts; they are added up per block and then over the
+// blocks in a fixed order, so the loss has the same bits in every run.
+//
+// The forward pass is bound by instruction issue, 430 a token with 250 experts in
+// 90% of the issue slots: the softmax and the loss's sums take 40 of them for a
+// lane's 8 logits, the choice most of the rest.  131071 x 250 fp32, k = 6: 63 us,
+// 2.1 TB/s (70 with a float and an index compared instead of one key, 66 with a
+// ballot for each of a lane's logits instead of one count).  The backward pass
+// reads the logits again, as keeping p would cost a write and the same read:
+// 48 us, 5.5 TB/s.  7168 x 64 bf16, k = 8: 10 us and 4.7, mostly the latency of
+// three launches.
 #include <cuda_runtime.h>
 #include <float.h>
 #include <math_constants.h>
@@ -45,6 +53,24 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
+
+// A key in the order in which experts are chosen, no two of a row alike: the
+// larger logit, then the lower expert.  The logits of one type take 32 bits where
+// their own keys leave 16 for the expert.
+template <typename T>
+struct ChoiceKey {
+  using type = uint64_t;
+  static __device__ __forceinline__ type of(float x, int e) {
+    return (static_cast<uint64_t>(order_key(x)) << 32) | static_cast<uint32_t>(~e);
+  }
+};
+template <>
+struct ChoiceKey<bf16_t> {
+  using type = uint32_t;
+  static __device__ __forceinline__ type of(float x, int e) {
+    return (order_key(x) & 0xFFFF0000u) | (0xFFFFu - static_cast<uint32_t>(e));
+  }
+};
 
 // Expert of register i of a lane: vectors of kV consecutive experts per lane.
 template <int kV>
@@ -173,10 +199,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* hist = reinterpret_cast<int32_t*>(by_warp + (kPer > 2 ? kPer : 2) * kThreads);  // [E]
   float* sums = reinterpret_cast<float*>(hist + s.E);       // [E]
   __shared__ int32_t routed_tokens;
-  __shared__ float2 few[kWarps][32];                        // the logits gathered, with their experts
+  using Key = typename ChoiceKey<T>::type;
+  __shared__ int few_n[kWarps];
+  __shared__ __align__(16) float2 few[kWarps][32];          // the logits gathered with their experts, then their keys
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   for (int e = tid; e < s.E; e += kThreads) hist[e] = 0;
   if (tid == 0) routed_tokens = 0;
+  if (lane == 0) few_n[warp] = 0;
   __syncthreads();
   pdl_wait();
   const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
@@ -225,26 +254,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float top = top_key != 0u ? key_value(top_key) : -CUDART_INF_F;
       const float from = bar != 0u ? key_value(bar) : -FLT_MAX;
       if (top_key != 0u) {
-        int n = 0;
+        // how many of them this lane has, and where it puts them, in any order
+        int own_n = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const bool in = x[i] >= from;  // false for NaN and -inf
-          const uint32_t who = __ballot_sync(0xFFFFFFFFu, in);
-          // past 32 they overwrite one another and are not used
-          if (in)
-            few[warp][(n + __popc(who & ((1u << lane) - 1u))) & 31] =
-                make_float2(x[i], __int_as_float(expert_of<kV>(i, lane)));
-          n += __popc(who);
-        }
+        for (int i = 0; i < kPer; ++i) own_n += x[i] >= from ? 1 : 0;  // not NaN and -inf
+        int at = 0;
+        if (own_n > 0) at = atomicAdd(&few_n[warp], own_n);
+        const int n = __reduce_add_sync(0xFFFFFFFFu, own_n);
         __syncwarp();
+        if (lane == 0) few_n[warp] = 0;  // for the next token
         if (n <= 32) {
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (x[i] >= from) few[warp][at++] = make_float2(x[i], __int_as_float(expert_of<kV>(i, lane)));
+          __syncwarp();
           const float2 own = few[warp][lane];
           const int e = __float_as_int(own.y);
+          const Key key = lane < n ? ChoiceKey<T>::of(own.x, e) : 0;
+          Key* keys = reinterpret_cast<Key*>(few[warp]);
+          __syncwarp();
+          keys[lane] = key;
+          __syncwarp();
           int before = 0;
-#pragma unroll 4
-          for (int i = 0; i < n; ++i) {
-            const float2 other = few[warp][i];
-            before += other.x > own.x || (other.x == own.x && __float_as_int(other.y) < e) ? 1 : 0;
+          constexpr int kAtOnce = 16 / sizeof(Key);
+          for (int i = 0; i < n; i += kAtOnce) {
+            const Vec<Key, kAtOnce> other = *reinterpret_cast<const Vec<Key, kAtOnce>*>(keys + i);
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) before += other.v[q] > key ? 1 : 0;
           }
           if (lane < n && before < s.k) {
             rank = before;

@@ -16,12 +16,13 @@
 // Powers of two keep small elements out of fp16's subnormal range: X is stored
 // times 2^13, A and P times powers taken from the coefficients' bounds.
 //
-// The rounding that matters is that of the diagonals of A and P, which hold most
-// of their weight once the singular values draw together: what fp16 leaves of
-// them is kept in fp32 vectors, d_A and d_P, and put back in the epilogues of
-// the products that read them (A A = A'A' + d A' + A'd + d d with the rounded
-// A'; P X = P'X + d X).  The error of the result before its own rounding to bf16
-// (1.7e-3) is then 0.8e-3, instead of 1.7e-3 to 2.7e-3 without.
+// The square is completed: with S = A + (b/2c) I, which the gram product's
+// epilogue stores in A's place, P = c S S + (a - b^2/4c) I.  So no epilogue reads
+// a second matrix (64 matrices of 1024x512: 501 us when the square read A and the
+// update X, both to put back what the rounding left of the diagonals, 468 without),
+// and S has the smaller diagonal to round.  The result's error before its own
+// rounding to bf16 (1.7e-3) is then 1.2e-3 to 1.5e-3.  Where b/2c is large or c is
+// zero (kCompletedSquare) the square adds b A from memory.
 // The iteration's map of a singular value has slopes of up to 1.6 around 1, and
 // the value of a small matrix hangs on few roundings, so its error can reach 1%
 // (sides up to 16 in a simulation; 0.14% from a side of 48 on).  Sides of at
@@ -180,15 +181,11 @@ struct Product {
   int32_t ksteps;          // stages along K of one product
   int32_t tiles_m, tiles_n, tiles;  // tiles: all of the batch and of the slices
   int32_t slices, per_slice;        // K in slices of that many stages, each summed by itself
-  float* partial;                   // [slices, batch, rows, d_ld] sums of the slices, or NULL
-  int64_t partial_stride;           // elements between the slices
+  float* partial;                   // [slices, batch, rows, partial_ld] sums of the slices, or NULL
+  int64_t partial_stride, partial_ld;  // elements between the slices and the rows
   int32_t a_mn, b_mn;      // operand lies with K along its rows
-  // output = scale * acc + (add_scale + scale * (d[row] + d[column])) * addend
-  //          and where row == column, + diagonal + add_scale * d + scale * d * d
+  // output = scale * acc + add_scale * addend, and + diagonal where row == column
   float scale, add_scale, diagonal;
-  const float *d_row, *d_col;       // [batch, d_ld]: what the rounding left of a diagonal; NULL: zero
-  float* d_out;                     // the same of this output's diagonal, or NULL
-  int64_t d_ld;
   // the last update writes bf16 to the caller's matrix
   bf16_t* out;             // NULL: fp16 through map d
   int64_t ldo, stride_o;
@@ -332,11 +329,11 @@ __device__ __forceinline__ void unpack8(const uint4 w, float (&v)[8]) {
   v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
 }
 
-// kSymmetric: one triangle of tiles, stored twice.  kAddends: parts of the
-// addend.  kColumns: the columns' d_col multiplies it (d_row, where given, always
-// does).  kBf16: the last update, to the caller's matrix.  kSplit: operands and
-// results are pairs, three products.  kPartial: the sums of a slice of K, in fp32.
-template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit, bool kPartial>
+// kSymmetric: one triangle of tiles, stored twice.  kAddends: parts of the addend
+// (of a symmetric product).  kBf16: the last update, to the caller's matrix.
+// kSplit: operands and results are pairs, three products.  kPartial: the sums of a
+// slice of K, in fp32.
+template <bool kSymmetric, int kAddends, bool kBf16, bool kSplit, bool kPartial>
 __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p) {
   extern __shared__ uint8_t raw[];
@@ -492,11 +489,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       const int64_t row0 = static_cast<int64_t>(at.i) * kTile + rank * kHalf + quarter * 32;
       const int64_t row = row0 + lane;
       const bool mirror = kSymmetric && at.i != at.j, both = needs_both(at) || kAddends == 2;
-      const float dr = p.d_row != nullptr && row < p.rows ? p.d_row[at.batch * p.d_ld + row] : 0.0f;
-      if (kColumns && lane < 4) {  // this warp's 128 columns, four lines
-        const int64_t col = static_cast<int64_t>(at.j) * kTile + 2 * (e >> 2) * kChunkCols + 32 * lane;
-        if (col < p.cols) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.d_col + at.batch * p.d_ld + col));
-      }
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(&bars.acc_full[acc]), (done >> 1) & 1, abort_flag,
                                                      &g_ortho_status, MXQ_DEV_TIMEOUT));
       if (!ok) break;
@@ -547,26 +539,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
         }
         if (!inside) continue;
         if (kPartial) {
-          float* to = p.partial + at.slice * p.partial_stride + (static_cast<int64_t>(at.batch) * p.rows + row) * p.d_ld + col0;
+          float* to = p.partial + at.slice * p.partial_stride + (static_cast<int64_t>(at.batch) * p.rows + row) * p.partial_ld + col0;
           if (row < p.rows)
 #pragma unroll
             for (int i = 0; i < 64; i += 4)
-              if (col0 + i < p.d_ld)  // a multiple of 8
+              if (col0 + i < p.partial_ld)  // a multiple of 8
                 *reinterpret_cast<uint4*>(to + i) =
                     make_uint4(raw[i / 32][i % 32], raw[i / 32][i % 32 + 1], raw[i / 32][i % 32 + 2], raw[i / 32][i % 32 + 3]);
           continue;
         }
-        const float k0 = fmaf(p.scale, dr, p.add_scale);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // 32 columns at a time
           const int64_t col = col0 + 32 * h;
-          float4 dc[8];
-          if (kColumns) {
-            const float4* d = reinterpret_cast<const float4*>(p.d_col + at.batch * p.d_ld + col);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)  // d_ld is a multiple of 8
-              dc[q] = col + 4 * q < p.cols ? d[q] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          }
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[h][i]) * p.scale;
@@ -582,24 +566,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
                 for (int i = 0; i < 8; ++i) a[i] += l[i];
               }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 d = dc[2 * q + i / 4];
-                const float k = kColumns ? fmaf(p.scale, i % 4 == 0 ? d.x : i % 4 == 1 ? d.y : i % 4 == 2 ? d.z : d.w, k0) : k0;
-                v[8 * q + i] = fmaf(k, a[i], v[8 * q + i]);
-              }
+              for (int i = 0; i < 8; ++i) v[8 * q + i] = fmaf(p.add_scale, a[i], v[8 * q + i]);
             }
           }
           if (kSymmetric && row0 < col + 32 && col < row0 + 32) {  // the warp's rows meet these columns
             const int own_column = static_cast<int>(row - col);
-            const float on = p.diagonal + p.add_scale * dr + p.scale * dr * dr;
-            float own = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              v[i] += i == own_column ? on : 0.0f;
-              own = i == own_column ? v[i] : own;
-            }
-            if (!kSplit && own_column >= 0 && own_column < 32 && row < p.rows)
-              p.d_out[at.batch * p.d_ld + row] = own - half_rounded(own);
+            for (int i = 0; i < 32; ++i) v[i] += i == own_column ? p.diagonal : 0.0f;
           }
           uint32_t w[16];
 #pragma unroll
@@ -634,8 +607,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
               bf16_t* to = out + (row0 + r) * p.ldo + col0 + i;
               if (col0 + i < p.cols && in_buf(to, 2, out, bytes, &g_ortho_status)) *to = value;
             }
-          fence_proxy_async_smem();  // read before the next addend comes in
-          __syncwarp();
+          __syncwarp();  // read before the next chunk is staged
           continue;
         }
         fence_proxy_async_smem();
@@ -650,20 +622,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       }
       if (ok && kAddends > 0 && t + step < p.tiles) {
         const TileAt next = tile_at<kSymmetric>(p, t + step);
-        // the first chunk's store has been read once at most the second's is left
-        const bool second = (static_cast<int64_t>(at.j) * kTile + (2 * (e >> 2) + 1) * kChunkCols) < p.cols;
-        if (kSymmetric || kAddends == 2 || !second) {
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          load_addends(next);
-        } else {
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
-          load_addend(0, 0, next, 0);
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          load_addend(1, 0, next, 1);
-        }
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        load_addends(next);
       }
     }
     for (int b = 0; b < 2; ++b)  // after a wait that ran out
@@ -691,9 +652,8 @@ struct Join {
   const float* partial;
   int64_t batch, side, ld, stride;
   int slices;
-  float scale;
-  __half *high, *low;
-  float* d_out;
+  float scale, diagonal;
+  __half *high, *low;  // low: or NULL
 };
 __global__ void __launch_bounds__(kThreads) join_kernel(const Join a) {
   pdl_wait();
@@ -706,19 +666,21 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Join a) {
   float sum = 0.0f;
 #pragma unroll 8
   for (int s = 0; s < a.slices; ++s) sum += p[s * a.stride];
-  const float v = sum * a.scale, h = half_rounded(v);
+  const float v = sum * a.scale + (i == j ? a.diagonal : 0.0f), h = half_rounded(v);
   const uint64_t bytes = static_cast<uint64_t>(n) * 2;
   if (!in_buf(a.high + at, 2, a.high, bytes, &g_ortho_status)) return;
   a.high[at] = __float2half_rn(v);
-  if (a.low != nullptr)
-    a.low[at] = __float2half_rn(v - h);
-  else if (i == j)
-    a.d_out[row / a.side * a.ld + i] = v - h;
+  if (a.low != nullptr) a.low[at] = __float2half_rn(v - h);
 }
 
 // ---------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------
+// The square is completed where |b| is at most this many |c|, so that |b/2c| stays
+// within the bound of A: beyond it the rounding of S would be that of the shift.
+// (Completed and not: 16x16 70 and 80 us, 200 matrices of 128x512 205 and 224, 64
+// of 1024x512 470 and 483, 4096x8192 1646 and 1651.)
+constexpr float kCompletedSquare = 4.0f;
 // Sides up to this carry pairs of fp16 (see the head of the file).
 constexpr int64_t kSplitSide = 64;
 
@@ -751,7 +713,7 @@ struct Layout {
   int parts;                         // 2 with low parts
   int64_t x[2][2];                   // X of the even and of the odd steps: high, low
   int64_t gram[2], poly[2];
-  int64_t d_gram, d_poly, sums, partial, bytes;
+  int64_t sums, partial, bytes;
 };
 Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   Layout l;
@@ -770,8 +732,6 @@ Layout layout_of(int64_t batch, int64_t m, int64_t n) {
     l.gram[q] = take(there ? sb : 0);
     l.poly[q] = take(there ? sb : 0);
   }
-  l.d_gram = take(up(batch * l.lds * 4, 256));
-  l.d_poly = take(up(batch * l.lds * 4, 256));
   l.sums = take(up(batch * kMaxParts * 4, 256));
   l.partial = take(up(gram_slices(batch, l.side, l.side == m ? n : m) * batch * l.side * l.lds * 4, 256));
   l.bytes = at;
@@ -797,7 +757,7 @@ bool encode_half(CUtensorMap* map, const Stack& t, uint32_t box_cols, uint32_t b
   return encode(map, t, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, box_cols, box_rows, swizzle);
 }
 
-template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit, bool kPartial>
+template <bool kSymmetric, int kAddends, bool kBf16, bool kSplit, bool kPartial>
 int launch_product(const Maps& maps, Product p, int64_t batch, int sms, cudaStream_t stream) {
   p.tiles_m = static_cast<int32_t>(ceil_div(p.rows, kTile));
   p.tiles_n = static_cast<int32_t>(ceil_div(p.cols, kTile));
@@ -808,7 +768,7 @@ int launch_product(const Maps& maps, Product p, int64_t batch, int sms, cudaStre
     p.per_slice = INT32_MAX / 2;
   }
   p.tiles = static_cast<int32_t>(per * batch * p.slices);
-  const auto kernel = product_kernel<kSymmetric, kAddends, kColumns, kBf16, kSplit, kPartial>;
+  const auto kernel = product_kernel<kSymmetric, kAddends, kBf16, kSplit, kPartial>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ECUDA;
   static bool attr_done[64] = {};  // benign race: the same attribute set twice
@@ -944,11 +904,12 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
       encode(&final_rows, Stack{out, batch, m, n, ldo, so}, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, 32, true);
 
   // |X| <= 1.5 and so |A| <= 2 are taken as bounds of the iterates
-  const float sa = scale_for(2.0), sp = scale_for(fabs(ca) + 2 * fabs(cb) + 4 * fabs(cc));
+  // P = c (A + b/2c I)^2 + (a - b^2/4c) I where b/2c is no larger than those bounds
+  const bool completed = cc != 0.0f && fabsf(cb) <= kCompletedSquare * fabsf(cc);
+  const double shift = completed ? 0.5 * cb / cc : 0.0;
+  const float sa = scale_for(2.0 + fabs(shift)), sp = scale_for(fabs(ca) + 2 * fabs(cb) + 4 * fabs(cc));
   const int parts = l.parts;
   const bool split = parts == 2;
-  float* d_gram = reinterpret_cast<float*>(workspace + l.d_gram);
-  float* d_poly = reinterpret_cast<float*>(workspace + l.d_poly);
   for (int s = 0; s < steps; ++s) {
     const int from = s & 1, to = from ^ 1;
     Maps maps = {};
@@ -963,24 +924,24 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.ksteps = static_cast<int32_t>(ceil_div(length, kStepK));
     p.a_mn = p.b_mn = !wide;
     p.scale = sa / (kXScale * kXScale);
-    p.d_ld = l.lds;
-    p.d_out = d_gram;
+    p.diagonal = static_cast<float>(shift * sa);
     if (const int64_t slices = gram_slices(batch, side, length); slices > 0) {
       p.partial = reinterpret_cast<float*>(workspace + l.partial);
       p.partial_stride = batch * side * l.lds;
+      p.partial_ld = l.lds;
       const int64_t stages = p.ksteps * (split ? 3 : 1);
       p.per_slice = static_cast<int32_t>(ceil_div(stages, slices));
       p.slices = static_cast<int32_t>(ceil_div(stages, p.per_slice));
-      rc = split ? launch_product<true, 0, false, false, true, true>(maps, p, batch, sms, stream)
-                 : launch_product<true, 0, false, false, false, true>(maps, p, batch, sms, stream);
+      rc = split ? launch_product<true, 0, false, true, true>(maps, p, batch, sms, stream)
+                 : launch_product<true, 0, false, false, true>(maps, p, batch, sms, stream);
       if (rc != MXQ_OK) return rc;
-      const Join join = {p.partial, batch, side, l.lds, p.partial_stride, p.slices, p.scale,
+      const Join join = {p.partial, batch, side, l.lds, p.partial_stride, p.slices, p.scale, p.diagonal,
                          reinterpret_cast<__half*>(workspace + l.gram[0]),
-                         split ? reinterpret_cast<__half*>(workspace + l.gram[1]) : nullptr, d_gram};
+                         split ? reinterpret_cast<__half*>(workspace + l.gram[1]) : nullptr};
       rc = launch_pdl(join_kernel, static_cast<unsigned>(ceil_div(p.partial_stride, kThreads)), kThreads, 0, stream, join);
     } else {
-      rc = split ? launch_product<true, 0, false, false, true, false>(maps, p, batch, sms, stream)
-                 : launch_product<true, 0, false, false, false, false>(maps, p, batch, sms, stream);
+      rc = split ? launch_product<true, 0, false, true, false>(maps, p, batch, sms, stream)
+                 : launch_product<true, 0, false, false, false>(maps, p, batch, sms, stream);
     }
     if (rc != MXQ_OK) return rc;
     // P = aI + bA + cAA
@@ -994,15 +955,15 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.rows = p.cols = side;
     p.ksteps = static_cast<int32_t>(ceil_div(side, kStepK));
     p.scale = cc * sp / (sa * sa);
-    p.add_scale = cb * sp / sa;
-    p.diagonal = ca * sp;
-    p.d_ld = l.lds;
-    if (!split) {
-      p.d_row = p.d_col = d_gram;
-      p.d_out = d_poly;
+    p.diagonal = static_cast<float>((ca - 0.5 * shift * cb) * sp);
+    if (completed) {
+      rc = split ? launch_product<true, 0, false, true, false>(maps, p, batch, sms, stream)
+                 : launch_product<true, 0, false, false, false>(maps, p, batch, sms, stream);
+    } else {
+      p.add_scale = cb * sp / sa;
+      rc = split ? launch_product<true, 2, false, true, false>(maps, p, batch, sms, stream)
+                 : launch_product<true, 1, false, false, false>(maps, p, batch, sms, stream);
     }
-    rc = split ? launch_product<true, 2, false, false, true, false>(maps, p, batch, sms, stream)
-               : launch_product<true, 1, true, false, false, false>(maps, p, batch, sms, stream);
     if (rc != MXQ_OK) return rc;
     // X <- P X, or X P
     p = {};
@@ -1016,11 +977,6 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.cols = n;
     p.ksteps = static_cast<int32_t>(ceil_div(side, kStepK));
     p.scale = 1.0f / sp;
-    if (!split) {
-      maps.add[0] = x[from][0].rows;
-      p.d_ld = l.lds;
-      (wide ? p.d_row : p.d_col) = d_poly;
-    }
     const bool last = s + 1 == steps;
     if (last) {
       if (out_map) maps.d[0] = final_rows;
@@ -1031,14 +987,11 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
       p.scale = scale / (sp * kXScale);
     }
     if (split)
-      rc = last ? launch_product<false, 0, false, true, true, false>(maps, p, batch, sms, stream)
-                : launch_product<false, 0, false, false, true, false>(maps, p, batch, sms, stream);
-    else if (wide)
-      rc = last ? launch_product<false, 1, false, true, false, false>(maps, p, batch, sms, stream)
-                : launch_product<false, 1, false, false, false, false>(maps, p, batch, sms, stream);
+      rc = last ? launch_product<false, 0, true, true, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 0, false, true, false>(maps, p, batch, sms, stream);
     else
-      rc = last ? launch_product<false, 1, true, true, false, false>(maps, p, batch, sms, stream)
-                : launch_product<false, 1, true, false, false, false>(maps, p, batch, sms, stream);
+      rc = last ? launch_product<false, 0, true, false, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 0, false, false, false>(maps, p, batch, sms, stream);
     if (rc != MXQ_OK) return rc;
   }
   return MXQ_OK;

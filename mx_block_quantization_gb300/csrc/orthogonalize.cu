@@ -538,7 +538,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           if (lane == 0) arrive_cluster(at_leader(smem_u32(&bars.acc_empty[acc])));
         }
         if (!inside) continue;
-        if (kPartial) {
+        const auto store_partial = [&] {
+          if (!kPartial) return false;
           float* to = p.partial + at.slice * p.partial_stride + (static_cast<int64_t>(at.batch) * p.rows + row) * p.partial_ld + col0;
           if (row < p.rows)
 #pragma unroll
@@ -546,8 +547,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
               if (col0 + i < p.partial_ld)  // a multiple of 8
                 *reinterpret_cast<uint4*>(to + i) =
                     make_uint4(raw[i / 32][i % 32], raw[i / 32][i % 32 + 1], raw[i / 32][i % 32 + 2], raw[i / 32][i % 32 + 3]);
-          continue;
-        }
+          return true;
+        };
+        if (store_partial()) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // 32 columns at a time
           const int64_t col = col0 + 32 * h;

@@ -22,9 +22,9 @@
 //
 // The forward pass is bound by instruction issue, 430 a token with 250 experts in
 // 90% of the issue slots: the softmax and the loss's sums take 40 of them for a
-// lane's 8 logits, the choice most of the rest.  131071 x 250 fp32, k = 6: 63 us,
-// 2.1 TB/s (70 with a float and an index compared instead of one key, 66 with a
-// ballot for each of a lane's logits instead of one count).  The backward pass
+// lane's 8 logits, the choice most of the rest.  131071 x 250 fp32, k = 6: 56 us,
+// 2.3 TB/s (a float and an index compared instead of one key cost 4 us more, a
+// ballot for each of a lane's logits instead of one count 2).  The backward pass
 // reads the logits again, as keeping p would cost a write and the same read:
 // 48 us, 5.5 TB/s.  7168 x 64 bf16, k = 8: 10 us and 4.7, mostly the latency of
 // three launches.
@@ -128,62 +128,30 @@ struct RouteShape {
   int E, k, renorm;
 };
 
-// Sums over the blocks: counts, routed tokens and loss.  part_p/part_c are
-// [blocks, E], part_n [blocks].  The threads form `groups` teams with a thread
-// per expert; a team adds up every groups-th block and the teams' sums are
-// added in order.  `red` holds 2 * blockDim.x words.
-__device__ void join_blocks(const RouteShape s, int blocks, const float* part_p, const int32_t* part_c,
-                            const int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out,
-                            float* red) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  int team = 32;
-  while (team < s.E && team < nt) team *= 2;
-  const int groups = nt / team, group = tid / team;
-  float* sum_p = red;
-  int32_t* sum_c = reinterpret_cast<int32_t*>(red + nt);
-  __shared__ float warp_loss[32];
-  __shared__ int32_t all_n;
-  if (tid < 32) {
-    int n = 0;
-    for (int b = tid; b < blocks; b += 32) n += part_n[b];
-    n = __reduce_add_sync(0xFFFFFFFFu, n);
-    if (tid == 0) all_n = n;
+// The loss from sum_e counts_e sum_t p_te over n tokens.
+__device__ __forceinline__ float loss_of(const RouteShape& s, float sum, int n) {
+  const float f = static_cast<float>(n);
+  return n > 0 ? sum * (static_cast<float>(s.E) / (static_cast<float>(s.k) * f * f)) : 0.0f;
+}
+
+// Counts, routed tokens and loss of a grid of one block, from its sums.
+__device__ __forceinline__ void finish_alone(const RouteShape& s, const float* p, const int32_t* c, int n, int32_t* counts,
+                                             float* loss, int32_t* n_out) {
+  __shared__ float by_warp[32];
+  const int tid = threadIdx.x;
+  float sum = 0.0f;
+  for (int e = tid; e < s.E; e += blockDim.x) {
+    counts[e] = c[e];
+    sum += static_cast<float>(c[e]) * p[e];
   }
-  float local = 0.0f;
-  for (int e0 = 0; e0 < s.E; e0 += team) {
-    const int e = e0 + tid % team;
-    float p = 0.0f;
-    int c = 0;
-    if (e < s.E) {
-#pragma unroll 8
-      for (int b = group; b < blocks; b += groups) {
-        p += part_p[static_cast<int64_t>(b) * s.E + e];
-        c += part_c[static_cast<int64_t>(b) * s.E + e];
-      }
-    }
-    sum_p[tid] = p;
-    sum_c[tid] = c;
-    __syncthreads();
-    if (group == 0 && e < s.E) {
-      for (int g = 1; g < groups; ++g) {
-        p += sum_p[g * team + tid];
-        c += sum_c[g * team + tid];
-      }
-      counts[e] = c;
-      local += static_cast<float>(c) * p;
-    }
-    __syncthreads();
-  }
-  local = warp_sum(local);
-  if ((tid & 31) == 0) warp_loss[tid >> 5] = local;
+  sum = warp_sum(sum);
+  if ((tid & 31) == 0) by_warp[tid >> 5] = sum;
   __syncthreads();
-  if (tid < 32) {
-    local = warp_sum(tid < nt / 32 ? warp_loss[tid] : 0.0f);
-    if (tid == 0) {
-      const float n = static_cast<float>(all_n);
-      *loss = all_n > 0 ? local * (static_cast<float>(s.E) / (static_cast<float>(s.k) * n * n)) : 0.0f;
-      *n_out = all_n;
-    }
+  if (tid >= 32) return;
+  sum = warp_sum(tid < static_cast<int>(blockDim.x) / 32 ? by_warp[tid] : 0.0f);
+  if (tid == 0) {
+    *loss = loss_of(s, sum, n);
+    *n_out = n;
   }
 }
 
@@ -191,12 +159,11 @@ template <typename T, int kPer, int kV, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1)
     route_kernel(const T* __restrict__ logits, const RouteShape s, const uint8_t* __restrict__ mask,
                  float* __restrict__ weights, int32_t* __restrict__ ids, float* part_p,
-                 int32_t* part_c, int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out) {
+                 int32_t* part_c, int32_t* part_n, uint32_t* joined, int32_t* counts, float* loss, int32_t* n_out) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kWarps = kThreads / 32;
-  float* by_warp = reinterpret_cast<float*>(smem);          // [warps, 32 * kPer]; then
-  float* red = by_warp;                                     // [2 * threads] for the join
-  int32_t* hist = reinterpret_cast<int32_t*>(by_warp + (kPer > 2 ? kPer : 2) * kThreads);  // [E]
+  float* by_warp = reinterpret_cast<float*>(smem);          // [warps, 32 * kPer]
+  int32_t* hist = reinterpret_cast<int32_t*>(by_warp + kPer * kThreads);  // [E]
   float* sums = reinterpret_cast<float*>(hist + s.E);       // [E]
   __shared__ int32_t routed_tokens;
   using Key = typename ChoiceKey<T>::type;
@@ -210,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();
   const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
   const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
-  if (gridDim.x > 1) pdl_launch_dependents();  // the join that follows has one block
+  if (gridDim.x > 1) pdl_launch_dependents();  // the join's few blocks wait beside this one
   float acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
@@ -350,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   if (gridDim.x == 1) {
-    join_blocks(s, 1, sums, hist, &routed_tokens, counts, loss, n_out, red);
+    finish_alone(s, sums, hist, routed_tokens, counts, loss, n_out);
     return;
   }
   const int64_t base = static_cast<int64_t>(blockIdx.x) * s.E;
@@ -358,16 +325,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     part_p[base + e] = sums[e];
     part_c[base + e] = hist[e];
   }
-  if (tid == 0) part_n[blockIdx.x] = routed_tokens;
+  if (tid == 0) {
+    part_n[blockIdx.x] = routed_tokens;
+    if (blockIdx.x == 0) *joined = 0u;
+  }
 }
 
-constexpr int kJoinThreads = 1024;
-__global__ void __launch_bounds__(kJoinThreads)
+// Sums over the blocks, part_p and part_c [blocks, E], part_n [blocks]: a block
+// for 32 experts, whose warps take every kJoinWarps-th block of the grid before
+// and are added in order.  The block that is last to write its part of the loss
+// adds the parts up.  (With one block for all experts the forward pass takes 64.6 us
+// instead of 58.3 at 131071 tokens x 250 experts, 87.8 instead of 59.3 at 32768 x
+// 1024: its threads' loads come in several turns.)
+constexpr int kJoinWarps = 16, kMaxBlocks = 256, kMaxJoins = 32;
+static_assert(MXQ_MAX_GROUPS <= 32 * kMaxJoins, "a lane for each block's part of the loss");
+__global__ void __launch_bounds__(32 * kJoinWarps)
     route_join_kernel(const RouteShape s, int blocks, const float* part_p, const int32_t* part_c,
-                      const int32_t* part_n, int32_t* counts, float* loss, int32_t* n_out) {
-  __shared__ float red[2 * kJoinThreads];
+                      const int32_t* part_n, uint32_t* joined, float* part_loss, int32_t* counts, float* loss,
+                      int32_t* n_out) {
+  __shared__ float sum_p[kJoinWarps][32];
+  __shared__ int32_t sum_c[kJoinWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x * 32 + lane;
   pdl_wait();
-  join_blocks(s, blocks, part_p, part_c, part_n, counts, loss, n_out, red);
+  float p = 0.0f;
+  int c = 0, n = 0;
+  if (e < s.E)
+#pragma unroll 10
+    for (int b = warp; b < blocks; b += kJoinWarps) {
+      p += part_p[static_cast<int64_t>(b) * s.E + e];
+      c += part_c[static_cast<int64_t>(b) * s.E + e];
+    }
+  if (warp == 0)
+    for (int b = lane; b < blocks; b += 32) n += part_n[b];
+  sum_p[warp][lane] = p;
+  sum_c[warp][lane] = c;
+  __syncthreads();
+  if (warp > 0) return;
+  for (int w = 1; w < kJoinWarps; ++w) {
+    p += sum_p[w][lane];
+    c += sum_c[w][lane];
+  }
+  if (e < s.E) counts[e] = c;
+  const float own = warp_sum(e < s.E ? static_cast<float>(c) * p : 0.0f);
+  uint32_t before = 0;
+  if (lane == 0) {
+    part_loss[blockIdx.x] = own;
+    __threadfence();
+    before = atomicAdd(joined, 1u);
+    __threadfence();
+  }
+  if (__shfl_sync(0xFFFFFFFFu, before, 0) + 1 != gridDim.x) return;
+  const float all = warp_sum(lane < static_cast<int>(gridDim.x) ? __ldcg(part_loss + lane) : 0.0f);
+  n = __reduce_add_sync(0xFFFFFFFFu, n);
+  if (lane == 0) {
+    *loss = loss_of(s, all, n);
+    *n_out = n;
+  }
 }
 
 template <typename T, int kPer, int kV, int kThreads>
@@ -544,12 +557,14 @@ int launch_route(const RouteCall& a) {
   float* part_p = reinterpret_cast<float*>(a.workspace);
   int32_t* part_c = reinterpret_cast<int32_t*>(part_p + static_cast<int64_t>(blocks) * a.s.E);
   int32_t* part_n = part_c + static_cast<int64_t>(blocks) * a.s.E;
-  int rc = launch_pdl(route_kernel<T, kPer, kV, kThreads>, blocks, kThreads, a.s.E * 8 + (kPer > 2 ? kPer : 2) * kThreads * 4, a.stream,
-                      static_cast<const T*>(a.logits), a.s, a.mask, a.weights, a.ids, part_p, part_c, part_n,
+  uint32_t* joined = reinterpret_cast<uint32_t*>(part_n + blocks);
+  float* part_loss = reinterpret_cast<float*>(joined + 1);
+  int rc = launch_pdl(route_kernel<T, kPer, kV, kThreads>, blocks, kThreads, a.s.E * 8 + kPer * kThreads * 4, a.stream,
+                      static_cast<const T*>(a.logits), a.s, a.mask, a.weights, a.ids, part_p, part_c, part_n, joined,
                       a.counts, a.loss, a.n);
   if (rc != MXQ_OK || blocks == 1) return rc;
-  return launch_pdl(route_join_kernel, 1, kJoinThreads, 0, a.stream, a.s, blocks, part_p, part_c, part_n,
-                    a.counts, a.loss, a.n);
+  return launch_pdl(route_join_kernel, static_cast<unsigned>(ceil_div(a.s.E, 32)), 32 * kJoinWarps, 0, a.stream, a.s, blocks,
+                    part_p, part_c, part_n, joined, part_loss, a.counts, a.loss, a.n);
 }
 
 template <typename T, int kPer, int kV>
@@ -594,8 +609,6 @@ int check_route_shape(int dtype, int64_t tokens, int32_t experts, int32_t k, int
   return MXQ_OK;
 }
 
-constexpr int kMaxBlocks = 256;  // partial sums held in the workspace
-
 }  // namespace
 
 namespace mxq {
@@ -607,7 +620,8 @@ int route_status_read(unsigned int* out, bool clear) {
 extern "C" int64_t mxq_moe_route_workspace(int64_t tokens, int32_t experts) {
   if (tokens < 0 || tokens > INT32_MAX || experts < 1 || experts > MXQ_MAX_GROUPS) return MXQ_EBADSHAPE;
   const int64_t blocks = ceil_div(tokens, warps_for(experts));
-  return blocks <= 1 ? 0 : (static_cast<int64_t>(experts) * 8 + 4) * (blocks < kMaxBlocks ? blocks : kMaxBlocks);
+  // per block the experts' sums and counts and the routed tokens; the join's counter and losses
+  return blocks <= 1 ? 0 : (static_cast<int64_t>(experts) * 8 + 4) * (blocks < kMaxBlocks ? blocks : kMaxBlocks) + 4 * (1 + kMaxJoins);
 }
 
 extern "C" int mxq_moe_route(const void* logits, int dtype, int64_t tokens, int32_t experts, int64_t ld, int32_t k,

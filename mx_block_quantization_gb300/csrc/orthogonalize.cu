@@ -38,6 +38,14 @@
 // columns let the epilogue of a tile run under the next tile's products.  The
 // grid is persistent, one CTA pair per two SMs.  Ragged edges are the tensor
 // maps': loads fill with zero, stores are clipped.
+//
+// Bound: by the way of the operands from L2, 64 KB a stage and pair at about 55
+// bytes a clock and SM, where a stage's MMAs take 512 clocks and its loads 590 or
+// more.  4096x8192 in five steps: 1.63 ms, 1.48 PFLOP/s of the products' one
+// triangle, the tensor pipe active 69 to 75% (1.19 ms with the loads left out, 1.39
+// with the MMAs left out).  64 matrices of 1024x512: 443 us, 0.68 PFLOP/s: 192 and
+// 512 tiles on 76 pairs leave part of the last round idle, and each of 17 launches
+// begins and ends alone.  One small matrix: 4 to 6 us a launch.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -689,9 +697,9 @@ constexpr int64_t kSplitSide = 64;
 // Slices of K for the gram matrix: where its tiles are few and K is long, the CTA
 // pairs left over take slices of K, and a further launch adds the slices up.
 // A stage takes a pair 0.3 us, a slice's sums pass through L2 twice at 4 TB/s, and
-// the further launch costs 5 us (64x8192: 671 us with one slice, 140 with 64;
-// 512x8192: a few slices; 1000x2000: 224 us with one, 282 with five).  Returns 0
-// for one slice.  Sized for the pairs of the whole GPU, whatever it has.
+// the further launch costs 5 us (64x8192: 661 us with one slice, 128 with 64, the
+// choice here; 512x8192: 321 and 212; 300x5000: 236 and 154; 1000x2000: 209 us with
+// one, the choice, and 234 with two).  Returns 0 for one slice.  Sized for the pairs of the whole GPU, whatever it has.
 constexpr int64_t kPairs = 76, kSliceStages = 6;
 int64_t gram_slices(int64_t batch, int64_t side, int64_t length) {
   const int64_t tiles_m = ceil_div(side, kTile), tiles = batch * tiles_m * (tiles_m + 1) / 2;

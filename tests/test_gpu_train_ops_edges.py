@@ -165,3 +165,20 @@ def test_masks_of_the_lowest_value(kind):
     np.testing.assert_allclose(r.weights[1:].cpu().numpy(), 1 / 70, rtol=2.0**-20)
     d = mxq.moe_route_backward(x, r, torch.ones(3, 3, device="cuda"), torch.tensor(1.0, device="cuda"), renorm=False)
     assert d.isfinite().all()
+
+
+@pytest.mark.parametrize("batch,m,n,pad", [
+    (1, 5, 9, 0), (3, 64, 40, 0), (1, 64, 8192, 0), (2, 65, 130, 0), (1, 300, 520, 4), (4, 600, 257, 0), (1, 200, 7000, 0),
+])
+def test_coefficients_without_a_square_to_complete(batch, m, n, pad):
+    """c zero, and b much larger than c: the polynomial adds b A from memory."""
+    g = momentum(batch, m, n, pad=pad)
+    for co in ((1.5, -0.5, 0.0), (1.6, -0.65, 0.05)):
+        assert off(mxq.orthogonalize(g, coefficients=co), iteration(g, coefficients=co)) <= BOUND
+
+
+def test_coefficients_without_a_polynomial():
+    """b = c = 0 only scales: five times a."""
+    g = momentum(1, 90, 150)[0]
+    want = g.double().cpu() / g.double().cpu().norm() * 1.125**5
+    assert off(mxq.orthogonalize(g, coefficients=(1.125, 0.0, 0.0), eps=0.0), want) <= BOUND

@@ -29,7 +29,6 @@ __device__ unsigned int g_exchange_status = 0;
 constexpr int kGroupRows = 128;
 constexpr int kMaxK = 32;
 constexpr int kThreads = 256;
-constexpr int kFillRows = 8;  // rows looked at by a block that zeroes unused rows
 
 // ---------------------------------------------------------------------------
 // plan
@@ -103,24 +102,53 @@ struct ExchangeShape {
   int64_t tokens, M, D;
   int64_t ldt, ldm;  // elements between the rows of the token matrix and of the group matrix
   int k, tx;         // tx: threads per token (a power of two)
+  int fill;          // rows that a block looks at to zero unused ones
 };
 
-// Zeroes those of kFillRows rows that no assignment fills.
+// The part of the 16-byte unit u of `bytes` bytes at `to` (counted from the last
+// 16-byte boundary at or before it) that lies within them: from its offset `start`,
+// whole if it can be written by one access.
+struct Unit {
+  int64_t start;
+  bool whole;
+};
+__device__ __forceinline__ Unit unit_of(int64_t u, int misaligned, int64_t bytes) {
+  const int64_t start = 16 * u - misaligned;
+  return {start, start >= 0 && start + 16 <= bytes};
+}
+__device__ __forceinline__ int misalignment(const void* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u); }
+
+// Rows looked at by a block that zeroes unused rows: 8, whose columns its threads
+// share, or 256 where rows are narrow and many, 32 for each warp (800000 rows of 64
+// bf16: 26 us for the dispatch, 96 with 8; 36000 of 1001: 29, and 33 with 32; 2000
+// of 7: 3.2, and 5.7 with 256).
+constexpr int kFewRows = 8, kManyRows = kThreads;
+inline int fill_rows(const ExchangeShape& s, int esize) {
+  return s.D * esize <= 1024 && s.M >= 128 * kManyRows ? kManyRows : kFewRows;
+}
+
+// Zeroes those of a block's rows that no assignment fills.  The rows' assignments
+// are read at once, a row a lane.
 template <typename T, int kV>
 __device__ void zero_unused(const ExchangeShape& s, const int32_t* source, T* rows, int64_t block) {
   const int64_t nv = s.D / kV;
   const uint64_t bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
-  for (int r = 0; r < kFillRows; ++r) {
-    const int64_t m = block * kFillRows + r;
-    if (m >= s.M) return;
-    if (source[m] >= 0) continue;
-    for (int64_t c = threadIdx.x; c < nv; c += kThreads)
-      if (in_buf(rows + m * s.ldm + c * kV, kV * sizeof(T), rows, bytes, &g_exchange_status))
-        *reinterpret_cast<Vec<T, kV>*>(rows + m * s.ldm + c * kV) = Vec<T, kV>{};
+  const bool narrow = s.fill == kManyRows;
+  const int lane = threadIdx.x & 31, first = narrow ? lane : threadIdx.x, step = narrow ? 32 : kThreads;
+  const int64_t m0 = block * s.fill + (narrow ? threadIdx.x & ~31u : 0u);
+  uint32_t unused = __ballot_sync(0xFFFFFFFFu, (narrow || lane < kFewRows) && m0 + lane < s.M && source[m0 + lane] < 0);
+  for (; unused != 0u; unused &= unused - 1) {
+    T* row = rows + (m0 + __ffs(unused) - 1) * s.ldm;
+    for (int64_t c = first; c < nv; c += step)
+      if (in_buf(row + c * kV, kV * sizeof(T), rows, bytes, &g_exchange_status))
+        *reinterpret_cast<Vec<T, kV>*>(row + c * kV) = Vec<T, kV>{};
   }
 }
 
-template <typename T, int kV>
+// kJ slots are read at once, before the columns: one by one each would wait for
+// the one before.  kMore: there may be more of them.  7168 tokens of 7168 bf16, k 8:
+// 160 us, 6.5 TB/s.
+template <typename T, int kV, int kJ, bool kMore>
 __global__ void __launch_bounds__(kThreads)
     dispatch_kernel(const T* __restrict__ x, const ExchangeShape s, const int32_t* __restrict__ slots,
                     const int32_t* __restrict__ source, T* __restrict__ rows, int64_t token_blocks) {
@@ -135,17 +163,112 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t nv = s.D / kV;
   const uint64_t bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
   bool bad = false;
+  int32_t first[kJ];
+  const auto read = [&](int j0, int32_t (&m)[kJ]) {
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) m[j] = j0 + j < s.k ? slots[t * s.k + j0 + j] : -1;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      if (m[j] >= s.M || m[j] < -1) bad = true;
+      if (m[j] >= s.M) m[j] = -1;
+    }
+  };
+  const auto write = [&](const int32_t (&m)[kJ], const Vec<T, kV>& v, int64_t c) {
+#pragma unroll
+    for (int j = 0; j < kJ; ++j)
+      if (m[j] >= 0 && in_buf(rows + m[j] * s.ldm + c * kV, kV * sizeof(T), rows, bytes, &g_exchange_status))
+        *reinterpret_cast<Vec<T, kV>*>(rows + m[j] * s.ldm + c * kV) = v;
+  };
+  read(0, first);
   for (int64_t c = threadIdx.x % s.tx; c < nv; c += s.tx) {
     const Vec<T, kV> v = load_once<T, kV>(x + t * s.ldt + c * kV);
-    for (int j = 0; j < s.k; ++j) {
-      const int64_t m = slots[t * s.k + j];
-      const bool live = m >= 0 && m < s.M;
-      bad |= !live && m != -1;
-      if (live && in_buf(rows + m * s.ldm + c * kV, kV * sizeof(T), rows, bytes, &g_exchange_status))
-        *reinterpret_cast<Vec<T, kV>*>(rows + m * s.ldm + c * kV) = v;
+    write(first, v, c);
+    for (int j0 = kJ; kMore && j0 < s.k; j0 += kJ) {
+      int32_t m[kJ];
+      read(j0, m);
+      write(m, v, c);
     }
   }
   if (bad) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
+}
+
+constexpr int kUnits = 4;  // 16-byte units that a thread loads
+
+// Rows whose lengths, pitches or addresses allow narrow accesses only, kIn elements
+// of x at a time.  A token's elements are staged in shared memory and written from
+// there in whole 16-byte units of each row, wherever it begins (36000 rows of 1001
+// bf16: 32 us, 62 with 2-byte stores; 40000 rows of 1001 fp32: 57 and 83; 32768 of
+// 4098 bf16: 65 and 93).  Where rows can begin at any 2 bytes a second copy, 2 bytes
+// further on, makes every unit begin at a word of the one or the other.
+template <typename T, int kIn>
+__global__ void __launch_bounds__(kThreads)
+    dispatch_narrow_kernel(const T* __restrict__ x, const ExchangeShape s, const int32_t* __restrict__ slots,
+                           const int32_t* __restrict__ source, T* __restrict__ rows, int64_t token_blocks, int tiles, int tile) {
+  constexpr bool kTwo = sizeof(T) * kIn == 2;
+  constexpr int kLoads = kUnits * 16 / (sizeof(T) * kIn);
+  // a group of tx threads stages kUnits * 16 * tx bytes and a word
+  __shared__ uint32_t stage[kTwo ? 2 : 1][kThreads * kUnits * 4 + kThreads / 8];
+  pdl_wait();
+  if (static_cast<int64_t>(blockIdx.x) >= token_blocks) {
+    zero_unused<T, kIn>(s, source, rows, blockIdx.x - token_blocks);
+    return;
+  }
+  const int group = threadIdx.x / s.tx, own = threadIdx.x % s.tx;
+  const int64_t t = static_cast<int64_t>(blockIdx.x / tiles) * (kThreads / s.tx) + group;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x % tiles) * tile;
+  const int n = t < s.tokens ? static_cast<int>(min(static_cast<int64_t>(tile), s.D - c0)) : 0;
+  T* even = reinterpret_cast<T*>(stage[0] + group * (4 * kUnits * s.tx + 1));
+  T* odd = reinterpret_cast<T*>(stage[kTwo ? 1 : 0] + group * (4 * kUnits * s.tx + 1)) + 1;  // one element further on
+  Vec<T, kIn> v[kLoads];
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldt + s.D) * sizeof(T);
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    const int i = (q * s.tx + own) * kIn;
+    const T* p = x + t * s.ldt + c0 + i;
+    v[q] = load_if<T, kIn>(p, i < n && in_buf(p, sizeof v[q], x, in_bytes, &g_exchange_status));
+  }
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    const int i = (q * s.tx + own) * kIn;
+    if (i >= n) continue;
+#pragma unroll
+    for (int e = 0; e < kIn; ++e) even[i + e] = v[q].v[e];
+    if (kTwo) odd[i] = v[q].v[0];
+  }
+  __syncthreads();
+  const uint64_t out_bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
+  const int bytes = n * static_cast<int>(sizeof(T)), turn = threadIdx.x >> 3 & 3;
+  bool bad = false;
+  for (int j = 0; n > 0 && j < s.k; ++j) {
+    const int64_t m = slots[t * s.k + j];
+    if (m < 0 || m >= s.M) {
+      bad |= m != -1;
+      continue;
+    }
+    uint8_t* row = reinterpret_cast<uint8_t*>(rows + m * s.ldm + c0);
+    const int mis = misalignment(row);
+    const T* from = kTwo && (mis & 2) != 0 ? odd : even;
+    for (int u = own; u < (bytes + mis + 15) / 16; u += s.tx) {
+      const Unit at = unit_of(u, mis, bytes);
+      const int start = static_cast<int>(at.start);
+      if (at.whole) {
+        // four words, every eight lanes in another order: no two in one bank
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(from) + start);
+        uint32_t a = w[turn], b = w[(1 + turn) & 3], c = w[(2 + turn) & 3], d = w[(3 + turn) & 3];
+        if (turn & 1) {
+          const uint32_t last = d;
+          d = c, c = b, b = a, a = last;
+        }
+        const uint4 out = turn & 2 ? make_uint4(c, d, a, b) : make_uint4(a, b, c, d);
+        if (in_buf(row + start, 16, rows, out_bytes, &g_exchange_status)) *reinterpret_cast<uint4*>(row + start) = out;
+      } else {
+        for (int i = max(start, 0); i < min(start + 16, bytes); i += static_cast<int>(sizeof(T)))
+          if (in_buf(row + i, sizeof(T), rows, out_bytes, &g_exchange_status))
+            *reinterpret_cast<T*>(row + i) = even[i / static_cast<int>(sizeof(T))];
+      }
+    }
+  }
+  if (bad && own == 0) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
 }
 
 // The rows and weights of kJ choices of a token, from choice j0 on: loaded once,
@@ -169,14 +292,20 @@ struct Choices {
   }
 };
 
-// kJ choices and kU columns (kJ * kU = kAtOnce row pieces) are loaded before the
-// first is used: enough in flight for HBM with few choices as with many.  Four
+// kJ choices and kU columns (kJ * kU = combine_at_once row pieces) are loaded before
+// the first is used: enough in flight for HBM with few choices as with many, and
+// more of narrow pieces (30021 rows of 2050 fp32, 16 against 8: 54 us and 59; 36000
+// rows of 1001 bf16: 26 and 29; 8 choices of 7164 bf16 lack the registers: 173 and
+// 158).  Four
 // blocks of 256 threads on a multiprocessor (64 registers) and 64 threads a token
 // read fastest: 57344 rows of 7168 bf16 in 140 us (6.6 TB/s); 157 with six blocks,
 // 234 with 32 threads a token, and 52 us against 28 with 256 threads a token at
 // 32768 rows of 2048.  With the choices read inside the column loop the loads
 // went one by one (462 us).
-constexpr int kAtOnce = 8;
+template <typename T, int kV, int kJ>
+__host__ __device__ constexpr int combine_at_once() {
+  return sizeof(T) * kV == 16 || (sizeof(T) * kV == 8 && kJ == 8) ? 8 : 16;
+}
 constexpr int kCombineBlocks = 4;
 
 // kMore: there may be more than kJ choices.
@@ -185,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, kCombineBlocks)
     combine_kernel(const T* __restrict__ rows, const ExchangeShape s, const int32_t* __restrict__ slots,
                    const float* __restrict__ weights, T* __restrict__ y) {
   pdl_wait();
-  constexpr int kU = kAtOnce / kJ;
+  constexpr int kU = combine_at_once<T, kV, kJ>() / kJ;
   const int ty = kThreads / s.tx;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * ty + threadIdx.x / s.tx;
   if (t >= s.tokens) return;
@@ -339,20 +468,47 @@ struct RowsCall {
   cudaStream_t stream;
 };
 
+// 8-byte accesses are staged for long rows with many copies only (60000 rows of
+// 2050 fp32, direct and staged: 216 and 240 us with one choice, 117 and 108 with
+// eight; of 514 fp32, 200000 rows: 113 and 122 with eight).
 template <typename T, int kV>
-int launch_dispatch(const RowsCall& a) {
-  const int64_t token_blocks = ceil_div(a.s.tokens, kThreads / a.s.tx);
-  const int64_t blocks = token_blocks + ceil_div(a.s.M, kFillRows);
-  return launch_pdl(dispatch_kernel<T, kV>, static_cast<unsigned>(blocks), kThreads, 0, a.stream,
-                    static_cast<const T*>(a.in), a.s, a.slots, a.source, static_cast<T*>(a.out), token_blocks);
+int launch_dispatch(RowsCall a) {
+  const int64_t fill_blocks = ceil_div(a.s.M, a.s.fill);
+  const int64_t bytes = a.s.D * sizeof(T);
+  if constexpr (sizeof(T) * kV >= 8) {
+    if (sizeof(T) * kV == 16 || a.s.k < 8 || bytes < 4096) {
+      const int64_t token_blocks = ceil_div(a.s.tokens, kThreads / a.s.tx);
+      const auto kernel = a.s.k <= 2   ? dispatch_kernel<T, kV, 2, false>
+                          : a.s.k <= 4 ? dispatch_kernel<T, kV, 4, false>
+                          : a.s.k <= 8 ? dispatch_kernel<T, kV, 8, false>
+                                       : dispatch_kernel<T, kV, 8, true>;
+      return launch_pdl(kernel, static_cast<unsigned>(token_blocks + fill_blocks), kThreads, 0, a.stream,
+                        static_cast<const T*>(a.in), a.s, a.slots, a.source, static_cast<T*>(a.out), token_blocks);
+    }
+  }
+  if constexpr (sizeof(T) * kV < 16) {
+    // threads for a row's units, and a unit less for where it begins; longer rows
+    // in equal tiles
+    a.s.tx = 8;
+    while (a.s.tx < kThreads && 16 * kUnits * a.s.tx - 16 < bytes) a.s.tx *= 2;
+    const int64_t tiles = ceil_div(bytes, 16 * kUnits * a.s.tx - 16);
+    const int64_t tile = ceil_div(ceil_div(a.s.D, kV), tiles) * kV, token_blocks = ceil_div(a.s.tokens, kThreads / a.s.tx) * tiles;
+    return launch_pdl(dispatch_narrow_kernel<T, kV>, static_cast<unsigned>(token_blocks + fill_blocks), kThreads, 0, a.stream,
+                      static_cast<const T*>(a.in), a.s, a.slots, a.source, static_cast<T*>(a.out), token_blocks,
+                      static_cast<int>(tiles), static_cast<int>(tile));
+  }
 }
 // Choices handled at once: 2, 4 or 8, the smallest that holds k.
 template <typename T, int kV, int kJ, bool kMore>
 int launch_combine(RowsCall a) {
-  // 64 threads a token, more where the tokens are too few to fill the GPU
+  // 64 threads a token, fewer for rows that have no columns for them (50000 tokens
+  // of 35 fp32: 26 us with 64, 10 with 16), more where the tokens are too few to
+  // fill the GPU
+  constexpr int kU = combine_at_once<T, kV, kJ>() / kJ;
+  const int64_t nv = a.s.D / kV;
   const int64_t fill = static_cast<int64_t>(a.sms) * kCombineBlocks * kThreads;
   int tx = 8;
-  while (tx < a.s.tx && (tx < 64 || tx * a.s.tokens < fill)) tx *= 2;
+  while (tx < a.s.tx && ((tx < 64 && tx * kU < nv) || tx * a.s.tokens < fill)) tx *= 2;
   a.s.tx = tx;
   return launch_pdl(combine_kernel<T, kV, kJ, kMore>, static_cast<unsigned>(ceil_div(a.s.tokens, kThreads / tx)), kThreads,
                     0, a.stream, static_cast<const T*>(a.in), a.s, a.slots, a.weights, static_cast<T*>(a.out));
@@ -367,7 +523,7 @@ int launch_combine(const RowsCall& a) {
 template <typename T, int kV, int kJ, int kWarps>
 int launch_combine_backward(const RowsCall& a) {
   const int64_t token_blocks = ceil_div(a.s.tokens, kThreads / 32 / kWarps);
-  const int64_t blocks = token_blocks + ceil_div(a.s.M, kFillRows);
+  const int64_t blocks = token_blocks + ceil_div(a.s.M, a.s.fill);
   return launch_pdl(combine_backward_kernel<T, kV, kJ, kWarps>, static_cast<unsigned>(blocks), kThreads, 0, a.stream,
                     static_cast<const T*>(a.in2), static_cast<const T*>(a.in), a.s, a.ldr, a.slots, a.source, a.weights,
                     static_cast<T*>(a.out), a.dweights, token_blocks);
@@ -393,6 +549,7 @@ int launch_rows(RowsCall a) {
   int tx = 8;
   while (tx < kThreads && tx < nv) tx *= 2;
   a.s.tx = tx;
+  a.s.fill = fill_rows(a.s, sizeof(T));
   if constexpr (kWhat == Rows::kDispatch) return launch_dispatch<T, kV>(a);
   if constexpr (kWhat == Rows::kCombine) return launch_combine<T, kV>(a);
   return launch_combine_backward<T, kV>(a);
@@ -487,7 +644,7 @@ extern "C" int mxq_moe_dispatch(const void* x, int dtype, int64_t tokens, int64_
   RowsCall a = {};
   a.dtype = dtype;
   a.in = x;
-  a.s = {tokens, M, D, ldx, ldr, k, 0};
+  a.s = {tokens, M, D, ldx, ldr, k, 0, 0};
   a.slots = slots;
   a.source = source;
   a.out = rows;
@@ -511,7 +668,7 @@ extern "C" int mxq_moe_combine(const void* rows, int dtype, int64_t M, int64_t D
   RowsCall a = {};
   a.dtype = dtype;
   a.in = rows;
-  a.s = {tokens, M, D, ldy, ldr, k, 0};
+  a.s = {tokens, M, D, ldy, ldr, k, 0, 0};
   a.slots = slots;
   a.weights = weights;
   a.out = y;
@@ -545,7 +702,7 @@ extern "C" int mxq_moe_combine_backward(const void* dy, int dtype, int64_t token
   a.dtype = dtype;
   a.in = rows;
   a.in2 = dy;
-  a.s = {tokens, M, D, ldy, ldd, k, 0};
+  a.s = {tokens, M, D, ldy, ldd, k, 0, 0};
   a.ldr = ldr;
   a.slots = slots;
   a.source = source;

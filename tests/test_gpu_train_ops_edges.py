@@ -182,3 +182,25 @@ def test_coefficients_without_a_polynomial():
     g = momentum(1, 90, 150)[0]
     want = g.double().cpu() / g.double().cpu().norm() * 1.125**5
     assert off(mxq.orthogonalize(g, coefficients=(1.125, 0.0, 0.0), eps=0.0), want) <= BOUND
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,D,E,k", [
+    (5, 1, 3, 2), (200, 3, 4, 1), (33, 31, 5, 3), (40, 63, 5, 8), (70, 129, 3, 2), (64, 1023, 6, 8), (20, 4089, 4, 2),
+    (9, 8183, 3, 3), (7, 16377, 2, 2), (6, 20001, 3, 1), (30, 2050, 9, 8), (30, 4100, 9, 9), (12, 8202, 4, 8),
+])
+@pytest.mark.parametrize("shift,pad", [(0, 0), (1, 1), (3, 6)])
+def test_dispatched_rows_at_any_address(T, D, E, k, shift, pad, kind):
+    """Rows that begin anywhere: equal bits inside, nothing written outside."""
+    k = min(k, E)
+    plan, _, source = check_plan(routing(T, E, k), E)
+    M = source.size
+    x = torch.randn(T, D + pad + shift, generator=torch.Generator().manual_seed(D)).to(kind).cuda()[:, shift:shift + D]
+    room = torch.full((M * (D + pad) + shift + 8,), 7.0, dtype=kind, device="cuda")
+    rows = room[shift:shift + M * (D + pad)].view(M, D + pad)
+    mxq.moe_dispatch(x, plan, out=rows[:, :D])
+    want = torch.zeros(M, D, dtype=kind, device="cuda")
+    live = torch.from_numpy(np.flatnonzero(source >= 0)).cuda()
+    want[live] = x[torch.from_numpy(source[source >= 0] // k).cuda()]
+    assert torch.equal(rows[:, :D], want)
+    assert (rows[:, D:] == 7).all() and (room[:shift] == 7).all() and (room[shift + M * (D + pad):] == 7).all()

@@ -34,35 +34,101 @@ constexpr int kDigitBits = 10;     // at most kRankMaxBins bins
 // ---------------------------------------------------------------------------
 // lookup
 // ---------------------------------------------------------------------------
+constexpr int64_t kFullGpu = 262144;  // threads that the GPU has at work, or nearly
 struct LookupShape {
   int64_t tokens, rows, D, ldw, ldy;
   int tx;
 };
 
-template <typename I, typename T, typename U, int kV>
+// Bound by DRAM where tokens are many: both the ids and the rows are waited for, so
+// a group of threads reads the ids of kTokens tokens and then has a column vector of
+// each row in flight.  Four tokens a group of at most 64 threads, and one token with
+// as many threads as it has columns for: 65536 tokens of 2048 fp32 to bf16 119 us and
+// 140, 16384 of 7168 bf16 74 and 86, 10^6 of 16 fp32 14 and 41, 65536 of 4096 bf16
+// 161 and 158 (6.7 TB/s); with eight tokens 125, 72, 17 and 233.
+template <typename I, typename T, typename U, int kV, int kTokens>
 __global__ void __launch_bounds__(kThreads)
     lookup_kernel(const I* __restrict__ ids, const T* __restrict__ table, const LookupShape s, float scale,
                   U* __restrict__ y) {
   pdl_wait();
-  const int ty = kThreads / s.tx;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * ty + threadIdx.x / s.tx;
-  if (t >= s.tokens) return;
-  const int64_t id = ids[t];
-  const bool live = id >= 0 && id < s.rows;
-  if (!live) atomicOr(&g_embedding_status, MXQ_DEV_BADINDEX);
+  const int groups = kThreads / s.tx;
+  // the groups' tokens take turns, so that a block's stores lie side by side
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * groups * kTokens + threadIdx.x / s.tx;
+  const T* row[kTokens];
+  bool live[kTokens];
+  int64_t id[kTokens];
+#pragma unroll
+  for (int k = 0; k < kTokens; ++k) id[k] = t0 + k * groups < s.tokens ? static_cast<int64_t>(ids[t0 + k * groups]) : 0;
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < kTokens; ++k) {
+    live[k] = t0 + k * groups < s.tokens && id[k] >= 0 && id[k] < s.rows;
+    bad |= t0 + k * groups < s.tokens && !live[k];
+    row[k] = table + (live[k] ? id[k] * s.ldw : 0);
+  }
+  if (bad) atomicOr(&g_embedding_status, MXQ_DEV_BADINDEX);
   const int64_t nv = s.D / kV;
   const uint64_t in_bytes = (static_cast<uint64_t>(s.rows - 1) * s.ldw + s.D) * sizeof(T);
   const uint64_t out_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldy + s.D) * sizeof(U);
   for (int64_t c = threadIdx.x % s.tx; c < nv; c += s.tx) {
-    Vec<T, kV> v = {};
-    if (live && in_buf(table + id * s.ldw + c * kV, sizeof v, table, in_bytes, &g_embedding_status))
-      v = *reinterpret_cast<const Vec<T, kV>*>(table + id * s.ldw + c * kV);
-    Vec<U, kV> out;
+    Vec<T, kV> v[kTokens];
 #pragma unroll
-    for (int i = 0; i < kV; ++i) out.v[i] = live ? narrow<U>(scale * widen(v.v[i])) : U{};
-    if (in_buf(y + t * s.ldy + c * kV, sizeof out, y, out_bytes, &g_embedding_status))
-      *reinterpret_cast<Vec<U, kV>*>(y + t * s.ldy + c * kV) = out;
+    for (int k = 0; k < kTokens; ++k)
+      v[k] = load_if<T, kV>(row[k] + c * kV, live[k] && in_buf(row[k] + c * kV, sizeof v[k], table, in_bytes, &g_embedding_status));
+#pragma unroll
+    for (int k = 0; k < kTokens; ++k) {
+      Vec<U, kV> out;
+#pragma unroll
+      for (int i = 0; i < kV; ++i) out.v[i] = live[k] ? narrow<U>(scale * widen(v[k].v[i])) : U{};
+      U* to = y + (t0 + k * groups) * s.ldy + c * kV;
+      if (t0 + k * groups < s.tokens && in_buf(to, sizeof out, y, out_bytes, &g_embedding_status)) *reinterpret_cast<Vec<U, kV>*>(to) = out;
+    }
   }
+}
+
+// Rows whose lengths, pitches or addresses allow accesses of 4 bytes or less of y,
+// kIn elements at a time: staged as y's, and written in 16-byte units (65536 tokens
+// of 1001 bf16 76 us, 136 with 2-byte stores; of 1001 fp32 to bf16 79 and 146; of 33
+// fp32 10 and 15).  Not for rows of few bytes: most of a group would have nothing to do.
+template <typename I, typename T, typename U, int kIn>
+__global__ void __launch_bounds__(kThreads)
+    lookup_narrow_kernel(const I* __restrict__ ids, const T* __restrict__ table, const LookupShape s, float scale,
+                         U* __restrict__ y, int tiles, int tile) {
+  constexpr bool kTwo = sizeof(U) * kIn == 2;
+  constexpr int kLoads = kUnits * 16 / (sizeof(U) * kIn);
+  __shared__ uint32_t stage[kTwo ? 2 : 1][kThreads * kUnits * 4 + kThreads / 8];
+  pdl_wait();
+  const int group = threadIdx.x / s.tx, own = threadIdx.x % s.tx;
+  const int64_t t = static_cast<int64_t>(blockIdx.x / tiles) * (kThreads / s.tx) + group;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x % tiles) * tile;
+  const int n = t < s.tokens ? static_cast<int>(min(static_cast<int64_t>(tile), s.D - c0)) : 0;
+  const int64_t id = n > 0 ? static_cast<int64_t>(ids[t]) : -1;
+  const bool live = id >= 0 && id < s.rows;
+  if (n > 0 && !live && own == 0) atomicOr(&g_embedding_status, MXQ_DEV_BADINDEX);
+  const T* row = table + (live ? id * s.ldw + c0 : 0);
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.rows - 1) * s.ldw + s.D) * sizeof(T);
+  const uint64_t out_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldy + s.D) * sizeof(U);
+  U* even = reinterpret_cast<U*>(stage[0] + group * (4 * kUnits * s.tx + 1));
+  U* odd = reinterpret_cast<U*>(stage[kTwo ? 1 : 0] + group * (4 * kUnits * s.tx + 1)) + 1;  // one element further on
+  Vec<T, kIn> v[kLoads];
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    const T* p = row + (q * s.tx + own) * kIn;
+    v[q] = load_if<T, kIn>(p, live && (q * s.tx + own) * kIn < n && in_buf(p, sizeof v[q], table, in_bytes, &g_embedding_status));
+  }
+#pragma unroll
+  for (int q = 0; q < kLoads; ++q) {
+    const int i = (q * s.tx + own) * kIn;
+    if (i >= n) continue;
+#pragma unroll
+    for (int e = 0; e < kIn; ++e) even[i + e] = live ? narrow<U>(scale * widen(v[q].v[e])) : U{};
+    if (kTwo) odd[i] = even[i];
+  }
+  __syncthreads();
+  if (n > 0)
+    write_staged<U, kTwo>(even, odd, y + t * s.ldy + c0, n, own, s.tx, [&](const void* at, int size) {
+      return in_buf(at, size, y, out_bytes, &g_embedding_status);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -565,10 +631,29 @@ struct LookupCall {
 };
 template <typename I, typename T, typename U, int kV>
 int launch_lookup(LookupCall a) {
-  a.s.tx = threads_per_row(a.s.D / kV);
-  return launch_pdl(lookup_kernel<I, T, U, kV>, static_cast<unsigned>(ceil_div(a.s.tokens, kThreads / a.s.tx)), kThreads,
-                    0, a.stream, static_cast<const I*>(a.ids), static_cast<const T*>(a.table), a.s, a.scale,
-                    static_cast<U*>(a.y));
+  const I* ids = static_cast<const I*>(a.ids);
+  const T* table = static_cast<const T*>(a.table);
+  U* y = static_cast<U*>(a.y);
+  if constexpr (sizeof(U) * kV <= 4) {
+    if (a.s.D * sizeof(U) >= 64) {
+      const StagedTiles split = staged_tiles(a.s.D, sizeof(U), kV, kThreads);
+      a.s.tx = split.tx;
+      return launch_pdl(lookup_narrow_kernel<I, T, U, kV>,
+                        static_cast<unsigned>(ceil_div(a.s.tokens, kThreads / a.s.tx) * split.tiles), kThreads, 0, a.stream, ids,
+                        table, a.s, a.scale, y, split.tiles, split.tile);
+    }
+  }
+  const int64_t nv = a.s.D / kV;
+  a.s.tx = 1;
+  while (a.s.tx < 64 && a.s.tx < nv) a.s.tx *= 2;
+  const int64_t groups = kThreads / a.s.tx;
+  constexpr int kTokens = 4;
+  if (a.s.tokens * a.s.tx >= kTokens * kFullGpu)
+    return launch_pdl(lookup_kernel<I, T, U, kV, kTokens>, static_cast<unsigned>(ceil_div(a.s.tokens, groups * kTokens)), kThreads,
+                      0, a.stream, ids, table, a.s, a.scale, y);
+  a.s.tx = threads_per_row(nv);
+  return launch_pdl(lookup_kernel<I, T, U, kV, 1>, static_cast<unsigned>(ceil_div(a.s.tokens, kThreads / a.s.tx)), kThreads, 0,
+                    a.stream, ids, table, a.s, a.scale, y);
 }
 template <typename I, typename T, typename U>
 int lookup_vector(const LookupCall& a) {

@@ -105,19 +105,6 @@ struct ExchangeShape {
   int fill;          // rows that a block looks at to zero unused ones
 };
 
-// The part of the 16-byte unit u of `bytes` bytes at `to` (counted from the last
-// 16-byte boundary at or before it) that lies within them: from its offset `start`,
-// whole if it can be written by one access.
-struct Unit {
-  int64_t start;
-  bool whole;
-};
-__device__ __forceinline__ Unit unit_of(int64_t u, int misaligned, int64_t bytes) {
-  const int64_t start = 16 * u - misaligned;
-  return {start, start >= 0 && start + 16 <= bytes};
-}
-__device__ __forceinline__ int misalignment(const void* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) & 15u); }
-
 // Rows looked at by a block that zeroes unused rows: 8, whose columns its threads
 // share, or 256 where rows are narrow and many, 32 for each warp (800000 rows of 64
 // bf16: 26 us for the dispatch, 96 with 8; 36000 of 1001: 29, and 33 with 32; 2000
@@ -192,8 +179,6 @@ __global__ void __launch_bounds__(kThreads)
   if (bad) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
 }
 
-constexpr int kUnits = 4;  // 16-byte units that a thread loads
-
 // Rows whose lengths, pitches or addresses allow narrow accesses only, kIn elements
 // of x at a time.  A token's elements are staged in shared memory and written from
 // there in whole 16-byte units of each row, wherever it begins (36000 rows of 1001
@@ -206,7 +191,6 @@ __global__ void __launch_bounds__(kThreads)
                            const int32_t* __restrict__ source, T* __restrict__ rows, int64_t token_blocks, int tiles, int tile) {
   constexpr bool kTwo = sizeof(T) * kIn == 2;
   constexpr int kLoads = kUnits * 16 / (sizeof(T) * kIn);
-  // a group of tx threads stages kUnits * 16 * tx bytes and a word
   __shared__ uint32_t stage[kTwo ? 2 : 1][kThreads * kUnits * 4 + kThreads / 8];
   pdl_wait();
   if (static_cast<int64_t>(blockIdx.x) >= token_blocks) {
@@ -237,7 +221,6 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   const uint64_t out_bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
-  const int bytes = n * static_cast<int>(sizeof(T)), turn = threadIdx.x >> 3 & 3;
   bool bad = false;
   for (int j = 0; n > 0 && j < s.k; ++j) {
     const int64_t m = slots[t * s.k + j];
@@ -245,28 +228,10 @@ __global__ void __launch_bounds__(kThreads)
       bad |= m != -1;
       continue;
     }
-    uint8_t* row = reinterpret_cast<uint8_t*>(rows + m * s.ldm + c0);
-    const int mis = misalignment(row);
-    const T* from = kTwo && (mis & 2) != 0 ? odd : even;
-    for (int u = own; u < (bytes + mis + 15) / 16; u += s.tx) {
-      const Unit at = unit_of(u, mis, bytes);
-      const int start = static_cast<int>(at.start);
-      if (at.whole) {
-        // four words, every eight lanes in another order: no two in one bank
-        const uint32_t* w = reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint8_t*>(from) + start);
-        uint32_t a = w[turn], b = w[(1 + turn) & 3], c = w[(2 + turn) & 3], d = w[(3 + turn) & 3];
-        if (turn & 1) {
-          const uint32_t last = d;
-          d = c, c = b, b = a, a = last;
-        }
-        const uint4 out = turn & 2 ? make_uint4(c, d, a, b) : make_uint4(a, b, c, d);
-        if (in_buf(row + start, 16, rows, out_bytes, &g_exchange_status)) *reinterpret_cast<uint4*>(row + start) = out;
-      } else {
-        for (int i = max(start, 0); i < min(start + 16, bytes); i += static_cast<int>(sizeof(T)))
-          if (in_buf(row + i, sizeof(T), rows, out_bytes, &g_exchange_status))
-            *reinterpret_cast<T*>(row + i) = even[i / static_cast<int>(sizeof(T))];
-      }
-    }
+    T* row = rows + m * s.ldm + c0;
+    write_staged<T, kTwo>(even, odd, row, n, own, s.tx, [&](const void* at, int size) {
+      return in_buf(at, size, rows, out_bytes, &g_exchange_status);
+    });
   }
   if (bad && own == 0) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
 }
@@ -489,15 +454,12 @@ int launch_dispatch(RowsCall a) {
     }
   }
   if constexpr (sizeof(T) * kV < 16) {
-    // threads for a row's units, and a unit less for where it begins; longer rows
-    // in equal tiles
-    a.s.tx = 8;
-    while (a.s.tx < kThreads && 16 * kUnits * a.s.tx - 16 < bytes) a.s.tx *= 2;
-    const int64_t tiles = ceil_div(bytes, 16 * kUnits * a.s.tx - 16);
-    const int64_t tile = ceil_div(ceil_div(a.s.D, kV), tiles) * kV, token_blocks = ceil_div(a.s.tokens, kThreads / a.s.tx) * tiles;
+    const StagedTiles split = staged_tiles(a.s.D, sizeof(T), kV, kThreads);
+    a.s.tx = split.tx;
+    const int64_t token_blocks = ceil_div(a.s.tokens, kThreads / a.s.tx) * split.tiles;
     return launch_pdl(dispatch_narrow_kernel<T, kV>, static_cast<unsigned>(token_blocks + fill_blocks), kThreads, 0, a.stream,
                       static_cast<const T*>(a.in), a.s, a.slots, a.source, static_cast<T*>(a.out), token_blocks,
-                      static_cast<int>(tiles), static_cast<int>(tile));
+                      split.tiles, split.tile);
   }
 }
 // Choices handled at once: 2, 4 or 8, the smallest that holds k.

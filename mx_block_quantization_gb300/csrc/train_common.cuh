@@ -87,6 +87,58 @@ __device__ __forceinline__ Vec<T, kN> load_once(const T* p) {
   return load_if<T, kN>(p, true);
 }
 
+// Rows that begin anywhere, written in whole 16-byte units out of shared memory.
+// A group of tx threads stages the elements of a row, or of a tile of one, at
+// `even` (4-byte aligned), at most kUnits units a thread; where rows can begin at any
+// 2 bytes also at `odd`, a second copy's base 2 bytes past a word, so that every unit
+// begins at a word of one of them.  A group takes kUnits * 16 * tx bytes and a word.
+constexpr int kUnits = 4;
+
+// Writes n staged elements to `row`, by thread `own` of the group's tx; may(address,
+// bytes) says whether an access is allowed.
+template <typename T, bool kTwo, typename May>
+__device__ __forceinline__ void write_staged(const T* even, const T* odd, T* row, int n, int own, int tx, const May& may) {
+  constexpr int kSize = static_cast<int>(sizeof(T));
+  const int bytes = n * kSize, turn = threadIdx.x >> 3 & 3;
+  const int before = static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u);  // bytes of the first unit before the row
+  uint8_t* to = reinterpret_cast<uint8_t*>(row);
+  const uint8_t* from = reinterpret_cast<const uint8_t*>(kTwo && (before & 2) != 0 ? odd : even);
+  for (int u = own; u < (bytes + before + 15) / 16; u += tx) {
+    const int start = 16 * u - before;
+    if (start >= 0 && start + 16 <= bytes) {
+      // four words, every eight lanes in another order: no two in one bank
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(from + start);
+      uint32_t a = w[turn], b = w[(1 + turn) & 3], c = w[(2 + turn) & 3], d = w[(3 + turn) & 3];
+      if (turn & 1) {
+        const uint32_t last = d;
+        d = c, c = b, b = a, a = last;
+      }
+      if (may(to + start, 16)) *reinterpret_cast<uint4*>(to + start) = turn & 2 ? make_uint4(c, d, a, b) : make_uint4(a, b, c, d);
+    } else {
+      const int end = start + 16 < bytes ? start + 16 : bytes;
+      for (int i = start > 0 ? start : 0; i < end; i += kSize)
+        if (may(to + i, kSize)) *reinterpret_cast<T*>(to + i) = even[i / kSize];
+    }
+  }
+}
+
+// Threads for a row's units, and a unit less for where it begins; longer rows in
+// equal tiles of whole accesses of kV elements.
+struct StagedTiles {
+  int tx, tiles, tile;  // tile: elements
+};
+inline StagedTiles staged_tiles(int64_t D, int esize, int kV, int threads) {
+  StagedTiles s;
+  const int64_t bytes = D * esize;
+  s.tx = 8;
+  while (s.tx < threads && 16 * kUnits * s.tx - 16 < bytes) s.tx *= 2;
+  const int64_t tiles = (bytes + 16 * kUnits * s.tx - 17) / (16 * kUnits * s.tx - 16);
+  const int64_t pieces = D / kV;
+  s.tiles = static_cast<int>(tiles);
+  s.tile = static_cast<int>((pieces + tiles - 1) / tiles * kV);
+  return s;
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);

@@ -204,3 +204,28 @@ def test_dispatched_rows_at_any_address(T, D, E, k, shift, pad, kind):
     want[live] = x[torch.from_numpy(source[source >= 0] // k).cuda()]
     assert torch.equal(rows[:, :D], want)
     assert (rows[:, D:] == 7).all() and (room[:shift] == 7).all() and (room[shift + M * (D + pad):] == 7).all()
+
+
+@pytest.mark.parametrize("types", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32")])
+@pytest.mark.parametrize("T,V,D", [
+    (300, 40, 33), (300, 40, 1001), (70, 9, 4097), (65, 9, 16411), (1, 5, 127), (70000, 50, 128), (70000, 50, 2), (20001, 50, 520),
+    (5000, 20, 2052), (90000, 60, 31),
+])
+@pytest.mark.parametrize("shift,pad", [(0, 0), (1, 2)])
+def test_looked_up_rows_at_any_address(T, V, D, shift, pad, types):
+    """Rows that begin anywhere, many tokens and few, ids out of range among them."""
+    a, b = ({"f32": torch.float32, "bf16": torch.bfloat16}[t] for t in types)
+    g = torch.Generator().manual_seed(T + D)
+    table = torch.randn(V, D + shift + pad, generator=g).to(a).cuda()[:, shift:shift + D]
+    ids = torch.randint(0, V, (T,), generator=g).cuda()
+    room = torch.full((T * (D + pad) + shift + 8,), 7.0, dtype=b, device="cuda")
+    rows = room[shift:shift + T * (D + pad)].view(T, D + pad)
+    mxq.embedding(ids, table, out=rows[:, :D])
+    assert torch.equal(rows[:, :D], table[ids].to(b))
+    assert (rows[:, D:] == 7).all() and (room[:shift] == 7).all() and (room[shift + T * (D + pad):] == 7).all()
+    ids[T // 2], ids[0] = V, -7
+    got = mxq.embedding(ids, table, dtype=b)
+    assert mxq.device_status(clear=True) == mxq.DEV_BADINDEX
+    want = table[ids.clamp(0, V - 1)].to(b)
+    want[T // 2], want[0] = 0, 0
+    assert torch.equal(got, want)

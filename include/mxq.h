@@ -401,7 +401,7 @@ int mxq_embedding_backward(const void *ids, int ids_bytes, int64_t tokens, const
  *   steps    1 .. 64; a, b, c finite; eps >= 0.  m, n at most 2^20, batch at
  *            most 65535.
  * The products take fp16 operands and accumulate in fp32 (tcgen05): an error of
- * about 1.5e-3 (Frobenius, of the result's norm) for five steps of the usual
+ * about 1e-3 (Frobenius, of the result's norm) for five steps of the usual
  * coefficients, beside the 1.7e-3 of the rounding to bf16; sides up to 64 carry
  * pairs of fp16 and are exact to the rounding.  The norm is fp32, its square
  * within fp32's range: |g| between 1e-19 and 1e19, beyond it out is 0 (or NaN

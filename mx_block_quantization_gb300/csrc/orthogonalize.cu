@@ -17,12 +17,18 @@
 // times 2^13, A and P times powers taken from the coefficients' bounds.
 //
 // The square is completed: with S = A + (b/2c) I, which the gram product's
-// epilogue stores in A's place, P = c S S + (a - b^2/4c) I.  So no epilogue reads
-// a second matrix (64 matrices of 1024x512: 501 us when the square read A and the
-// update X, both to put back what the rounding left of the diagonals, 468 without),
-// and S has the smaller diagonal to round.  The result's error before its own
-// rounding to bf16 (1.7e-3) is then 1.2e-3 to 1.5e-3.  Where b/2c is large or c is
-// zero (kCompletedSquare) the square adds b A from memory.
+// epilogue stores in A's place, P = c S S + (a - b^2/4c) I, and the square reads no
+// second matrix in its epilogue (64 matrices of 1024x512: 482 us, 501 with b A added
+// from memory).  Where b/2c is large or c is zero (kCompletedSquare) it does.
+//
+// The rounding that matters is that of the diagonals of S (or A) and P, which hold
+// most of their weight once the singular values draw together.  What fp16 leaves of
+// them is kept in fp32 vectors and put back: of S as the remainder of its squares,
+// onto the square's diagonal; of P as d X in the epilogue of P X = P'X + d X (and of
+// A, where it is added, as A'A' + d A' + A'd + d d).  The result's error before its
+// own rounding to bf16 (1.7e-3) is then 0.6e-3 to 1.1e-3, over square and long
+// matrices alike; without S's part up to 1.8e-3, without either up to 2.5e-3.
+// Putting back P's costs 2% with 1024x512 and 13% with 128x512.
 // The iteration's map of a singular value has slopes of up to 1.6 around 1, and
 // the value of a small matrix hangs on few roundings, so its error can reach 1%
 // (sides up to 16 in a simulation; 0.14% from a side of 48 on).  Sides of at
@@ -43,7 +49,7 @@
 // bytes a clock and SM, where a stage's MMAs take 512 clocks and its loads 590 or
 // more.  4096x8192 in five steps: 1.63 ms, 1.48 PFLOP/s of the products' one
 // triangle, the tensor pipe active 69 to 75% (1.19 ms with the loads left out, 1.39
-// with the MMAs left out).  64 matrices of 1024x512: 443 us, 0.68 PFLOP/s: 192 and
+// with the MMAs left out).  64 matrices of 1024x512 bf16: 457 us, 0.66 PFLOP/s: 192 and
 // 512 tiles on 76 pairs leave part of the last round idle, and each of 17 launches
 // begins and ends alone.  One small matrix: 4 to 6 us a launch.
 #include <cuda.h>
@@ -189,11 +195,17 @@ struct Product {
   int32_t ksteps;          // stages along K of one product
   int32_t tiles_m, tiles_n, tiles;  // tiles: all of the batch and of the slices
   int32_t slices, per_slice;        // K in slices of that many stages, each summed by itself
-  float* partial;                   // [slices, batch, rows, partial_ld] sums of the slices, or NULL
-  int64_t partial_stride, partial_ld;  // elements between the slices and the rows
+  float* partial;                   // [slices, batch, rows, d_ld] sums of the slices, or NULL
+  int64_t partial_stride;           // elements between the slices
   int32_t a_mn, b_mn;      // operand lies with K along its rows
-  // output = scale * acc + add_scale * addend, and + diagonal where row == column
+  // output = scale * acc + (add_scale + scale * (d[row] + d[column])) * addend
+  //          and where row == column, + diagonal + add_scale * d + scale * d * d
   float scale, add_scale, diagonal;
+  const float *d_row, *d_col;       // [batch, d_ld]: what the rounding left of a diagonal; NULL: zero
+  float* d_out;                     // the same of this output's diagonal, or NULL;
+  int32_t d_squares;                // of the squares of its diagonal instead
+  const float* square_rest;         // [batch, d_ld] such squares' remainders: times scale, onto the diagonal; or NULL
+  int64_t d_ld;
   // the last update writes bf16 to the caller's matrix
   bf16_t* out;             // NULL: fp16 through map d
   int64_t ldo, stride_o;
@@ -331,17 +343,22 @@ struct alignas(8) Barriers {
 };
 
 __device__ __forceinline__ float half_rounded(float v) { return __half2float(__float2half_rn(v)); }
+// What rounding to fp16 leaves of v, or of its square.
+__device__ __forceinline__ float diagonal_rest(float v, bool square) {
+  const float h = half_rounded(v);
+  return square ? (v - h) * (v + h) : v - h;
+}
 
 __device__ __forceinline__ void unpack8(const uint4 w, float (&v)[8]) {
   const float2 a = half2_values(w.x), b = half2_values(w.y), c = half2_values(w.z), d = half2_values(w.w);
   v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
 }
 
-// kSymmetric: one triangle of tiles, stored twice.  kAddends: parts of the addend
-// (of a symmetric product).  kBf16: the last update, to the caller's matrix.
-// kSplit: operands and results are pairs, three products.  kPartial: the sums of a
-// slice of K, in fp32.
-template <bool kSymmetric, int kAddends, bool kBf16, bool kSplit, bool kPartial>
+// kSymmetric: one triangle of tiles, stored twice.  kAddends: parts of the
+// addend.  kColumns: the columns' d_col multiplies it (d_row, where given, always
+// does).  kBf16: the last update, to the caller's matrix.  kSplit: operands and
+// results are pairs, three products.  kPartial: the sums of a slice of K, in fp32.
+template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit, bool kPartial>
 __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Product p) {
   extern __shared__ uint8_t raw[];
@@ -497,6 +514,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       const int64_t row0 = static_cast<int64_t>(at.i) * kTile + rank * kHalf + quarter * 32;
       const int64_t row = row0 + lane;
       const bool mirror = kSymmetric && at.i != at.j, both = needs_both(at) || kAddends == 2;
+      const float dr = p.d_row != nullptr && row < p.rows ? p.d_row[at.batch * p.d_ld + row] : 0.0f;
+      if (kColumns && lane < 4) {  // this warp's 128 columns, four lines
+        const int64_t col = static_cast<int64_t>(at.j) * kTile + 2 * (e >> 2) * kChunkCols + 32 * lane;
+        if (col < p.cols) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.d_col + at.batch * p.d_ld + col));
+      }
       ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(&bars.acc_full[acc]), (done >> 1) & 1, abort_flag,
                                                      &g_ortho_status, MXQ_DEV_TIMEOUT));
       if (!ok) break;
@@ -548,19 +570,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
         if (!inside) continue;
         const auto store_partial = [&] {
           if (!kPartial) return false;
-          float* to = p.partial + at.slice * p.partial_stride + (static_cast<int64_t>(at.batch) * p.rows + row) * p.partial_ld + col0;
+          float* to = p.partial + at.slice * p.partial_stride + (static_cast<int64_t>(at.batch) * p.rows + row) * p.d_ld + col0;
           if (row < p.rows)
 #pragma unroll
             for (int i = 0; i < 64; i += 4)
-              if (col0 + i < p.partial_ld)  // a multiple of 8
+              if (col0 + i < p.d_ld)  // a multiple of 8
                 *reinterpret_cast<uint4*>(to + i) =
                     make_uint4(raw[i / 32][i % 32], raw[i / 32][i % 32 + 1], raw[i / 32][i % 32 + 2], raw[i / 32][i % 32 + 3]);
           return true;
         };
         if (store_partial()) continue;
+        const float k0 = fmaf(p.scale, dr, p.add_scale);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // 32 columns at a time
           const int64_t col = col0 + 32 * h;
+          float4 dc[8];
+          if (kColumns) {
+            const float4* d = reinterpret_cast<const float4*>(p.d_col + at.batch * p.d_ld + col);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)  // d_ld is a multiple of 8
+              dc[q] = col + 4 * q < p.cols ? d[q] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
           float v[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[h][i]) * p.scale;
@@ -576,13 +606,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
                 for (int i = 0; i < 8; ++i) a[i] += l[i];
               }
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[8 * q + i] = fmaf(p.add_scale, a[i], v[8 * q + i]);
+              for (int i = 0; i < 8; ++i) {
+                const float4 d = dc[2 * q + i / 4];
+                const float k = kColumns ? fmaf(p.scale, i % 4 == 0 ? d.x : i % 4 == 1 ? d.y : i % 4 == 2 ? d.z : d.w, k0) : k0;
+                v[8 * q + i] = fmaf(k, a[i], v[8 * q + i]);
+              }
             }
           }
           if (kSymmetric && row0 < col + 32 && col < row0 + 32) {  // the warp's rows meet these columns
             const int own_column = static_cast<int>(row - col);
+            float on = p.diagonal + p.add_scale * dr + p.scale * dr * dr;
+            if (p.square_rest != nullptr && row < p.rows) on = fmaf(p.scale, p.square_rest[at.batch * p.d_ld + row], on);
+            float own = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] += i == own_column ? p.diagonal : 0.0f;
+            for (int i = 0; i < 32; ++i) {
+              v[i] += i == own_column ? on : 0.0f;
+              own = i == own_column ? v[i] : own;
+            }
+            if (!kSplit && p.d_out != nullptr && own_column >= 0 && own_column < 32 && row < p.rows)
+              p.d_out[at.batch * p.d_ld + row] = diagonal_rest(own, p.d_squares);
           }
           uint32_t w[16];
 #pragma unroll
@@ -617,7 +659,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
               bf16_t* to = out + (row0 + r) * p.ldo + col0 + i;
               if (col0 + i < p.cols && in_buf(to, 2, out, bytes, &g_ortho_status)) *to = value;
             }
-          __syncwarp();  // read before the next chunk is staged
+          fence_proxy_async_smem();  // read before the next addend comes in
+          __syncwarp();
           continue;
         }
         fence_proxy_async_smem();
@@ -632,9 +675,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       }
       if (ok && kAddends > 0 && t + step < p.tiles) {
         const TileAt next = tile_at<kSymmetric>(p, t + step);
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-        load_addends(next);
+        // the first chunk's store has been read once at most the second's is left
+        const bool second = (static_cast<int64_t>(at.j) * kTile + (2 * (e >> 2) + 1) * kChunkCols) < p.cols;
+        if (kSymmetric || kAddends == 2 || !second) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          load_addends(next);
+        } else {
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+          load_addend(0, 0, next, 0);
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          load_addend(1, 0, next, 1);
+        }
       }
     }
     for (int b = 0; b < 2; ++b)  // after a wait that ran out
@@ -663,7 +717,9 @@ struct Join {
   int64_t batch, side, ld, stride;
   int slices;
   float scale, diagonal;
-  __half *high, *low;  // low: or NULL
+  __half *high, *low;
+  float* d_out;  // or NULL
+  int32_t d_squares;
 };
 __global__ void __launch_bounds__(kThreads) join_kernel(const Join a) {
   pdl_wait();
@@ -680,7 +736,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Join a) {
   const uint64_t bytes = static_cast<uint64_t>(n) * 2;
   if (!in_buf(a.high + at, 2, a.high, bytes, &g_ortho_status)) return;
   a.high[at] = __float2half_rn(v);
-  if (a.low != nullptr) a.low[at] = __float2half_rn(v - h);
+  if (a.low != nullptr)
+    a.low[at] = __float2half_rn(v - h);
+  else if (i == j && a.d_out != nullptr)
+    a.d_out[row / a.side * a.ld + i] = diagonal_rest(v, a.d_squares);
 }
 
 // ---------------------------------------------------------------------------
@@ -688,8 +747,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Join a) {
 // ---------------------------------------------------------------------------
 // The square is completed where |b| is at most this many |c|, so that |b/2c| stays
 // within the bound of A: beyond it the rounding of S would be that of the shift.
-// (Completed and not: 16x16 70 and 80 us, 200 matrices of 128x512 205 and 224, 64
-// of 1024x512 470 and 483, 4096x8192 1646 and 1651.)
+// (Completed and not: 16x16 74 and 80 us, 200 matrices of 128x512 237 and 258, 64
+// of 1024x512 482 and 501, 4096x8192 1632 and 1644.)
 constexpr float kCompletedSquare = 4.0f;
 // Sides up to this carry pairs of fp16 (see the head of the file).
 constexpr int64_t kSplitSide = 64;
@@ -723,7 +782,7 @@ struct Layout {
   int parts;                         // 2 with low parts
   int64_t x[2][2];                   // X of the even and of the odd steps: high, low
   int64_t gram[2], poly[2];
-  int64_t sums, partial, bytes;
+  int64_t d_gram, d_poly, sums, partial, bytes;
 };
 Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   Layout l;
@@ -742,6 +801,8 @@ Layout layout_of(int64_t batch, int64_t m, int64_t n) {
     l.gram[q] = take(there ? sb : 0);
     l.poly[q] = take(there ? sb : 0);
   }
+  l.d_gram = take(up(batch * l.lds * 4, 256));
+  l.d_poly = take(up(batch * l.lds * 4, 256));
   l.sums = take(up(batch * kMaxParts * 4, 256));
   l.partial = take(up(gram_slices(batch, l.side, l.side == m ? n : m) * batch * l.side * l.lds * 4, 256));
   l.bytes = at;
@@ -767,7 +828,7 @@ bool encode_half(CUtensorMap* map, const Stack& t, uint32_t box_cols, uint32_t b
   return encode(map, t, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, box_cols, box_rows, swizzle);
 }
 
-template <bool kSymmetric, int kAddends, bool kBf16, bool kSplit, bool kPartial>
+template <bool kSymmetric, int kAddends, bool kColumns, bool kBf16, bool kSplit, bool kPartial>
 int launch_product(const Maps& maps, Product p, int64_t batch, int sms, cudaStream_t stream) {
   p.tiles_m = static_cast<int32_t>(ceil_div(p.rows, kTile));
   p.tiles_n = static_cast<int32_t>(ceil_div(p.cols, kTile));
@@ -778,7 +839,7 @@ int launch_product(const Maps& maps, Product p, int64_t batch, int sms, cudaStre
     p.per_slice = INT32_MAX / 2;
   }
   p.tiles = static_cast<int32_t>(per * batch * p.slices);
-  const auto kernel = product_kernel<kSymmetric, kAddends, kBf16, kSplit, kPartial>;
+  const auto kernel = product_kernel<kSymmetric, kAddends, kColumns, kBf16, kSplit, kPartial>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ECUDA;
   static bool attr_done[64] = {};  // benign race: the same attribute set twice
@@ -920,6 +981,8 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
   const float sa = scale_for(2.0 + fabs(shift)), sp = scale_for(fabs(ca) + 2 * fabs(cb) + 4 * fabs(cc));
   const int parts = l.parts;
   const bool split = parts == 2;
+  float* d_gram = reinterpret_cast<float*>(workspace + l.d_gram);
+  float* d_poly = reinterpret_cast<float*>(workspace + l.d_poly);
   for (int s = 0; s < steps; ++s) {
     const int from = s & 1, to = from ^ 1;
     Maps maps = {};
@@ -935,23 +998,27 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.a_mn = p.b_mn = !wide;
     p.scale = sa / (kXScale * kXScale);
     p.diagonal = static_cast<float>(shift * sa);
+    p.d_ld = l.lds;
+    if (!split) {
+      p.d_out = d_gram;
+      p.d_squares = completed;
+    }
     if (const int64_t slices = gram_slices(batch, side, length); slices > 0) {
       p.partial = reinterpret_cast<float*>(workspace + l.partial);
       p.partial_stride = batch * side * l.lds;
-      p.partial_ld = l.lds;
       const int64_t stages = p.ksteps * (split ? 3 : 1);
       p.per_slice = static_cast<int32_t>(ceil_div(stages, slices));
       p.slices = static_cast<int32_t>(ceil_div(stages, p.per_slice));
-      rc = split ? launch_product<true, 0, false, true, true>(maps, p, batch, sms, stream)
-                 : launch_product<true, 0, false, false, true>(maps, p, batch, sms, stream);
+      rc = split ? launch_product<true, 0, false, false, true, true>(maps, p, batch, sms, stream)
+                 : launch_product<true, 0, false, false, false, true>(maps, p, batch, sms, stream);
       if (rc != MXQ_OK) return rc;
       const Join join = {p.partial, batch, side, l.lds, p.partial_stride, p.slices, p.scale, p.diagonal,
                          reinterpret_cast<__half*>(workspace + l.gram[0]),
-                         split ? reinterpret_cast<__half*>(workspace + l.gram[1]) : nullptr};
+                         split ? reinterpret_cast<__half*>(workspace + l.gram[1]) : nullptr, p.d_out, p.d_squares};
       rc = launch_pdl(join_kernel, static_cast<unsigned>(ceil_div(p.partial_stride, kThreads)), kThreads, 0, stream, join);
     } else {
-      rc = split ? launch_product<true, 0, false, true, false>(maps, p, batch, sms, stream)
-                 : launch_product<true, 0, false, false, false>(maps, p, batch, sms, stream);
+      rc = split ? launch_product<true, 0, false, false, true, false>(maps, p, batch, sms, stream)
+                 : launch_product<true, 0, false, false, false, false>(maps, p, batch, sms, stream);
     }
     if (rc != MXQ_OK) return rc;
     // P = aI + bA + cAA
@@ -966,13 +1033,17 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.ksteps = static_cast<int32_t>(ceil_div(side, kStepK));
     p.scale = cc * sp / (sa * sa);
     p.diagonal = static_cast<float>((ca - 0.5 * shift * cb) * sp);
+    p.d_ld = l.lds;
+    if (!split) p.d_out = d_poly;
     if (completed) {
-      rc = split ? launch_product<true, 0, false, true, false>(maps, p, batch, sms, stream)
-                 : launch_product<true, 0, false, false, false>(maps, p, batch, sms, stream);
+      if (!split) p.square_rest = d_gram;
+      rc = split ? launch_product<true, 0, false, false, true, false>(maps, p, batch, sms, stream)
+                 : launch_product<true, 0, false, false, false, false>(maps, p, batch, sms, stream);
     } else {
       p.add_scale = cb * sp / sa;
-      rc = split ? launch_product<true, 2, false, true, false>(maps, p, batch, sms, stream)
-                 : launch_product<true, 1, false, false, false>(maps, p, batch, sms, stream);
+      if (!split) p.d_row = p.d_col = d_gram;
+      rc = split ? launch_product<true, 2, false, false, true, false>(maps, p, batch, sms, stream)
+                 : launch_product<true, 1, true, false, false, false>(maps, p, batch, sms, stream);
     }
     if (rc != MXQ_OK) return rc;
     // X <- P X, or X P
@@ -987,6 +1058,11 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.cols = n;
     p.ksteps = static_cast<int32_t>(ceil_div(side, kStepK));
     p.scale = 1.0f / sp;
+    if (!split) {
+      maps.add[0] = x[from][0].rows;
+      p.d_ld = l.lds;
+      (wide ? p.d_row : p.d_col) = d_poly;
+    }
     const bool last = s + 1 == steps;
     if (last) {
       if (out_map) maps.d[0] = final_rows;
@@ -997,11 +1073,14 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
       p.scale = scale / (sp * kXScale);
     }
     if (split)
-      rc = last ? launch_product<false, 0, true, true, false>(maps, p, batch, sms, stream)
-                : launch_product<false, 0, false, true, false>(maps, p, batch, sms, stream);
+      rc = last ? launch_product<false, 0, false, true, true, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 0, false, false, true, false>(maps, p, batch, sms, stream);
+    else if (wide)
+      rc = last ? launch_product<false, 1, false, true, false, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 1, false, false, false, false>(maps, p, batch, sms, stream);
     else
-      rc = last ? launch_product<false, 0, true, false, false>(maps, p, batch, sms, stream)
-                : launch_product<false, 0, false, false, false>(maps, p, batch, sms, stream);
+      rc = last ? launch_product<false, 1, true, true, false, false>(maps, p, batch, sms, stream)
+                : launch_product<false, 1, true, false, false, false>(maps, p, batch, sms, stream);
     if (rc != MXQ_OK) return rc;
   }
   return MXQ_OK;

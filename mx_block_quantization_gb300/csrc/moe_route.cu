@@ -155,6 +155,25 @@ __device__ __forceinline__ void finish_alone(const RouteShape& s, const float* p
   }
 }
 
+// A block's sums, counts and tokens: its part for the join, or the results.
+__device__ __forceinline__ void finish_block(const RouteShape& s, const float* sums, const int32_t* hist, int tokens,
+                                             float* part_p, int32_t* part_c, int32_t* part_n, uint32_t* joined,
+                                             int32_t* counts, float* loss, int32_t* n_out) {
+  if (gridDim.x == 1) {
+    finish_alone(s, sums, hist, tokens, counts, loss, n_out);
+    return;
+  }
+  const int64_t base = static_cast<int64_t>(blockIdx.x) * s.E;
+  for (int e = threadIdx.x; e < s.E; e += blockDim.x) {
+    part_p[base + e] = sums[e];
+    part_c[base + e] = hist[e];
+  }
+  if (threadIdx.x == 0) {
+    part_n[blockIdx.x] = tokens;
+    if (blockIdx.x == 0) *joined = 0u;
+  }
+}
+
 template <typename T, int kPer, int kV, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1)
     route_kernel(const T* __restrict__ logits, const RouteShape s, const uint8_t* __restrict__ mask,
@@ -316,18 +335,228 @@ __global__ void __launch_bounds__(kThreads, 1)
     sums[e] = sum;
   }
   __syncthreads();
-  if (gridDim.x == 1) {
-    finish_alone(s, sums, hist, routed_tokens, counts, loss, n_out);
-    return;
+  finish_block(s, sums, hist, routed_tokens, part_p, part_c, part_n, joined, counts, loss, n_out);
+}
+
+// At most 32 experts: eight lanes a token, lane l with the experts l, l + 8, ..., four
+// tokens a warp.  Every logit counts those before it, so there is nothing to gather.
+// (131072 tokens of 8 experts fp32, k = 2: 13.5 us forward and 8.3 backward, 48 and 33
+// with a warp a token; of 32, k = 4: 31 and 16, 52 and 35.)
+constexpr int kFewThreads = 1024, kFewBackThreads = 256, kFewExperts = 32;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+template <typename V, typename Op>
+__device__ __forceinline__ V over_eight(V v, Op op) {
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1) v = op(v, __shfl_xor_sync(kAll, v, d));
+  return v;
+}
+__device__ __forceinline__ float sum_eight(float v) {
+  return over_eight(v, [](float a, float b) { return a + b; });
+}
+// A token's logits in its eight lanes: loaded ahead, -inf past E and past the tokens.
+template <typename T, int kPer>
+struct FewRow {
+  T v[kPer];
+  __device__ __forceinline__ void load(const T* logits, const RouteShape& s, int64_t t, int sub, uint64_t bytes) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const T* p = logits + t * s.ld + sub + 8 * i;
+      v[i] = minus_infinity<T>();
+      if (t < s.tokens && sub + 8 * i < s.E && in_buf(p, sizeof(T), logits, bytes, &g_route_status)) v[i] = *p;
+    }
   }
-  const int64_t base = static_cast<int64_t>(blockIdx.x) * s.E;
-  for (int e = tid; e < s.E; e += kThreads) {
-    part_p[base + e] = sums[e];
-    part_c[base + e] = hist[e];
+};
+// The softmax of a token over its eight lanes; whether it takes part.
+template <int kPer>
+struct FewSoftmax {
+  float p[kPer];
+  uint32_t key[kPer];
+  bool routed;
+  template <typename T>
+  __device__ __forceinline__ FewSoftmax(const FewRow<T, kPer>& row, bool unmasked) {
+    uint32_t best = 0u;
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      p[i] = widen(row.v[i]);
+      key[i] = order_key(p[i]);
+      best = max(best, key[i]);
+      nan |= p[i] != p[i];
+    }
+    best = over_eight(best, [](uint32_t a, uint32_t b) { return max(a, b); });
+    const uint32_t nans = __ballot_sync(kAll, nan) >> (threadIdx.x & 24u) & 0xFFu;
+    routed = unmasked && (best != 0u || nans != 0u);
+    const float top = best != 0u ? key_value(best) : -CUDART_INF_F;
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      p[i] = exp2_ftz((p[i] - top) * kLog2E);  // 0 past E: those are -inf
+      sum += p[i];
+    }
+    const float inv = reciprocal(sum_eight(sum));
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) p[i] *= inv;
   }
-  if (tid == 0) {
-    part_n[blockIdx.x] = routed_tokens;
-    if (blockIdx.x == 0) *joined = 0u;
+};
+
+template <typename T, int kPer>
+__global__ void __launch_bounds__(kFewThreads)
+    route_few_kernel(const T* __restrict__ logits, const RouteShape s, const uint8_t* __restrict__ mask,
+                     float* __restrict__ weights, int32_t* __restrict__ ids, float* part_p, int32_t* part_c,
+                     int32_t* part_n, uint32_t* joined, int32_t* counts, float* loss, int32_t* n_out) {
+  __shared__ float by_group[kFewThreads / 8][8 * kPer];
+  __shared__ float sums[8 * kPer];
+  __shared__ int32_t hist[8 * kPer], routed_tokens;
+  const int tid = threadIdx.x, sub = tid & 7, base = tid & 24;
+  if (tid < 8 * kPer) hist[tid] = 0;
+  if (tid == 0) routed_tokens = 0;
+  __syncthreads();
+  pdl_wait();
+  if (gridDim.x > 1) pdl_launch_dependents();  // the join's few blocks wait beside this one
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
+  const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kFewThreads / 8);
+  float acc[kPer] = {};
+  int routed_here = 0;
+  FewRow<T, kPer> ahead;
+  int64_t t = static_cast<int64_t>(blockIdx.x) * (kFewThreads / 8) + tid / 8;
+  ahead.load(logits, s, t, sub, in_bytes);
+  for (; t - base / 8 < s.tokens; t += step) {  // the warp's first token
+    const FewRow<T, kPer> row = ahead;
+    ahead.load(logits, s, t + step, sub, in_bytes);
+    const bool in = t < s.tokens;
+    const FewSoftmax<kPer> soft(row, in && (mask == nullptr || mask[t] != 0));
+    int rank[kPer] = {};
+#pragma unroll
+    for (int j = 0; j < 8 * kPer; ++j) {
+      const uint32_t other = __shfl_sync(kAll, soft.key[j / 8], base | (j & 7));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) rank[i] += other > soft.key[i] || (other == soft.key[i] && j < sub + 8 * i) ? 1 : 0;
+    }
+    float w[kPer], all = 0.0f;
+    int chosen = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const bool own = soft.routed && soft.key[i] != 0u && rank[i] < s.k;
+      if (!own) rank[i] = kFewExperts;
+      w[i] = own ? soft.p[i] : 0.0f;
+      all += w[i];
+      chosen += __popc(__ballot_sync(kAll, own) >> base & 0xFFu);
+      if (soft.routed) acc[i] += soft.p[i];
+    }
+    all = sum_eight(all);
+    if (soft.routed && sub == 0) ++routed_here;
+    const auto write = [&](int place, float weight, int32_t e) {
+      if (in_buf(weights + t * s.k + place, 4, weights, out_bytes, &g_route_status) &&
+          in_buf(ids + t * s.k + place, 4, ids, out_bytes, &g_route_status)) {
+        weights[t * s.k + place] = weight;
+        ids[t * s.k + place] = e;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (rank[i] < kFewExperts) {
+        write(rank[i], s.renorm ? w[i] / all : w[i], sub + 8 * i);
+        atomicAdd(&hist[sub + 8 * i], 1);
+      }
+    for (int place = chosen + sub; in && place < s.k; place += 8) write(place, 0.0f, -1);
+  }
+  if (routed_here) atomicAdd(&routed_tokens, routed_here);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) by_group[tid / 8][sub + 8 * i] = acc[i];
+  __syncthreads();
+  if (tid < s.E) {
+    float sum = 0.0f;
+#pragma unroll 16
+    for (int g = 0; g < kFewThreads / 8; ++g) sum += by_group[g][tid];
+    sums[tid] = sum;
+  }
+  __syncthreads();
+  finish_block(s, sums, hist, routed_tokens, part_p, part_c, part_n, joined, counts, loss, n_out);
+}
+
+template <typename T, int kPer>
+__global__ void __launch_bounds__(kFewBackThreads)
+    route_backward_few_kernel(const T* __restrict__ logits, const RouteShape s, const uint8_t* __restrict__ mask,
+                              const int32_t* __restrict__ ids, const int32_t* __restrict__ counts,
+                              const int32_t* __restrict__ n_in, const float* __restrict__ dweights,
+                              const float* __restrict__ dloss, T* __restrict__ dlogits, int64_t ldd) {
+  const int tid = threadIdx.x, sub = tid & 7, base = tid & 24;
+  pdl_wait();
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
+  const uint64_t out_bytes = (static_cast<uint64_t>(s.tokens - 1) * ldd + s.E) * sizeof(T);
+  float c[kPer];
+  const float n = static_cast<float>(*n_in);
+  const float f = dloss != nullptr && n > 0.0f ? *dloss * (static_cast<float>(s.E) / (static_cast<float>(s.k) * n * n)) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) c[i] = dloss != nullptr && sub + 8 * i < s.E ? f * static_cast<float>(counts[sub + 8 * i]) : 0.0f;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kFewBackThreads / 8);
+  FewRow<T, kPer> ahead;
+  int32_t e_ahead[kPer];
+  float dw_ahead[kPer];
+  const auto fetch = [&](int64_t t) {
+    ahead.load(logits, s, t, sub, in_bytes);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const bool there = dweights != nullptr && t < s.tokens && sub + 8 * i < s.k;
+      e_ahead[i] = there ? ids[t * s.k + sub + 8 * i] : -1;
+      dw_ahead[i] = there ? dweights[t * s.k + sub + 8 * i] : 0.0f;
+    }
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * (kFewBackThreads / 8) + tid / 8;
+  fetch(t);
+  for (; t - base / 8 < s.tokens; t += step) {  // the warp's first token
+    const FewRow<T, kPer> row = ahead;
+    int32_t e[kPer];
+    float dw[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) e[i] = e_ahead[i], dw[i] = dw_ahead[i];
+    fetch(t + step);
+    const bool in = t < s.tokens;
+    const FewSoftmax<kPer> soft(row, in && (mask == nullptr || mask[t] != 0));
+    // the chosen experts' gradients in their own lanes
+    float own_dw[kPer] = {};
+    bool own[kPer] = {};
+#pragma unroll
+    for (int j = 0; j < 8 * kPer; ++j) {
+      if (j >= s.k) break;
+      const int32_t id = __shfl_sync(kAll, e[j / 8], base | (j & 7));
+      const float d = __shfl_sync(kAll, dw[j / 8], base | (j & 7));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (id == sub + 8 * i) own[i] = true, own_dw[i] = d;
+    }
+    float pc = 0.0f, all = 0.0f, part[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      pc = fmaf(soft.p[i], c[i], pc);
+      all += own[i] ? soft.p[i] : 0.0f;
+    }
+    if (s.renorm) {
+      all = sum_eight(all);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        part[i] = own[i] ? soft.p[i] / all : 0.0f;
+        dot = own[i] ? fmaf(part[i], own_dw[i], dot) : dot;
+      }
+      dot = sum_eight(dot);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) part[i] = own[i] ? part[i] * (own_dw[i] - dot) : 0.0f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        part[i] = own[i] ? soft.p[i] * own_dw[i] : 0.0f;
+        pc += part[i];
+      }
+    }
+    const float total = sum_eight(pc);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      T* to = dlogits + t * ldd + sub + 8 * i;
+      const float d = soft.routed ? fmaf(soft.p[i], c[i] - total, part[i]) : 0.0f;
+      if (in && sub + 8 * i < s.E && in_buf(to, sizeof(T), dlogits, out_bytes, &g_route_status)) *to = narrow<T>(d);
+    }
   }
 }
 
@@ -518,8 +747,9 @@ template <int kPer>
 constexpr int route_threads() {
   return kPer <= 8 ? 1024 : kPer == 16 ? 512 : 256;
 }
-// warps of a block for that many experts
-int warps_for(int experts) {
+// tokens that a block works on at a time, for that many experts
+int tokens_at_once(int experts) {
+  if (experts <= kFewExperts) return kFewThreads / 8;
   return (experts <= 256 ? route_threads<8>() : experts <= 512 ? route_threads<16>() : route_threads<32>()) / 32;
 }
 // threads of a block of the backward pass: its shared rows stay within 32 KB
@@ -550,21 +780,41 @@ int route_blocks(int64_t tokens, int warps, int sms) {
   return static_cast<int>(want < 1 ? 1 : want < sms ? want : sms);
 }
 
-template <typename T, int kPer, int kV>
-int launch_route(const RouteCall& a) {
-  constexpr int kThreads = route_threads<kPer>();
-  const int blocks = route_blocks(a.s.tokens, kThreads / 32, a.sms);
+// A forward kernel of that block size, and the join where there is more than one.
+template <typename Kernel>
+int launch_forward(const RouteCall& a, Kernel kernel, int threads, size_t smem) {
+  const int blocks = route_blocks(a.s.tokens, tokens_at_once(a.s.E), a.sms);
   float* part_p = reinterpret_cast<float*>(a.workspace);
   int32_t* part_c = reinterpret_cast<int32_t*>(part_p + static_cast<int64_t>(blocks) * a.s.E);
   int32_t* part_n = part_c + static_cast<int64_t>(blocks) * a.s.E;
   uint32_t* joined = reinterpret_cast<uint32_t*>(part_n + blocks);
   float* part_loss = reinterpret_cast<float*>(joined + 1);
-  int rc = launch_pdl(route_kernel<T, kPer, kV, kThreads>, blocks, kThreads, a.s.E * 8 + kPer * kThreads * 4, a.stream,
-                      static_cast<const T*>(a.logits), a.s, a.mask, a.weights, a.ids, part_p, part_c, part_n, joined,
-                      a.counts, a.loss, a.n);
+  const int rc = kernel(blocks, threads, smem, part_p, part_c, part_n, joined);
   if (rc != MXQ_OK || blocks == 1) return rc;
   return launch_pdl(route_join_kernel, static_cast<unsigned>(ceil_div(a.s.E, 32)), 32 * kJoinWarps, 0, a.stream, a.s, blocks,
                     part_p, part_c, part_n, joined, part_loss, a.counts, a.loss, a.n);
+}
+template <typename T, int kPer, int kV>
+int launch_route(const RouteCall& a) {
+  constexpr int kThreads = route_threads<kPer>();
+  return launch_forward(a, [&](int blocks, int threads, size_t smem, float* part_p, int32_t* part_c, int32_t* part_n, uint32_t* joined) {
+    return launch_pdl(route_kernel<T, kPer, kV, kThreads>, blocks, threads, smem, a.stream, static_cast<const T*>(a.logits), a.s,
+                      a.mask, a.weights, a.ids, part_p, part_c, part_n, joined, a.counts, a.loss, a.n);
+  }, kThreads, a.s.E * 8 + kPer * kThreads * 4);
+}
+template <typename T, int kPer, bool kBack>
+int launch_few(const RouteCall& a) {
+  if constexpr (kBack) {
+    const int64_t want = ceil_div(a.s.tokens, kFewBackThreads / 8), cap = static_cast<int64_t>(a.sms) * (2048 / kFewBackThreads);
+    return launch_pdl(route_backward_few_kernel<T, kPer>, static_cast<unsigned>(want < cap ? want : cap), kFewBackThreads, 0,
+                      a.stream, static_cast<const T*>(a.logits), a.s, a.mask, a.ids, a.counts, a.n, a.dweights, a.dloss,
+                      static_cast<T*>(a.dlogits), a.ldd);
+  } else {
+    return launch_forward(a, [&](int blocks, int threads, size_t smem, float* part_p, int32_t* part_c, int32_t* part_n, uint32_t* joined) {
+      return launch_pdl(route_few_kernel<T, kPer>, blocks, threads, smem, a.stream, static_cast<const T*>(a.logits), a.s, a.mask,
+                        a.weights, a.ids, part_p, part_c, part_n, joined, a.counts, a.loss, a.n);
+    }, kFewThreads, 0);
+  }
 }
 
 template <typename T, int kPer, int kV>
@@ -594,6 +844,9 @@ int launch_typed(const RouteCall& a) {
   const int align = common_alignment({address_of(a.logits), pitch, kBack ? address_of(a.dlogits) : 0, dpitch});
   const bool v4 = align >= static_cast<int>(4 * sizeof(T)), v2 = align >= static_cast<int>(2 * sizeof(T));
   const int E = a.s.E;
+  if (E <= 8) return launch_few<T, 1, kBack>(a);
+  if (E <= 16) return launch_few<T, 2, kBack>(a);
+  if (E <= kFewExperts) return launch_few<T, 4, kBack>(a);
   if (E <= 64) return v2 ? launch_one<T, 2, 2, kBack>(a) : launch_one<T, 2, 1, kBack>(a);
   if (E <= 128) return v4 ? launch_one<T, 4, 4, kBack>(a) : launch_one<T, 4, 1, kBack>(a);
   if (E <= 256) return v4 ? launch_one<T, 8, 4, kBack>(a) : launch_one<T, 8, 1, kBack>(a);
@@ -619,7 +872,7 @@ int route_status_read(unsigned int* out, bool clear) {
 
 extern "C" int64_t mxq_moe_route_workspace(int64_t tokens, int32_t experts) {
   if (tokens < 0 || tokens > INT32_MAX || experts < 1 || experts > MXQ_MAX_GROUPS) return MXQ_EBADSHAPE;
-  const int64_t blocks = ceil_div(tokens, warps_for(experts));
+  const int64_t blocks = ceil_div(tokens, tokens_at_once(experts));
   // per block the experts' sums and counts and the routed tokens; the join's counter and losses
   return blocks <= 1 ? 0 : (static_cast<int64_t>(experts) * 8 + 4) * (blocks < kMaxBlocks ? blocks : kMaxBlocks) + 4 * (1 + kMaxJoins);
 }

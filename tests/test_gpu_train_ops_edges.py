@@ -13,6 +13,7 @@ import torch
 import mx_block_quantization_gb300 as mxq
 from tests.gpu_util import require_gpu
 from tests.test_gpu_moe_exchange import check_plan, routing
+from tests.test_gpu_moe_route import check, logits
 from tests.test_gpu_orthogonalize import BOUND, iteration, momentum, off
 
 pytestmark = pytest.mark.gpu
@@ -240,3 +241,48 @@ def test_long_matrices_are_as_exact_as_square_ones(batch, m, n):
     iteration's slope, beside the 1.7e-3 of bf16: 2.2e-3."""
     g = momentum(batch, m, n)
     assert off(mxq.orthogonalize(g), iteration(g)) <= 2.2e-3
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k,pad", [
+    (1, 1, 1, 0), (1, 8, 8, 0), (127, 5, 2, 0), (128, 8, 2, 1), (129, 8, 1, 0), (130, 9, 9, 0), (300, 16, 16, 0), (257, 12, 3, 3),
+    (5000, 8, 2, 0), (40003, 16, 4, 0), (3, 15, 10, 1), (200, 17, 5, 0), (1000, 32, 32, 0), (131, 31, 9, 1),
+])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_few_experts(T, E, k, pad, kind, renorm):
+    x = logits(T, E, kind, pad)
+    check(x, k, renorm=renorm)
+    mask = torch.rand(T, generator=torch.Generator().manual_seed(T)).cuda() > 0.3
+    check(x, k, mask=mask, renorm=renorm)
+
+
+@pytest.mark.parametrize("E,k", [(7, 3), (8, 8), (16, 5), (30, 12)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_few_experts_agree_with_many(E, k, renorm):
+    """Experts of -inf added up to 40 change nothing but the loss's factor: ties, rows
+    without experts, with too few of them, with NaN, infinities and lowest values."""
+    inf, nan, low = float("inf"), float("nan"), torch.finfo(torch.float32).min
+    g = torch.Generator().manual_seed(E)
+    x = torch.randint(-2, 3, (400, E), generator=g).float()
+    x[5] = -inf
+    x[6, 2:] = -inf
+    x[7, 1], x[8, 3], x[9, 0], x[10] = nan, inf, low, low
+    x[11], x[12, 0], x[13, 2] = nan, -inf, 1e30
+    x[12, 1:] = nan
+    x = x.cuda()
+    wide = torch.full((400, 40), -inf, device="cuda")
+    wide[:, :E] = x
+    mask = torch.rand(400, generator=g).cuda() > 0.1
+    mask[5:14] = True
+    a, b = (mxq.moe_route(t, k, mask=mask, renorm=renorm) for t in (x, wide))
+    assert torch.equal(a.ids, b.ids) and torch.equal(a.counts, b.counts[:E]) and torch.equal(a.routed, b.routed)
+    torch.testing.assert_close(a.weights, b.weights, rtol=2.0**-19, atol=0, equal_nan=True)
+    assert a.loss.isnan() and b.loss.isnan()
+    ok = ~x.isnan().any(1) & ~(x == inf).any(1)
+    a, b = (mxq.moe_route(t, k, mask=mask & ok, renorm=renorm) for t in (x, wide))
+    assert float(a.loss) == pytest.approx(float(b.loss) * E / 40, rel=2.0**-18)
+    dw, dl = torch.randn(400, k, generator=g).cuda(), torch.tensor(0.3, device="cuda")
+    da = mxq.moe_route_backward(x, a, dw, dl, mask=mask & ok, renorm=renorm)
+    db = mxq.moe_route_backward(wide, b, dw, dl * E / 40, mask=mask & ok, renorm=renorm)
+    torch.testing.assert_close(da, db[:, :E], rtol=2.0**-18, atol=2.0**-18 * 5)
+    assert (da[~(mask & ok)] == 0).all()

@@ -10,8 +10,9 @@
 //   w_j (dw_j - sum w dw) at the chosen experts for weights over their sum, and
 //   p_e ([e chosen] dw_e - sum_chosen p dw) otherwise.
 //
-// One warp owns a token; a lane keeps kPer of its logits in registers, so the
-// logits are read once each way, the next token's while this one is worked on.
+// One warp owns a token (eight lanes with at most 32 experts, see below); a lane
+// keeps kPer of its logits in registers, so the logits are read once each way, the
+// next token's while this one is worked on.
 // The k-th largest of the lanes' own maxima is at most the k-th largest logit, so
 // only the few logits from there on (k to a dozen of random ones) are gathered,
 // one per lane, and each counts those before it by keys that no two share.  With

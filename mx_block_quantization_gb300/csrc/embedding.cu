@@ -6,10 +6,11 @@
 // The gradient sorts the tokens by id, stably, so that the tokens of a row lie side
 // by side.  Most of its time is writing the table, most rows of which no token has:
 // the launches of the sort, which keep few blocks busy, zero the whole table with
-// the others (6.2 TB/s), and the last launch writes the rows that have tokens,
-// found from the places where a run of equal ids begins.  (Writing every row once,
-// by its number, needs the runs before any of it and a search for each block of
-// rows: 259 us at 131072x4096 bf16 with 16384 tokens, now 213.)
+// the others (6.2 TB/s), and the last launch writes the rows that have tokens, found
+// from the places where a run of equal ids begins.  (Writing every row once, by its
+// number, needs the runs before any of it and a search for each block of rows: 259
+// us at 131072x4096 bf16 with 16384 tokens, now 213.)  With many tokens and no more
+// rows than tokens the last launch zeroes the rows without any (zeroed_late).
 // A frequent id would keep one block busy for long, so a run of more than kChunk
 // tokens is first summed in pieces, one per chunk of kChunk sorted places, by a
 // launch of its own; the row then adds the pieces in order.  Sums are in fp32 and
@@ -492,6 +493,37 @@ __host__ __device__ constexpr int row_columns() {
   return sizeof(T) * kV >= 16 ? 1 : sizeof(T) * kV >= 8 ? 2 : 4;
 }
 
+// Zeroes those of kAbsentRows rows of the table that no token has, each found by a
+// search among the sorted ids.
+constexpr int kAbsentRows = 64;
+template <typename U>
+__device__ __forceinline__ void zero_absent(const int32_t* __restrict__ keys, const GradShape& s, int64_t block,
+                                            U* __restrict__ dtable) {
+  __shared__ uint32_t absent[kAbsentRows / 32];
+  const int64_t r0 = block * kAbsentRows;
+  if (threadIdx.x < kAbsentRows) {
+    const int64_t r = r0 + threadIdx.x;
+    int64_t lo = 0, hi = s.tokens;
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (keys[mid] < r)
+        lo = mid + 1;
+      else
+        hi = mid;
+    }
+    const uint32_t gone = __ballot_sync(0xFFFFFFFFu, r < s.rows && (lo == s.tokens || keys[lo] != r));
+    if ((threadIdx.x & 31) == 0) absent[threadIdx.x / 32] = gone;
+  }
+  __syncthreads();
+  Fill table = {};
+  table.table = reinterpret_cast<const uint8_t*>(dtable);
+  table.table_bytes = (static_cast<uint64_t>(s.rows - 1) * s.ldw + s.D) * sizeof(U);
+  for (int w = 0; w < kAbsentRows / 32; ++w)
+    for (uint32_t left = absent[w]; left != 0u; left &= left - 1)
+      zero_bytes(reinterpret_cast<uint8_t*>(dtable + (r0 + 32 * w + __ffs(left) - 1) * s.ldw), s.D * sizeof(U), threadIdx.x,
+                 blockDim.x, table);
+}
+
 // The rows of the runs that begin at one of the block's kStarts places.  A thread
 // loads its columns of all those places' tokens before it adds any up: which run
 // a place belongs to only decides where the sums are cut.  The last run is
@@ -500,10 +532,14 @@ __host__ __device__ constexpr int row_columns() {
 template <typename T, typename U, int kV>
 __global__ void __launch_bounds__(kThreads, 4)
     rows_kernel(const int32_t* __restrict__ keys, const int32_t* __restrict__ tokens, const T* __restrict__ dy,
-                const GradShape s, const float* __restrict__ pieces, float scale, U* __restrict__ dtable) {
+                const GradShape s, const float* __restrict__ pieces, float scale, U* __restrict__ dtable, int64_t run_blocks) {
   __shared__ int32_t near_key[64], near_token[64];
   __shared__ uint64_t starts_of;
   pdl_wait();
+  if (static_cast<int64_t>(blockIdx.x) >= run_blocks) {
+    zero_absent<U>(keys, s, blockIdx.x - run_blocks, dtable);
+    return;
+  }
   static_assert(kStarts + kChunk < 64, "the ends of short runs lie within the places looked at");
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kStarts;
   if (threadIdx.x < 64) {
@@ -701,6 +737,15 @@ Fill fill_share(void* dtable, const GradShape& s, int esize, int q, int parts) {
   return f;
 }
 
+// Where most rows may have a token, those that have none are zeroed by the last
+// launch instead of all of them by the sort's, and none is written twice: 65536
+// tokens of 4096 bf16, 32768 rows, 155 us instead of 182 (ids drawn evenly; 173 and
+// 189 with frequent ones), 65536 rows of 2048 127 and 140 (141 and 140).  Not with
+// more rows than tokens (131072 rows, frequent ids: 185 and 182), nor with few
+// tokens, whose sort is one block beside which the zeroing costs nothing (16384
+// tokens, 32768 rows of 4096: 113 and 94).
+inline bool zeroed_late(const GradShape& s) { return s.tokens > kSmallTokens && s.rows <= s.tokens; }
+
 template <typename T, typename U, int kV>
 int launch_table(GradCall a) {
   const int64_t nv = a.s.D / kV;
@@ -716,8 +761,10 @@ int launch_table(GradCall a) {
   // as many threads as a row has columns for them, 64 to 256
   int threads = 64;
   while (threads < kThreads && threads * row_columns<T, kV>() < nv) threads *= 2;
-  return launch_pdl(rows_kernel<T, U, kV>, static_cast<unsigned>(ceil_div(a.s.tokens, kStarts)), threads, 0, a.stream,
-                    a.keys, a.tokens, static_cast<const T*>(a.dy), a.s, a.pieces, a.scale, static_cast<U*>(a.dtable));
+  const int64_t run_blocks = ceil_div(a.s.tokens, kStarts);
+  const int64_t absent_blocks = zeroed_late(a.s) ? ceil_div(a.s.rows, kAbsentRows) : 0;
+  return launch_pdl(rows_kernel<T, U, kV>, static_cast<unsigned>(run_blocks + absent_blocks), threads, 0, a.stream, a.keys,
+                    a.tokens, static_cast<const T*>(a.dy), a.s, a.pieces, a.scale, static_cast<U*>(a.dtable), run_blocks);
 }
 template <typename T, typename U>
 int table_vector(const GradCall& a) {
@@ -801,7 +848,7 @@ int launch_gradient(const void* ids, const GradPlan& p, int64_t padding, uint8_t
   const int launches = small ? 1 : p.d.passes * per_digit;
   Fill fills[kMaxLaunches];
   for (int q = 0; q < launches; ++q) fills[q] = fill_share(a.dtable, a.s, element_bytes(out_dtype), q, launches);
-  const int64_t want = ceil_div(fills[0].rows * fills[0].row_bytes, 16 * kThreads * 4);
+  const int64_t want = zeroed_late(a.s) ? 0 : ceil_div(fills[0].rows * fills[0].row_bytes, 16 * kThreads * 4);
   const int fill_blocks = static_cast<int>(want < 8 * sms ? want : 8 * sms);
   const IdKey<I> source{static_cast<const I*>(ids), a.s.rows, padding};
   if (small) {

@@ -286,3 +286,22 @@ def test_few_experts_agree_with_many(E, k, renorm):
     db = mxq.moe_route_backward(wide, b, dw, dl * E / 40, mask=mask & ok, renorm=renorm)
     torch.testing.assert_close(da, db[:, :E], rtol=2.0**-18, atol=2.0**-18 * 5)
     assert (da[~(mask & ok)] == 0).all()
+
+
+@pytest.mark.parametrize("T,V,D,pad", [
+    (16385, 16385, 8, 0), (20000, 3, 1001, 2), (30011, 20000, 33, 0), (40000, 40001, 16, 0), (17000, 64, 130, 1), (17000, 65, 24, 0),
+])
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+def test_rows_without_tokens_are_zero(T, V, D, pad, kind):
+    """Many tokens, rows and runs of rows that none has; the rest exact sums, and
+    nothing written beside the rows."""
+    g = np.random.Generator(np.random.PCG64(T + V))
+    live = np.sort(g.choice(V, max(1, V // 3), replace=False))
+    ids = torch.from_numpy(live[g.integers(0, live.size, T)]).cuda()
+    ids[:3] = torch.tensor([-1, V, 2**40])
+    dy = torch.randint(-2, 3, (T, D), device="cuda").to(kind)
+    room = torch.full((V, D + pad), 7.0, dtype=torch.float32, device="cuda")
+    mxq.embedding_backward(ids, dy, V, out=room[:, :D])
+    assert mxq.device_status(clear=True) == mxq.DEV_BADINDEX
+    want = torch.zeros(V, D, dtype=torch.float64, device="cuda").index_add_(0, ids[3:], dy[3:].double())
+    assert torch.equal(room[:, :D].double(), want) and (room[:, D:] == 7).all()

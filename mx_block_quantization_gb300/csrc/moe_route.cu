@@ -871,9 +871,16 @@ int route_status_read(unsigned int* out, bool clear) {
 }
 }  // namespace mxq
 
+// Sized for blocks of at most kWorkspaceTokens tokens: whether a call needs a workspace
+// goes by its tokens, the same for every number of experts up to 256 and whichever
+// kernel serves them.  (A block takes 128 tokens where there are at most 32 experts.
+// Sized for those, calls of 33 to 128 tokens asked for none, and one with too small a
+// workspace, or none, was accepted beside 32 experts and refused beside 33.)
+constexpr int kWorkspaceTokens = 32;
 extern "C" int64_t mxq_moe_route_workspace(int64_t tokens, int32_t experts) {
   if (tokens < 0 || tokens > INT32_MAX || experts < 1 || experts > MXQ_MAX_GROUPS) return MXQ_EBADSHAPE;
-  const int64_t blocks = ceil_div(tokens, tokens_at_once(experts));
+  const int at_once = tokens_at_once(experts);
+  const int64_t blocks = ceil_div(tokens, at_once < kWorkspaceTokens ? at_once : kWorkspaceTokens);
   // per block the experts' sums and counts and the routed tokens; the join's counter and losses
   return blocks <= 1 ? 0 : (static_cast<int64_t>(experts) * 8 + 4) * (blocks < kMaxBlocks ? blocks : kMaxBlocks) + 4 * (1 + kMaxJoins);
 }

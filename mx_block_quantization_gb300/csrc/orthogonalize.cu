@@ -58,6 +58,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "pair_drain.h"
 #include "train_common.cuh"
 
 namespace {
@@ -220,10 +221,14 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t at_leader(uint32_t addr) {
+__device__ __forceinline__ uint32_t at_rank(uint32_t addr, uint32_t rank) {
   uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
+}
+__device__ __forceinline__ uint32_t at_leader(uint32_t addr) { return at_rank(addr, 0); }
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   // relaxed: what it orders are tensor memory reads, by their own fence; a release
@@ -260,6 +265,10 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       "{\n\t.reg .b16 both;\n\tmov.b16 both, 3;\n\t"
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n\t}" ::"r"(bar)
       : "memory");
+}
+// The same in this CTA alone.
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -339,7 +348,9 @@ __device__ __forceinline__ uint32_t bf162_bits(float lo, float hi) {
 struct alignas(8) Barriers {
   uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
   uint64_t addend[kEpilogueWarps][kWarpChunks];
+  uint64_t drained;        // the leader's: its MMAs are done, after a wait that ran out
   uint32_t tmem, abort_flag;
+  uint32_t leader_gave_up, issued[2];  // by the leader; to the leader: stages each CTA has issued
 };
 
 __device__ __forceinline__ float half_rounded(float v) { return __half2float(__float2half_rn(v)); }
@@ -380,7 +391,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int w = 0; w < kEpilogueWarps; ++w)
       for (int c = 0; c < kWarpChunks; ++c) mbar_init(smem_u32(&bars.addend[w][c]), 1);
-    bars.abort_flag = 0u;
+    mbar_init(smem_u32(&bars.drained), 1);
+    bars.abort_flag = bars.leader_gave_up = 0u;
     mbar_init_fence();
     tma_prefetch_desc(&maps.a[0]);
     tma_prefetch_desc(&maps.b[0]);
@@ -400,9 +412,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
   pdl_launch_dependents();
 
   const int ksteps = kSplit ? 3 * p.ksteps : p.ksteps;
-  int issued = 0;  // stages loaded so far (the producer's; its pair takes the same number)
   if (warp == 0 && lane == 0) {
     // ---- producer: this CTA's half of A and of B -------------------------
+    int issued = 0;  // stages loaded so far
     bool ok = true;
     for (int t = first; ok && t < p.tiles; t += step) {
       const TileAt at = tile_at<kSymmetric>(p, t);
@@ -436,6 +448,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
     }
+    store_cluster(at_leader(smem_u32(&bars.issued[rank])), static_cast<uint32_t>(issued));
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- MMA issue for the pair -------------------------------------------
     const uint64_t step_a = (p.a_mn ? 16 * 128 : 32) >> 4, step_b = (p.b_mn ? 16 * 128 : 32) >> 4;  // 16 of K
@@ -461,6 +474,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
         commit_pair(smem_u32(&bars.empty[s]));
       }
       if (ok) commit_pair(smem_u32(&bars.acc_full[acc]));
+    }
+    if (!ok) {  // products under way read both CTAs' stages and write their tensor memory
+      commit_here(smem_u32(&bars.drained));
+      mbar_wait_drain(smem_u32(&bars.drained), 0);
     }
   } else if (warp >= 4) {
     // ---- epilogue: 32 of this CTA's 128 rows and half of the columns per warp --
@@ -696,14 +713,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
     if (lane == 0) bulk_wait_all<0>();
     __syncwarp();
   }
-  // Neither CTA leaves while the other may still signal it or read its memory;
-  // after a wait that ran out, loads still in flight are waited for (again with
-  // a limit) by the CTA whose barriers count them.
+  // Neither CTA leaves while the other may still signal it or read its memory.  After a
+  // wait that ran out the leader, whose barriers count both CTAs' loads, waits for
+  // those still in flight (again with a limit) before either lets go of its memory.
+  // A leader whose waits all ended has seen every load and product of the pair.
+  __syncthreads();
+  if (rank == 0 && tid == 0 && bars.abort_flag) store_cluster(at_rank(smem_u32(&bars.leader_gave_up), 1), 1u);
   __syncwarp();
   cluster_sync_all();
-  if (rank == 0 && tid == 0 && bars.abort_flag) {
-    for (int n = issued < kStages ? 0 : issued - kStages; n < issued; ++n)
-      mbar_wait_drain(smem_u32(&bars.full[n % kStages]), (n / kStages) & 1);
+  if (rank == 0 ? bars.abort_flag : bars.leader_gave_up) {
+    if (rank == 0 && tid == 0) {
+      const int own = static_cast<int>(bars.issued[0]), peer = static_cast<int>(bars.issued[1]);
+      const PairDrain range = pair_drain(own, peer, kStages);
+      for (int n = range.first; n < range.end; ++n) {
+        const uint32_t bar = smem_u32(&bars.full[n % kStages]);
+        if (pair_unannounced(n, own)) mbar_arrive_expect_tx(bar, kStageBytes);
+        if (pair_half_missing(n, peer)) mbar_complete_tx(bar, kStageBytes);
+        mbar_wait_drain(bar, (n / kStages) & 1);
+      }
+    }
+    __syncthreads();
+    cluster_sync_all();
   }
   __syncthreads();
   fence_after();

@@ -403,9 +403,9 @@ int mxq_embedding_backward(const void *ids, int ids_bytes, int64_t tokens, const
  * The products take fp16 operands and accumulate in fp32 (tcgen05): an error of
  * about 1e-3 (Frobenius, of the result's norm) for five steps of the usual
  * coefficients, beside the 1.7e-3 of the rounding to bf16; sides up to 64 carry
- * pairs of fp16 and are exact to the rounding.  The norm is fp32, its square
- * within fp32's range: |g| between 1e-19 and 1e19, beyond it out is 0 (or NaN
- * for a norm of 0 with eps == 0).  The iterates are taken to stay within |X| <= 1.5 in the spectral norm,
+ * pairs of fp16 and are exact to the rounding.  The norm is right for any finite g (its
+ * squares are summed in three ranges of fp32); a matrix of zeros gives 0, or NaN with
+ * eps == 0.  The iterates are taken to stay within |X| <= 1.5 in the spectral norm,
  * as they do for the usual coefficients (3.4445, -4.775, 2.0315); beyond eight
  * times that fp16 overflows.  Directions in which g is zero, or below 2^-12 of
  * its norm, carry rounding noise that the iteration magnifies up to a^steps.

@@ -80,19 +80,45 @@ struct Matrix {
   int64_t last;                     // elements of the last row
 };
 
+// The norm of values anywhere in fp32's range.  A square of a value below 2^-75 is 0 in
+// fp32 and one above 2^64 infinite, so the sum is held in three parts: of pieces whose
+// largest value is below 2^-43, times 2^85 before they are squared; of those up to
+// 2^43; and of larger ones, times 2^-86.  (What a piece loses of its smaller values is
+// below 2^-63 of its largest square.)  Every part of up to 2^40 squares stays within
+// 2^-128 and 2^126.  A piece is what a thread loads at once, so ordinary values cost one
+// comparison each.
+constexpr float kSmall = 0x1p-43f, kLarge = 0x1p43f, kSmallUp = 0x1p85f, kLargeDown = 0x1p-86f;
+struct Squares {
+  float small, plain, large;
+};
+// The norm as r / unit, unit a power of two.
+struct Norm {
+  float r, unit;
+  __device__ __forceinline__ explicit Norm(const Squares& s) {
+    const float lower = s.plain + s.small / kSmallUp / kSmallUp;
+    // compared so that a NaN in any part reaches r
+    if (!(s.large == 0.0f))
+      r = sqrtf(s.large + lower * kLargeDown * kLargeDown), unit = kLargeDown;
+    else if (!(s.plain == 0.0f))
+      r = sqrtf(lower), unit = 1.0f;
+    else
+      r = sqrtf(s.small), unit = kSmallUp;
+  }
+};
+
 // Blocks of a matrix take rows in turn; tx threads (a power of two) share a row.
 // Where the matrix and X have no gaps between their rows, the rows are pieces of
 // kThreads * kAhead loads instead (launch_scale).  Both kernels are bound by DRAM;
 // what they need is loads in flight: with rows of 512 floats a thread had one.
 template <typename T, int kV>
 __global__ void __launch_bounds__(kThreads)
-    norm_kernel(const T* __restrict__ g, const Matrix a, int parts, int tx, float* __restrict__ sums) {
-  __shared__ float red[kThreads / 32];
+    norm_kernel(const T* __restrict__ g, const Matrix a, int parts, int tx, Squares* __restrict__ sums) {
+  __shared__ float red[kThreads / 32][3];
   pdl_wait();
   const int64_t b = blockIdx.x / parts, part = blockIdx.x % parts;
   const int ty = kThreads / tx;
   const uint64_t bytes = ((a.batch - 1) * a.stride + (a.m - 1) * a.ld + a.last) * sizeof(T);
-  float sum = 0.0f;
+  Squares sum = {};
   for (int64_t r = part * ty + threadIdx.x / tx; r < a.m; r += static_cast<int64_t>(parts) * ty) {
     const T* row = g + b * a.stride + r * a.ld;
     const int64_t nv = (r == a.m - 1 ? a.last : a.n) / kV;
@@ -102,38 +128,61 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int q = 0; q < kAhead; ++q)
         v[q] = c + q * tx < nv ? *reinterpret_cast<const Vec<T, kV>*>(row + (c + q * tx) * kV) : Vec<T, kV>{};
+      float most = 0.0f;
 #pragma unroll
       for (int q = 0; q < kAhead; ++q)
 #pragma unroll
-        for (int j = 0; j < kV; ++j) sum = fmaf(widen(v[q].v[j]), widen(v[q].v[j]), sum);
+        for (int j = 0; j < kV; ++j) most = fmaxf(most, fabsf(widen(v[q].v[j])));
+      const auto squares = [&](float unit, float& to) {
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+          for (int j = 0; j < kV; ++j) to = fmaf(widen(v[q].v[j]) * unit, widen(v[q].v[j]) * unit, to);
+      };
+      if (most >= kSmall && most <= kLarge)
+        squares(1.0f, sum.plain);
+      else if (most > kLarge)
+        squares(kLargeDown, sum.large);
+      else
+        squares(kSmallUp, sum.small);
     }
   }
-  sum = warp_sum(sum);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+  sum = {warp_sum(sum.small), warp_sum(sum.plain), warp_sum(sum.large)};
+  if ((threadIdx.x & 31) == 0) {
+    float* own = red[threadIdx.x >> 5];
+    own[0] = sum.small, own[1] = sum.plain, own[2] = sum.large;
+  }
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x < 3) {  // a thread for each part
     float all = 0.0f;
-    for (int w = 0; w < kThreads / 32; ++w) all += red[w];
-    sums[blockIdx.x] = all;
+    for (int w = 0; w < kThreads / 32; ++w) all += red[w][threadIdx.x];
+    reinterpret_cast<float*>(sums + blockIdx.x)[threadIdx.x] = all;
   }
 }
 
 template <typename T, int kV>
 __global__ void __launch_bounds__(kThreads)
-    scale_kernel(const T* __restrict__ g, const Matrix a, int parts, int tx, const float* __restrict__ sums, float eps,
+    scale_kernel(const T* __restrict__ g, const Matrix a, int parts, int tx, const Squares* __restrict__ sums, float eps,
                  __half* __restrict__ x, __half* __restrict__ x_low, int64_t ldx, int64_t stride_x) {
-  __shared__ float factor;
+  __shared__ float shared_unit, shared_factor;
   pdl_wait();
   const int64_t b = blockIdx.x / parts, part = blockIdx.x % parts;
   const int ty = kThreads / tx;
   if (threadIdx.x < 32) {
-    float s = 0.0f;
-    for (int i = threadIdx.x; i < parts; i += 32) s += sums[b * parts + i];
-    s = warp_sum(s);
-    if (threadIdx.x == 0) factor = kXScale / (sqrtf(s) + eps);
+    Squares s = {};
+    for (int i = threadIdx.x; i < parts; i += 32) {
+      const Squares part_sums = sums[b * parts + i];
+      s.small += part_sums.small, s.plain += part_sums.plain, s.large += part_sums.large;
+    }
+    s = {warp_sum(s.small), warp_sum(s.plain), warp_sum(s.large)};
+    if (threadIdx.x == 0) {
+      const Norm norm(s);
+      shared_unit = norm.unit;
+      shared_factor = kXScale / (norm.r + eps * norm.unit);
+    }
   }
   __syncthreads();
-  const float f = factor;
+  const float unit = shared_unit, f = shared_factor;
   const uint64_t in_bytes = ((a.batch - 1) * a.stride + (a.m - 1) * a.ld + a.last) * sizeof(T);
   const uint64_t out_bytes = static_cast<uint64_t>((a.batch - 1) * stride_x + (a.m - 1) * ldx + a.last) * 2;
   for (int64_t r = part * ty + threadIdx.x / tx; r < a.m; r += static_cast<int64_t>(parts) * ty) {
@@ -154,12 +203,12 @@ __global__ void __launch_bounds__(kThreads)
         __half* at = to + (c + q * tx) * kV;
         Vec<uint16_t, kV> o;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) o.v[j] = __half_as_ushort(__float2half_rn(widen(v[q].v[j]) * f));
+        for (int j = 0; j < kV; ++j) o.v[j] = __half_as_ushort(__float2half_rn(widen(v[q].v[j]) * unit * f));
         *reinterpret_cast<Vec<uint16_t, kV>*>(at) = o;
         if (x_low == nullptr) continue;
 #pragma unroll
         for (int j = 0; j < kV; ++j)
-          o.v[j] = __half_as_ushort(__float2half_rn(widen(v[q].v[j]) * f - __half2float(__ushort_as_half(o.v[j]))));
+          o.v[j] = __half_as_ushort(__float2half_rn(widen(v[q].v[j]) * unit * f - __half2float(__ushort_as_half(o.v[j]))));
         *reinterpret_cast<Vec<uint16_t, kV>*>(x_low + (at - x)) = o;
       }
     }
@@ -833,7 +882,7 @@ Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   }
   l.d_gram = take(up(batch * l.lds * 4, 256));
   l.d_poly = take(up(batch * l.lds * 4, 256));
-  l.sums = take(up(batch * kMaxParts * 4, 256));
+  l.sums = take(up(batch * kMaxParts * static_cast<int64_t>(sizeof(Squares)), 256));
   l.partial = take(up(gram_slices(batch, l.side, l.side == m ? n : m) * batch * l.side * l.lds * 4, 256));
   l.bytes = at;
   return l;
@@ -908,7 +957,7 @@ int launch_scale(const void* g, Matrix a, float eps, uint8_t* ws, const Layout& 
   if (parts > most) parts = most;
   if (parts > kMaxParts) parts = kMaxParts;
   const unsigned blocks = static_cast<unsigned>(a.batch * parts);
-  float* sums = reinterpret_cast<float*>(ws + l.sums);
+  Squares* sums = reinterpret_cast<Squares*>(ws + l.sums);
   const int rc = launch_pdl(norm_kernel<T, kV>, blocks, kThreads, 0, stream, static_cast<const T*>(g), a,
                             static_cast<int>(parts), tx, sums);
   if (rc != MXQ_OK) return rc;

@@ -404,8 +404,8 @@ int mxq_embedding_backward(const void *ids, int ids_bytes, int64_t tokens, const
  * about 1e-3 (Frobenius, of the result's norm) for five steps of the usual
  * coefficients, beside the 1.7e-3 of the rounding to bf16; sides up to 64 carry
  * pairs of fp16 and are exact to the rounding.  The norm is right for any finite g (its
- * squares are summed in three ranges of fp32); a matrix of zeros gives 0, or NaN with
- * eps == 0.  The iterates are taken to stay within |X| <= 1.5 in the spectral norm,
+ * squares are summed in three ranges of fp32), and X has the same relative error where
+ * |g| is far below eps; a matrix of zeros gives 0, or NaN with eps == 0.  The iterates are taken to stay within |X| <= 1.5 in the spectral norm,
  * as they do for the usual coefficients (3.4445, -4.775, 2.0315); beyond eight
  * times that fp16 overflows.  Directions in which g is zero, or below 2^-12 of
  * its norm, carry rounding noise that the iteration magnifies up to a^steps.

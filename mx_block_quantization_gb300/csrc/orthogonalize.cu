@@ -14,7 +14,8 @@
 // about 1.2 for the usual coefficients, so no element is larger), and the three
 // more mantissa bits make the rounding of an operand 2^-12 instead of 2^-9.
 // Powers of two keep small elements out of fp16's subnormal range: X is stored
-// times 2^13, A and P times powers taken from the coefficients' bounds.
+// times 2^13 (and more where |g| is far below eps, see Lift), A and P times powers
+// taken from the coefficients' bounds.
 //
 // The square is completed: with S = A + (b/2c) I, which the gram product's
 // epilogue stores in A's place, P = c S S + (a - b^2/4c) I, and the square reads no
@@ -106,6 +107,26 @@ struct Norm {
   }
 };
 
+// Where |g| is far below eps, X starts far below 1, and fp16 at a fixed scale would have
+// no bits for it (|g| = 1e-14 with an eps of 1e-7: two steps of a subnormal).  Such a
+// matrix's X is stored 2^h times larger, h = max(0, lift - drop): `lift`, by how many
+// whole powers of two |g| + eps exceeds |g|, is the matrix's own, and `drop` grows with
+// the steps by what a step can magnify at most.  So |X| 2^h stays at most 1, and X leaves
+// the lift behind before it reaches the size of other matrices' X.  At most kMaxLift,
+// with which the last product's factor is still a normal number.
+constexpr int kMaxLift = 96;
+struct Lift {
+  const int32_t* of;            // [batch], or NULL: none
+  int32_t drop_from, drop_to;   // of the X read and of the X written
+  int32_t out_from, in_to;      // powers of 2^-h and 2^h in the product's factor
+  __device__ __forceinline__ float factor(int64_t batch) const {
+    if (of == nullptr) return 1.0f;
+    const int lift = of[batch], from = max(0, lift - drop_from), to = max(0, lift - drop_to);
+    const int e = in_to * to - out_from * from;  // at most 0: what is stored never grows in a product
+    return __int_as_float(max(0, e + 127) << 23);
+  }
+};
+
 // Blocks of a matrix take rows in turn; tx threads (a power of two) share a row.
 // Where the matrix and X have no gaps between their rows, the rows are pieces of
 // kThreads * kAhead loads instead (launch_scale).  Both kernels are bound by DRAM;
@@ -163,7 +184,7 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, int kV>
 __global__ void __launch_bounds__(kThreads)
     scale_kernel(const T* __restrict__ g, const Matrix a, int parts, int tx, const Squares* __restrict__ sums, float eps,
-                 __half* __restrict__ x, __half* __restrict__ x_low, int64_t ldx, int64_t stride_x) {
+                 int32_t* __restrict__ lifts, __half* __restrict__ x, __half* __restrict__ x_low, int64_t ldx, int64_t stride_x) {
   __shared__ float shared_unit, shared_factor;
   pdl_wait();
   const int64_t b = blockIdx.x / parts, part = blockIdx.x % parts;
@@ -178,7 +199,13 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0) {
       const Norm norm(s);
       shared_unit = norm.unit;
-      shared_factor = kXScale / (norm.r + eps * norm.unit);
+      // (|g| + eps) / |g|, without the overflow of eps in units of a small norm
+      const float over = 1.0f + eps / norm.r * norm.unit;
+      const bool lifted = norm.r > 0.0f && over >= 2.0f;
+      const int lift = lifted ? min((__float_as_int(over) >> 23) - 127, kMaxLift) : 0;  // its exponent; infinity: the most
+      const float less = __int_as_float((127 - lift) << 23);
+      shared_factor = kXScale / (lifted ? norm.r * (over * less) : norm.r + eps * norm.unit);
+      if (part == 0) lifts[b] = lift;
     }
   }
   __syncthreads();
@@ -260,6 +287,7 @@ struct Product {
   bf16_t* out;             // NULL: fp16 through map d
   int64_t ldo, stride_o;
   int32_t out_map;         // bf16 through map d
+  Lift lift;               // in `scale`
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -580,6 +608,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       const int64_t row0 = static_cast<int64_t>(at.i) * kTile + rank * kHalf + quarter * 32;
       const int64_t row = row0 + lane;
       const bool mirror = kSymmetric && at.i != at.j, both = needs_both(at) || kAddends == 2;
+      const float scale = p.scale * p.lift.factor(at.batch);
       const float dr = p.d_row != nullptr && row < p.rows ? p.d_row[at.batch * p.d_ld + row] : 0.0f;
       if (kColumns && lane < 4) {  // this warp's 128 columns, four lines
         const int64_t col = static_cast<int64_t>(at.j) * kTile + 2 * (e >> 2) * kChunkCols + 32 * lane;
@@ -646,7 +675,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           return true;
         };
         if (store_partial()) continue;
-        const float k0 = fmaf(p.scale, dr, p.add_scale);
+        const float k0 = fmaf(scale, dr, p.add_scale);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // 32 columns at a time
           const int64_t col = col0 + 32 * h;
@@ -659,7 +688,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           }
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[h][i]) * p.scale;
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(raw[h][i]) * scale;
           if (kAddends > 0) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -674,15 +703,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 const float4 d = dc[2 * q + i / 4];
-                const float k = kColumns ? fmaf(p.scale, i % 4 == 0 ? d.x : i % 4 == 1 ? d.y : i % 4 == 2 ? d.z : d.w, k0) : k0;
+                const float k = kColumns ? fmaf(scale, i % 4 == 0 ? d.x : i % 4 == 1 ? d.y : i % 4 == 2 ? d.z : d.w, k0) : k0;
                 v[8 * q + i] = fmaf(k, a[i], v[8 * q + i]);
               }
             }
           }
           if (kSymmetric && row0 < col + 32 && col < row0 + 32) {  // the warp's rows meet these columns
             const int own_column = static_cast<int>(row - col);
-            float on = p.diagonal + p.add_scale * dr + p.scale * dr * dr;
-            if (p.square_rest != nullptr && row < p.rows) on = fmaf(p.scale, p.square_rest[at.batch * p.d_ld + row], on);
+            float on = p.diagonal + p.add_scale * dr + scale * dr * dr;
+            if (p.square_rest != nullptr && row < p.rows) on = fmaf(scale, p.square_rest[at.batch * p.d_ld + row], on);
             float own = 0.0f;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -796,6 +825,7 @@ struct Join {
   int64_t batch, side, ld, stride;
   int slices;
   float scale, diagonal;
+  Lift lift;
   __half *high, *low;
   float* d_out;  // or NULL
   int32_t d_squares;
@@ -811,7 +841,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Join a) {
   float sum = 0.0f;
 #pragma unroll 8
   for (int s = 0; s < a.slices; ++s) sum += p[s * a.stride];
-  const float v = sum * a.scale + (i == j ? a.diagonal : 0.0f), h = half_rounded(v);
+  const float v = sum * (a.scale * a.lift.factor(row / a.side)) + (i == j ? a.diagonal : 0.0f), h = half_rounded(v);
   const uint64_t bytes = static_cast<uint64_t>(n) * 2;
   if (!in_buf(a.high + at, 2, a.high, bytes, &g_ortho_status)) return;
   a.high[at] = __float2half_rn(v);
@@ -861,7 +891,7 @@ struct Layout {
   int parts;                         // 2 with low parts
   int64_t x[2][2];                   // X of the even and of the odd steps: high, low
   int64_t gram[2], poly[2];
-  int64_t d_gram, d_poly, sums, partial, bytes;
+  int64_t d_gram, d_poly, sums, lifts, partial, bytes;
 };
 Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   Layout l;
@@ -883,6 +913,7 @@ Layout layout_of(int64_t batch, int64_t m, int64_t n) {
   l.d_gram = take(up(batch * l.lds * 4, 256));
   l.d_poly = take(up(batch * l.lds * 4, 256));
   l.sums = take(up(batch * kMaxParts * static_cast<int64_t>(sizeof(Squares)), 256));
+  l.lifts = take(up(batch * 4, 256));
   l.partial = take(up(gram_slices(batch, l.side, l.side == m ? n : m) * batch * l.side * l.lds * 4, 256));
   l.bytes = at;
   return l;
@@ -962,7 +993,8 @@ int launch_scale(const void* g, Matrix a, float eps, uint8_t* ws, const Layout& 
                             static_cast<int>(parts), tx, sums);
   if (rc != MXQ_OK) return rc;
   return launch_pdl(scale_kernel<T, kV>, blocks, kThreads, 0, stream, static_cast<const T*>(g), a,
-                    static_cast<int>(parts), tx, sums, eps, reinterpret_cast<__half*>(ws + l.x[0][0]),
+                    static_cast<int>(parts), tx, sums, eps, reinterpret_cast<int32_t*>(ws + l.lifts),
+                    reinterpret_cast<__half*>(ws + l.x[0][0]),
                     l.parts == 2 ? reinterpret_cast<__half*>(ws + l.x[0][1]) : nullptr, ldx, stride_x);
 }
 template <typename T>
@@ -1062,6 +1094,12 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
   const bool split = parts == 2;
   float* d_gram = reinterpret_cast<float*>(workspace + l.d_gram);
   float* d_poly = reinterpret_cast<float*>(workspace + l.d_poly);
+  // what a step can magnify X by at most while |X| <= 1/2, in powers of two
+  const double growth = log2(fmax(1.0, fabs(ca) + fabs(cb) / 4 + fabs(cc) / 16));
+  const auto lift = [&](int s, int32_t out_from, int32_t in_to) {
+    return Lift{reinterpret_cast<const int32_t*>(workspace + l.lifts), static_cast<int32_t>(ceil(s * growth)),
+                static_cast<int32_t>(ceil((s + 1) * growth)), out_from, in_to};
+  };
   for (int s = 0; s < steps; ++s) {
     const int from = s & 1, to = from ^ 1;
     Maps maps = {};
@@ -1076,6 +1114,7 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.ksteps = static_cast<int32_t>(ceil_div(length, kStepK));
     p.a_mn = p.b_mn = !wide;
     p.scale = sa / (kXScale * kXScale);
+    p.lift = lift(s, 2, 0);
     p.diagonal = static_cast<float>(shift * sa);
     p.d_ld = l.lds;
     if (!split) {
@@ -1091,7 +1130,7 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
       rc = split ? launch_product<true, 0, false, false, true, true>(maps, p, batch, sms, stream)
                  : launch_product<true, 0, false, false, false, true>(maps, p, batch, sms, stream);
       if (rc != MXQ_OK) return rc;
-      const Join join = {p.partial, batch, side, l.lds, p.partial_stride, p.slices, p.scale, p.diagonal,
+      const Join join = {p.partial, batch, side, l.lds, p.partial_stride, p.slices, p.scale, p.diagonal, p.lift,
                          reinterpret_cast<__half*>(workspace + l.gram[0]),
                          split ? reinterpret_cast<__half*>(workspace + l.gram[1]) : nullptr, p.d_out, p.d_squares};
       rc = launch_pdl(join_kernel, static_cast<unsigned>(ceil_div(p.partial_stride, kThreads)), kThreads, 0, stream, join);
@@ -1151,6 +1190,7 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
       p.out_map = out_map;
       p.scale = scale / (sp * kXScale);
     }
+    p.lift = lift(s, 1, last ? 0 : 1);
     if (split)
       rc = last ? launch_product<false, 0, false, true, true, false>(maps, p, batch, sms, stream)
                 : launch_product<false, 0, false, false, true, false>(maps, p, batch, sms, stream);

@@ -868,7 +868,11 @@ constexpr int64_t kSplitSide = 64;
 // the further launch costs 5 us (64x8192: 661 us with one slice, 128 with 64, the
 // choice here; 512x8192: 321 and 212; 300x5000: 236 and 154; 1000x2000: 209 us with
 // one, the choice, and 234 with two).  Returns 0 for one slice.  Sized for the pairs of the whole GPU, whatever it has.
-constexpr int64_t kPairs = 76, kSliceStages = 6;
+// K is sliced in any case after kMostStages: the tensor cores' additions to an fp32
+// accumulator cut off what does not fit, a third of a unit in the last place on
+// average, and the diagonal's sum of squares loses that with every 16 of K (0.8% of the
+// result for 1 x 2^20 in one slice).  512 stages lose 9e-5 of it.
+constexpr int64_t kPairs = 76, kSliceStages = 6, kMostStages = 512;
 int64_t gram_slices(int64_t batch, int64_t side, int64_t length) {
   const int64_t tiles_m = ceil_div(side, kTile), tiles = batch * tiles_m * (tiles_m + 1) / 2;
   if (tiles == 0) return 0;
@@ -877,10 +881,14 @@ int64_t gram_slices(int64_t batch, int64_t side, int64_t length) {
   const double slice_us = 8.0 * static_cast<double>(batch * side * side) / 4.0e6;
   int64_t most = kPairs / tiles;
   if (most > stages / kSliceStages) most = stages / kSliceStages;
-  int64_t best = 0;
-  double best_us = product_us;
-  for (int64_t n = 2; n <= most; ++n) {
-    const double us = product_us / static_cast<double>(n) + slice_us * static_cast<double>(n) + 5.0;
+  const int64_t least = ceil_div(stages, kMostStages);
+  int64_t best = least > 1 ? least : 0;
+  const auto us_of = [&](int64_t n) {
+    return product_us / static_cast<double>(n) + slice_us * static_cast<double>(n) + 5.0;
+  };
+  double best_us = best > 0 ? us_of(best) : product_us;
+  for (int64_t n = least > 2 ? least : 2; n <= most; ++n) {
+    const double us = us_of(n);
     if (us < best_us) best = n, best_us = us;
   }
   return best;
@@ -1017,6 +1025,10 @@ int check_ortho_shape(int64_t batch, int64_t m, int64_t n) {
       batch * ceil_div(m, kTile) * ceil_div(m, kTile) > INT32_MAX / 2 ||
       batch * ceil_div(n, kTile) * ceil_div(n, kTile) > INT32_MAX / 2)
     return MXQ_EBADSHAPE;
+  // and with K in slices those of all slices, and the blocks that add them up
+  const int64_t side = m < n ? m : n, tiles = ceil_div(side, kTile);
+  if (const int64_t slices = gram_slices(batch, side, m < n ? n : m); slices > 0)
+    if (batch * tiles * tiles * slices > INT32_MAX / 2 || batch * side * (side + 7) / kThreads >= INT32_MAX) return MXQ_EBADSHAPE;
   return MXQ_OK;
 }
 

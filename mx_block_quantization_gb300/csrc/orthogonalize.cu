@@ -1020,15 +1020,13 @@ constexpr int64_t kMaxSide = int64_t{1} << 20;
 
 int check_ortho_shape(int64_t batch, int64_t m, int64_t n) {
   if (batch < 0 || m < 0 || n < 0 || batch > 65535 || m > kMaxSide || n > kMaxSide) return MXQ_EBADSHAPE;
-  // tiles of a launch and elements of the stack within the kernels' counters
-  if (batch * ceil_div(m, kTile) * ceil_div(n, kTile) > INT32_MAX / 2 ||
-      batch * ceil_div(m, kTile) * ceil_div(m, kTile) > INT32_MAX / 2 ||
-      batch * ceil_div(n, kTile) * ceil_div(n, kTile) > INT32_MAX / 2)
+  // tiles of a launch within the kernels' counters: the square matrices', with K in slices
+  // those of all slices, and X's; and the blocks that add slices up
+  const int64_t side = m < n ? m : n, length = m < n ? n : m, slices = gram_slices(batch, side, length);
+  const int64_t tiles = ceil_div(side, kTile);
+  if (batch * tiles * tiles * (slices > 0 ? slices : 1) > INT32_MAX / 2 || batch * tiles * ceil_div(length, kTile) > INT32_MAX / 2 ||
+      (slices > 0 && batch * side * (side + 7) / kThreads >= INT32_MAX))
     return MXQ_EBADSHAPE;
-  // and with K in slices those of all slices, and the blocks that add them up
-  const int64_t side = m < n ? m : n, tiles = ceil_div(side, kTile);
-  if (const int64_t slices = gram_slices(batch, side, m < n ? n : m); slices > 0)
-    if (batch * tiles * tiles * slices > INT32_MAX / 2 || batch * side * (side + 7) / kThreads >= INT32_MAX) return MXQ_EBADSHAPE;
   return MXQ_OK;
 }
 

@@ -110,3 +110,16 @@ def test_very_long_sums(batch, m, n):
     for y, want in zip(got, on_the_gpu(g)):
         y = y.double() if m <= n else y.double().t()
         assert float((y - want).norm() / want.norm()) <= (2.0**-9 if min(m, n) <= 64 else 2.25e-3)
+
+
+@pytest.mark.parametrize("m,n", [(1 << 20, 1), (1, 1 << 20)])
+def test_stacks_of_the_longest_vectors(m, n):
+    """A vector's only singular value is its norm: the result is a multiple of it."""
+    g = torch.randn(64, m, n, device="cuda")
+    norm = g.double().flatten(1).norm(dim=1)
+    s = norm / (norm + 1e-7)
+    for _ in range(5):
+        s = s * (3.4445 - 4.775 * s**2 + 2.0315 * s**4)
+    got = mxq.orthogonalize(g).double()
+    want = g.double() * (s / norm)[:, None, None]
+    assert float(((got - want).flatten(1).norm(dim=1) / s).max()) <= 2.0**-9

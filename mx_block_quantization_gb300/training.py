@@ -9,7 +9,8 @@ each operation; there is no CPU path.
 
 Matrices may have strided rows (unit column stride).  With ``stream`` a call runs
 on that stream, and the outputs and workspaces that it allocates belong to it;
-otherwise it runs on the current stream of the tensors' device.
+it has to be a stream of the tensors' device.  Otherwise the call runs on the current
+stream of that device.
 """
 from __future__ import annotations
 
@@ -81,6 +82,8 @@ def _elsewhere(device, stream):
     """None when a call on `device` may run as things are, else the context in
     which its allocations and launches belong to its device and stream."""
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream must be one of {device}, where the tensors are, not of {stream.device}")
         return torch.cuda.stream(stream)
     return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 

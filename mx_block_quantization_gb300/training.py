@@ -14,11 +14,12 @@ stream of that device.
 """
 from __future__ import annotations
 
+from operator import index
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import BF16, F32, OK, MxqError, lib
+from . import BF16, EBADSHAPE, F32, OK, MxqError, lib
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16}
 
@@ -35,6 +36,14 @@ class MoePlan(NamedTuple):
     offs: torch.Tensor    # int32 [E]: cumulative group ends, multiples of 128
     slots: torch.Tensor   # int32 [T, k]: row of each assignment, -1 for none
     source: torch.Tensor  # int32 [M]: assignment of each row, -1 for none
+
+
+def _count(value, what):
+    """A count as the C entries take it; ctypes would cut it to its lowest bits."""
+    value = index(value)
+    if not -1 << 31 <= value < 1 << 31:
+        raise MxqError(EBADSHAPE, what)
+    return value
 
 
 def _code(t, name):
@@ -117,6 +126,7 @@ def moe_route(logits, k: int, *, mask=None, renorm: bool = True, out: Optional[R
     dev = logits.device
     ld = _matrix(logits, "logits")
     code = _code(logits, "logits")
+    k = _count(k, "mxq_moe_route")
     where = _elsewhere(dev, stream)
     if where is not None:
         with where:
@@ -183,7 +193,8 @@ def moe_route_backward(logits, routing: Routing, dweights=None, dloss=None, *, m
 
 def moe_rows(tokens: int, k: int, experts: int) -> int:
     """Rows that hold every routing of these sizes in groups of whole 128 rows."""
-    m = lib().mxq_moe_rows(tokens, k, experts)
+    what = "mxq_moe_rows"
+    m = lib().mxq_moe_rows(_count(tokens, what), _count(k, what), _count(experts, what))
     if m < 0:
         raise MxqError(int(m), "mxq_moe_rows")
     return int(m)
@@ -199,6 +210,8 @@ def moe_plan(ids, experts: int, *, rows: Optional[int] = None, out: Optional[Moe
     T, k = ids.shape
     dev = ids.device
     p = _flat(ids, "ids", torch.int32, (T, k), dev)
+    experts = _count(experts, "mxq_moe_plan")
+    rows = None if rows is None else _count(rows, "mxq_moe_plan")
     where = _elsewhere(dev, stream)
     if where is not None:
         with where:
@@ -207,7 +220,7 @@ def moe_plan(ids, experts: int, *, rows: Optional[int] = None, out: Optional[Moe
     size = L.mxq_moe_plan_workspace(T, k, experts)
     ws, wp = _workspace(size, "mxq_moe_plan", dev)
     if out is None:
-        M = L.mxq_moe_rows(T, k, experts) if rows is None else int(rows)
+        M = L.mxq_moe_rows(T, k, experts) if rows is None else rows
         out = MoePlan(torch.empty(experts, dtype=torch.int32, device=dev),
                       torch.empty((T, k), dtype=torch.int32, device=dev),
                       torch.empty(max(M, 0), dtype=torch.int32, device=dev))
@@ -376,6 +389,7 @@ def embedding_backward(ids, dy, rows: int, *, scale: float = 1.0, padding_idx: O
     D = dy.shape[-1]
     T = ids.numel()
     ldd = _matrix(dy if dy.dim() == 2 else dy.view(-1, D) if T and D else dy.reshape(T, D), "dy", T, D)
+    rows = _count(rows, "mxq_embedding_backward")
     if padding_idx is not None and not 0 <= padding_idx < rows:
         raise ValueError(f"padding_idx must be in [0, {rows})")
     where = _elsewhere(dev, stream)
@@ -429,6 +443,7 @@ def orthogonalize(g, *, steps: int = 5, coefficients=(3.4445, -4.775, 2.0315), e
     code = _code(g, "g")
     batch, m, n, ld, stride = _stacked(g, "g")
     a, b, c = coefficients
+    steps = _count(steps, "mxq_orthogonalize")
     dev = g.device
     where = _elsewhere(dev, stream)
     if where is not None:

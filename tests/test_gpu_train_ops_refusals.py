@@ -23,7 +23,7 @@ def test_counts_past_32_bits_are_refused():
     room = mxq.moe_plan(ids, 2)
     for call in (lambda: mxq.orthogonalize(g, steps=far + 5), lambda: mxq.moe_route(g, far + 2),
                  lambda: mxq.moe_plan(ids, far + 2, out=room), lambda: mxq.moe_plan(ids, 2, rows=far + 256),
-                 lambda: mxq.embedding_backward(ids[:, 0], g[:4], far + 3, out=torch.empty(3, 9, device="cuda"))):
+                 lambda: mxq.embedding_backward(ids[:, 0].contiguous(), g[:4], far + 3, out=torch.empty(3, 9, device="cuda"))):
         with pytest.raises(mxq.MxqError) as e:
             call()
         assert e.value.code == mxq.EBADSHAPE

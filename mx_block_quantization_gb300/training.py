@@ -74,6 +74,16 @@ def _matrix(t, name, rows=None, cols=None, device=None):
     return ld
 
 
+def _rows_of(t, name, T, D):
+    """[..., D] as a matrix [T, D] of the same memory."""
+    if t.dim() == 2 or T == 0 or D == 0:
+        return t.reshape(T, D)
+    try:
+        return t.view(T, D)
+    except RuntimeError:
+        raise ValueError(f"{name} must have rows a fixed distance apart") from None
+
+
 def _flat(t, name, dtype, shape, device):
     """A contiguous CUDA tensor of one type and shape."""
     if not t.is_cuda:
@@ -365,7 +375,7 @@ def embedding(ids, table, *, scale: float = 1.0, dtype=None, out=None, stream=No
             raise ValueError(f"out must be {dtype}")
         if out.shape != (*ids.shape, D):
             raise ValueError(f"out must be {[*ids.shape, D]}")
-        ldy = _matrix(out if out.dim() == 2 else out.view(-1, D), "out", T, D, dev)
+        ldy = _matrix(_rows_of(out, "out", T, D), "out", T, D, dev)
     rc = lib().mxq_embedding(p, ib, T, table.data_ptr(), code, V, D, ldw, scale, out.data_ptr(), _code(out, "out"), ldy,
                              _stream(dev.index))
     if rc != OK:
@@ -388,7 +398,7 @@ def embedding_backward(ids, dy, rows: int, *, scale: float = 1.0, padding_idx: O
     code = _code(dy, "dy")
     D = dy.shape[-1]
     T = ids.numel()
-    ldd = _matrix(dy if dy.dim() == 2 else dy.view(-1, D) if T and D else dy.reshape(T, D), "dy", T, D)
+    ldd = _matrix(_rows_of(dy, "dy", T, D), "dy", T, D)
     rows = _count(rows, "mxq_embedding_backward")
     if padding_idx is not None and not 0 <= padding_idx < rows:
         raise ValueError(f"padding_idx must be in [0, {rows})")

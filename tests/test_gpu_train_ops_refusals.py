@@ -29,3 +29,26 @@ def test_counts_past_32_bits_are_refused():
         assert e.value.code == mxq.EBADSHAPE
     with pytest.raises(TypeError):
         mxq.orthogonalize(g, steps=5.0)
+
+
+def test_rows_at_no_fixed_distance_and_rows_of_nothing():
+    table = torch.randn(10, 8, device="cuda")
+    ids = torch.randint(0, 10, (3, 5), device="cuda")
+    dy = torch.randn(5, 3, 8, device="cuda").transpose(0, 1)
+    for call in (lambda: mxq.embedding(ids, table, out=torch.empty_like(dy)),
+                 lambda: mxq.embedding(ids, table, out=torch.empty(5, 3, 8, device="cuda").transpose(0, 1)),
+                 lambda: mxq.embedding_backward(ids, dy, 10)):
+        with pytest.raises(ValueError, match="rows"):
+            call()
+    for n, rows in ((5, 0), (0, 8)):
+        none = torch.empty(3, n, rows, device="cuda")
+        some = ids[:, :n].contiguous()
+        assert mxq.embedding(some, table[:, :rows], out=none) is none
+        grad = mxq.embedding_backward(some, none, 10)
+        assert grad.shape == (10, rows) and (grad == 0).all()
+    # single rows and single tokens of wider tensors
+    one = torch.randn(1, 1, 20, device="cuda")[..., 3:11]
+    got = mxq.embedding_backward(ids[:1, :1].contiguous(), one, 10)
+    want = torch.zeros(10, 8, device="cuda")
+    want[ids[0, 0]] = one[0, 0]
+    assert torch.equal(got, want)

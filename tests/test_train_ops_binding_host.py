@@ -39,3 +39,20 @@ def test_counts_past_32_bits_are_refused(args):
     with pytest.raises(mxq.MxqError) as e:
         mxq.moe_rows(*args)
     assert e.value.code == mxq.EBADSHAPE
+
+
+def test_rows_of_a_tensor_share_its_memory_or_are_refused():
+    """Rows at no fixed distance were torch's RuntimeError, and rows of no elements too."""
+    x = torch.arange(2 * 3 * 8.0).view(2, 3, 8)
+    for t in (x, x[..., 1:6], x[:, :1], x[:1], x[0], x[0, 1]):
+        D = t.shape[-1]
+        r = training._rows_of(t, "x", t.numel() // D, D)
+        assert torch.equal(r, t.reshape(-1, D)) and r.data_ptr() == t.data_ptr()
+    for t in (x.transpose(0, 1), x[:, :2], x.permute(1, 0, 2)[..., :4]):
+        with pytest.raises(ValueError, match="x must have rows"):
+            training._rows_of(t, "x", t.shape[0] * t.shape[1], t.shape[2])
+    for shape in ((2, 3, 0), (0, 3, 8), (2, 0, 8), (0,), (0, 0)):
+        T = 1
+        for n in shape[:-1]:
+            T *= n
+        assert training._rows_of(torch.empty(shape), "x", T, shape[-1]).shape == (T, shape[-1])

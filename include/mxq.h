@@ -453,9 +453,15 @@ int mxq_selftest_wait_timeout(uint64_t limit_ns, cudaStream_t stream);
  * tests a range lying past a 64-byte dummy buffer, without any access: a
  * checked build records MXQ_DEV_OOB, a release build records nothing.
  * Returns MXQ_OK or MXQ_ECUDA.
+ * mxq_selftest_watch() makes a checked build count every access of the
+ * training operators' kernels that touches `address` (device memory; NULL: no
+ * address) as one outside its buffer, which is left out and recorded, so that
+ * a test can see that an access is checked; a release build takes the call and
+ * does nothing.  It waits for the device.
  */
 int mxq_debug_bounds(void);
 int mxq_selftest_bounds(cudaStream_t stream);
+int mxq_selftest_watch(const void *address);
 
 /* Static description of a status code (never NULL). */
 const char *mxq_status_string(int status);

@@ -140,6 +140,8 @@ def lib() -> ctypes.CDLL:
         L.mxq_debug_bounds.argtypes = []
         L.mxq_selftest_bounds.restype = ctypes.c_int
         L.mxq_selftest_bounds.argtypes = [vp]
+        L.mxq_selftest_watch.restype = ctypes.c_int
+        L.mxq_selftest_watch.argtypes = [vp]
         L.mxq_device_status.restype = ctypes.c_int
         L.mxq_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
         L.mxq_status_string.restype = ctypes.c_char_p
@@ -191,6 +193,14 @@ def selftest_bounds(stream=None) -> None:
     rc = lib().mxq_selftest_bounds(ctypes.c_void_p(s.cuda_stream))
     if rc != OK:
         raise MxqError(rc, "mxq_selftest_bounds")
+
+
+def selftest_watch(address: int = 0) -> None:
+    """Checked library: the training operators' accesses of this device address count
+    as outside their buffers, are left out and reported as DEV_OOB (0: none)."""
+    rc = lib().mxq_selftest_watch(address)
+    if rc != OK:
+        raise MxqError(rc, "mxq_selftest_watch")
 
 
 # ---------------------------------------------------------------------------

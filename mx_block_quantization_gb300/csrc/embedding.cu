@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kThreads)
   bool live[kTokens];
   int64_t id[kTokens];
 #pragma unroll
-  for (int k = 0; k < kTokens; ++k) id[k] = t0 + k * groups < s.tokens ? static_cast<int64_t>(ids[t0 + k * groups]) : 0;
+  for (int k = 0; k < kTokens; ++k) id[k] = t0 + k * groups < s.tokens ? static_cast<int64_t>(read_at(ids, t0 + k * groups, s.tokens, I{0}, &g_embedding_status)) : 0;
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kTokens; ++k) {
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kThreads)
   const int64_t t = static_cast<int64_t>(blockIdx.x / tiles) * (kThreads / s.tx) + group;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x % tiles) * tile;
   const int n = t < s.tokens ? static_cast<int>(min(static_cast<int64_t>(tile), s.D - c0)) : 0;
-  const int64_t id = n > 0 ? static_cast<int64_t>(ids[t]) : -1;
+  const int64_t id = n > 0 ? static_cast<int64_t>(read_at(ids, t, s.tokens, I{0}, &g_embedding_status)) : -1;
   const bool live = id >= 0 && id < s.rows;
   if (n > 0 && !live && own == 0) atomicOr(&g_embedding_status, MXQ_DEV_BADINDEX);
   const T* row = table + (live ? id * s.ldw + c0 : 0);
@@ -151,8 +151,11 @@ __device__ __forceinline__ void zero_bytes(uint8_t* p, int64_t n, int64_t first,
   uint4* q = reinterpret_cast<uint4*>(p + head);
   for (int64_t i = first; i < body; i += step)
     if (in_buf(q + i, 16, f.table, f.table_bytes, &g_embedding_status)) q[i] = make_uint4(0u, 0u, 0u, 0u);
-  if (first < head / 2) reinterpret_cast<uint16_t*>(p)[first] = 0;
-  if (first < tail / 2) reinterpret_cast<uint16_t*>(p + head + 16 * body)[first] = 0;
+  const auto zero_two = [&](uint8_t* at) {
+    if (in_buf(at, 2, f.table, f.table_bytes, &g_embedding_status)) *reinterpret_cast<uint16_t*>(at) = 0;
+  };
+  if (first < head / 2) zero_two(p + 2 * first);
+  if (first < tail / 2) zero_two(p + head + 16 * body + 2 * first);
 }
 
 // Blocks past the launch's own zero the fill; true for those.
@@ -177,9 +180,9 @@ __device__ __forceinline__ bool fill_block(const Fill& f, int own_blocks) {
 template <typename I>
 struct IdKey {
   const I* ids;
-  int64_t rows, padding;
+  int64_t rows, padding, n;
   __device__ int full(int64_t i) const {
-    const int64_t id = ids[i];
+    const int64_t id = read_at(ids, i, n, I{0}, &g_embedding_status);
     if (id < 0 || id >= rows) {
       atomicOr(&g_embedding_status, MXQ_DEV_BADINDEX);
       return static_cast<int>(rows);
@@ -190,8 +193,9 @@ struct IdKey {
 };
 struct SortedKey {
   const int32_t *keys, *tokens;
-  __device__ int full(int64_t i) const { return keys[i]; }
-  __device__ int token(int64_t i) const { return tokens[i]; }
+  int64_t n;
+  __device__ int full(int64_t i) const { return read_at(keys, i, n, 0, &g_embedding_status); }
+  __device__ int token(int64_t i) const { return read_at(tokens, i, n, 0, &g_embedding_status); }
 };
 
 template <typename Source>
@@ -202,8 +206,7 @@ __global__ void __launch_bounds__(kRankThreads)
   pdl_launch_dependents();  // the sort's blocks wait beside the zeroing ones
   if (fill_block<kRankThreads>(fill, s.chunks)) return;
   rank_count(s, bins, [&](int64_t i) { return (src.full(i) >> shift) & (bins - 1); }, counts);
-  for (int b = threadIdx.x; b < bins; b += kRankThreads)
-    chunk_counts[static_cast<int64_t>(blockIdx.x) * bins + b] = counts[b];
+  rank_keep_counts(s, bins, counts, chunk_counts, &g_embedding_status);
 }
 
 template <typename Source>
@@ -223,18 +226,16 @@ __global__ void __launch_bounds__(kRankThreads)
     rank_count(s, bins, key, total);
     for (int b = threadIdx.x; b < bins; b += kRankThreads) next[b] = 0;
   } else {
-    rank_totals(s, bins, chunk_counts, total, next);
+    rank_totals(s, bins, chunk_counts, total, next, &g_embedding_status);
   }
   rank_begins<1>(bins, total, begin, work);
   for (int b = threadIdx.x; b < bins; b += kRankThreads) next[b] += begin[b];
   __syncthreads();
-  const uint64_t bytes = static_cast<uint64_t>(s.n) * 4;
   rank_chunk(
       s, bins, key,
       [&](int64_t i, int, int32_t place) {
-        if (!in_buf(keys + place, 4, keys, bytes, &g_embedding_status)) return;
-        keys[place] = src.full(i);
-        tokens[place] = src.token(i);
+        write_at(keys, place, s.n, src.full(i), &g_embedding_status);
+        write_at(tokens, place, s.n, src.token(i), &g_embedding_status);
       },
       next, counts);
 }
@@ -335,11 +336,9 @@ __global__ void __launch_bounds__(kSmallThreads)
       __syncthreads();
     }
   }
-  const uint64_t bytes = static_cast<uint64_t>(n) * 4;
   for (int i = tid; i < n; i += kSmallThreads) {
-    if (!in_buf(keys + i, 4, keys, bytes, &g_embedding_status)) continue;
-    keys[i] = sorted_keys[i];
-    tokens[i] = sorted_tokens[i];
+    write_at(keys, i, n, sorted_keys[i], &g_embedding_status);
+    write_at(tokens, i, n, sorted_tokens[i], &g_embedding_status);
   }
 }
 
@@ -349,6 +348,7 @@ __global__ void __launch_bounds__(kSmallThreads)
 struct GradShape {
   int64_t tokens, rows, D, ldd, ldw;
 };
+__host__ __device__ inline int64_t piece_floats(const GradShape& s) { return ceil_div(s.tokens, kChunk) * 2 * s.D; }
 
 // First place whose key is >= v, by a whole warp: each step splits the range in
 // 33 with 32 probes at once (3 dependent loads for 32768 keys, where a binary
@@ -359,7 +359,7 @@ __device__ __forceinline__ int64_t warp_lower_bound(const int32_t* __restrict__ 
   while (lo < hi) {
     const int64_t step = (hi - lo) / 33 + 1;
     const int64_t at = lo + step * (lane + 1) - 1;  // probes lo + step - 1, lo + 2 step - 1, ...
-    const bool below = at < hi && keys[at] < v;
+    const bool below = at < hi && read_at(keys, at, n, 0, &g_embedding_status) < v;
     const int k = __popc(__ballot_sync(0xFFFFFFFFu, below));  // the first k probes lie below v
     const int64_t next = lo + step * k;
     hi = min(hi, next + step - 1);
@@ -391,7 +391,7 @@ __device__ __forceinline__ void add_tokens(const T* __restrict__ dy, const GradS
     Vec<T, kV> v[kAhead][kU];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const T* row = dy + (p + a < hi ? static_cast<int64_t>(tokens[p + a]) * s.ldd : 0);
+      const T* row = dy + (p + a < hi ? static_cast<int64_t>(read_at(tokens, p + a, s.tokens, 0, &g_embedding_status)) * s.ldd : 0);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const T* src = row + (c + u * tx) * kV;
@@ -427,12 +427,13 @@ __global__ void __launch_bounds__(kPieceThreads)
     // warp 0: the run of the chunk's first place; warp 1: that of its last one
     const int q = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t at = q == 0 ? lo : hi - 1;
-    const int32_t key = keys[at], first = keys[lo];
+    const auto key_at = [&](int64_t i) { return read_at(keys, i, s.tokens, 0, &g_embedding_status); };
+    const int32_t key = key_at(at), first = key_at(lo);
     // equal keys side by side, up to kChunk of them before the place and from it on
-    const bool before = at - 1 - lane >= 0 && keys[at - 1 - lane] == key;
-    const bool after = at + lane < s.tokens && keys[at + lane] == key;
+    const bool before = at - 1 - lane >= 0 && key_at(at - 1 - lane) == key;
+    const bool after = at + lane < s.tokens && key_at(at + lane) == key;
     const int left = __ffs(~__ballot_sync(0xFFFFFFFFu, before)) - 1, right = __ffs(~__ballot_sync(0xFFFFFFFFu, after)) - 1;
-    const bool next = at + kChunk < s.tokens && keys[at + kChunk] == key;  // one more than a whole chunk
+    const bool next = at + kChunk < s.tokens && key_at(at + kChunk) == key;  // one more than a whole chunk
     const int n_left = left < 0 ? 32 : left, n_right = right < 0 ? 32 + next : right;
     if (lane == 0) {
       const bool used = key < s.rows && n_left + n_right > kChunk && (q == 0 || key != first);
@@ -446,7 +447,6 @@ __global__ void __launch_bounds__(kPieceThreads)
   const int tx = column_blocks * kPieceThreads;
   for (int q = 0; q < 2; ++q) {
     if (part_lo[q] == part_hi[q]) continue;
-    float* out = pieces + (2 * chunk + q) * s.D;
     for (int64_t c = (blockIdx.x % column_blocks) * kPieceThreads + threadIdx.x; c < nv; c += kU * tx) {
       float acc[kU][kV] = {};
       add_tokens<T, kV, kU>(dy, s, tokens, lo + part_lo[q], lo + part_hi[q], c, tx, nv, acc);
@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(kPieceThreads)
       for (int u = 0; u < kU; ++u)
         if (c + u * tx < nv)
 #pragma unroll
-          for (int i = 0; i < kV; ++i) out[(c + u * tx) * kV + i] = acc[u][i];
+          for (int i = 0; i < kV; ++i)
+            write_at(pieces, (2 * chunk + q) * s.D + (c + u * tx) * kV + i, piece_floats(s), acc[u][i], &g_embedding_status);
     }
   }
 }
@@ -475,8 +476,9 @@ __device__ __forceinline__ void add_pieces(const float* __restrict__ pieces, con
 #pragma unroll
         for (int f = 0; f < kV / kF; ++f) {
           v[a][u][f] = Vec<float, kF>{};
-          if (q + a <= last && c + u * tx < nv)
-            v[a][u][f] = *reinterpret_cast<const Vec<float, kF>*>(piece + (c + u * tx) * kV + f * kF);
+          const float* p = piece + (c + u * tx) * kV + f * kF;
+          if (q + a <= last && c + u * tx < nv && in_buf(p, sizeof(float) * kF, pieces, piece_floats(s) * 4, &g_embedding_status))
+            v[a][u][f] = *reinterpret_cast<const Vec<float, kF>*>(p);
         }
     }
 #pragma unroll
@@ -506,12 +508,12 @@ __device__ __forceinline__ void zero_absent(const int32_t* __restrict__ keys, co
     int64_t lo = 0, hi = s.tokens;
     while (lo < hi) {
       const int64_t mid = (lo + hi) / 2;
-      if (keys[mid] < r)
+      if (read_at(keys, mid, s.tokens, 0, &g_embedding_status) < r)
         lo = mid + 1;
       else
         hi = mid;
     }
-    const uint32_t gone = __ballot_sync(0xFFFFFFFFu, r < s.rows && (lo == s.tokens || keys[lo] != r));
+    const uint32_t gone = __ballot_sync(0xFFFFFFFFu, r < s.rows && (lo == s.tokens || read_at(keys, lo, s.tokens, 0, &g_embedding_status) != r));
     if ((threadIdx.x & 31) == 0) absent[threadIdx.x / 32] = gone;
   }
   __syncthreads();
@@ -544,10 +546,10 @@ __global__ void __launch_bounds__(kThreads, 4)
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kStarts;
   if (threadIdx.x < 64) {
     const int64_t at = first + threadIdx.x;
-    near_key[threadIdx.x] = at < s.tokens ? keys[at] : -1;
-    near_token[threadIdx.x] = at < s.tokens ? tokens[at] : 0;
+    near_key[threadIdx.x] = at < s.tokens ? read_at(keys, at, s.tokens, -1, &g_embedding_status) : -1;
+    near_token[threadIdx.x] = at < s.tokens ? read_at(tokens, at, s.tokens, 0, &g_embedding_status) : 0;
   }
-  const int32_t before = first > 0 ? keys[first - 1] : -1;
+  const int32_t before = first > 0 ? read_at(keys, first - 1, s.tokens, -1, &g_embedding_status) : -1;
   __syncthreads();
   if (threadIdx.x < 32) {  // a bit for each place where another id than before begins, or past the end
     const int i = threadIdx.x;
@@ -850,7 +852,7 @@ int launch_gradient(const void* ids, const GradPlan& p, int64_t padding, uint8_t
   for (int q = 0; q < launches; ++q) fills[q] = fill_share(a.dtable, a.s, element_bytes(out_dtype), q, launches);
   const int64_t want = zeroed_late(a.s) ? 0 : ceil_div(fills[0].rows * fills[0].row_bytes, 16 * kThreads * 4);
   const int fill_blocks = static_cast<int>(want < 8 * sms ? want : 8 * sms);
-  const IdKey<I> source{static_cast<const I*>(ids), a.s.rows, padding};
+  const IdKey<I> source{static_cast<const I*>(ids), a.s.rows, padding, n};
   if (small) {
     const int blocks = static_cast<int>(ceil_div(fill_blocks, kSmallThreads / kThreads));
     const int rc = n <= kSmallThreads
@@ -866,7 +868,7 @@ int launch_gradient(const void* ids, const GradPlan& p, int64_t padding, uint8_t
       const int shift = q * p.d.bits, to = q & 1;
       const Fill* f = fills + q * per_digit;
       const int rc = q == 0 ? launch_digit(source, p, shift, counts, keys[to], tokens[to], f, fill_blocks, a.stream)
-                            : launch_digit(SortedKey{keys[to ^ 1], tokens[to ^ 1]}, p, shift, counts, keys[to],
+                            : launch_digit(SortedKey{keys[to ^ 1], tokens[to ^ 1], n}, p, shift, counts, keys[to],
                                            tokens[to], f, fill_blocks, a.stream);
       if (rc != MXQ_OK) return rc;
     }
@@ -893,6 +895,7 @@ int check_table_shape(int64_t tokens, int ids_bytes, int64_t rows, int64_t D, in
 
 namespace mxq {
 int embedding_status_read(unsigned int* out, bool clear) { return read_status_word(g_embedding_status, out, clear); }
+int embedding_watch(uint64_t address) { return watch_address(address); }
 }  // namespace mxq
 
 extern "C" int mxq_embedding(const void* ids, int ids_bytes, int64_t tokens, const void* table, int dtype,

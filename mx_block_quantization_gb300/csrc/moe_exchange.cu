@@ -36,8 +36,9 @@ constexpr int kThreads = 256;
 struct ExpertKey {
   const int32_t* ids;
   int E;
+  int64_t n;
   __device__ int operator()(int64_t i) const {
-    const int32_t e = ids[i];
+    const int32_t e = read_at(ids, i, n, -1, &g_exchange_status);
     if (e >= 0 && e < E) return e;
     if (e != -1) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
     return -1;
@@ -49,9 +50,8 @@ __global__ void __launch_bounds__(kRankThreads)
   extern __shared__ int32_t counts[];
   pdl_wait();
   pdl_launch_dependents();  // as few blocks follow
-  rank_count(s, E, ExpertKey{ids, E}, counts);
-  for (int e = threadIdx.x; e < E; e += kRankThreads)
-    chunk_counts[static_cast<int64_t>(blockIdx.x) * E + e] = counts[e];
+  rank_count(s, E, ExpertKey{ids, E, s.n}, counts);
+  rank_keep_counts(s, E, counts, chunk_counts, &g_exchange_status);
 }
 
 __global__ void __launch_bounds__(kRankThreads)
@@ -62,12 +62,12 @@ __global__ void __launch_bounds__(kRankThreads)
   int32_t* counts = smem + E;   // [warps, E]
   __shared__ int32_t total[kRankMaxBins], begin[kRankMaxBins], work[kRankWarps];
   pdl_wait();
-  const ExpertKey key{ids, E};
+  const ExpertKey key{ids, E, s.n};
   if (s.chunks == 1) {
     rank_count(s, E, key, total);
     for (int e = threadIdx.x; e < E; e += kRankThreads) next[e] = 0;
   } else {
-    rank_totals(s, E, chunk_counts, total, next);
+    rank_totals(s, E, chunk_counts, total, next, &g_exchange_status);
   }
   const int32_t end = rank_begins<kGroupRows>(E, total, begin, work);
   const uint64_t m_bytes = static_cast<uint64_t>(M) * 4;
@@ -77,11 +77,11 @@ __global__ void __launch_bounds__(kRankThreads)
     const int64_t hi = begin[e] + (total[e] + kGroupRows - 1) / kGroupRows * kGroupRows;
     for (int64_t m = lo + (threadIdx.x & 31); m < hi; m += 32)
       if (in_buf(source + m, 4, source, m_bytes, &g_exchange_status)) source[m] = -1;
-    if ((threadIdx.x & 31) == 0) offs[e] = static_cast<int32_t>(hi);
+    if ((threadIdx.x & 31) == 0) write_at(offs, e, E, static_cast<int32_t>(hi), &g_exchange_status);
   }
   for (int64_t m = end + static_cast<int64_t>(blockIdx.x) * kRankThreads + threadIdx.x; m < M;
        m += static_cast<int64_t>(gridDim.x) * kRankThreads)
-    source[m] = -1;
+    write_at(source, m, M, -1, &g_exchange_status);
   for (int e = threadIdx.x; e < E; e += kRankThreads) next[e] += begin[e];
   __syncthreads();
   const uint64_t s_bytes = static_cast<uint64_t>(s.n) * 4;
@@ -123,7 +123,8 @@ __device__ void zero_unused(const ExchangeShape& s, const int32_t* source, T* ro
   const bool narrow = s.fill == kManyRows;
   const int lane = threadIdx.x & 31, first = narrow ? lane : threadIdx.x, step = narrow ? 32 : kThreads;
   const int64_t m0 = block * s.fill + (narrow ? threadIdx.x & ~31u : 0u);
-  uint32_t unused = __ballot_sync(0xFFFFFFFFu, (narrow || lane < kFewRows) && m0 + lane < s.M && source[m0 + lane] < 0);
+  uint32_t unused = __ballot_sync(0xFFFFFFFFu, (narrow || lane < kFewRows) && m0 + lane < s.M &&
+                                                       read_at(source, m0 + lane, s.M, 0, &g_exchange_status) < 0);
   for (; unused != 0u; unused &= unused - 1) {
     T* row = rows + (m0 + __ffs(unused) - 1) * s.ldm;
     for (int64_t c = first; c < nv; c += step)
@@ -149,11 +150,12 @@ __global__ void __launch_bounds__(kThreads)
   if (t >= s.tokens) return;
   const int64_t nv = s.D / kV;
   const uint64_t bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldt + s.D) * sizeof(T);
   bool bad = false;
   int32_t first[kJ];
   const auto read = [&](int j0, int32_t (&m)[kJ]) {
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) m[j] = j0 + j < s.k ? slots[t * s.k + j0 + j] : -1;
+    for (int j = 0; j < kJ; ++j) m[j] = j0 + j < s.k ? read_at(slots, t * s.k + j0 + j, s.tokens * s.k, -1, &g_exchange_status) : -1;
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
       if (m[j] >= s.M || m[j] < -1) bad = true;
@@ -168,7 +170,8 @@ __global__ void __launch_bounds__(kThreads)
   };
   read(0, first);
   for (int64_t c = threadIdx.x % s.tx; c < nv; c += s.tx) {
-    const Vec<T, kV> v = load_once<T, kV>(x + t * s.ldt + c * kV);
+    const T* p = x + t * s.ldt + c * kV;
+    const Vec<T, kV> v = load_if<T, kV>(p, in_buf(p, sizeof v, x, in_bytes, &g_exchange_status));
     write(first, v, c);
     for (int j0 = kJ; kMore && j0 < s.k; j0 += kJ) {
       int32_t m[kJ];
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(kThreads)
   const uint64_t out_bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
   bool bad = false;
   for (int j = 0; n > 0 && j < s.k; ++j) {
-    const int64_t m = slots[t * s.k + j];
+    const int64_t m = read_at(slots, t * s.k + j, s.tokens * s.k, -1, &g_exchange_status);
     if (m < 0 || m >= s.M) {
       bad |= m != -1;
       continue;
@@ -247,11 +250,11 @@ struct Choices {
     bool bad = false;
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
-      const int32_t m = j0 + j < s.k ? slots[t * s.k + j0 + j] : -1;
+      const int32_t m = j0 + j < s.k ? read_at(slots, t * s.k + j0 + j, s.tokens * s.k, -1, &g_exchange_status) : -1;
       const bool live = m >= 0 && m < s.M;
       bad |= !live && m != -1;
       row[j] = live ? m * ld : -1;
-      w[j] = live ? (weights != nullptr ? weights[t * s.k + j0 + j] : 1.0f) : 0.0f;
+      w[j] = live ? (weights != nullptr ? read_at(weights, t * s.k + j0 + j, s.tokens * s.k, 0.0f, &g_exchange_status) : 1.0f) : 0.0f;
     }
     if (bad) atomicOr(&g_exchange_status, MXQ_DEV_BADINDEX);
   }
@@ -357,13 +360,14 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks)
   const int64_t nv = s.D / kV;
   const uint64_t in_bytes = (static_cast<uint64_t>(s.M - 1) * ldr + s.D) * sizeof(T);
   const uint64_t out_bytes = (static_cast<uint64_t>(s.M - 1) * s.ldm + s.D) * sizeof(T);
+  const uint64_t dy_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ldt + s.D) * sizeof(T);
   for (int j0 = 0; j0 < s.k; j0 += kJ) {
     const Choices<kJ> from(slots, weights, s, live ? t : 0, j0, ldr);
     int64_t to[kJ];
     float dot[kJ];
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
-      to[j] = from.row[j] >= 0 && live ? static_cast<int64_t>(slots[t * s.k + j0 + j]) * s.ldm : -1;
+      to[j] = from.row[j] >= 0 && live ? static_cast<int64_t>(read_at(slots, t * s.k + j0 + j, s.tokens * s.k, -1, &g_exchange_status)) * s.ldm : -1;
       dot[j] = 0.0f;
     }
     for (int64_t c = threadIdx.x % kGroup; live && c < nv; c += kU * kGroup) {
@@ -371,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks)
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         const int64_t col = (c + u * kGroup) * kV;
-        g[u] = load_if<T, kV>(dy + t * s.ldt + col, c + u * kGroup < nv);
+        const T* d = dy + t * s.ldt + col;
+        g[u] = load_if<T, kV>(d, c + u * kGroup < nv && in_buf(d, sizeof g[u], dy, dy_bytes, &g_exchange_status));
 #pragma unroll
         for (int j = 0; j < kJ; ++j) {
           const T* p = rows + from.row[j] + col;
@@ -414,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, kBackBlocks)
     if (live && threadIdx.x % kGroup == 0)
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
-        if (j0 + j < s.k) dweights[t * s.k + j0 + j] = from.row[j] >= 0 ? dot[j] : 0.0f;
+        if (j0 + j < s.k)
+          write_at(dweights, t * s.k + j0 + j, s.tokens * s.k, from.row[j] >= 0 ? dot[j] : 0.0f, &g_exchange_status);
   }
 }
 
@@ -552,6 +558,7 @@ int check_rows_shape(int dtype, int64_t tokens, int64_t D, int64_t ldt, int64_t 
 
 namespace mxq {
 int exchange_status_read(unsigned int* out, bool clear) { return read_status_word(g_exchange_status, out, clear); }
+int exchange_watch(uint64_t address) { return watch_address(address); }
 }  // namespace mxq
 
 extern "C" int64_t mxq_moe_rows(int64_t tokens, int32_t k, int32_t experts) {

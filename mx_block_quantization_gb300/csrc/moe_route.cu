@@ -142,7 +142,7 @@ __device__ __forceinline__ void finish_alone(const RouteShape& s, const float* p
   const int tid = threadIdx.x;
   float sum = 0.0f;
   for (int e = tid; e < s.E; e += blockDim.x) {
-    counts[e] = c[e];
+    write_at(counts, e, s.E, c[e], &g_route_status);
     sum += static_cast<float>(c[e]) * p[e];
   }
   sum = warp_sum(sum);
@@ -166,11 +166,11 @@ __device__ __forceinline__ void finish_block(const RouteShape& s, const float* s
   }
   const int64_t base = static_cast<int64_t>(blockIdx.x) * s.E;
   for (int e = threadIdx.x; e < s.E; e += blockDim.x) {
-    part_p[base + e] = sums[e];
-    part_c[base + e] = hist[e];
+    write_at(part_p, base + e, static_cast<int64_t>(gridDim.x) * s.E, sums[e], &g_route_status);
+    write_at(part_c, base + e, static_cast<int64_t>(gridDim.x) * s.E, hist[e], &g_route_status);
   }
   if (threadIdx.x == 0) {
-    part_n[blockIdx.x] = tokens;
+    write_at(part_n, blockIdx.x, gridDim.x, tokens, &g_route_status);
     if (blockIdx.x == 0) *joined = 0u;
   }
 }
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mine == bar) mine = 0u;
       bar = __reduce_max_sync(0xFFFFFFFFu, mine);
     }
-    bool routed = mask == nullptr || mask[t] != 0;
+    bool routed = mask == nullptr || read_at(mask, t, s.tokens, uint8_t{0}, &g_route_status) != 0;
     if (routed && top_key == 0u) {  // no logit to choose: counted only if one is NaN
       bool nan = false;
 #pragma unroll
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kFewThreads)
     const FewRow<T, kPer> row = ahead;
     ahead.load(logits, s, t + step, sub, in_bytes);
     const bool in = t < s.tokens;
-    const FewSoftmax<kPer> soft(row, in && (mask == nullptr || mask[t] != 0));
+    const FewSoftmax<kPer> soft(row, in && (mask == nullptr || read_at(mask, t, s.tokens, uint8_t{0}, &g_route_status) != 0));
     int rank[kPer] = {};
 #pragma unroll
     for (int j = 0; j < 8 * kPer; ++j) {
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kFewBackThreads)
   const float n = static_cast<float>(*n_in);
   const float f = dloss != nullptr && n > 0.0f ? *dloss * (static_cast<float>(s.E) / (static_cast<float>(s.k) * n * n)) : 0.0f;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) c[i] = dloss != nullptr && sub + 8 * i < s.E ? f * static_cast<float>(counts[sub + 8 * i]) : 0.0f;
+  for (int i = 0; i < kPer; ++i) c[i] = dloss != nullptr && sub + 8 * i < s.E ? f * static_cast<float>(read_at(counts, sub + 8 * i, s.E, 0, &g_route_status)) : 0.0f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * (kFewBackThreads / 8);
   FewRow<T, kPer> ahead;
   int32_t e_ahead[kPer];
@@ -500,8 +500,8 @@ __global__ void __launch_bounds__(kFewBackThreads)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const bool there = dweights != nullptr && t < s.tokens && sub + 8 * i < s.k;
-      e_ahead[i] = there ? ids[t * s.k + sub + 8 * i] : -1;
-      dw_ahead[i] = there ? dweights[t * s.k + sub + 8 * i] : 0.0f;
+      e_ahead[i] = there ? read_at(ids, t * s.k + sub + 8 * i, s.tokens * s.k, -1, &g_route_status) : -1;
+      dw_ahead[i] = there ? read_at(dweights, t * s.k + sub + 8 * i, s.tokens * s.k, 0.0f, &g_route_status) : 0.0f;
     }
   };
   int64_t t = static_cast<int64_t>(blockIdx.x) * (kFewBackThreads / 8) + tid / 8;
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kFewBackThreads)
     for (int i = 0; i < kPer; ++i) e[i] = e_ahead[i], dw[i] = dw_ahead[i];
     fetch(t + step);
     const bool in = t < s.tokens;
-    const FewSoftmax<kPer> soft(row, in && (mask == nullptr || mask[t] != 0));
+    const FewSoftmax<kPer> soft(row, in && (mask == nullptr || read_at(mask, t, s.tokens, uint8_t{0}, &g_route_status) != 0));
     // the chosen experts' gradients in their own lanes
     float own_dw[kPer] = {};
     bool own[kPer] = {};
@@ -582,11 +582,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   if (e < s.E)
 #pragma unroll 10
     for (int b = warp; b < blocks; b += kJoinWarps) {
-      p += part_p[static_cast<int64_t>(b) * s.E + e];
-      c += part_c[static_cast<int64_t>(b) * s.E + e];
+      p += read_at(part_p, static_cast<int64_t>(b) * s.E + e, static_cast<int64_t>(blocks) * s.E, 0.0f, &g_route_status);
+      c += read_at(part_c, static_cast<int64_t>(b) * s.E + e, static_cast<int64_t>(blocks) * s.E, 0, &g_route_status);
     }
   if (warp == 0)
-    for (int b = lane; b < blocks; b += 32) n += part_n[b];
+    for (int b = lane; b < blocks; b += 32) n += read_at(part_n, b, blocks, 0, &g_route_status);
   sum_p[warp][lane] = p;
   sum_c[warp][lane] = c;
   __syncthreads();
@@ -595,17 +595,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     p += sum_p[w][lane];
     c += sum_c[w][lane];
   }
-  if (e < s.E) counts[e] = c;
+  if (e < s.E) write_at(counts, e, s.E, c, &g_route_status);
   const float own = warp_sum(e < s.E ? static_cast<float>(c) * p : 0.0f);
   uint32_t before = 0;
   if (lane == 0) {
-    part_loss[blockIdx.x] = own;
+    write_at(part_loss, blockIdx.x, gridDim.x, own, &g_route_status);
     __threadfence();
     before = atomicAdd(joined, 1u);
     __threadfence();
   }
   if (__shfl_sync(0xFFFFFFFFu, before, 0) + 1 != gridDim.x) return;
-  const float all = warp_sum(lane < static_cast<int>(gridDim.x) ? __ldcg(part_loss + lane) : 0.0f);
+  const float all = warp_sum(
+      lane < static_cast<int>(gridDim.x) && in_array(part_loss, lane, gridDim.x, &g_route_status) ? __ldcg(part_loss + lane) : 0.0f);
   n = __reduce_add_sync(0xFFFFFFFFu, n);
   if (lane == 0) {
     *loss = loss_of(s, all, n);
@@ -638,7 +639,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int e = expert_of<kV>(i, lane);
-      c[i] = dloss != nullptr && e < s.E ? f * static_cast<float>(counts[e]) : 0.0f;
+      c[i] = dloss != nullptr && e < s.E ? f * static_cast<float>(read_at(counts, e, s.E, 0, &g_route_status)) : 0.0f;
     }
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -651,8 +652,8 @@ __global__ void __launch_bounds__(kThreads)
     if (in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status))
       ahead.load(logits + t * s.ld, s.E, lane);
     if (dweights != nullptr && lane < s.k) {
-      e_ahead = ids[t * s.k + lane];
-      dw_ahead = dweights[t * s.k + lane];
+      e_ahead = read_at(ids, t * s.k + lane, s.tokens * s.k, -1, &g_route_status);
+      dw_ahead = read_at(dweights, t * s.k + lane, s.tokens * s.k, 0.0f, &g_route_status);
     }
   };
   int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
@@ -672,7 +673,7 @@ __global__ void __launch_bounds__(kThreads)
     }
     top = key_value(__reduce_max_sync(0xFFFFFFFFu, order_key(top)));
     const bool some = top > -CUDART_INF_F;  // false for NaN, the value of key 0
-    const bool routed = (mask == nullptr || mask[t] != 0) && (some || __any_sync(0xFFFFFFFFu, nan));
+    const bool routed = (mask == nullptr || read_at(mask, t, s.tokens, uint8_t{0}, &g_route_status) != 0) && (some || __any_sync(0xFFFFFFFFu, nan));
     T* out = dlogits + t * ldd;
     if (routed) {
       float sum = 0.0f;
@@ -869,6 +870,7 @@ namespace mxq {
 int route_status_read(unsigned int* out, bool clear) {
   return read_status_word(g_route_status, out, clear);
 }
+int route_watch(uint64_t address) { return watch_address(address); }
 }  // namespace mxq
 
 // Sized for blocks of at most kWorkspaceTokens tokens: whether a call needs a workspace

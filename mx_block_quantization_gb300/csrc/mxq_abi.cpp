@@ -1,4 +1,6 @@
 // mxq_abi.cpp -- status strings and version of the C ABI declared in mxq.h.
+#include <initializer_list>
+
 #include "mxq.h"
 
 extern "C" const char* mxq_status_string(int status) {
@@ -20,3 +22,18 @@ extern "C" const char* mxq_status_string(int status) {
 }
 
 extern "C" int mxq_version(void) { return (1 << 16) | 0; }
+
+namespace mxq {
+int route_watch(uint64_t address);      // moe_route.cu
+int exchange_watch(uint64_t address);   // moe_exchange.cu
+int embedding_watch(uint64_t address);  // embedding.cu
+int ortho_watch(uint64_t address);      // orthogonalize.cu
+}  // namespace mxq
+
+extern "C" int mxq_selftest_watch(const void *address) {
+  for (auto *watch : {mxq::route_watch, mxq::exchange_watch, mxq::embedding_watch, mxq::ortho_watch}) {
+    const int rc = watch(reinterpret_cast<uintptr_t>(address));
+    if (rc != MXQ_OK) return rc;
+  }
+  return MXQ_OK;
+}

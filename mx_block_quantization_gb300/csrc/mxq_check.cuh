@@ -16,12 +16,23 @@
 
 namespace mxq {
 
+#if MXQ_DEBUG_BOUNDS && defined(MXQ_WATCHED)
+// An access that touches this address counts as one outside its buffer, so that a test
+// can see which accesses are checked (mxq_selftest_watch); 0: none.
+static __device__ unsigned long long g_watched = 0;
+#endif
+
 // true when the bytes [p, p + n) lie inside the buffer [buf, buf + size).
 __device__ __forceinline__ bool in_buf(const void* p, uint64_t n, const void* buf, uint64_t size,
                                        unsigned int* status) {
 #if MXQ_DEBUG_BOUNDS
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), lo = reinterpret_cast<uintptr_t>(buf);
-  if (a >= lo && n <= size && a - lo <= size - n) return true;
+#ifdef MXQ_WATCHED
+  const bool watched = g_watched - a < n;
+#else
+  const bool watched = false;
+#endif
+  if (!watched && a >= lo && n <= size && a - lo <= size - n) return true;
   atomicOr(status, MXQ_DEV_OOB);
   return false;
 #else

@@ -119,9 +119,10 @@ struct Lift {
   const int32_t* of;            // [batch], or NULL: none
   int32_t drop_from, drop_to;   // of the X read and of the X written
   int32_t out_from, in_to;      // powers of 2^-h and 2^h in the product's factor
+  int32_t batches;
   __device__ __forceinline__ float factor(int64_t batch) const {
     if (of == nullptr) return 1.0f;
-    const int lift = of[batch], from = max(0, lift - drop_from), to = max(0, lift - drop_to);
+    const int lift = read_at(of, batch, batches, 0, &g_ortho_status), from = max(0, lift - drop_from), to = max(0, lift - drop_to);
     const int e = in_to * to - out_from * from;  // at most 0: what is stored never grows in a product
     return __int_as_float(max(0, e + 127) << 23);
   }
@@ -177,7 +178,8 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x < 3) {  // a thread for each part
     float all = 0.0f;
     for (int w = 0; w < kThreads / 32; ++w) all += red[w][threadIdx.x];
-    reinterpret_cast<float*>(sums + blockIdx.x)[threadIdx.x] = all;
+    write_at(reinterpret_cast<float*>(sums), 3 * static_cast<int64_t>(blockIdx.x) + threadIdx.x, 3 * static_cast<int64_t>(gridDim.x),
+             all, &g_ortho_status);
   }
 }
 
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kThreads)
   if (threadIdx.x < 32) {
     Squares s = {};
     for (int i = threadIdx.x; i < parts; i += 32) {
-      const Squares part_sums = sums[b * parts + i];
+      const Squares part_sums = read_at(sums, b * parts + i, gridDim.x, Squares{}, &g_ortho_status);
       s.small += part_sums.small, s.plain += part_sums.plain, s.large += part_sums.large;
     }
     s = {warp_sum(s.small), warp_sum(s.plain), warp_sum(s.large)};
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(kThreads)
       const int lift = lifted ? min((__float_as_int(over) >> 23) - 127, kMaxLift) : 0;  // its exponent; infinity: the most
       const float less = __int_as_float((127 - lift) << 23);
       shared_factor = kXScale / (lifted ? norm.r * (over * less) : norm.r + eps * norm.unit);
-      if (part == 0) lifts[b] = lift;
+      if (part == 0) write_at(lifts, b, a.batch, lift, &g_ortho_status);
     }
   }
   __syncthreads();
@@ -236,7 +238,8 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int j = 0; j < kV; ++j)
           o.v[j] = __half_as_ushort(__float2half_rn(widen(v[q].v[j]) * unit * f - __half2float(__ushort_as_half(o.v[j]))));
-        *reinterpret_cast<Vec<uint16_t, kV>*>(x_low + (at - x)) = o;
+        if (in_buf(x_low + (at - x), sizeof o, x_low, out_bytes, &g_ortho_status))
+          *reinterpret_cast<Vec<uint16_t, kV>*>(x_low + (at - x)) = o;
       }
     }
   }
@@ -278,6 +281,7 @@ struct Product {
   // output = scale * acc + (add_scale + scale * (d[row] + d[column])) * addend
   //          and where row == column, + diagonal + add_scale * d + scale * d * d
   float scale, add_scale, diagonal;
+  int64_t d_count;                  // batch * d_ld
   const float *d_row, *d_col;       // [batch, d_ld]: what the rounding left of a diagonal; NULL: zero
   float* d_out;                     // the same of this output's diagonal, or NULL;
   int32_t d_squares;                // of the squares of its diagonal instead
@@ -609,7 +613,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
       const int64_t row = row0 + lane;
       const bool mirror = kSymmetric && at.i != at.j, both = needs_both(at) || kAddends == 2;
       const float scale = p.scale * p.lift.factor(at.batch);
-      const float dr = p.d_row != nullptr && row < p.rows ? p.d_row[at.batch * p.d_ld + row] : 0.0f;
+      const float dr = p.d_row != nullptr && row < p.rows
+                           ? read_at(p.d_row, at.batch * p.d_ld + row, p.d_count, 0.0f, &g_ortho_status) : 0.0f;
       if (kColumns && lane < 4) {  // this warp's 128 columns, four lines
         const int64_t col = static_cast<int64_t>(at.j) * kTile + 2 * (e >> 2) * kChunkCols + 32 * lane;
         if (col < p.cols) asm volatile("prefetch.global.L1 [%0];" ::"l"(p.d_col + at.batch * p.d_ld + col));
@@ -666,10 +671,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
         const auto store_partial = [&] {
           if (!kPartial) return false;
           float* to = p.partial + at.slice * p.partial_stride + (static_cast<int64_t>(at.batch) * p.rows + row) * p.d_ld + col0;
+          const uint64_t bytes = static_cast<uint64_t>(p.slices) * p.partial_stride * 4;
           if (row < p.rows)
 #pragma unroll
             for (int i = 0; i < 64; i += 4)
-              if (col0 + i < p.d_ld)  // a multiple of 8
+              if (col0 + i < p.d_ld && in_buf(to + i, 16, p.partial, bytes, &g_ortho_status))  // d_ld: a multiple of 8
                 *reinterpret_cast<uint4*>(to + i) =
                     make_uint4(raw[i / 32][i % 32], raw[i / 32][i % 32 + 1], raw[i / 32][i % 32 + 2], raw[i / 32][i % 32 + 3]);
           return true;
@@ -684,7 +690,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
             const float4* d = reinterpret_cast<const float4*>(p.d_col + at.batch * p.d_ld + col);
 #pragma unroll
             for (int q = 0; q < 8; ++q)  // d_ld is a multiple of 8
-              dc[q] = col + 4 * q < p.cols ? d[q] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              dc[q] = col + 4 * q < p.cols && in_buf(d + q, 16, p.d_col, static_cast<uint64_t>(p.d_count) * 4, &g_ortho_status)
+                          ? d[q] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
           }
           float v[32];
 #pragma unroll
@@ -711,7 +718,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           if (kSymmetric && row0 < col + 32 && col < row0 + 32) {  // the warp's rows meet these columns
             const int own_column = static_cast<int>(row - col);
             float on = p.diagonal + p.add_scale * dr + scale * dr * dr;
-            if (p.square_rest != nullptr && row < p.rows) on = fmaf(scale, p.square_rest[at.batch * p.d_ld + row], on);
+            if (p.square_rest != nullptr && row < p.rows)
+              on = fmaf(scale, read_at(p.square_rest, at.batch * p.d_ld + row, p.d_count, 0.0f, &g_ortho_status), on);
             float own = 0.0f;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -719,7 +727,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
               own = i == own_column ? v[i] : own;
             }
             if (!kSplit && p.d_out != nullptr && own_column >= 0 && own_column < 32 && row < p.rows)
-              p.d_out[at.batch * p.d_ld + row] = diagonal_rest(own, p.d_squares);
+              write_at(p.d_out, at.batch * p.d_ld + row, p.d_count, diagonal_rest(own, p.d_squares), &g_ortho_status);
           }
           uint32_t w[16];
 #pragma unroll
@@ -840,15 +848,13 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Join a) {
   const float* p = a.partial + (i / kTile >= j / kTile ? at : (row - i + j) * a.ld + i);
   float sum = 0.0f;
 #pragma unroll 8
-  for (int s = 0; s < a.slices; ++s) sum += p[s * a.stride];
+  for (int s = 0; s < a.slices; ++s) sum += read_at(a.partial, p - a.partial + s * a.stride, a.slices * a.stride, 0.0f, &g_ortho_status);
   const float v = sum * (a.scale * a.lift.factor(row / a.side)) + (i == j ? a.diagonal : 0.0f), h = half_rounded(v);
-  const uint64_t bytes = static_cast<uint64_t>(n) * 2;
-  if (!in_buf(a.high + at, 2, a.high, bytes, &g_ortho_status)) return;
-  a.high[at] = __float2half_rn(v);
+  write_at(a.high, at, n, __float2half_rn(v), &g_ortho_status);
   if (a.low != nullptr)
-    a.low[at] = __float2half_rn(v - h);
+    write_at(a.low, at, n, __float2half_rn(v - h), &g_ortho_status);
   else if (i == j && a.d_out != nullptr)
-    a.d_out[row / a.side * a.ld + i] = diagonal_rest(v, a.d_squares);
+    write_at(a.d_out, row / a.side * a.ld + i, a.batch * a.ld, diagonal_rest(v, a.d_squares), &g_ortho_status);
 }
 
 // ---------------------------------------------------------------------------
@@ -1034,6 +1040,7 @@ int check_ortho_shape(int64_t batch, int64_t m, int64_t n) {
 
 namespace mxq {
 int ortho_status_read(unsigned int* out, bool clear) { return read_status_word(g_ortho_status, out, clear); }
+int ortho_watch(uint64_t address) { return watch_address(address); }
 }  // namespace mxq
 
 extern "C" int64_t mxq_orthogonalize_workspace(int64_t batch, int64_t m, int64_t n) {
@@ -1108,7 +1115,7 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
   const double growth = log2(fmax(1.0, fabs(ca) + fabs(cb) / 4 + fabs(cc) / 16));
   const auto lift = [&](int s, int32_t out_from, int32_t in_to) {
     return Lift{reinterpret_cast<const int32_t*>(workspace + l.lifts), static_cast<int32_t>(ceil(s * growth)),
-                static_cast<int32_t>(ceil((s + 1) * growth)), out_from, in_to};
+                static_cast<int32_t>(ceil((s + 1) * growth)), out_from, in_to, static_cast<int32_t>(batch)};
   };
   for (int s = 0; s < steps; ++s) {
     const int from = s & 1, to = from ^ 1;
@@ -1127,6 +1134,7 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.lift = lift(s, 2, 0);
     p.diagonal = static_cast<float>(shift * sa);
     p.d_ld = l.lds;
+    p.d_count = batch * l.lds;
     if (!split) {
       p.d_out = d_gram;
       p.d_squares = completed;
@@ -1162,6 +1170,7 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     p.scale = cc * sp / (sa * sa);
     p.diagonal = static_cast<float>((ca - 0.5 * shift * cb) * sp);
     p.d_ld = l.lds;
+    p.d_count = batch * l.lds;
     if (!split) p.d_out = d_poly;
     if (completed) {
       if (!split) p.square_rest = d_gram;
@@ -1189,6 +1198,7 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
     if (!split) {
       maps.add[0] = x[from][0].rows;
       p.d_ld = l.lds;
+      p.d_count = batch * l.lds;
       (wide ? p.d_row : p.d_col) = d_poly;
     }
     const bool last = s + 1 == steps;

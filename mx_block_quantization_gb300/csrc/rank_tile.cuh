@@ -139,15 +139,22 @@ __device__ void rank_chunk(const RankSplit& s, int bins, Key key, Emit emit, int
   }
 }
 
+// A block's counts for the second launch, one chunk's row of [chunks, bins].
+__device__ __forceinline__ void rank_keep_counts(const RankSplit& s, int bins, const int32_t* counts,
+                                                 int32_t* chunk_counts, unsigned int* status) {
+  for (int b = threadIdx.x; b < bins; b += kRankThreads)
+    write_at(chunk_counts, static_cast<int64_t>(blockIdx.x) * bins + b, static_cast<int64_t>(s.chunks) * bins, counts[b], status);
+}
+
 // Totals over all chunks and the sum over the chunks before this block's, from
 // the [chunks, bins] counts of the first launch.
 __device__ __forceinline__ void rank_totals(const RankSplit& s, int bins, const int32_t* chunk_counts,
-                                            int32_t* total, int32_t* before) {
+                                            int32_t* total, int32_t* before, unsigned int* status) {
   for (int b = threadIdx.x; b < bins; b += kRankThreads) {
     int32_t all = 0, mine = 0;
 #pragma unroll 8
     for (int c = 0; c < s.chunks; ++c) {
-      const int32_t v = chunk_counts[static_cast<int64_t>(c) * bins + b];
+      const int32_t v = read_at(chunk_counts, static_cast<int64_t>(c) * bins + b, static_cast<int64_t>(s.chunks) * bins, 0, status);
       all += v;
       if (c < static_cast<int>(blockIdx.x)) mine += v;
     }

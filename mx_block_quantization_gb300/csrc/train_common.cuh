@@ -9,6 +9,7 @@
 #include <initializer_list>
 
 #include "mxq.h"
+#define MXQ_WATCHED 1
 #include "mxq_check.cuh"
 #include "mxq_device.cuh"
 #include "mxq_host.h"
@@ -38,6 +39,21 @@ template <typename T, int kN>
 struct alignas(sizeof(T) * kN) Vec {
   T v[kN];
 };
+
+// Element i of an array of n elements, checked like every computed access: `other`
+// where it lies outside, and nothing written there.
+template <typename T>
+__device__ __forceinline__ bool in_array(const T* a, int64_t i, int64_t n, unsigned int* status) {
+  return in_buf(a + i, sizeof(T), a, static_cast<uint64_t>(n) * sizeof(T), status);
+}
+template <typename T>
+__device__ __forceinline__ T read_at(const T* a, int64_t i, int64_t n, T other, unsigned int* status) {
+  return in_array(a, i, n, status) ? a[i] : other;
+}
+template <typename T>
+__device__ __forceinline__ void write_at(T* a, int64_t i, int64_t n, T v, unsigned int* status) {
+  if (in_array(a, i, n, status)) a[i] = v;
+}
 
 // Load of data that this launch does not write, not kept in L1; zero where `wanted`
 // is false.  The condition is the load's own predicate: as a branch around each
@@ -204,6 +220,17 @@ inline int read_status_word(const unsigned int& symbol, unsigned int* out, bool 
   const unsigned int zero = 0;
   if (clear && cudaMemcpyToSymbol(symbol, &zero, sizeof zero) != cudaSuccess) return MXQ_ECUDA;
   return MXQ_OK;
+}
+
+// Sets the address that this file's checks take as outside (mxq_selftest_watch).
+static inline int watch_address(uint64_t address) {
+#if MXQ_DEBUG_BOUNDS
+  const unsigned long long v = address;
+  return cudaMemcpyToSymbol(g_watched, &v, sizeof v) == cudaSuccess ? MXQ_OK : MXQ_ECUDA;
+#else
+  (void)address;
+  return MXQ_OK;
+#endif
 }
 
 }  // namespace mxq

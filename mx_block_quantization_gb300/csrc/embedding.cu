@@ -222,12 +222,7 @@ __global__ void __launch_bounds__(kRankThreads)
   pdl_launch_dependents();
   if (fill_block<kRankThreads>(fill, s.chunks)) return;
   const auto key = [&](int64_t i) { return (src.full(i) >> shift) & (bins - 1); };
-  if (s.chunks == 1) {
-    rank_count(s, bins, key, total);
-    for (int b = threadIdx.x; b < bins; b += kRankThreads) next[b] = 0;
-  } else {
-    rank_totals(s, bins, chunk_counts, total, next, &g_embedding_status);
-  }
+  rank_totals(s, bins, chunk_counts, total, next, &g_embedding_status);
   rank_begins<1>(bins, total, begin, work);
   for (int b = threadIdx.x; b < bins; b += kRankThreads) next[b] += begin[b];
   __syncthreads();
@@ -808,13 +803,11 @@ template <typename Source>
 int launch_digit(const Source& src, const GradPlan& p, int shift, int32_t* counts, int32_t* keys, int32_t* tokens,
                  const Fill* fills, int fill_blocks, cudaStream_t stream) {
   const int bins = 1 << p.d.bits;
-  if (p.s.chunks > 1) {
-    const int rc = launch_pdl(digit_count_kernel<Source>, p.s.chunks + fill_blocks, kRankThreads, bins * 4, stream, src, p.s,
-                              shift, bins, counts, *fills++);
-    if (rc != MXQ_OK) return rc;
-  }
+  const int rc = launch_pdl(digit_count_kernel<Source>, p.s.chunks + fill_blocks, kRankThreads, bins * 4, stream, src, p.s,
+                            shift, bins, counts, fills[0]);
+  if (rc != MXQ_OK) return rc;
   return launch_pdl(digit_sort_kernel<Source>, p.s.chunks + fill_blocks, kRankThreads, rank_smem(bins), stream, src, p.s,
-                    shift, bins, counts, keys, tokens, *fills);
+                    shift, bins, counts, keys, tokens, fills[1]);
 }
 
 template <int kRounds, typename Source>
@@ -846,8 +839,7 @@ int launch_gradient(const void* ids, const GradPlan& p, int64_t padding, uint8_t
   int32_t* tokens[2] = {buf + n, buf + 3 * n};
   // every launch of the sort zeroes an equal share of the table
   const bool small = n <= kSmallTokens;
-  const int per_digit = p.s.chunks > 1 ? 2 : 1;
-  const int launches = small ? 1 : p.d.passes * per_digit;
+  const int launches = small ? 1 : p.d.passes * 2;  // a digit's counting and its sort
   Fill fills[kMaxLaunches];
   for (int q = 0; q < launches; ++q) fills[q] = fill_share(a.dtable, a.s, element_bytes(out_dtype), q, launches);
   const int64_t want = zeroed_late(a.s) ? 0 : ceil_div(fills[0].rows * fills[0].row_bytes, 16 * kThreads * 4);
@@ -866,7 +858,7 @@ int launch_gradient(const void* ids, const GradPlan& p, int64_t padding, uint8_t
   } else {
     for (int q = 0; q < p.d.passes; ++q) {
       const int shift = q * p.d.bits, to = q & 1;
-      const Fill* f = fills + q * per_digit;
+      const Fill* f = fills + 2 * q;
       const int rc = q == 0 ? launch_digit(source, p, shift, counts, keys[to], tokens[to], f, fill_blocks, a.stream)
                             : launch_digit(SortedKey{keys[to ^ 1], tokens[to ^ 1], n}, p, shift, counts, keys[to],
                                            tokens[to], f, fill_blocks, a.stream);

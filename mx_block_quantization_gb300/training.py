@@ -41,9 +41,9 @@ class MoePlan(NamedTuple):
 def _count(value, what):
     """A count as the C entries take it; ctypes would cut it to its lowest bits."""
     value = index(value)
-    if not -1 << 31 <= value < 1 << 31:
-        raise MxqError(EBADSHAPE, what)
-    return value
+    if -0x80000000 <= value <= 0x7FFFFFFF:
+        return value
+    raise MxqError(EBADSHAPE, what)
 
 
 def _code(t, name):
@@ -76,7 +76,9 @@ def _matrix(t, name, rows=None, cols=None, device=None):
 
 def _rows_of(t, name, T, D):
     """[..., D] as a matrix [T, D] of the same memory."""
-    if t.dim() == 2 or T == 0 or D == 0:
+    if t.dim() == 2:
+        return t  # as it is: another view takes 2 us
+    if T == 0 or D == 0:
         return t.reshape(T, D)
     try:
         return t.view(T, D)

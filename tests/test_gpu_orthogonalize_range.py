@@ -1,11 +1,11 @@
 """orthogonalize of matrices of any magnitude that fp32 holds.
 
 The norm is right to a few roundings of fp32 whatever the elements' size, so the error
-is that of ordinary matrices: a rounding to bf16 (2^-9 at most, 1.7e-3 in the norm) and,
+is that of ordinary matrices: a rounding to bf16 (1.7e-3 in the norm of many elements) and,
 for sides above 64, the fp16 roundings of five steps' operands without a common sign,
 1.26e-3 (four of 2^-12 / sqrt(3), five times, in squares, twice for the iteration's
 slope): sqrt(1.7^2 + 1.26^2) = 2.1e-3, held to 2.2e-3.  Sides up to 64 carry pairs of
-fp16: 2^-9 alone.
+fp16: the rounding to bf16 alone, held to 2^-9.
 """
 import pytest
 import torch

@@ -13,8 +13,10 @@
 // rows than tokens the last launch zeroes the rows without any (zeroed_late).
 // A frequent id would keep one block busy for long, so a run of more than kChunk
 // tokens is first summed in pieces, one per chunk of kChunk sorted places, by a
-// launch of its own; the row then adds the pieces in order.  Sums are in fp32 and
-// their order depends on the ids alone.
+// launch of its own; the row then adds the pieces in order.  That takes the tokens off
+// one block, but the pieces of a row are still added by one: 65536 tokens of 4096 bf16
+// on 32768 rows take 160 us drawn evenly, 176 with a tenth of them on one id, 524 with
+// half and 944 with all.  Sums are in fp32 and their order depends on the ids alone.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -13,7 +13,10 @@
 //   combine_backward   drows[slots[i]] = w_i dy[i / k], the other rows zero;
 //                      dweights[i] = <dy[i / k], rows[slots[i]]>
 // All of it is bound by HBM: a token's row is read once and its k rows written
-// or read by the same threads, with sums over j in ascending order in fp32.
+// or read by the same threads, with sums over j in ascending order in fp32.  Only
+// combine_backward reads dy again, for every four choices, out of L2 as a rule (7168
+// tokens of 7168 bf16: k 4 160 us where the bytes take 153, k 8 301 and 274; 2048 of
+// 4096, k 32: 199 and 170).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

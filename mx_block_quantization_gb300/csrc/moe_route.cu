@@ -21,6 +21,10 @@
 // the probabilities of its experts; they are added up per block and then over the
 // blocks in a fixed order, so the loss has the same bits in every run.
 //
+// Exponentials and the sums' reciprocals are the hardware's approximations, a few units
+// in the last place: the exact forms' steps are worth more here than their last bits
+// (131071 x 250: probabilities off by 1.2e-7, 4e-8 with them).
+//
 // The forward pass is bound by instruction issue, 430 a token with 250 experts in
 // 90% of the issue slots: the softmax and the loss's sums take 40 of them for a
 // lane's 8 logits, the choice most of the rest.  131071 x 250 fp32, k = 6: 56 us,

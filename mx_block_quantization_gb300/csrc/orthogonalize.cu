@@ -19,7 +19,7 @@
 //
 // The square is completed: with S = A + (b/2c) I, which the gram product's
 // epilogue stores in A's place, P = c S S + (a - b^2/4c) I, and the square reads no
-// second matrix in its epilogue (64 matrices of 1024x512: 482 us, 501 with b A added
+// second matrix in its epilogue (64 fp32 matrices of 1024x512: 482 us, 501 with b A added
 // from memory).  Where b/2c is large or c is zero (kCompletedSquare) it does.
 //
 // The rounding that matters is that of the diagonals of S (or A) and P, which hold
@@ -46,13 +46,15 @@
 // grid is persistent, one CTA pair per two SMs.  Ragged edges are the tensor
 // maps': loads fill with zero, stores are clipped.
 //
-// Bound: by the way of the operands from L2, 64 KB a stage and pair at about 55
-// bytes a clock and SM, where a stage's MMAs take 512 clocks and its loads 590 or
-// more.  4096x8192 in five steps: 1.63 ms, 1.48 PFLOP/s of the products' one
-// triangle, the tensor pipe active 69 to 75% (1.19 ms with the loads left out, 1.39
-// with the MMAs left out).  64 matrices of 1024x512 bf16: 457 us, 0.66 PFLOP/s: 192 and
-// 512 tiles on 76 pairs leave part of the last round idle, and each of 17 launches
-// begins and ends alone.  One small matrix: 4 to 6 us a launch.
+// Bound, for large matrices: by the way of the operands from L2, 64 KB a stage and pair
+// at about 55 bytes a clock and SM, where a stage's MMAs take 512 clocks and its loads
+// 590 or more.  4096x8192 fp32 in five steps: 1.70 to 1.73 ms, 1.4 PFLOP/s of the
+// products' one triangle, the tensor pipe active 69 to 75% (of 1.63 ms on the fastest
+// GPU met, 1.19 with the loads left out, 1.39 with the MMAs left out).  64 matrices of
+// 1024x512 bf16: 452 us, 0.66 PFLOP/s.  Their tiles of the update and of the square have
+// 8 stages of K, 2.5 us of operands, but take 5.8 and 7 us: the rest is the epilogue (two chunks of a warp one after the other, each after the store before
+// it), and 192 and 512 tiles on 76 pairs leave part of the last round idle.  One small
+// matrix: 17 launches of 4 to 6 us, 0.1 of each for the exit that waits for the pair.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -862,7 +864,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const Join a) {
 // ---------------------------------------------------------------------------
 // The square is completed where |b| is at most this many |c|, so that |b/2c| stays
 // within the bound of A: beyond it the rounding of S would be that of the shift.
-// (Completed and not: 16x16 74 and 80 us, 200 matrices of 128x512 237 and 258, 64
+// (Completed and not, fp32: 16x16 74 and 80 us, 200 matrices of 128x512 237 and 258, 64
 // of 1024x512 482 and 501, 4096x8192 1632 and 1644.)
 constexpr float kCompletedSquare = 4.0f;
 // Sides up to this carry pairs of fp16 (see the head of the file).
@@ -877,7 +879,8 @@ constexpr int64_t kSplitSide = 64;
 // K is sliced in any case after kMostStages: the tensor cores' additions to an fp32
 // accumulator cut off what does not fit, a third of a unit in the last place on
 // average, and the diagonal's sum of squares loses that with every 16 of K (0.8% of the
-// result for 1 x 2^20 in one slice).  512 stages lose 9e-5 of it.
+// result for 1 x 2^20 in one slice).  512 stages lose 9e-5 of it.  (4096x65536 pays 7%
+// for its two slices' way through memory: 11.7 ms, 10.9 in one; others nothing.)
 constexpr int64_t kPairs = 76, kSliceStages = 6, kMostStages = 512;
 int64_t gram_slices(int64_t batch, int64_t side, int64_t length) {
   const int64_t tiles_m = ceil_div(side, kTile), tiles = batch * tiles_m * (tiles_m + 1) / 2;

@@ -52,9 +52,10 @@
 // products' one triangle, the tensor pipe active 69 to 75% (of 1.63 ms on the fastest
 // GPU met, 1.19 with the loads left out, 1.39 with the MMAs left out).  64 matrices of
 // 1024x512 bf16: 452 us, 0.66 PFLOP/s.  Their tiles of the update and of the square have
-// 8 stages of K, 2.5 us of operands, but take 5.8 and 7 us: the rest is the epilogue (two chunks of a warp one after the other, each after the store before
-// it), and 192 and 512 tiles on 76 pairs leave part of the last round idle.  One small
-// matrix: 17 launches of 4 to 6 us, 0.1 of each for the exit that waits for the pair.
+// 8 stages of K, 2.5 us of operands, but take 5.8 and 7 us: the rest is the epilogue
+// (two chunks of a warp one after the other, each after the store before it), and 192
+// and 512 tiles on 76 pairs leave part of the last round idle.  One small matrix: 17
+// launches of 4 to 6 us, 0.1 of each for the exit that waits for the pair.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

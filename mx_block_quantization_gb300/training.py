@@ -238,6 +238,8 @@ def moe_plan(ids, experts: int, *, rows: Optional[int] = None, out: Optional[Moe
                       torch.empty(max(M, 0), dtype=torch.int32, device=dev))
     else:
         M = out.source.numel()
+        if rows is not None and rows != M:
+            raise ValueError(f"out.source must have {rows} rows")
         for t, name, shape in zip(out, MoePlan._fields, ((experts,), (T, k), (M,))):
             _flat(t, name, torch.int32, shape, dev)
     rc = L.mxq_moe_plan(p, T, k, experts, M, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), wp, size,

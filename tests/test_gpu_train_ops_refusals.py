@@ -52,3 +52,13 @@ def test_rows_at_no_fixed_distance_and_rows_of_nothing():
     want = torch.zeros(10, 8, device="cuda")
     want[ids[0, 0]] = one[0, 0]
     assert torch.equal(got, want)
+
+
+def test_rows_of_a_plan_and_of_its_out_have_to_agree():
+    """`rows` beside an `out` of another size was left out of account."""
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    out = mxq.moe_plan(ids, 2)
+    M = out.source.numel()
+    with pytest.raises(ValueError, match=str(M + 128)):
+        mxq.moe_plan(ids, 2, rows=M + 128, out=out)
+    assert mxq.moe_plan(ids, 2, rows=M, out=out) is out

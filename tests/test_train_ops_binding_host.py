@@ -56,3 +56,10 @@ def test_rows_of_a_tensor_share_its_memory_or_are_refused():
         for n in shape[:-1]:
             T *= n
         assert training._rows_of(torch.empty(shape), "x", T, shape[-1]).shape == (T, shape[-1])
+
+
+def test_a_release_library_takes_a_watched_address_and_does_nothing():
+    import mx_block_quantization_gb300 as mxq
+    if not mxq.debug_bounds():
+        mxq.selftest_watch(1 << 40)
+        mxq.selftest_watch()

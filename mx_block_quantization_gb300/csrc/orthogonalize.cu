@@ -752,7 +752,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) __cluster_dims__(2, 1, 1)
           }
         }
         if (kBf16 && !p.out_map) {
-          // a matrix whose pitch or address no tensor map takes
+          // a matrix whose pitch or address no tensor map takes, or rows of part of a
+          // 16-byte piece
           __syncwarp();
           bf16_t* out = p.out + at.batch * p.stride_o;
           const uint64_t bytes = ((p.rows - 1) * p.ldo + p.cols) * 2;
@@ -1102,8 +1103,10 @@ extern "C" int mxq_orthogonalize(const void* g, int dtype, int64_t batch, int64_
   }
   if (!ok) return MXQ_ECUDA;
   const int64_t so = batch > 1 ? stride_o : (m * ldo + 7) / 8 * 8;
+  // a tensor store clips rows to whole 16-byte pieces: one of another length would write
+  // up to 14 bytes behind every row
   const bool out_map =
-      aligned_to(out, 16) && ldo % 8 == 0 && so % 8 == 0 &&
+      n % 8 == 0 && aligned_to(out, 16) && ldo % 8 == 0 && so % 8 == 0 &&
       encode(&final_rows, Stack{out, batch, m, n, ldo, so}, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, 32, true);
 
   // |X| <= 1.5 and so |A| <= 2 are taken as bounds of the iterates

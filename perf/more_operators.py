@@ -564,7 +564,7 @@ def _values64(q, s, first=0):
 
 def _act64(z, name):
     if name == "relu":
-        return z.clamp(min=0)
+        return torch.relu(z)
     if name == "silu":
         return z * torch.sigmoid(z)
     if name == "gelu":

@@ -335,6 +335,42 @@ int mxq_moe_route_backward(const void *logits, int dtype, int64_t tokens, int32_
                            cudaStream_t stream);
 
 /*
+ * Routing by scores with a bias, among the best groups of experts.  As mxq_moe_route but
+ * for these:
+ *   scores   s = 1 / (1 + e^-logit) (MXQ_SCORES_SIGMOID) or softmax(logits)
+ *            (MXQ_SCORES_SOFTMAX).
+ *   bias     fp32 [experts] or NULL: experts are chosen by s + bias, and their weights
+ *            are of s alone.  An expert whose s + bias is -inf or NaN is never chosen.
+ *   groups, best   the experts lie in `groups` (1 .. 32, a divisor of experts) equal
+ *            groups of consecutive ones; a group's value is the sum of its two largest
+ *            s + bias (of one where there is one), and the k experts are chosen among those
+ *            of the `best` groups with the largest values, ties to the lowest index.
+ *            k at most experts / groups * best.
+ *   ids      int32 [tokens, k]: the chosen experts, largest s + bias first, ties to the
+ *            lowest index.  The choice is that of exact sums: near ties are computed in
+ *            64 bits.
+ *   weights  fp32 [tokens, k]: scale * s at the ids (renorm 0), or scale * s over the sum
+ *            of the chosen s (renorm 1; 0 where that sum is 0).
+ *   loss     as there, with p = s / sum_e s_e (0 where that sum is 0).
+ * workspace: of mxq_moe_route_workspace.
+ *
+ * mxq_moe_route_groups_backward: the logits' gradient, the choice held fixed.  The bias
+ * has none: it moves by the counts.
+ */
+#define MXQ_SCORES_SIGMOID 0
+#define MXQ_SCORES_SOFTMAX 1
+int mxq_moe_route_groups(const void *logits, int dtype, int64_t tokens, int32_t experts, int64_t ld,
+                         int32_t k, const float *bias, int scores, int32_t groups, int32_t best,
+                         const uint8_t *mask, int renorm, float scale, float *weights, int32_t *ids,
+                         int32_t *counts, float *loss, int32_t *routed, uint8_t *workspace,
+                         int64_t workspace_bytes, cudaStream_t stream);
+int mxq_moe_route_groups_backward(const void *logits, int dtype, int64_t tokens, int32_t experts,
+                                  int64_t ld, int32_t k, int scores, const uint8_t *mask,
+                                  int renorm, float scale, const int32_t *ids, const int32_t *counts,
+                                  const int32_t *routed, const float *dweights, const float *dloss,
+                                  void *dlogits, int64_t ldd, cudaStream_t stream);
+
+/*
  * The exchange of rows between tokens and expert groups.  Assignment
  * i = token*k + j takes row slots[i] of a matrix of M rows in which the groups
  * follow one another, each in token order and filled up to a multiple of 128
@@ -372,6 +408,60 @@ int mxq_moe_combine_backward(const void *dy, int dtype, int64_t tokens, int64_t 
                              void *drows, int64_t ldd, float *dweights, cudaStream_t stream);
 
 /*
+ * The experts' products on the cast's bytes, block-scaled MXFP8 on the tensor cores
+ * (tcgen05), and the gradients around them.  Rows lie in groups that end at offs
+ * (int32 [G] on the device, as for mxq_quantize_2d_dual; NULL and G 0: one group of
+ * all M rows, and one matrix of everything below that has G); M, N and K are
+ * multiples of 128, at most 2^24.
+ *   mxq_moe_linear   z[m, n] = sum_k x[m, k] w[e, n, k] + bias[e, n],
+ *                    y = act(z) + residual, e the group of row m; rows behind the
+ *                    last group are written as 0 in y and z.
+ *     x, sx     E4M3 [M, K], rows ldx bytes apart, and its blocked E8M0 scales
+ *               [M*K/32]: q_row and s_row of the cast.
+ *     w, sw     E4M3 [G, N, K], rows ldw and matrices stride_w bytes apart, and the
+ *               matrices' blocked scales one after another [G*N*K/32]: of one cast of
+ *               [G*N, K] q_row and s_row; for the rows' gradient (x = the cast dz
+ *               [M, N], K the weights' N) its q_col, with ldw = G*N and stride_w = N,
+ *               and the s_col of a cast with offs N, 2N, ..., G*N.  Pitches are
+ *               multiples of 16.
+ *     bias      [G, N] of type bias_dtype, or NULL.
+ *     activation  MXQ_ACT_NONE, _RELU, _SILU (z / (1 + e^-z)) or _GELU (the tanh form,
+ *               0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))).
+ *     residual  [M, N] of the output's type, rows ldr apart, or NULL; may be y itself.
+ *     y, z      [M, N] of type dtype, each rounded once from fp32; z may be NULL.
+ *   mxq_moe_weight_gradient   dw[e, n, k] = sum over the rows m of group e of
+ *               a[n, m] b[k, m], added to what dw holds with `accumulate`; a group
+ *               without rows gives 0 (or leaves dw).
+ *     a, sa     q_col [N, M] and s_col [N*M/32] of the cast dz; b, sb of the cast x.
+ *     dw        [G, N, K] of type dtype, rows ldd and matrices stride_d apart.
+ *   mxq_moe_linear_backward   dz = dy act'(z) (rows behind the last group: 0) and
+ *               dbias[e, n] = the sum of dz (in fp32, before its rounding) over the
+ *               rows of group e.  dy, z, dz [M, N] of type dtype; dz may be dy itself;
+ *               dz or dbias (fp32 [G, N]) may be NULL, z with MXQ_ACT_NONE.
+ * Sums are fp32.  Scale byte 255 is NaN.  Invalid offs are detected on the device:
+ * nothing is written and MXQ_DEV_BADOFFS is set.  Every internal wait is bounded
+ * (MXQ_DEV_TIMEOUT in the status word).
+ */
+#define MXQ_ACT_NONE 0
+#define MXQ_ACT_RELU 1
+#define MXQ_ACT_SILU 2
+#define MXQ_ACT_GELU 3
+int mxq_moe_linear(const uint8_t *x, int64_t ldx, const uint8_t *sx, const uint8_t *w, int64_t ldw,
+                   int64_t stride_w, const uint8_t *sw, const int32_t *offs, int32_t G, int64_t M,
+                   int64_t N, int64_t K, const void *bias, int bias_dtype, int activation,
+                   const void *residual, int64_t ldr, int dtype, void *y, int64_t ldy, void *z,
+                   int64_t ldz, cudaStream_t stream);
+int mxq_moe_weight_gradient(const uint8_t *a, int64_t lda, const uint8_t *sa, const uint8_t *b,
+                            int64_t ldb, const uint8_t *sb, const int32_t *offs, int32_t G,
+                            int64_t M, int64_t N, int64_t K, int accumulate, int dtype, void *dw,
+                            int64_t ldd, int64_t stride_d, cudaStream_t stream);
+int64_t mxq_moe_linear_backward_workspace(int64_t M, int64_t N);
+int mxq_moe_linear_backward(const void *dy, int dtype, int64_t ld_dy, const void *z, int64_t ldz,
+                            int activation, const int32_t *offs, int32_t G, int64_t M, int64_t N,
+                            void *dz, int64_t ld_dz, float *dbias, uint8_t *workspace,
+                            int64_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Scaled lookup in a table [rows, D], and the table's gradient.
  *   ids      int32 or int64 (ids_bytes 4 or 8, else MXQ_EBADDTYPE) [tokens].  An id
  *            outside [0, rows) gives a row of zeros, adds to no gradient and sets
@@ -391,6 +481,41 @@ int mxq_embedding_backward(const void *ids, int ids_bytes, int64_t tokens, const
                            int dtype, int64_t D, int64_t ldd, int64_t rows, int64_t padding,
                            float scale, void *dtable, int out_dtype, int64_t ldw,
                            uint8_t *workspace, int64_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * An AdamW step over many tensors in one launch, in place:
+ *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2;
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *   tensors   host array of `count` (at most MXQ_ADAMW_TENSORS) entries, read during the
+ *             call: n contiguous elements p of type dtype, their gradient of type
+ *             grad_dtype, a bf16 copy that the new values are also rounded to (or NULL),
+ *             and `start`, the place of its moments in m and v, a multiple of 128.
+ *             Nothing is done for n == 0.  A bf16 p is rounded to nearest.
+ *   bits      32: m and v fp32 [total].  8: m and the root of v as E4M3 [total] with E8M0
+ *             scales m_scale and v_scale [total/32], one for 32 elements by the cast's
+ *             rule; rounded at random from (seed, t, place) so that the mean is exact,
+ *             a root that is not 0 never to 0; a block with a value that is not finite
+ *             becomes NaN.  All bytes of a tensor's last 32 are written, 0 behind its
+ *             end.  total is a multiple of 128; m and v 16-byte aligned.
+ *   t         *step_at (device memory) or, with step_at NULL, step; at least 1.
+ *   lr        *lr_at (device memory) or, with lr_at NULL, lr.
+ *   grad_scale  device memory, or NULL: 1.
+ *   beta1, beta2 in [0, 1), eps >= 0.
+ * No two outputs may overlap, nor an output and an input.
+ */
+#define MXQ_ADAMW_TENSORS 512
+typedef struct mxq_adamw_tensor {
+  void *p;
+  const void *grad;
+  void *copy;
+  int64_t n, start;
+  int32_t dtype, grad_dtype;
+} mxq_adamw_tensor;
+int mxq_adamw(const mxq_adamw_tensor *tensors, int32_t count, int32_t bits, void *m, void *v,
+              uint8_t *m_scale, uint8_t *v_scale, int64_t total, int64_t step,
+              const int64_t *step_at, double lr, const float *lr_at, double beta1, double beta2,
+              double eps, double weight_decay, const float *grad_scale, uint64_t seed,
+              cudaStream_t stream);
 
 /*
  * Newton-Schulz orthogonalisation of a momentum matrix, or of a stack of them:

@@ -113,20 +113,30 @@ def lib() -> ctypes.CDLL:
                                        ctypes.c_int, vp]
         L.mxq_mxfp8_scaled_mm.restype = ctypes.c_int
         L.mxq_mxfp8_scaled_mm.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i64, i64, vp]
-        f32, ci = ctypes.c_float, ctypes.c_int
+        f32, f64, ci = ctypes.c_float, ctypes.c_double, ctypes.c_int
         for name, restype, argtypes in (
                 ("mxq_moe_route_workspace", i64, [i64, i32]),
                 ("mxq_moe_route", ci, [vp, ci, i64, i32, i64, i32, vp, ci, vp, vp, vp, vp, vp, vp, i64, vp]),
                 ("mxq_moe_route_backward", ci, [vp, ci, i64, i32, i64, i32, vp, ci, vp, vp, vp, vp, vp, vp, i64, vp]),
+                ("mxq_moe_route_groups", ci, [vp, ci, i64, i32, i64, i32, vp, ci, i32, i32, vp, ci, f32, vp, vp, vp, vp, vp, vp, i64,
+                                              vp]),
+                ("mxq_moe_route_groups_backward", ci, [vp, ci, i64, i32, i64, i32, ci, vp, ci, f32, vp, vp, vp, vp, vp, vp, i64, vp]),
                 ("mxq_moe_rows", i64, [i64, i32, i32]),
                 ("mxq_moe_plan_workspace", i64, [i64, i32, i32]),
                 ("mxq_moe_plan", ci, [vp, i64, i32, i32, i64, vp, vp, vp, vp, i64, vp]),
                 ("mxq_moe_dispatch", ci, [vp, ci, i64, i64, i64, i32, vp, vp, i64, vp, i64, vp]),
                 ("mxq_moe_combine", ci, [vp, ci, i64, i64, i64, i64, i32, vp, vp, vp, i64, vp]),
                 ("mxq_moe_combine_backward", ci, [vp, ci, i64, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i64, vp, vp]),
+                ("mxq_moe_linear", ci, [vp, i64, vp, vp, i64, i64, vp, vp, i32, i64, i64, i64, vp, ci, ci, vp, i64, ci, vp, i64,
+                                        vp, i64, vp]),
+                ("mxq_moe_weight_gradient", ci, [vp, i64, vp, vp, i64, vp, vp, i32, i64, i64, i64, ci, ci, vp, i64, i64, vp]),
+                ("mxq_moe_linear_backward_workspace", i64, [i64, i64]),
+                ("mxq_moe_linear_backward", ci, [vp, ci, i64, vp, i64, ci, vp, i32, i64, i64, vp, i64, vp, vp, i64, vp]),
                 ("mxq_embedding", ci, [vp, ci, i64, vp, ci, i64, i64, i64, f32, vp, ci, i64, vp]),
                 ("mxq_embedding_backward_workspace", i64, [i64, i64, i64]),
                 ("mxq_embedding_backward", ci, [vp, ci, i64, vp, ci, i64, i64, i64, i64, f32, vp, ci, i64, vp, i64, vp]),
+                ("mxq_adamw", ci, [vp, i32, i32, vp, vp, vp, vp, i64, i64, vp, f64, vp, f64, f64, f64, f64, vp, ctypes.c_uint64,
+                                   vp]),
                 ("mxq_orthogonalize_workspace", i64, [i64, i64, i64]),
                 ("mxq_orthogonalize", ci, [vp, ci, i64, i64, i64, i64, i64, i32, f32, f32, f32, f32, f32, vp, i64, i64,
                                            vp, i64, vp])):
@@ -599,8 +609,10 @@ def mxfp8_scaled_mm(a, sa, b, sb, *, out=None, stream=None):
 # operators of a mixture-of-experts training step (training.py)
 # ---------------------------------------------------------------------------
 
-_TRAINING = ("Routing", "MoePlan", "moe_route", "moe_route_backward", "moe_rows", "moe_plan", "moe_dispatch",
-             "moe_combine", "moe_combine_backward", "embedding", "embedding_backward", "orthogonalize")
+_TRAINING = ("Routing", "MoePlan", "moe_route", "moe_route_backward",
+             "moe_route_groups", "moe_route_groups_backward", "moe_rows", "moe_plan", "moe_dispatch",
+             "moe_combine", "moe_combine_backward", "moe_linear", "moe_linear_backward", "moe_weight_gradient", "embedding", "embedding_backward", "orthogonalize",
+             "Moments", "adamw_moments", "adamw_step")
 
 
 def __getattr__(name):

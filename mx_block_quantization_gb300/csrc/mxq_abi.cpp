@@ -25,13 +25,17 @@ extern "C" int mxq_version(void) { return (1 << 16) | 0; }
 
 namespace mxq {
 int route_watch(uint64_t address);      // moe_route.cu
+int route_groups_watch(uint64_t address);  // moe_route_groups.cu
 int exchange_watch(uint64_t address);   // moe_exchange.cu
 int embedding_watch(uint64_t address);  // embedding.cu
 int ortho_watch(uint64_t address);      // orthogonalize.cu
+int linear_watch(uint64_t address);     // moe_linear.cu
+int adamw_watch(uint64_t address);      // adamw.cu
 }  // namespace mxq
 
 extern "C" int mxq_selftest_watch(const void *address) {
-  for (auto *watch : {mxq::route_watch, mxq::exchange_watch, mxq::embedding_watch, mxq::ortho_watch}) {
+  for (auto *watch : {mxq::route_watch, mxq::exchange_watch, mxq::embedding_watch, mxq::ortho_watch,
+                      mxq::linear_watch, mxq::adamw_watch, mxq::route_groups_watch}) {
     const int rc = watch(reinterpret_cast<uintptr_t>(address));
     if (rc != MXQ_OK) return rc;
   }

@@ -169,6 +169,22 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 }
 constexpr float kLog2E = 1.4426950408889634f;
 
+// 1/x to one unit in the last place, without the exact division's branches.
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 1 / (1 + e^-x), a few units in the last place.
+__device__ __forceinline__ float logistic(float x) { return reciprocal(1.0f + exp2_ftz(-kLog2E * x)); }
+// And 1 - logistic(x) by its own formula: the difference would lose its digits.
+__device__ __forceinline__ void logistic_pair(float x, float& s, float& rest) {
+  const float e = exp2_ftz(-kLog2E * x);
+  s = reciprocal(1.0f + e);
+  rest = e > 0x1p64f ? 1.0f : e * s;  // not infinity times 0; a NaN stays
+}
+
 // The widest power of two of bytes, up to 16, that divides every value.
 inline int common_alignment(std::initializer_list<uint64_t> values) {
   uint64_t all = 16;

@@ -14,6 +14,8 @@ stream of that device.
 """
 from __future__ import annotations
 
+import ctypes
+from contextlib import nullcontext
 from operator import index
 from typing import NamedTuple, Optional
 
@@ -36,6 +38,13 @@ class MoePlan(NamedTuple):
     offs: torch.Tensor    # int32 [E]: cumulative group ends, multiples of 128
     slots: torch.Tensor   # int32 [T, k]: row of each assignment, -1 for none
     source: torch.Tensor  # int32 [M]: assignment of each row, -1 for none
+
+
+class Moments(NamedTuple):
+    m: torch.Tensor                   # float32, or uint8 E4M3 [total]
+    v: torch.Tensor                   # float32; in 8 bits the bytes of its root
+    m_scale: Optional[torch.Tensor]   # None, or uint8 E8M0 [total / 32]
+    v_scale: Optional[torch.Tensor]
 
 
 def _count(value, what):
@@ -199,6 +208,96 @@ def moe_route_backward(logits, routing: Routing, dweights=None, dloss=None, *, m
     return out
 
 
+_SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def _score_code(scores):
+    code = _SCORES.get(scores)
+    if code is None:
+        raise ValueError(f"scores must be one of {list(_SCORES)}")
+    return code
+
+
+def moe_route_groups(logits, k: int, *, bias=None, scores: str = "sigmoid", groups: int = 1, best_groups: int = 1,
+                     mask=None, renorm: bool = True, scale: float = 1.0, out: Optional[Routing] = None,
+                     stream=None) -> Routing:
+    """The k experts of each token by their scores s ("sigmoid" or "softmax" of the logits
+    [T, E]) plus ``bias`` (fp32 [E]), among the ``best_groups`` of the ``groups`` equal
+    groups of experts whose two best sum highest.  Weights are ``scale`` times s of the
+    chosen (over their sum with ``renorm``); tokens of each expert and the balance loss as
+    in :func:`moe_route`, with s over its sum as the probabilities.  Near ties are decided
+    in 64 bits."""
+    dev = logits.device
+    ld = _matrix(logits, "logits")
+    code = _code(logits, "logits")
+    what = "mxq_moe_route_groups"
+    k, groups, best_groups = _count(k, what), _count(groups, what), _count(best_groups, what)
+    score = _score_code(scores)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_route_groups(logits, k, bias=bias, scores=scores, groups=groups, best_groups=best_groups, mask=mask,
+                                    renorm=renorm, scale=scale, out=out)
+    T, E = logits.shape
+    mask_p = None if mask is None else _mask_pointer(mask, T, dev)
+    bias_p = None if bias is None else _flat(bias, "bias", torch.float32, (E,), dev)
+    L = lib()
+    size = L.mxq_moe_route_workspace(T, E)
+    ws, wp = _workspace(size, what, dev)
+    if out is None:
+        out = Routing(torch.empty((T, max(k, 0)), dtype=torch.float32, device=dev),
+                      torch.empty((T, max(k, 0)), dtype=torch.int32, device=dev),
+                      torch.empty(E, dtype=torch.int32, device=dev),
+                      torch.empty((), dtype=torch.float32, device=dev),
+                      torch.empty((), dtype=torch.int32, device=dev))
+    else:
+        for t, name, dtype, shape in zip(out, Routing._fields,
+                                         (torch.float32, torch.int32, torch.int32, torch.float32, torch.int32),
+                                         ((T, k), (T, k), (E,), (), ())):
+            _flat(t, name, dtype, shape, dev)
+    rc = L.mxq_moe_route_groups(logits.data_ptr(), code, T, E, ld, k, bias_p, score, groups, best_groups, mask_p, bool(renorm),
+                                scale, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+                                out[4].data_ptr(), wp, size, _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, what)
+    return out
+
+
+def moe_route_groups_backward(logits, routing: Routing, dweights=None, dloss=None, *, scores: str = "sigmoid", mask=None,
+                              renorm: bool = True, scale: float = 1.0, out=None, stream=None):
+    """Gradient of the logits of :func:`moe_route_groups` from those of the weights [T, k]
+    and of the loss [] (fp32; None for zero), the choice held fixed; scores, mask, renorm
+    and scale as there."""
+    dev = logits.device
+    ld = _matrix(logits, "logits")
+    code = _code(logits, "logits")
+    score = _score_code(scores)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_route_groups_backward(logits, routing, dweights, dloss, scores=scores, mask=mask, renorm=renorm,
+                                             scale=scale, out=out)
+    T, E = logits.shape
+    k = routing.ids.shape[-1]
+    i = _flat(routing.ids, "ids", torch.int32, (T, k), dev)
+    c = _flat(routing.counts, "counts", torch.int32, (E,), dev)
+    n = _flat(routing.routed, "routed", torch.int32, (), dev)
+    dw = None if dweights is None else _flat(dweights, "dweights", torch.float32, (T, k), dev)
+    dl = None if dloss is None else _flat(dloss, "dloss", torch.float32, (), dev)
+    mask_p = None if mask is None else _mask_pointer(mask, T, dev)
+    if out is None:
+        out, ldd = torch.empty((T, E), dtype=logits.dtype, device=dev), E
+    else:
+        ldd = _matrix(out, "out", T, E, dev)
+        if out.dtype != logits.dtype:
+            raise ValueError("out must have the logits' type")
+    rc = lib().mxq_moe_route_groups_backward(logits.data_ptr(), code, T, E, ld, k, score, mask_p, bool(renorm), scale, i, c, n,
+                                             dw, dl, out.data_ptr(), ldd, _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_route_groups_backward")
+    return out
+
+
 # ---------------------------------------------------------------------------
 # exchange
 # ---------------------------------------------------------------------------
@@ -344,6 +443,191 @@ def moe_combine_backward(dy, rows, plan: MoePlan, weights, *, out=None, stream=N
 
 
 # ---------------------------------------------------------------------------
+# the experts' products
+# ---------------------------------------------------------------------------
+
+_ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def _activation(name):
+    code = _ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"activation must be one of {list(_ACTIVATIONS)}")
+    return code
+
+
+def _offs_pointer(offs, device):
+    """(pointer, G) of the groups' ends."""
+    if offs is None:
+        return None, 0
+    if offs.dim() != 1:
+        raise ValueError("offs must be 1-D")
+    return _flat(offs, "offs", torch.int32, offs.shape, device), offs.numel()
+
+
+def _e4m3(t, name, rows=None, cols=None, device=None):
+    if t.dtype != torch.uint8:
+        raise ValueError(f"{name} must be uint8 E4M3 bytes")
+    return _matrix(t, name, rows, cols, device)
+
+
+def _scales(t, name, count, device):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.dtype != torch.uint8 or t.numel() != count or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous uint8 tensor of {count} scales on {device}")
+    return t.data_ptr()
+
+
+def _output(t, name, shape, dtype, device):
+    """(pitch, distance of matrices) of an output of this shape, type and device."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on {device}")
+    _, _, _, ld, stride = _stacked(t, name)
+    return ld, stride
+
+
+def moe_linear(q, s, w, sw, offs=None, *, bias=None, activation: Optional[str] = None, residual=None,
+               preactivation: bool = False, dtype=None, out=None, stream=None):
+    """The experts' product act(x w^T + bias) + residual [M, N] of rows x, given as the
+    cast's row-wise bytes q [M, K] and scales s, with each group's weights, the bytes w
+    [G, N, K] and scales sw of their cast.  ``offs``: the groups' ends as for
+    :func:`quantize_2d_dual`; without, one group and w [N, K].  Rows behind the last
+    group are zero.
+
+    ``bias`` [G, N] ([N] without offs; fp32 or bf16), ``activation`` "relu", "silu" or
+    "gelu" (tanh form), ``residual`` [M, N] of the output's type (it may be ``out``).
+    With ``preactivation`` also returns z = x w^T + bias.  ``dtype``: bf16 unless given,
+    or fp32.  The gradient of x is the same product of the cast dz with the column-wise
+    cast of the weights (q_col of [G*N, K] as [G, K, N])."""
+    dev = q.device
+    ldx = _e4m3(q, "q")
+    M, K = q.shape
+    if w.dtype != torch.uint8:
+        raise ValueError("w must be uint8 E4M3 bytes")
+    if w.dim() != (2 if offs is None else 3):
+        raise ValueError("w must be 3-D with offs and 2-D without")
+    op, G = _offs_pointer(offs, dev)
+    lead = w.shape[:-2]
+    if offs is not None and w.shape[0] != G:
+        raise ValueError(f"w must have {G} matrices")
+    N = w.shape[-2]
+    first = w if offs is None else w[0] if G > 0 else w.new_empty(N, K)
+    ldw = _matrix(first, "w", N, K, dev)
+    stride_w = w.stride(0) if G > 1 else 0
+    code = _activation(activation)
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else (out[0] if preactivation else out).dtype
+    if dtype not in _CODES:
+        raise ValueError("dtype must be float32 or bfloat16")
+    sx_p = _scales(s, "s", M * K // 32, dev)
+    sw_p = _scales(sw, "sw", max(G, 1) * N * K // 32, dev)
+    bias_p = bias_code = 0
+    if bias is not None:
+        bias_code = _code(bias, "bias")
+        bias_p = _flat(bias, "bias", bias.dtype, torch.Size((*lead, N)), dev)
+    ldr = res_p = 0
+    if residual is not None:
+        if residual.dtype != dtype:
+            raise ValueError("residual must have the output's type")
+        ldr, res_p = _matrix(residual, "residual", M, N, dev), residual.data_ptr()
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_linear(q, s, w, sw, offs, bias=bias, activation=activation, residual=residual,
+                              preactivation=preactivation, dtype=dtype, out=out)
+    if out is None:
+        y = torch.empty((M, N), dtype=dtype, device=dev)
+        z = torch.empty((M, N), dtype=dtype, device=dev) if preactivation else None
+        ldy = ldz = max(N, 1)
+    else:
+        y, z = out if preactivation else (out, None)
+        ldy = _output(y, "out", (M, N), dtype, dev)[0]
+        ldz = 0 if z is None else _output(z, "z", (M, N), dtype, dev)[0]
+    rc = lib().mxq_moe_linear(q.data_ptr(), ldx, sx_p, w.data_ptr(), ldw, stride_w, sw_p, op, G, M, N, K, bias_p, bias_code,
+                              code, res_p, ldr, _CODES[dtype], y.data_ptr(), ldy, None if z is None else z.data_ptr(), ldz,
+                              _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_linear")
+    return (y, z) if preactivation else y
+
+
+def moe_linear_backward(dy, z=None, offs=None, *, activation: Optional[str] = None, out=None, stream=None):
+    """Gradients (dz [M, N], dbias fp32 [G, N], or [N] without offs) of what
+    :func:`moe_linear` adds to the product: dz = dy act'(z) with the pre-activation z,
+    zero behind the last group, and its sum over each group.  Without an activation dz is
+    dy itself.  The residual's gradient is dy."""
+    dev = dy.device
+    dtype_code = _code(dy, "dy")
+    ld = _matrix(dy, "dy")
+    M, N = dy.shape
+    code = _activation(activation)
+    op, G = _offs_pointer(offs, dev)
+    ldz = 0
+    if code:
+        if z is None:
+            raise ValueError("z is needed with an activation")
+        if z.dtype != dy.dtype:
+            raise ValueError("z must have dy's type")
+        ldz = _matrix(z, "z", M, N, dev)
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_linear_backward(dy, z, offs, activation=activation, out=out)
+    L = lib()
+    size = L.mxq_moe_linear_backward_workspace(M, N)
+    ws, wp = _workspace(size, "mxq_moe_linear_backward", dev)
+    shape = (N,) if offs is None else (G, N)
+    if out is None:
+        dz = torch.empty((M, N), dtype=dy.dtype, device=dev) if code else dy
+        dbias = torch.empty(shape, dtype=torch.float32, device=dev)
+    else:
+        dz, dbias = out
+        if not code and dz is not dy:
+            raise ValueError("without an activation dz is dy itself")
+    ld_dz = _output(dz, "dz", (M, N), dy.dtype, dev)[0]
+    db = _flat(dbias, "dbias", torch.float32, torch.Size(shape), dev)
+    rc = L.mxq_moe_linear_backward(dy.data_ptr(), dtype_code, ld, z.data_ptr() if code else None, ldz, code, op, G, M, N,
+                                   dz.data_ptr() if code else None, ld_dz, db, wp, size, _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_linear_backward")
+    return dz, dbias
+
+
+def moe_weight_gradient(a, sa, b, sb, offs=None, *, dtype=None, out=None, accumulate: bool = False, stream=None):
+    """The weights' gradient [G, N, K] of :func:`moe_linear`: for each group the product
+    dz^T x over its rows, from the column-wise bytes and scales of the cast dz (a [N, M],
+    sa) and of the cast x (b [K, M], sb), both with these ``offs``; [N, K] without.  fp32
+    unless ``dtype`` says bf16.  With ``accumulate`` it is added to ``out``."""
+    dev = a.device
+    lda = _e4m3(a, "a")
+    N, M = a.shape
+    ldb = _e4m3(b, "b", None, M, dev)
+    K = b.shape[0]
+    op, G = _offs_pointer(offs, dev)
+    sa_p, sb_p = _scales(sa, "sa", N * M // 32, dev), _scales(sb, "sb", K * M // 32, dev)
+    if dtype is None:
+        dtype = torch.float32 if out is None else out.dtype
+    if dtype not in _CODES:
+        raise ValueError("dtype must be float32 or bfloat16")
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    where = _elsewhere(dev, stream)
+    if where is not None:
+        with where:
+            return moe_weight_gradient(a, sa, b, sb, offs, dtype=dtype, out=out, accumulate=accumulate)
+    shape = (N, K) if offs is None else (G, N, K)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    ldd, stride_d = _output(out, "out", shape, dtype, dev)
+    rc = lib().mxq_moe_weight_gradient(a.data_ptr(), lda, sa_p, b.data_ptr(), ldb, sb_p, op, G, M, N, K, bool(accumulate),
+                                       _CODES[dtype], out.data_ptr(), ldd, stride_d, _stream(dev.index))
+    if rc != OK:
+        raise MxqError(rc, "mxq_moe_weight_gradient")
+    return out
+
+
+# ---------------------------------------------------------------------------
 # embedding table
 # ---------------------------------------------------------------------------
 
@@ -476,3 +760,112 @@ def orthogonalize(g, *, steps: int = 5, coefficients=(3.4445, -4.775, 2.0315), e
     if rc != OK:
         raise MxqError(rc, "mxq_orthogonalize")
     return out
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------
+
+_START = 128           # a tensor's moments begin at a multiple of it
+_TENSORS = 512         # MXQ_ADAMW_TENSORS
+
+
+def _moment_starts(sizes):
+    """Where each tensor's moments begin, and the elements of all."""
+    starts, total = [], 0
+    for n in sizes:
+        starts.append(total)
+        total += -(-n // _START) * _START
+    return starts, total
+
+
+def adamw_moments(params, bits: int = 32) -> Moments:
+    """Moments of zero for :func:`adamw_step` of these parameters, on their device: fp32, or
+    with ``bits`` 8 bytes and scales of MXFP8.  Those of each tensor begin at a multiple of
+    128, in the order of the list."""
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+    params = list(params)
+    total = _moment_starts([p.numel() for p in params])[1]
+    dev = params[0].device if params else torch.device("cuda", torch.cuda.current_device())
+    kind = torch.float32 if bits == 32 else torch.uint8
+    m, v = (torch.zeros(total, dtype=kind, device=dev) for _ in range(2))
+    if bits == 32:
+        return Moments(m, v, None, None)
+    return Moments(m, v, *(torch.zeros(total // 32, dtype=torch.uint8, device=dev) for _ in range(2)))
+
+
+def _scalar(value, name, dtype, device):
+    """(number, address) of an argument that may lie on the device."""
+    if not isinstance(value, torch.Tensor):
+        return value, None
+    return 0, _flat(value, name, dtype, (), device)
+
+
+def adamw_step(params, grads, moments: Moments, step, *, lr, betas=(0.9, 0.999), eps: float = 1e-8,
+               weight_decay: float = 0.01, grad_scale=None, copies=None, seed: int = 0, stream=None):
+    """One AdamW step on all tensors of ``params`` in place, with their gradients, and of
+    their ``moments`` (:func:`adamw_moments`):
+
+        m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+        p = p (1 - lr weight_decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
+
+    Parameters and gradients are contiguous and fp32 or bf16, each as it is; a gradient of
+    None leaves its tensor and moments.  ``copies``: bf16 tensors (or None) that the new
+    parameters are also rounded to.  ``step`` t counts from 1; ``step`` (int64) and ``lr``
+    (fp32) may be tensors [] on the device, read as the step runs, so that a captured step
+    can be replayed.  ``grad_scale``: an fp32 tensor [] that multiplies the gradients.
+    Moments in 8 bits are rounded at random by ``seed`` and the step."""
+    params, grads = list(params), list(grads)
+    n = len(params)
+    if len(grads) != n or (copies is not None and len(copies) != n):
+        raise ValueError("params, grads and copies must be of one length")
+    if n == 0:
+        return
+    dev = params[0].device
+    sizes = [p.numel() for p in params]
+    starts, total = _moment_starts(sizes)
+    bits = 32 if moments.m.dtype == torch.float32 else 8
+    kind = torch.float32 if bits == 32 else torch.uint8
+    m, v = (_flat(t, name, kind, (total,), dev) for t, name in ((moments.m, "m"), (moments.v, "v")))
+    ms = vs = None
+    if bits == 8:
+        if moments.m_scale is None or moments.v_scale is None:
+            raise ValueError("moments in 8 bits have scales")
+        ms, vs = (_flat(t, name, torch.uint8, (total // 32,), dev)
+                  for t, name in ((moments.m_scale, "m_scale"), (moments.v_scale, "v_scale")))
+    table, live = [], set()
+    for i, (p, g) in enumerate(zip(params, grads)):
+        if g is None or sizes[i] == 0:
+            continue
+        code, gcode = _code(p, "params"), _code(g, "grads")
+        if p.device != dev or g.device != dev or not dev.type == "cuda":
+            raise ValueError("params and grads must be CUDA tensors of one device (no CPU path)")
+        if not p.is_contiguous() or not g.is_contiguous() or g.shape != p.shape:
+            raise ValueError("params and grads must be contiguous and of one shape")
+        at, copy = p.data_ptr(), 0
+        if copies is not None and copies[i] is not None:
+            copy = _flat(copies[i], "copies", torch.bfloat16, p.shape, dev)
+        live.add(at)
+        table += (at, g.data_ptr(), copy, sizes[i], starts[i], code | gcode << 32)
+    if len(live) * 6 != len(table):
+        raise ValueError("params must be different tensors")
+    if grad_scale is not None:
+        grad_scale = _flat(grad_scale, "grad_scale", torch.float32, (), dev)
+    step, step_at = _scalar(step, "step", torch.int64, dev)
+    lr, lr_at = _scalar(lr, "lr", torch.float32, dev)
+    step, seed = index(step), index(seed)
+    if not 0 <= seed < 1 << 64:
+        raise ValueError("seed must be in [0, 2^64)")
+    if step_at is None and not 1 <= step <= 0x7FFFFFFF:
+        raise ValueError("step must count from 1")
+    b1, b2 = betas
+    where = _elsewhere(dev, stream)
+    with where if where is not None else nullcontext():
+        handle = _stream(dev.index)
+        for at in range(0, len(table), 6 * _TENSORS):
+            part = table[at:at + 6 * _TENSORS]
+            rc = lib().mxq_adamw((ctypes.c_int64 * len(part))(*part), len(part) // 6, bits, m, v, ms, vs, total, step, step_at,
+                                 lr, lr_at, b1, b2, eps, weight_decay, grad_scale, seed, handle)
+            if rc != OK:
+                raise MxqError(rc, "mxq_adamw")

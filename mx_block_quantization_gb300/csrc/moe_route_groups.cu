@@ -19,9 +19,9 @@
 // Experts with the same logit and the same bias are equal and go by their index at once.
 //
 // One warp owns a token, a lane keeps kPer of its logits in registers, and the next
-// token's are loaded ahead, as in moe_route.cu.  For the groups the keys of all c go
-// through shared memory, rows of a group apart so that the lanes of different groups read
-// different banks; 32 / groups lanes find the two largest of a group.
+// token's are loaded ahead, as in moe_route.cu.  For the groups all c go through shared
+// memory, the groups' rows so far apart that the lanes of different groups read different
+// banks; 32 / groups lanes find the two largest of a group.
 #include "moe_route_common.cuh"
 
 namespace {
@@ -31,21 +31,25 @@ constexpr int kMaxGroups = 32;  // a group per lane
 
 struct Grouped {
   int groups, best, size;       // size: experts of a group
-  int lanes, pitch;             // lanes that work on a group; floats between groups' keys
+  int lanes, shift, pitch;      // lanes that work on a group, their logarithm; floats between groups' rows
   float scale;
 };
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, d));
-  return v;
+// Keys in the order of values of 64 bits, 0 for -inf and NaN: what is compared, so that
+// the slow pipe for 64 bits sees the scores alone.
+__device__ __forceinline__ uint64_t wide_key(double v) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+  return v > -CUDART_INF ? b ^ ((b >> 63) != 0 ? ~0ull : 1ull << 63) : 0ull;
 }
-__device__ __forceinline__ double warp_max(double v) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v = fmax(v, __shfl_xor_sync(kAll, v, d));
-  return v;
+__device__ __forceinline__ double wide_value(uint64_t k) {
+  return __longlong_as_double(static_cast<long long>((k >> 63) != 0 ? k ^ 1ull << 63 : ~k));
 }
-__device__ __forceinline__ double warp_sum(double v) {
+__device__ __forceinline__ uint64_t wide_max(uint64_t k) {
+  const uint32_t high = __reduce_max_sync(kAll, static_cast<uint32_t>(k >> 32));
+  const uint32_t low = __reduce_max_sync(kAll, static_cast<uint32_t>(k >> 32) == high ? static_cast<uint32_t>(k) : 0u);
+  return static_cast<uint64_t>(high) << 32 | low;
+}
+__device__ __forceinline__ double wide_sum(double v) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(kAll, v, d);
   return v;
@@ -55,71 +59,72 @@ __device__ __forceinline__ double warp_sum(double v) {
 // lane j the j-th of the chosen, -1 where there are no more.
 template <typename T, int kPer, bool kLogistic>
 __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int E, int k, int groups, int best, int size) {
+  constexpr int kAtOnce = kPer < 4 ? kPer : 4;  // chains of the scores in flight
   const int lane = threadIdx.x & 31;
-  const double none = -CUDART_INF;
   double c[kPer];
-  double top = none, sum = 0.0;
-  if (!kLogistic) {
+  uint64_t key[kPer];
+  float top = -CUDART_INF_F;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) top = fmaxf(top, lane + 32 * i < E ? widen(row[lane + 32 * i]) : -CUDART_INF_F);
+  top = key_value(max(__reduce_max_sync(kAll, order_key(top)), order_key(-FLT_MAX)));
+  double sum = 0.0;
 #pragma unroll 1
-    for (int e = lane; e < E; e += 32) top = fmax(top, static_cast<double>(widen(row[e])));
-    top = warp_max(top);
+  for (int i = 0; i < kPer; i += kAtOnce)
+#pragma unroll
+    for (int j = i; j < i + kAtOnce; ++j) {
+      const double x = lane + 32 * j < E ? widen(row[lane + 32 * j]) : -CUDART_INF_F;
+      c[j] = exp(kLogistic ? -x : x - top);
+      sum += c[j];
+    }
+  if (!kLogistic) sum = 1.0 / wide_sum(sum);
 #pragma unroll 1
-    for (int e = lane; e < E; e += 32) sum += exp(static_cast<double>(widen(row[e])) - top);
-    sum = warp_sum(sum);
-  }
-#pragma unroll 1
-  for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 32 * i;
-    c[i] = none;
-    if (e >= E) continue;
-    const double x = widen(row[e]);
-    if (!(x > none)) continue;
-    const double v = (kLogistic ? 1.0 / (1.0 + exp(-x)) : exp(x - top) / sum) + (bias != nullptr ? bias[e] : 0.0f);
-    if (v > none) c[i] = v;
-  }
+  for (int i = 0; i < kPer; i += kAtOnce)
+#pragma unroll
+    for (int j = i; j < i + kAtOnce; ++j) {
+      const int e = lane + 32 * j;
+      const double v = (kLogistic ? 1.0 / (1.0 + c[j]) : c[j] * sum) + (bias != nullptr && e < E ? bias[e] : 0.0f);
+      key[j] = e < E && widen(row[e]) > -CUDART_INF_F ? wide_key(v) : 0ull;
+    }
   if (groups > 1) {
-    double value = none;  // of the group of this lane
+    uint64_t value = 0;  // of the group of this lane
 #pragma unroll 1
     for (int g = 0; g < groups; ++g) {
-      double first = none, second = none;
-#pragma unroll 1
+      uint64_t first = 0, second = 0;
+#pragma unroll
       for (int i = 0; i < kPer; ++i)
-        if ((lane + 32 * i) / size == g) second = fmax(second, fmin(first, c[i])), first = fmax(first, c[i]);
-#pragma unroll 1
-      for (int d = 16; d > 0; d >>= 1) {
-        const double other = __shfl_xor_sync(kAll, first, d), next = __shfl_xor_sync(kAll, second, d);
-        second = fmax(fmax(second, next), fmin(first, other));
-        first = fmax(first, other);
-      }
-      if (lane == g) value = second > none ? first + second : first;
+        if ((lane + 32 * i) / size == g) second = max(second, min(first, key[i])), first = max(first, key[i]);
+      const uint64_t most = wide_max(first);
+      const int owner = __ffs(__ballot_sync(kAll, first == most)) - 1;
+      const uint64_t next = wide_max(lane == owner ? second : first);
+      if (lane == g && most != 0) value = next != 0 ? wide_key(wide_value(most) + wide_value(next)) : most;
     }
-    int before = 0;
+    uint32_t chosen = 0;
 #pragma unroll 1
-    for (int g = 0; g < groups; ++g) {
-      const double other = __shfl_sync(kAll, value, g);
-      before += other > value || (other == value && g < lane) ? 1 : 0;
+    for (int r = 0; r < best; ++r) {
+      const uint64_t most = wide_max(value);
+      if (most == 0) break;
+      const int g = __ffs(__ballot_sync(kAll, value == most)) - 1;
+      chosen |= 1u << g;
+      if (lane == g) value = 0;
     }
-    const uint32_t chosen = __ballot_sync(kAll, lane < groups && before < best);
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i < E && !(chosen >> ((lane + 32 * i) / size) & 1u)) c[i] = none;
+      if (lane + 32 * i < E && !(chosen >> ((lane + 32 * i) / size) & 1u)) key[i] = 0;
   }
   int mine = -1;
 #pragma unroll 1
   for (int j = 0; j < k; ++j) {
-    double most = none;
-#pragma unroll 1
-    for (int i = 0; i < kPer; ++i) most = fmax(most, c[i]);
-    most = warp_max(most);
-    if (!(most > none)) break;
-    int at = INT32_MAX;
-#pragma unroll 1
-    for (int i = kPer - 1; i >= 0; --i)
-      if (c[i] == most) at = lane + 32 * i;
-    at = static_cast<int>(__reduce_min_sync(kAll, static_cast<uint32_t>(at)));
-#pragma unroll 1
+    uint64_t own = 0;
+    int at = 0;
+#pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (lane + 32 * i == at) c[i] = none;
+      if (key[i] > own) own = key[i], at = lane + 32 * i;
+    const uint64_t most = wide_max(own);
+    if (most == 0) break;
+    at = static_cast<int>(__reduce_min_sync(kAll, own == most ? static_cast<uint32_t>(at) : ~0u));
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (lane + 32 * i == at) key[i] = 0;
     if (lane == j) mine = at;
   }
   return mine;
@@ -135,10 +140,72 @@ __device__ __forceinline__ float doubt(float s, float below, float c) {
   const float of_c = 0x1p-22f * fabsf(c);
   return kLogistic ? 0x1p-21f + of_c : fmaf(s * 0x1p-22f, kPer + 16 + below, of_c);
 }
+// The same of two groups' values v, sums of two c with biases of at most `bias`: twice
+// that, the distance at most 88 (where an exponential is 0), and the sums' rounding.
+template <int kPer, bool kLogistic>
+__device__ __forceinline__ float group_doubt(float v, float bias) {
+  const float size = fabsf(v);
+  return kLogistic ? fmaf(size, 0x1p-21f, 0x1p-20f) : fmaf(fmaf(2.0f, bias, size) * 0x1p-22f, kPer + 104, size * 0x1p-21f);
+}
 
-struct Candidate {
-  float c, x, b;
-  int32_t e;
+// The place in 64 bits of each of n candidates, one a lane, with logistic scores.
+__device__ __noinline__ int rank_exactly(float x, float b, int e, int n) {
+  const int lane = threadIdx.x & 31;
+  const uint64_t own = wide_key(1.0 / (1.0 + exp(-static_cast<double>(x))) + b);
+  int before = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const uint64_t other = __shfl_sync(kAll, own, i);
+    const int o = __shfl_sync(kAll, e, i);
+    before += other > own || (other == own && o < e) ? 1 : 0;
+  }
+  return lane < n ? before : kMaxK;
+}
+
+// Puts v at `at` and moves on where x >= from, under one predicate: as branches, each with
+// a few lanes, the slots of a lane cost three times as much.
+__device__ __forceinline__ void put_from(uint32_t& at, int32_t v, float x, float from) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %2, %3;\n\t@p st.shared.b32 [%0], %1;\n\t@p add.u32 %0, %0, 4;\n\t}"
+               : "+r"(at)
+               : "r"(v), "f"(x), "f"(from)
+               : "memory");
+}
+// A token's logits in the lanes, vectors that end past E left at -inf (E is a multiple of
+// kV); each load under its own predicate.
+template <typename T, int kPer, int kV>
+struct Ahead {
+  Vec<T, kV> v[kPer / kV];
+  uint32_t there;  // a bit for each vector
+  __device__ __forceinline__ Ahead(int E, int lane) : there(0u) {
+#pragma unroll
+    for (int q = 0; q < kPer / kV; ++q) {
+      if (expert_of<kV>(q * kV, lane) < E) there |= 1u << q;
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[q].v[j] = minus_infinity<T>();
+    }
+  }
+  __device__ __forceinline__ void load(const T* row, int lane) {
+#pragma unroll
+    for (int q = 0; q < kPer / kV; ++q) {
+      const T* at = row + expert_of<kV>(q * kV, lane);
+      const uint32_t p = there >> q & 1u;
+      if constexpr (sizeof v[q] == 16) {
+        uint4& w = *reinterpret_cast<uint4*>(&v[q]);
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                     : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w) : "l"(at), "r"(p));
+      } else if constexpr (sizeof v[q] == 8) {
+        uint2& w = *reinterpret_cast<uint2*>(&v[q]);
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];\n\t}"
+                     : "+r"(w.x), "+r"(w.y) : "l"(at), "r"(p));
+      } else if constexpr (sizeof v[q] == 4) {
+        uint32_t& w = *reinterpret_cast<uint32_t*>(&v[q]);
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.L1::no_allocate.b32 %0, [%1];\n\t}" : "+r"(w) : "l"(at), "r"(p));
+      } else {
+        uint16_t& w = *reinterpret_cast<uint16_t*>(&v[q]);
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.L1::no_allocate.b16 %0, [%1];\n\t}" : "+h"(w) : "l"(at), "r"(p));
+      }
+    }
+  }
 };
 
 template <typename T, int kPer, int kV, bool kLogistic, int kThreads>
@@ -149,121 +216,167 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kWarps = kThreads / 32;
   __shared__ int32_t routed_tokens;
-  __shared__ int few_n[kWarps];
-  __shared__ __align__(16) Candidate few[kWarps][32];
-  __shared__ __align__(16) uint64_t order[kWarps][32];
-  // the groups' keys while tokens are worked on; after that the warps' sums
+  __shared__ int32_t few[kWarps][32];                // experts near the top, in any order
+  __shared__ __align__(16) float few_c[kWarps][32];  // their c, then in order
+  __shared__ float2 few_xb[kWarps][32];              // in order, their logits and biases
+  // the groups' rows while tokens are worked on; after that the warps' sums
   float* by_warp = reinterpret_cast<float*>(smem);                        // [warps, 32 * kPer]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int keys_row = gr.groups > 1 ? gr.groups * gr.pitch : 0;
-  const int shared_rows = max(32 * kPer, keys_row);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem) + warp * shared_rows;
-  int32_t* hist = reinterpret_cast<int32_t*>(smem) + kWarps * shared_rows;  // [E]
-  float* sums = reinterpret_cast<float*>(hist + s.E);                       // [E]
+  const int shared_rows = max(32 * kPer, gr.groups > 1 ? gr.groups * gr.pitch : 0);
+  float* rows = reinterpret_cast<float*>(smem) + warp * shared_rows;
+  float* own_x = reinterpret_cast<float*>(smem) + kWarps * shared_rows + warp * (32 * kPer);  // the token's logits
+  float* sums = reinterpret_cast<float*>(smem) + kWarps * (shared_rows + 32 * kPer);  // [32 * kPer]: the biases while tokens are worked on
+  int32_t* hist = reinterpret_cast<int32_t*>(sums + 32 * kPer);                       // [E]
   for (int e = tid; e < s.E; e += kThreads) hist[e] = 0;
   if (tid == 0) routed_tokens = 0;
-  if (lane == 0) few_n[warp] = 0;
   __syncthreads();
   pdl_wait();
   const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
   const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
   if (gridDim.x > 1) pdl_launch_dependents();  // the join's few blocks wait beside this one
-  float acc[kPer], b[kPer];
-  int group_of[kPer];
+  constexpr int kVectors = kPer / kV;
+  float acc[kPer], most_bias = 0.0f;
+  int first_lane[kVectors], place[kVectors];  // of the vector's group, and in the groups' rows
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = expert_of<kV>(i, lane);
-    acc[i] = 0.0f;
-    b[i] = bias != nullptr && e < s.E ? read_at(bias, e, s.E, 0.0f, &g_route_status) : 0.0f;
-    group_of[i] = e < s.E ? e / gr.size : 0;
+  for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
+  for (int e = lane; e < 32 * kPer; e += 32) {
+    const float b = bias != nullptr && e < s.E ? read_at(bias, e, s.E, 0.0f, &g_route_status) : 0.0f;
+    most_bias = fmaxf(most_bias, fabsf(b));
+    if (warp == 0) sums[e] = b;
+  }
+#pragma unroll
+  for (int q = 0; q < kVectors; ++q) {
+    const int e = expert_of<kV>(q * kV, lane), g = e < s.E ? e / gr.size : 0;
+    first_lane[q] = g << gr.shift;
+    place[q] = e < s.E ? g * gr.pitch + e - g * gr.size : -1;
+  }
+  most_bias = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most_bias)));  // not negative: ordered as its bits
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < kVectors; ++q) {
+    const int e = expert_of<kV>(q * kV, lane), g = e < s.E ? e / gr.size : 0;
+    first_lane[q] = g << gr.shift;
+    place[q] = e < s.E ? g * gr.pitch + e - g * gr.size : -1;
   }
   int routed_here = 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  Row<T, kPer, kV> ahead;
+  Ahead<T, kPer, kV> ahead(s.E, lane);
+  uint32_t wanted_ahead = 1u;
   const auto fetch = [&](int64_t t) {
-    if (t < s.tokens && in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status))
-      ahead.load(logits + t * s.ld, s.E, lane);
+    if (t >= s.tokens) return;
+    if (in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status)) ahead.load(logits + t * s.ld, lane);
+    if (mask != nullptr) wanted_ahead = read_at(mask, t, s.tokens, uint8_t{0}, &g_route_status);
   };
   int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   fetch(t);
   for (; t < s.tokens; t += step) {
-    float x[kPer], sc[kPer];
-    ahead.values(x);
+    float x[kPer], c[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = widen(ahead.v[i / kV].v[i % kV]);
+    bool routed = wanted_ahead != 0u;
     fetch(t + step);
-    float top = -CUDART_INF_F;
-    bool nan = false;
+    float top = 0.0f, sum = 0.0f;
+    if (!kLogistic) {
+      top = x[0];
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);  // skips NaN
+      top = key_value(max(__reduce_max_sync(kAll, order_key(top)), order_key(-FLT_MAX)));
+    }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      top = fmaxf(top, x[i]);  // skips NaN
-      nan |= x[i] != x[i];
+      c[i] = kLogistic ? logistic(x[i]) : exp2_ftz((x[i] - top) * kLog2E);  // 0 past E: those are -inf
+      sum += c[i];
     }
-    top = key_value(max(__reduce_max_sync(kAll, order_key(top)), order_key(-FLT_MAX)));
-    const bool unmasked = mask == nullptr || read_at(mask, t, s.tokens, uint8_t{0}, &g_route_status) != 0;
-    bool some = false;
+    sum = warp_sum(sum);
+    if (sum == 0.0f) {  // no expert at all, or scores below fp32's range
+      bool alive = false;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) some |= x[i] > -CUDART_INF_F;
-    const bool routed = unmasked && __any_sync(kAll, some || nan);
+      for (int i = 0; i < kPer; ++i) alive |= x[i] != -CUDART_INF_F;
+      routed = __any_sync(kAll, alive) && routed;
+    }
     int rank = kMaxK, my_id = -1;
     float my_s = 0.0f;
     if (routed) {
       ++routed_here;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        sc[i] = kLogistic ? logistic(x[i]) : exp2_ftz((x[i] - top) * kLog2E);  // 0 past E: those are -inf
-        sum += sc[i];
-      }
-      sum = warp_sum(sum);
       const float inv = sum == 0.0f ? 0.0f : reciprocal(sum);
-      uint32_t key[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const float p = sc[i] * inv;
-        acc[i] += p;
-        if (!kLogistic) sc[i] = p;
-        key[i] = x[i] > -CUDART_INF_F ? order_key(sc[i] + b[i]) : 0u;
+      for (int q = 0; q < kVectors; ++q) {
+        const Vec<float, kV> b = *reinterpret_cast<const Vec<float, kV>*>(sums + expert_of<kV>(q * kV, lane));
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+          const int i = q * kV + j;
+          if (kLogistic) {
+            acc[i] = fmaf(c[i], inv, acc[i]);
+            c[i] += b.v[j];
+          } else {
+            const float p = c[i] * inv;
+            acc[i] += p;
+            c[i] = p + b.v[j];
+          }
+          c[i] = x[i] > -CUDART_INF_F ? fmaxf(c[i], -CUDART_INF_F) : -CUDART_INF_F;  // not NaN
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kVectors; ++q) {
+        Vec<float, kV> v;
+#pragma unroll
+        for (int i = 0; i < kV; ++i) v.v[i] = x[q * kV + i];
+        *reinterpret_cast<Vec<float, kV>*>(own_x + expert_of<kV>(q * kV, lane)) = v;
       }
       bool certain = true;
       if (gr.groups > 1) {
-        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int e = expert_of<kV>(i, lane);
-          if (e < s.E) keys[group_of[i] * gr.pitch + e - group_of[i] * gr.size] = key[i];
+        for (int q = 0; q < kVectors; ++q) {
+          Vec<float, kV> v;
+#pragma unroll
+          for (int i = 0; i < kV; ++i) v.v[i] = c[q * kV + i];
+          if (place[q] >= 0) *reinterpret_cast<Vec<float, kV>*>(rows + place[q]) = v;
         }
         __syncwarp();
-        const int g = lane / gr.lanes;
-        uint32_t first = 0u, second = 0u;
-        if (g < gr.groups)
-          for (int m = lane % gr.lanes; m < gr.size; m += gr.lanes) {
-            const uint32_t v = keys[g * gr.pitch + m];
-            second = max(second, min(first, v));
-            first = max(first, v);
+        const int g = lane >> gr.shift;
+        float first = -CUDART_INF_F, second = -CUDART_INF_F;
+        if (g < gr.groups) {
+          const float* row = rows + g * gr.pitch;
+#pragma unroll 1
+          for (int m = (lane & (gr.lanes - 1)) * kV; m < gr.size; m += gr.lanes * kV) {
+            const Vec<float, kV> v = *reinterpret_cast<const Vec<float, kV>*>(row + m);
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+              second = fmaxf(second, fminf(first, v.v[i]));
+              first = fmaxf(first, v.v[i]);
+            }
           }
-        for (int d = gr.lanes / 2; d > 0; d >>= 1) {
-          const uint32_t other = __shfl_xor_sync(kAll, first, d), next = __shfl_xor_sync(kAll, second, d);
-          second = max(max(second, next), min(first, other));
-          first = max(first, other);
         }
-        const float value = key_value(first) + (second != 0u ? key_value(second) : 0.0f);
-        const uint32_t own = first != 0u ? order_key(value) : 0u;
-        int before = 0;
-        for (int o = 0; o < gr.groups; ++o) {
-          const uint32_t other = __shfl_sync(kAll, own, o * gr.lanes);
-          before += other > own || (other == own && o < g) ? 1 : 0;
+#pragma unroll 1
+        for (int d = gr.lanes >> 1; d > 0; d >>= 1) {
+          const float other = __shfl_xor_sync(kAll, first, d), next = __shfl_xor_sync(kAll, second, d);
+          second = fmaxf(fmaxf(second, next), fminf(first, other));
+          first = fmaxf(first, other);
         }
-        const bool in = own != 0u && before < gr.best;
-        const uint32_t chosen = __ballot_sync(kAll, in);
-        const uint32_t last = __reduce_min_sync(kAll, in ? own : ~0u), next = __reduce_max_sync(kAll, in ? 0u : own);
-        // a sum of two values, and of which two: four times what one is off by, and its rounding
-        if (next != 0u) certain = key_value(last) - key_value(next) > 0x1p-18f * (1.0f + fabsf(key_value(last)));
+        uint32_t left = order_key(second > -CUDART_INF_F ? first + second : first), last = 0u, chosen = 0u;
+#pragma unroll 1
+        for (int r = 0; r < gr.best; ++r) {
+          const uint32_t most = __reduce_max_sync(kAll, left);
+          if (most == 0u) break;
+          const int lead = __ffs(__ballot_sync(kAll, left == most)) - 1;  // the first lane of the lowest of them
+          chosen |= 1u << lead;
+          if (g == lead >> gr.shift) left = 0u;
+          last = most;
+        }
+        const uint32_t next = __reduce_max_sync(kAll, left);
+        if (next != 0u) certain = key_value(last) - key_value(next) > group_doubt<kPer, kLogistic>(key_value(last), most_bias);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (!(chosen >> (group_of[i] * gr.lanes) & 1u)) key[i] = 0u;
+        for (int q = 0; q < kVectors; ++q) {
+          const bool in = chosen >> first_lane[q] & 1u;
+#pragma unroll
+          for (int i = 0; i < kV; ++i) c[q * kV + i] = in ? c[q * kV + i] : -CUDART_INF_F;
+        }
       }
-      uint32_t mine = 0u;
+      float most = c[0];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) mine = max(mine, key[i]);
+      for (int i = 1; i < kPer; ++i) most = fmaxf(most, c[i]);
+      uint32_t mine = order_key(most);
       // the k-th largest lane maximum, equal ones counted once; 0 when there are fewer
       uint32_t bar = __reduce_max_sync(kAll, mine);
       const bool any = bar != 0u;
@@ -274,42 +387,65 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (any && certain) {
         const float low = bar != 0u ? key_value(bar) : -FLT_MAX;
-        const uint32_t from = order_key(low - 0x1p-18f * (1.0f + fabsf(low)));
+        const float from = fmaxf(low - 0x1p-18f * (1.0f + fabsf(low)), -FLT_MAX);
+        // those from there on side by side, the lanes' one behind the other
         int own_n = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) own_n += key[i] != 0u && key[i] >= from ? 1 : 0;
-        int at = 0;
-        if (own_n > 0) at = atomicAdd(&few_n[warp], own_n);
-        const int n = __reduce_add_sync(kAll, own_n);
-        __syncwarp();
-        if (lane == 0) few_n[warp] = 0;  // for the next token
-        if (n <= 32) {
+        for (int i = 0; i < kPer; ++i) own_n += c[i] >= from ? 1 : 0;
+        int upto = own_n;
 #pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (key[i] != 0u && key[i] >= from) few[warp][at++] = Candidate{key_value(key[i]), x[i], b[i], expert_of<kV>(i, lane)};
+        for (int d = 1; d < 32; d *= 2) {
+          const int other = __shfl_up_sync(kAll, upto, d);
+          if (lane >= d) upto += other;
+        }
+        const int n = __shfl_sync(kAll, upto, 31);
+        if (n <= 32) {
+          uint32_t at = smem_u32(&few[warp][upto - own_n]);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) put_from(at, expert_of<kV>(i, lane), c[i], from);
           __syncwarp();
-          const Candidate own = few[warp][lane];
-          const uint64_t own_key = lane < n ? ChoiceKey<float>::of(own.c, own.e) : 0;
-          order[warp][lane] = own_key;
+          const int e = lane < n ? few[warp][lane] : 0;
+          const float x_e = own_x[e], own_b = sums[e];
+          my_s = kLogistic ? logistic(x_e) : exp2_ftz((x_e - top) * kLog2E) * inv;
+          const float own_c = lane < n ? my_s + own_b : -CUDART_INF_F;
+          few_c[warp][lane] = own_c;
           __syncwarp();
           int before = 0;
-          for (int i = 0; i < n; i += 2) {
-            const Vec<uint64_t, 2> other = *reinterpret_cast<const Vec<uint64_t, 2>*>(&order[warp][i]);
-            before += (other.v[0] > own_key ? 1 : 0) + (other.v[1] > own_key ? 1 : 0);
+          for (int i = 0; i < n; i += 4) {
+            const float4 other = *reinterpret_cast<const float4*>(&few_c[warp][i]);
+            before += (other.x > own_c ? 1 : 0) + (other.y > own_c ? 1 : 0) + (other.z > own_c ? 1 : 0) + (other.w > own_c ? 1 : 0);
           }
-          if (lane < n) few[warp][before] = own;
+          // equal ones by their index
+          const uint32_t places = __reduce_or_sync(kAll, lane < n ? 1u << before : 0u);
+          if (__popc(places) != n)
+            for (int i = 0; i < n; ++i) {
+              const float other = __shfl_sync(kAll, own_c, i);
+              const int o = __shfl_sync(kAll, e, i);
+              if (other == own_c && o < e) ++before;
+            }
+          __syncwarp();
+          if (lane < n) few_c[warp][before] = own_c;
           __syncwarp();
           bool clear = true;
-          if (lane < n && before < s.k) {
-            rank = before;
-            my_id = own.e;
-            my_s = kLogistic ? logistic(own.x) : exp2_ftz((own.x - top) * kLog2E) * inv;
-            if (before + 1 < n) {
-              const Candidate after = few[warp][before + 1];
-              clear = own.c - after.c > doubt<kPer, kLogistic>(my_s, top - own.x, own.c) || (own.x == after.x && own.b == after.b);
+          if (lane < n && before < s.k && before + 1 < n)
+            clear = own_c - few_c[warp][before + 1] > doubt<kPer, kLogistic>(my_s, top - x_e, own_c);
+          if (!__all_sync(kAll, clear)) {  // clear all the same where both logit and bias are alike
+            if (lane < n) few_xb[warp][before] = make_float2(x_e, own_b);
+            __syncwarp();
+            if (!clear) {
+              const float2 after = few_xb[warp][before + 1];
+              clear = x_e == after.x && own_b == after.y;
+            }
+            certain = __all_sync(kAll, clear);
+            if (kLogistic && !certain) {
+              before = rank_exactly(x_e, own_b, e, n);
+              certain = true;
             }
           }
-          certain = __all_sync(kAll, clear);
+          if (certain && lane < n && before < s.k) {
+            rank = before;
+            my_id = e;
+          }
         } else {
           certain = false;
         }
@@ -321,30 +457,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ? choose_exactly<T, kPer, kLogistic>(row, bias, s.E, s.k, gr.groups, gr.best, gr.size) : -1;
         rank = my_id >= 0 ? lane : kMaxK;
         const float own = my_id >= 0 ? widen(row[my_id]) : 0.0f;
-        my_s = my_id < 0 ? 0.0f : kLogistic ? logistic(own) : exp2_ftz((own - top) * kLog2E) * inv;
+        my_s = kLogistic ? logistic(own) : exp2_ftz((own - top) * kLog2E) * inv;
       }
       if (my_id >= 0) atomicAdd(&hist[my_id], 1);
     }
     float w = my_id >= 0 ? my_s : 0.0f;
     if (s.renorm) {
       const float all = warp_sum(w);
-      w = all == 0.0f ? 0.0f : w / all;
+      w = all == 0.0f ? 0.0f : w * reciprocal(all);
     }
     w *= gr.scale;
-    // the chosen ones' lanes write their places, and as many others the places left
     const uint32_t chosen = __ballot_sync(kAll, my_id >= 0);
-    if (my_id < 0) {
+    if (__popc(chosen) < s.k && my_id < 0) {  // as many other lanes write the places left
       rank = __popc(chosen) + __popc(~chosen & ((1u << lane) - 1u));
       w = 0.0f;
     }
-    if (rank < s.k && in_buf(weights + t * s.k + rank, 4, weights, out_bytes, &g_route_status) &&
-        in_buf(ids + t * s.k + rank, 4, ids, out_bytes, &g_route_status)) {
-      weights[t * s.k + rank] = w;
-      ids[t * s.k + rank] = my_id;
+    if (rank < s.k) {
+      const int64_t at = t * s.k + rank;
+      if (in_buf(weights + at, 4, weights, out_bytes, &g_route_status) && in_buf(ids + at, 4, ids, out_bytes, &g_route_status)) {
+        weights[at] = w;
+        ids[at] = my_id;
+      }
     }
   }
   if (lane == 0 && routed_here) atomicAdd(&routed_tokens, routed_here);
-  __syncthreads();  // the keys' last readers
+  __syncthreads();  // the last readers of the groups' rows and the biases
   // the warps' sums side by side, then added up in warp order
 #pragma unroll
   for (int i = 0; i < kPer; ++i) by_warp[warp * (32 * kPer) + expert_of<kV>(i, lane)] = acc[i];
@@ -389,12 +526,14 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
   // the next token's logits, chosen experts and their gradients
-  Row<T, kPer, kV> ahead;
+  Ahead<T, kPer, kV> ahead(s.E, lane);
+  uint32_t wanted_ahead = 1u;
   int32_t e_ahead = -1;
   float dw_ahead = 0.0f;
   const auto fetch = [&](int64_t t) {
     if (t >= s.tokens) return;
-    if (in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status)) ahead.load(logits + t * s.ld, s.E, lane);
+    if (in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status)) ahead.load(logits + t * s.ld, lane);
+    if (mask != nullptr) wanted_ahead = read_at(mask, t, s.tokens, uint8_t{0}, &g_route_status);
     if (dweights != nullptr && lane < s.k) {
       e_ahead = read_at(ids, t * s.k + lane, s.tokens * s.k, -1, &g_route_status);
       dw_ahead = read_at(dweights, t * s.k + lane, s.tokens * s.k, 0.0f, &g_route_status);
@@ -406,35 +545,32 @@ __global__ void __launch_bounds__(kThreads)
     const int e = e_ahead >= 0 && e_ahead < s.E ? e_ahead : -1;
     const float dw = e >= 0 ? dw_ahead * scale : 0.0f;
     float x[kPer];
-    ahead.values(x);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) x[i] = widen(ahead.v[i / kV].v[i % kV]);
+    bool routed = wanted_ahead != 0u;
     fetch(t + step);
-    float top = -CUDART_INF_F;
-    bool nan = false;
+    float top = 0.0f;
+    if (!kLogistic) {
+      top = x[0];
+#pragma unroll
+      for (int i = 1; i < kPer; ++i) top = fmaxf(top, x[i]);  // skips NaN
+      top = key_value(max(__reduce_max_sync(kAll, order_key(top)), order_key(-FLT_MAX)));
+    }
+    T* out = dlogits + t * ldd;
+    float d[kPer], rest[kPer], sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      top = fmaxf(top, x[i]);  // skips NaN
-      nan |= x[i] != x[i];
+      if (kLogistic)
+        logistic_pair(x[i], d[i], rest[i]);
+      else
+        d[i] = exp2_ftz((x[i] - top) * kLog2E);  // 0 past E: those are -inf
+      sum += d[i];
     }
-    const uint32_t top_key = __reduce_max_sync(kAll, order_key(top));
-    top = key_value(max(top_key, order_key(-FLT_MAX)));
-    const bool routed =
-        (mask == nullptr || read_at(mask, t, s.tokens, uint8_t{0}, &g_route_status) != 0) && (top_key != 0u || __any_sync(kAll, nan));
-    T* out = dlogits + t * ldd;
-    float d[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) d[i] = 0.0f;
-    if (routed) {
-      float sc[kPer], rest[kPer], sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (kLogistic)
-          logistic_pair(x[i], sc[i], rest[i]);
-        else
-          sc[i] = exp2_ftz((x[i] - top) * kLog2E);  // 0 past E: those are -inf
-        sum += sc[i];
-      }
-      sum = warp_sum(sum);
-      const float inv = sum == 0.0f ? 0.0f : reciprocal(sum);
+    sum = warp_sum(sum);
+    // with a sum of 0 every score is 0, and so is every gradient
+    if (routed && sum != 0.0f) {
+      float (&sc)[kPer] = d;
+      const float inv = reciprocal(sum);
       float pc = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
@@ -473,21 +609,19 @@ __global__ void __launch_bounds__(kThreads)
       }
       __syncwarp();
       if (e >= 0) chosen[e] = 0.0f;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) d[i] = 0.0f;
     }
     if (!in_buf(out, s.E * sizeof(T), dlogits, out_bytes, &g_route_status)) continue;
 #pragma unroll
     for (int q = 0; q < kPer / kV; ++q) {
       const int e0 = expert_of<kV>(q * kV, lane);
-      if (e0 + kV <= s.E) {
-        Vec<T, kV> v;
+      if (e0 >= s.E) continue;
+      Vec<T, kV> v;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) v.v[j] = narrow<T>(d[q * kV + j]);
-        *reinterpret_cast<Vec<T, kV>*>(out + e0) = v;
-      } else {
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-          if (e0 + j < s.E) out[e0 + j] = narrow<T>(d[q * kV + j]);
-      }
+      for (int j = 0; j < kV; ++j) v.v[j] = narrow<T>(d[q * kV + j]);
+      *reinterpret_cast<Vec<T, kV>*>(out + e0) = v;
     }
   }
 }
@@ -520,17 +654,21 @@ int launch_groups(const GroupsCall& a) {
   int32_t* part_n = part_c + static_cast<int64_t>(blocks) * a.s.E;
   uint32_t* joined = reinterpret_cast<uint32_t*>(part_n + blocks);
   float* part_loss = reinterpret_cast<float*>(joined + 1);
-  const int keys = a.gr.groups > 1 ? a.gr.groups * a.gr.pitch : 0;
-  const size_t smem = static_cast<size_t>(kWarps) * (keys > 32 * kPer ? keys : 32 * kPer) * 4 + static_cast<size_t>(a.s.E) * 8;
+  // the next number of floats that is a group's lanes' vectors past a multiple of 32 banks:
+  // neighbouring groups' lanes then read neighbouring banks
+  Grouped gr = a.gr;
+  gr.pitch = gr.size + ((gr.lanes * kV - gr.size) % 32 + 32) % 32;
+  const int rows = gr.groups > 1 ? gr.groups * gr.pitch : 0;
+  const size_t smem = static_cast<size_t>(kWarps) * ((rows > 32 * kPer ? rows : 32 * kPer) + 32 * kPer) * 4 + 32 * kPer * 4 + static_cast<size_t>(a.s.E) * 4;
   const auto kernel = route_groups_kernel<T, kPer, kV, kLogistic, kThreads>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ECUDA;
   static bool attr_done[64] = {};  // benign race: the same attribute set twice
   if (!attr_done[dev]) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024) != cudaSuccess) return MXQ_ECUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 184 * 1024) != cudaSuccess) return MXQ_ECUDA;
     attr_done[dev] = true;
   }
-  const int rc = launch_pdl(kernel, static_cast<unsigned>(blocks), kThreads, smem, a.stream, static_cast<const T*>(a.logits), a.s, a.gr,
+  const int rc = launch_pdl(kernel, static_cast<unsigned>(blocks), kThreads, smem, a.stream, static_cast<const T*>(a.logits), a.s, gr,
                             a.bias, a.mask, a.weights, a.ids, part_p, part_c, part_n, joined, a.counts, a.loss, a.n);
   if (rc != MXQ_OK || blocks == 1) return rc;
   return launch_pdl(route_join_kernel, static_cast<unsigned>(ceil_div(a.s.E, 32)), 32 * kJoinWarps, 0, a.stream, a.s, blocks, part_p,
@@ -552,14 +690,15 @@ int launch_scores(const GroupsCall& a, int scores) {
     return scores == MXQ_SCORES_SIGMOID ? launch_groups<T, kPer, kV, true>(a) : launch_groups<T, kPer, kV, false>(a);
 }
 
-// Vectors of 4 elements (2 for up to 64 experts) where base and row pitch are
-// aligned to them, else single elements.
+// Vectors of 4 elements (2 for up to 64 experts) where base and row pitch are aligned to
+// them and the experts, and those of a group, are whole vectors; else single elements.
 template <typename T, bool kBack>
 int launch_grouped(const GroupsCall& a, int scores) {
   const uint64_t pitch = static_cast<uint64_t>(a.s.ld) * sizeof(T);
   const uint64_t dpitch = kBack ? static_cast<uint64_t>(a.ldd) * sizeof(T) : 0;
   const int align = common_alignment({address_of(a.logits), pitch, kBack ? address_of(a.dlogits) : 0, dpitch});
-  const bool v4 = align >= static_cast<int>(4 * sizeof(T)), v2 = align >= static_cast<int>(2 * sizeof(T));
+  const int size = kBack ? a.s.E : a.gr.size;
+  const bool v4 = align >= static_cast<int>(4 * sizeof(T)) && size % 4 == 0, v2 = align >= static_cast<int>(2 * sizeof(T)) && size % 2 == 0;
   const int E = a.s.E;
   if (E <= 32) return launch_scores<T, 1, 1, kBack>(a, scores);
   if (E <= 64) return v2 ? launch_scores<T, 2, 2, kBack>(a, scores) : launch_scores<T, 2, 1, kBack>(a, scores);
@@ -612,12 +751,9 @@ extern "C" int mxq_moe_route_groups(const void* logits, int dtype, int64_t token
   a.gr.groups = best == groups ? 1 : groups;  // all of them: no choice
   a.gr.best = best == groups ? 1 : best;
   a.gr.size = experts / a.gr.groups;
-  int wide = 1;
-  while (wide < a.gr.groups) wide *= 2;
-  a.gr.lanes = 32 / wide;
-  // the next number of floats that is `lanes` past a multiple of 32 banks: neighbouring
-  // groups' lanes then read neighbouring banks
-  a.gr.pitch = a.gr.size + ((a.gr.lanes - a.gr.size) % 32 + 32) % 32;
+  a.gr.shift = 5;
+  while (32 >> a.gr.shift < a.gr.groups) --a.gr.shift;
+  a.gr.lanes = 1 << a.gr.shift;
   a.gr.scale = scale;
   a.bias = bias;
   a.mask = mask;

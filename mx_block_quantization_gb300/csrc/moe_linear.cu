@@ -21,7 +21,24 @@
 // Tensor memory: an accumulator takes 256 of the 512 columns and the scales need 24, so
 // two accumulators would not fit side by side.  They overlap by 32 columns (0..255 and
 // 224..479): the epilogue of a tile reads those first, and from then on runs under the
-// next tile's products.
+// next tile's products.  (An overlap of 48 columns, two chunks of the epilogue, costs 30 us
+// of the 652 below.)
+//
+// Bound, for large products, by the tensor pipe with what shares it.  57344 rows x 7168 x
+// 2048 in 64 groups, 1.80 TFLOP: 652 us, 2.77 PFLOP/s.  Parts left out: the products alone
+// 428 us (4.2 PFLOP/s); with the scales' copies 537 (53 clocks a copy whatever its shape,
+// three a stage, in line with the products); the operands' loads alone 361; the output's
+// stores are worth 58.  What was tried against the copies: scales written to tensor memory
+// by warps of their own (699 us: four stages of scales fit, too few for the way there and
+// back), two atoms a copy from shared memory where warps lay them out four times (685),
+// copies ahead of the products before them (865), copies and loads for two stages at a
+// time (no difference).  Every look at a barrier takes shared memory's bandwidth from the
+// operands: waits that are suspended, by one lane of a warp, are worth 31 us of 683.
+//
+// 128 routed rows to 64 experts of 7168 x 2048, one block of rows each: 166 us, 6.1 TB/s,
+// the weights' bytes.  Weights' gradient, 24 x [1408, 2176] fp32 onto what is there from
+// 40009 rows: 175 us, 4.3 TB/s, bound by the epilogue's reads and writes (142 without the
+// writes); loading a chunk's addend ahead changes nothing there and costs others 3%.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -167,9 +184,8 @@ __device__ __forceinline__ uint32_t instruction_desc(uint32_t rows, uint32_t k) 
   return (k << 4) | ((rows / 8u) << 17) | (1u << 23) | ((kCols / 16u) << 24) | (k << 29);
 }
 
-// act(z) and act'(z), NaN kept.  The logistic function by the hardware's exponential and
-// reciprocal, a few units in the last place of fp32.  gelu is the tanh form, written with
-// 0.5 (1 + tanh u) = logistic(2u).
+// act(z) and act'(z), NaN kept.  The logistic function is a few units in the last place of
+// fp32 off.  gelu is the tanh form, written with 0.5 (1 + tanh u) = logistic(2u).
 constexpr float kGeluA = 1.5957691216057308f, kGeluB = 0.044715f;  // 2 sqrt(2 / pi)
 template <int kAct>
 __device__ __forceinline__ float activate(float z) {
@@ -293,8 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const int32_t atom_a = at.a_atom + static_cast<int32_t>(rank) * at.a_next;
       for (int k = 0; k < at.count; ++k, ++issued) {
         const int s = issued % kStages;
-        if (!mbar_wait_bounded(smem_u32(&bars.empty[s]), ((issued / kStages) & 1) ^ 1, abort_flag, &g_linear_status,
-                               MXQ_DEV_TIMEOUT)) {
+        if (!wait_suspended(smem_u32(&bars.empty[s]), ((issued / kStages) & 1) ^ 1, abort_flag, &g_linear_status)) {
           ok = false;
           break;
         }
@@ -322,11 +337,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (at.count == 0) continue;
       const int acc = done & 1;
       const uint32_t d = tmem + (acc ? kAccAt : 0u), blocks = at.rows / kBlock;
-      ok = mbar_wait_bounded(smem_u32(&bars.acc_free), (done & 1) ^ 1, abort_flag, &g_linear_status, MXQ_DEV_TIMEOUT);
+      ok = wait_suspended(smem_u32(&bars.acc_free), (done & 1) ^ 1, abort_flag, &g_linear_status);
       fence_after();
       for (int k = 0; ok && k < at.count; ++k, ++n) {
         const int s = n % kStages;
-        ok = mbar_wait_bounded(smem_u32(&bars.full[s]), (n / kStages) & 1, abort_flag, &g_linear_status, MXQ_DEV_TIMEOUT);
+        ok = wait_suspended(smem_u32(&bars.full[s]), (n / kStages) & 1, abort_flag, &g_linear_status);
         if (!ok) break;
         fence_after();
         const uint32_t da = smem + s * kStageBytes, ds = da + 2 * kOperandBytes;
@@ -383,8 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (lane == 0) arrive_cluster(at_leader(smem_u32(&bars.acc_free)));
       };
       if (at.count != 0) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(smem_u32(&bars.acc_full[acc]), (done >> 1) & 1, abort_flag,
-                                                       &g_linear_status, MXQ_DEV_TIMEOUT));
+        ok = warp_wait(smem_u32(&bars.acc_full[acc]), (done >> 1) & 1, abort_flag, &g_linear_status);
         if (!ok) break;
         fence_after();
         if (!overlapped) let_go();

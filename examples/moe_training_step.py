@@ -4,9 +4,10 @@
 
 Token ids go through an embedding table, a router with its balance loss and one
 linear layer per expert, whose products run in MXFP8 on what the dual-axis cast
-gives: the row-wise bytes forward, the column-wise ones for the weights' gradients.
-Experts' weights move by orthogonalised momentum, the table and the router by
-their gradients.  The data is synthetic: each token id has a fixed target.
+gives: the row-wise bytes forward, the column-wise ones for the weights' gradients,
+all experts in one call each.  Experts' weights move by orthogonalised momentum, the
+table and the router by AdamW with moments in 8 bits.  The data is synthetic: each
+token id has a fixed target.
 """
 from __future__ import annotations
 
@@ -31,12 +32,10 @@ class MoeLayer:
         self.router = (torch.randn(experts, D, generator=g) / D**0.5).cuda()
         self.experts = (torch.randn(experts, D, D, generator=g) / D**0.5).to(torch.bfloat16).cuda()
         self.momentum = torch.zeros(experts, D, D, device="cuda")
-
-    def _product(self, q, s, at, w, e):
-        """Rows `at` of the cast (q, s), times expert e of the cast w: [rows, D] fp32."""
-        (lo, hi), D = at, self.D
-        wq, ws = w
-        return mxq.mxfp8_scaled_mm(q[lo:hi], s[lo * D // 32:hi * D // 32], wq[e], ws[e])
+        self.moments = mxq.adamw_moments([self.table, self.router], bits=8)
+        self.steps = 0
+        # the experts' weights are cast as one matrix: a group of rows for each
+        self.each = torch.arange(1, experts + 1, dtype=torch.int32, device="cuda") * D
 
     def forward(self, ids):
         """Layer output [T, D] and the balance loss; keeps what backward needs."""
@@ -45,39 +44,29 @@ class MoeLayer:
         self.logits = self.x.float() @ self.router.t()
         self.routing = mxq.moe_route(self.logits, self.k)
         self.plan = mxq.moe_plan(self.routing.ids, E)
-        ends = self.plan.offs.tolist()
-        self.groups = [(e, (lo, hi)) for e, (lo, hi) in enumerate(zip([0] + ends, ends)) if hi > lo]
         self.cast = mxq.quantize_2d_dual(mxq.moe_dispatch(self.x, self.plan), self.plan.offs)
-        w = [mxq.quantize_2d_dual(self.experts[e]) for e in range(E)]
-        self.w_rows = [c.q_row for c in w], [c.s_row for c in w]      # blocks along the input
-        self.w_cols = [c.q_col for c in w], [c.s_col for c in w]      # transposed, along the output
-        self.rows = torch.zeros(self.plan.source.numel(), D, dtype=torch.bfloat16, device="cuda")
-        for e, at in self.groups:
-            self.rows[slice(*at)] = self._product(self.cast.q_row, self.cast.s_row, at, self.w_rows, e)
+        self.w = mxq.quantize_2d_dual(self.experts.view(E * D, D), self.each)
+        self.rows = mxq.moe_linear(self.cast.q_row, self.cast.s_row, self.w.q_row.view(E, D, D), self.w.s_row, self.plan.offs)
         return mxq.moe_combine(self.rows, self.plan, self.routing.weights), self.routing.loss
 
     def backward(self, dy, dloss):
         """Gradients of the table, the router and the experts."""
-        D = self.D
+        D, E, offs = self.D, self.E, self.plan.offs
         drows, dweights = mxq.moe_combine_backward(dy, self.rows, self.plan, self.routing.weights)
-        cast = mxq.quantize_2d_dual(drows, self.plan.offs)
-        dx_rows = torch.zeros_like(self.rows)
-        dexperts = torch.zeros_like(self.momentum)
-        for e, at in self.groups:
-            lo, hi = at
-            slab = slice(D * lo // 32, D * hi // 32)
-            dx_rows[lo:hi] = self._product(cast.q_row, cast.s_row, at, self.w_cols, e)
-            mxq.mxfp8_scaled_mm(cast.q_col[:, lo:hi], cast.s_col[slab], self.cast.q_col[:, lo:hi], self.cast.s_col[slab],
-                                out=dexperts[e])
+        cast = mxq.quantize_2d_dual(drows, offs)
+        by_output = self.w.q_col.view(D, E, D).transpose(0, 1)      # blocks along the output, transposed
+        dx_rows = mxq.moe_linear(cast.q_row, cast.s_row, by_output, self.w.s_col, offs)
+        dexperts = mxq.moe_weight_gradient(cast.q_col, cast.s_col, self.cast.q_col, self.cast.s_col, offs)
         dlogits = mxq.moe_route_backward(self.logits, self.routing, dweights, dloss)
         dx = mxq.moe_combine(dx_rows, self.plan).float() + dlogits @ self.router
         dtable = mxq.embedding_backward(self.ids, dx, self.table.shape[0])
         return dtable, dlogits.t() @ self.x.float(), dexperts
 
-    def update(self, gradients, lr: float, lr_router: float, lr_experts: float, beta: float = 0.9):
+    def update(self, gradients, lr: float, lr_experts: float, beta: float = 0.9):
         dtable, drouter, dexperts = gradients
-        self.table -= (lr * dtable).to(torch.bfloat16)
-        self.router -= lr_router * drouter
+        self.steps += 1
+        mxq.adamw_step([self.table, self.router], [dtable, drouter], self.moments, self.steps, lr=lr, betas=(beta, 0.95),
+                       weight_decay=0.0)
         self.momentum.mul_(beta).add_(dexperts)
         self.experts -= mxq.orthogonalize(self.momentum, scale=lr_experts)
 
@@ -93,7 +82,7 @@ def train(steps: int, tokens: int = 4096, vocabulary: int = 1000, D: int = 256, 
         y, balance = layer.forward(ids)
         off = y.float() - target[ids]
         gradients = layer.backward((off * (2 / tokens)).to(torch.bfloat16), torch.tensor(0.01, device="cuda"))
-        layer.update(gradients, lr=1.0, lr_router=0.05, lr_experts=0.05)
+        layer.update(gradients, lr=0.02, lr_experts=0.05)
         history.append((float(off.square().mean()), float(balance)))
     status = mxq.device_status()
     if status:

@@ -347,8 +347,7 @@ int mxq_moe_route_backward(const void *logits, int dtype, int64_t tokens, int32_
  *            of the `best` groups with the largest values, ties to the lowest index.
  *            k at most experts / groups * best.
  *   ids      int32 [tokens, k]: the chosen experts, largest s + bias first, ties to the
- *            lowest index.  The choice is that of exact sums: near ties are computed in
- *            64 bits.
+ *            lowest index.  The choice is that of 64-bit sums: near ties are computed so.
  *   weights  fp32 [tokens, k]: scale * s at the ids (renorm 0), or scale * s over the sum
  *            of the chosen s (renorm 1; 0 where that sum is 0).
  *   loss     as there, with p = s / sum_e s_e (0 where that sum is 0).

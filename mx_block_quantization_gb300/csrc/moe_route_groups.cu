@@ -12,16 +12,21 @@
 //   logistic  s (1 - s) (g + (c_e - sum p c) / sum s)
 //   softmax   p (h - sum p h)  with  h = g + c.
 //
-// The choice is that of exact arithmetic: c is computed in fp32, where it is off by a few
+// The choice is that of 64-bit arithmetic: c is computed in fp32, where it is off by a few
 // 2^-23, and wherever two values that the choice hangs on lie nearer than that (the last
 // of the chosen groups and the first of the others, neighbours among the chosen experts
 // and the first of the others) the token is done again in 64 bits (choose_exactly).
 // Experts with the same logit and the same bias are equal and go by their index at once.
 //
-// One warp owns a token, a lane keeps kPer of its logits in registers, and the next
-// token's are loaded ahead, as in moe_route.cu.  For the groups all c go through shared
-// memory, the groups' rows so far apart that the lanes of different groups read different
-// banks; 32 / groups lanes find the two largest of a group.
+// One warp owns a token, a lane keeps some of its logits in registers, and the next
+// token's are loaded ahead, as in moe_route.cu.  Up to eight experts of one group a lane:
+// route_owned_kernel; else (more than 256 experts, or groups that fill their lanes badly)
+// route_groups_kernel.  Both are bound by the instructions they issue, at three quarters
+// of the issue slots: 131071 tokens, 256 experts in 8 groups, fp32, takes 115 us forward
+// (about 610 instructions a token; the logits' bytes alone take 20) and 52 backward
+// (40 for the bytes of logits and gradient); 10007 tokens, 150 experts in 5 groups,
+// bf16, softmax, 25 us, and some 10 more where a single token has to be done again in 64
+// bits, backward 13.
 #include "moe_route_common.cuh"
 
 namespace {
@@ -82,7 +87,9 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
 #pragma unroll
     for (int j = i; j < i + kAtOnce; ++j) {
       const int e = lane + 32 * j;
-      const double v = (kLogistic ? 1.0 / (1.0 + c[j]) : c[j] * sum) + (bias != nullptr && e < E ? bias[e] : 0.0f);
+      // the product rounded by itself: fused with the addition in some of a lane's experts
+      // and not in others, equal ones would differ
+      const double v = __dadd_rn(kLogistic ? 1.0 / (1.0 + c[j]) : __dmul_rn(c[j], sum), bias != nullptr && e < E ? bias[e] : 0.0f);
       key[j] = e < E && widen(row[e]) > -CUDART_INF_F ? wide_key(v) : 0ull;
     }
   if (groups > 1) {
@@ -140,12 +147,14 @@ __device__ __forceinline__ float doubt(float s, float below, float c) {
   const float of_c = 0x1p-22f * fabsf(c);
   return kLogistic ? 0x1p-21f + of_c : fmaf(s * 0x1p-22f, kPer + 16 + below, of_c);
 }
-// The same of two groups' values v, sums of two c with biases of at most `bias`: twice
-// that, the distance at most 88 (where an exponential is 0), and the sums' rounding.
+// The most that the two largest |c| of a group add up to, for scores up to `most`.
+__device__ __forceinline__ float group_bound(float most, float bias) { return 2.0f * (most + bias); }
+// How near two groups' values, sums of two c, may be: twice what is said above for the
+// scores (a softmax's s (kPer + 16 + below) is largest for the largest s, where below is
+// 0), and 2^-24 of the c for the additions of their biases and again for their sums.
 template <int kPer, bool kLogistic>
-__device__ __forceinline__ float group_doubt(float v, float bias) {
-  const float size = fabsf(v);
-  return kLogistic ? fmaf(size, 0x1p-21f, 0x1p-20f) : fmaf(fmaf(2.0f, bias, size) * 0x1p-22f, kPer + 104, size * 0x1p-21f);
+__device__ __forceinline__ float group_doubt(float most, float bias) {
+  return fmaf(group_bound(most, bias), 0x1p-22f, kLogistic ? 0x1p-20f : most * (0x1p-21f * (kPer + 16)));
 }
 
 // The place in 64 bits of each of n candidates, one a lane, with logistic scores.
@@ -160,6 +169,33 @@ __device__ __noinline__ int rank_exactly(float x, float b, int e, int n) {
     before += other > own || (other == own && o < e) ? 1 : 0;
   }
   return lane < n ? before : kMaxK;
+}
+
+// The places of n candidates, one a lane, some nearer than fp32 can tell: equal ones go by
+// their index where logit and bias are alike, others by 64 bits.  few_c and few_xb: 32 of
+// the warp's.  Less than 0 where that takes the whole row (choose_exactly).
+template <int kPer, bool kLogistic>
+__device__ __noinline__ int settle(int e, float x, float b, float score, float below, int n, int k, float* few_c, float2* few_xb) {
+  const int lane = threadIdx.x & 31;
+  const float c = lane < n ? score + b : -CUDART_INF_F;
+  int before = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const float other = __shfl_sync(kAll, c, i);
+    const int o = __shfl_sync(kAll, e, i);
+    before += other > c || (other == c && o < e) ? 1 : 0;
+  }
+  __syncwarp();
+  if (lane < n) few_c[before] = c, few_xb[before] = make_float2(x, b);
+  __syncwarp();
+  bool clear = true;
+  if (lane < n && before < k && before + 1 < n) {
+    const float2 after = few_xb[before + 1];
+    clear = c - few_c[before + 1] > doubt<kPer, kLogistic>(score, below, c) || (x == after.x && b == after.y);
+  }
+  __syncwarp();
+  if (__all_sync(kAll, clear)) return lane < n ? before : kMaxK;
+  return kLogistic ? rank_exactly(x, b, e, n) : -1;
 }
 
 // Puts v at `at` and moves on where x >= from, under one predicate: as branches, each with
@@ -208,6 +244,10 @@ struct Ahead {
   }
 };
 
+// For the groups all c go through shared memory, the groups' rows so far apart that the
+// lanes of different groups read different banks; 32 / groups lanes find the two largest
+// of a group.  The k-th largest of the lanes' maxima bounds the candidates from below;
+// those from there on go side by side and count the larger ones.
 template <typename T, int kPer, int kV, bool kLogistic, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1)
     route_groups_kernel(const T* __restrict__ logits, const RouteShape s, const Grouped gr, const float* __restrict__ bias,
@@ -243,12 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float b = bias != nullptr && e < s.E ? read_at(bias, e, s.E, 0.0f, &g_route_status) : 0.0f;
     most_bias = fmaxf(most_bias, fabsf(b));
     if (warp == 0) sums[e] = b;
-  }
-#pragma unroll
-  for (int q = 0; q < kVectors; ++q) {
-    const int e = expert_of<kV>(q * kV, lane), g = e < s.E ? e / gr.size : 0;
-    first_lane[q] = g << gr.shift;
-    place[q] = e < s.E ? g * gr.pitch + e - g * gr.size : -1;
   }
   most_bias = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most_bias)));  // not negative: ordered as its bits
   __syncthreads();
@@ -365,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           last = most;
         }
         const uint32_t next = __reduce_max_sync(kAll, left);
-        if (next != 0u) certain = key_value(last) - key_value(next) > group_doubt<kPer, kLogistic>(key_value(last), most_bias);
+        if (next != 0u) certain = key_value(last) - key_value(next) > group_doubt<kPer, kLogistic>(kLogistic ? 1.0f : inv, most_bias);
 #pragma unroll
         for (int q = 0; q < kVectors; ++q) {
           const bool in = chosen >> first_lane[q] & 1u;
@@ -490,6 +524,335 @@ __global__ void __launch_bounds__(kThreads, 1)
     float sum = 0.0f;
 #pragma unroll 8
     for (int w = 0; w < kWarps; ++w) sum += by_warp[w * (32 * kPer) + e];
+    sums[e] = sum;
+  }
+  __syncthreads();
+  finish_block(s, sums, hist, routed_tokens, part_p, part_c, part_n, joined, counts, loss, n_out);
+}
+
+// At most eight experts a lane: a lane's are consecutive ones of one group (gr.lanes lanes
+// a group), so that a group's two largest are two shuffles a step away from the lanes' own,
+// a group that is not chosen leaves its lanes out, and nothing goes by single experts.  A
+// lane sorts its experts' keys; each of the k + 1 rounds takes the largest of the lanes'
+// heads and moves one lane on.  A key's lowest bits give way to the expert's place in its
+// lane, lower places first, and what they held is added to the doubt.
+// A group's best is known without a pass through shared memory and a candidate without a
+// pass over all: 610 instructions a token in place of 860 with the kernel above, 115 us in
+// place of 124 (131071 tokens, 256 experts in 8 groups), and 25 to 35 in place of 38
+// (10007 tokens, 150 experts in 5 groups, softmax).
+template <int kW>
+__device__ __forceinline__ void sort_down(uint32_t (&k)[kW]) {
+  const auto order = [&](int a, int b) {
+    const uint32_t high = max(k[a], k[b]), low = min(k[a], k[b]);
+    k[a] = high, k[b] = low;
+  };
+  if constexpr (kW == 2) order(0, 1);
+  if constexpr (kW == 4) order(0, 1), order(2, 3), order(0, 2), order(1, 3), order(1, 2);
+  if constexpr (kW == 8) {
+    order(0, 1), order(2, 3), order(4, 5), order(6, 7);
+    order(0, 2), order(1, 3), order(4, 6), order(5, 7);
+    order(1, 2), order(5, 6), order(0, 4), order(3, 7);
+    order(1, 5), order(2, 6);
+    order(1, 4), order(3, 6);
+    order(2, 4), order(3, 5);
+    order(3, 4);
+  }
+}
+
+// A token's logits, kW consecutive ones a lane: in vectors where kVector (each lane has all
+// of its experts or none), else one by one; those that are not there stay -inf.
+template <typename T, int kW, bool kVector>
+struct OwnedAhead {
+  static constexpr int kV = kVector ? (kW * sizeof(T) > 16 ? 16 / static_cast<int>(sizeof(T)) : kW) : 1;
+  Vec<T, kV> v[kW / kV];
+  __device__ __forceinline__ OwnedAhead() {
+#pragma unroll
+    for (int i = 0; i < kW; ++i) v[i / kV].v[i % kV] = minus_infinity<T>();
+  }
+  __device__ __forceinline__ void load(const T* first, int there) {
+#pragma unroll
+    for (int q = 0; q < kW / kV; ++q) {
+      const T* at = first + q * kV;
+      const uint32_t p = q * kV < there ? 1u : 0u;
+      if constexpr (sizeof v[q] == 16) {
+        uint4& w = *reinterpret_cast<uint4*>(&v[q]);
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                     : "+r"(w.x), "+r"(w.y), "+r"(w.z), "+r"(w.w) : "l"(at), "r"(p));
+      } else if constexpr (sizeof v[q] == 8) {
+        uint2& w = *reinterpret_cast<uint2*>(&v[q]);
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p ld.global.nc.v2.b32 {%0, %1}, [%2];\n\t}"
+                     : "+r"(w.x), "+r"(w.y) : "l"(at), "r"(p));
+      } else if constexpr (sizeof v[q] == 4) {
+        uint32_t& w = *reinterpret_cast<uint32_t*>(&v[q]);
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.b32 %0, [%1];\n\t}" : "+r"(w) : "l"(at), "r"(p));
+      } else {
+        uint16_t& w = *reinterpret_cast<uint16_t*>(&v[q]);
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p ld.global.nc.b16 %0, [%1];\n\t}" : "+h"(w) : "l"(at), "r"(p));
+      }
+    }
+  }
+};
+
+// Where shared memory holds the value of place i of a lane: vectors side by side.
+template <int kW>
+__device__ __forceinline__ int owned_at(int lane, int i) {
+  constexpr int kU = kW < 4 ? kW : 4;
+  return i / kU * (32 * kU) + lane * kU + i % kU;
+}
+// Of c, which is neither NaN nor -0, at place i of its lane.
+template <int kW>
+__device__ __forceinline__ uint32_t owned_key(float c, int i) {
+  const uint32_t b = __float_as_uint(c);
+  return ((b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u)) & ~static_cast<uint32_t>(kW - 1)) |
+         static_cast<uint32_t>(kW - 1 - i);
+}
+template <int kW>
+__device__ __forceinline__ int owned_place(uint32_t key) { return kW - 1 - static_cast<int>(key & (kW - 1)); }
+template <int kW>
+__device__ __forceinline__ float owned_value(uint32_t key) { return key_value(key & ~static_cast<uint32_t>(kW - 1)); }
+// What a key may lack of the value.
+template <int kW>
+__device__ __forceinline__ float owned_cut(float v) { return kW > 1 ? fmaf(fabsf(v), kW * 0x1p-23f, kW * 0x1p-149f) : 0.0f; }
+
+// A token some of whose candidates have like keys or lie too near one another: the rounds
+// once more, a lane at a time, on until one is clearly behind the k-th or none is left, and
+// then by settle.  Lane j returns an expert and its place among the chosen, place << 16 |
+// expert, -1 where it has none; all -2 where it takes the whole row.
+template <int kW, bool kLogistic>
+__device__ __noinline__ int settle_owned(const uint32_t* lists, bool in, const float* own_x, const float* own_b, float top, float inv,
+                                         float most_bias, int k, int size, int lanes, int shift, float* few_c, float2* few_xb) {
+  const int lane = threadIdx.x & 31;
+  uint32_t head = in ? lists[lane] : 0u, kept = 0u;
+  int from = 0, taken = 1, n = 0;
+  const auto far = [&] {  // the last one from the k-th
+    const float low = owned_value<kW>(__shfl_sync(kAll, kept, k - 1)), end = owned_value<kW>(__shfl_sync(kAll, kept, n - 1));
+    return low - end > 4.0f * (doubt<kW, kLogistic>(fabsf(low) + most_bias, 88.0f, low) + owned_cut<kW>(low));
+  };
+  bool all = false;
+  while (!all) {
+    const uint32_t most = __reduce_max_sync(kAll, head);
+    if (most == 0u) break;
+    if (n == 32) return -2;
+    const int lead = __ffs(__ballot_sync(kAll, head == most)) - 1;
+    if (lane == n) kept = most, from = lead;
+    if (lane == lead) head = lists[32 * taken++ + lane];
+    all = ++n > k && far();
+  }
+  const int place = owned_place<kW>(kept);
+  const int e = (from >> shift) * size + (from & (lanes - 1)) * kW + place;
+  const float x = own_x[owned_at<kW>(from, place)], b = own_b[owned_at<kW>(from, place)];
+  const float score = kLogistic ? logistic(x) : exp2_ftz((x - top) * kLog2E) * inv;
+  const int before = settle<kW, kLogistic>(e, x, b, score, top - x, n, k, few_c, few_xb);
+  if (__any_sync(kAll, before < 0)) return -2;
+  return lane < n && before < k ? before << 16 | e : -1;
+}
+
+template <typename T, int kW, bool kVector, bool kLogistic>
+__global__ void __launch_bounds__(1024, 1)
+    route_owned_kernel(const T* __restrict__ logits, const RouteShape s, const Grouped gr, const float* __restrict__ bias,
+                       const uint8_t* __restrict__ mask, float* __restrict__ weights, int32_t* __restrict__ ids, float* part_p,
+                       int32_t* part_c, int32_t* part_n, uint32_t* joined, int32_t* counts, float* loss, int32_t* n_out) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kWarps = 32, kLane = 32 * kW, kU = kW < 4 ? kW : 4;
+  __shared__ int32_t routed_tokens;
+  __shared__ uint2 slots[kWarps][kMaxK + 1];  // the candidates' keys and lanes, largest first
+  __shared__ float few_c[kWarps][32];
+  __shared__ float2 few_xb[kWarps][32];
+  float* own_x = reinterpret_cast<float*>(smem);          // [warps][kW of 32 lanes]: the token's logits; then the warps' sums
+  uint32_t* lists = reinterpret_cast<uint32_t*>(own_x + kWarps * kLane);  // [warps][kW + 1, 32]: the lanes' keys, largest first, and 0
+  float* own_b = reinterpret_cast<float*>(lists + kWarps * (kLane + 32)); // [kW of 32 lanes]: the biases
+  float* sums = own_b + kLane;                                            // [E]
+  int32_t* hist = reinterpret_cast<int32_t*>(sums + s.E);                 // [E]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> gr.shift, at_g = (lane & (gr.lanes - 1)) * kW;    // the lane's group and its first expert's place there
+  const int there = g < gr.groups ? min(max(gr.size - at_g, 0), kW) : 0, e0 = there > 0 ? g * gr.size + at_g : 0;
+  for (int e = tid; e < s.E; e += 32 * kWarps) hist[e] = 0;
+  if (tid == 0) routed_tokens = 0;
+  own_x += warp * kLane, lists += warp * (kLane + 32);
+  lists[kLane + lane] = 0u;
+  pdl_wait();
+  const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
+  const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
+  if (gridDim.x > 1) pdl_launch_dependents();  // the join's few blocks wait beside this one
+  float most_bias = 0.0f, acc[kW];
+#pragma unroll
+  for (int i = 0; i < kW; ++i) {
+    acc[i] = 0.0f;
+    const float b = bias != nullptr && i < there ? read_at(bias, e0 + i, s.E, 0.0f, &g_route_status) : 0.0f;
+    if (warp == 0) own_b[owned_at<kW>(lane, i)] = b;
+    most_bias = fmaxf(most_bias, fabsf(b));
+  }
+  most_bias = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most_bias)));  // not negative: ordered as its bits
+  __syncthreads();
+  int routed_here = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
+  OwnedAhead<T, kW, kVector> ahead;
+  uint32_t wanted_ahead = 1u;
+  const auto fetch = [&](int64_t t) {
+    if (t >= s.tokens) return;
+    if (in_buf(logits + t * s.ld, s.E * sizeof(T), logits, in_bytes, &g_route_status)) ahead.load(logits + t * s.ld + e0, there);
+    if (mask != nullptr) wanted_ahead = read_at(mask, t, s.tokens, uint8_t{0}, &g_route_status);
+  };
+  int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+  fetch(t);
+  for (; t < s.tokens; t += step) {
+    float x[kW], c[kW];
+#pragma unroll
+    for (int i = 0; i < kW; ++i) x[i] = widen(ahead.v[i / ahead.kV].v[i % ahead.kV]);
+    bool routed = wanted_ahead != 0u;
+    float top = 0.0f, sum = 0.0f;
+    if (!kLogistic) {
+      top = x[0];
+#pragma unroll
+      for (int i = 1; i < kW; ++i) top = fmaxf(top, x[i]);  // skips NaN
+      top = key_value(max(__reduce_max_sync(kAll, order_key(top)), order_key(-FLT_MAX)));
+    }
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      c[i] = kLogistic ? logistic(x[i]) : exp2_ftz((x[i] - top) * kLog2E);  // 0 where there is no expert: those are -inf
+      sum += c[i];
+    }
+    sum = warp_sum(sum);
+    if (sum == 0.0f) {  // no expert at all, or scores below fp32's range
+      bool alive = false;
+#pragma unroll
+      for (int i = 0; i < kW; ++i) alive |= x[i] != -CUDART_INF_F;
+      routed = __any_sync(kAll, alive) && routed;
+    }
+    int rank = kMaxK, my_id = -1;
+    float my_s = 0.0f;
+    if (routed) {
+      ++routed_here;
+      const float inv = sum == 0.0f ? 0.0f : reciprocal(sum);
+      __syncwarp();
+      slots[warp][lane] = make_uint2(0u, 0u);
+      slots[warp][lane + 1] = make_uint2(0u, 0u);
+      uint32_t key[kW];
+#pragma unroll
+      for (int q = 0; q < kW; q += kU) {
+        const Vec<float, kU> b = *reinterpret_cast<const Vec<float, kU>*>(own_b + owned_at<kW>(lane, q));
+        Vec<float, kU> v;
+#pragma unroll
+        for (int j = 0; j < kU; ++j) {
+          const int i = q + j;
+          v.v[j] = x[i];
+          if (kLogistic)
+            acc[i] = fmaf(c[i], inv, acc[i]);
+          else
+            acc[i] += c[i] *= inv;
+          c[i] += b.v[j];
+          key[i] = x[i] > -CUDART_INF_F && c[i] > -CUDART_INF_F ? owned_key<kW>(c[i], i) : 0u;  // not NaN
+        }
+        *reinterpret_cast<Vec<float, kU>*>(own_x + owned_at<kW>(lane, q)) = v;
+      }
+      fetch(t + step);  // not before: x and c have taken the registers
+      sort_down<kW>(key);
+#pragma unroll
+      for (int i = 0; i < kW; ++i) lists[i * 32 + lane] = key[i];
+      bool certain = true, in = true;
+      if (gr.groups > 1) {
+        uint32_t first = key[0], second = kW > 1 ? key[kW > 1 ? 1 : 0] : 0u;
+#pragma unroll 1
+        for (int d = gr.lanes >> 1; d > 0; d >>= 1) {
+          const uint32_t other = __shfl_xor_sync(kAll, first, d), next = __shfl_xor_sync(kAll, second, d);
+          second = max(max(second, next), min(first, other));
+          first = max(first, other);
+        }
+        uint32_t left = order_key(owned_value<kW>(first) + (second != 0u ? owned_value<kW>(second) : 0.0f)), last = 0u;
+        if (first == 0u) left = 0u;
+        in = false;
+#pragma unroll 1
+        for (int r = 0; r < gr.best; ++r) {  // groups of like values at once
+          last = __reduce_max_sync(kAll, left);
+          if (left == last) in = true, left = 0u;
+        }
+        const uint32_t next = __reduce_max_sync(kAll, left);
+        const float score = kLogistic ? 1.0f : inv;
+        if (next != 0u)
+          certain = key_value(last) - key_value(next) > group_doubt<kW, kLogistic>(score, most_bias) + owned_cut<kW>(group_bound(score, most_bias));
+        if (__popc(__ballot_sync(kAll, in && first != 0u)) > gr.best << gr.shift) certain = false;
+      }
+      if (certain) {
+        uint32_t head = in ? key[0] : 0u, at = smem_u32(lists + 32 + lane), slot = smem_u32(&slots[warp][0]);
+        const uint32_t begin = at;
+        __syncwarp();
+#pragma unroll 3
+        for (int r = 0; r <= s.k; ++r) {  // all lanes whose head is the largest: nearly always one
+          const uint32_t most = __reduce_max_sync(kAll, head);
+          asm volatile(
+              "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\tsetp.eq.and.u32 p, %0, %2, p;\n\t@p st.shared.v2.b32 [%3], {%2, %4};\n\t"
+              "@p ld.shared.b32 %0, [%1];\n\t@p add.u32 %1, %1, 128;\n\t}"
+              : "+r"(head), "+r"(at)
+              : "r"(most), "r"(slot + 8 * r), "r"(lane)
+              : "memory");
+        }
+        __syncwarp();
+        const uint2 own = slots[warp][lane];
+        const uint32_t next = slots[warp][lane + 1].x;
+        const int n = __popc(__ballot_sync(kAll, own.x != 0u)) + (__ballot_sync(kAll, next != 0u) >> 31);
+        const int place = owned_place<kW>(own.x), from = static_cast<int>(own.y);
+        const float x_e = own_x[owned_at<kW>(from, place)];
+        my_s = kLogistic ? logistic(x_e) : exp2_ftz((x_e - top) * kLog2E) * inv;
+        const float own_c = my_s + own_b[owned_at<kW>(from, place)];
+        const bool clear = lane >= s.k || own.x == 0u || next == 0u ||
+                           own_c - owned_value<kW>(next) > doubt<kW, kLogistic>(my_s, top - x_e, own_c) + 2.0f * owned_cut<kW>(own_c);
+        if (__all_sync(kAll, clear) && __reduce_add_sync(kAll, at - begin) == 128u * n) {
+          if (lane < s.k && own.x != 0u) rank = lane, my_id = (from >> gr.shift) * gr.size + (from & (gr.lanes - 1)) * kW + place;
+        } else if (n > 0) {
+          const int found = settle_owned<kW, kLogistic>(lists, in, own_x, own_b, top, inv, most_bias, s.k, gr.size, gr.lanes, gr.shift,
+                                                        few_c[warp], few_xb[warp]);
+          certain = found != -2;
+          if (found >= 0) {
+            rank = found >> 16, my_id = found & 0xFFFF;
+            const int g_e = my_id / gr.size, j = my_id - g_e * gr.size;
+            const float chosen_x = own_x[owned_at<kW>((g_e << gr.shift) + j / kW, j % kW)];
+            my_s = kLogistic ? logistic(chosen_x) : exp2_ftz((chosen_x - top) * kLog2E) * inv;
+          }
+        }
+      }
+      if (!certain) {
+        const T* row = logits + t * s.ld;
+        my_id = in_buf(row, s.E * sizeof(T), logits, in_bytes, &g_route_status)
+                    ? choose_exactly<T, kW, kLogistic>(row, bias, s.E, s.k, gr.groups, gr.best, gr.size) : -1;
+        rank = my_id >= 0 ? lane : kMaxK;
+        const float own = my_id >= 0 ? widen(row[my_id]) : 0.0f;
+        my_s = kLogistic ? logistic(own) : exp2_ftz((own - top) * kLog2E) * inv;
+      }
+      if (my_id >= 0) atomicAdd(&hist[my_id], 1);
+    } else {
+      fetch(t + step);
+    }
+    float w = my_id >= 0 ? my_s : 0.0f;
+    if (s.renorm) {
+      const float all = warp_sum(w);
+      w = all == 0.0f ? 0.0f : w * reciprocal(all);
+    }
+    w *= gr.scale;
+    const uint32_t chosen = __ballot_sync(kAll, my_id >= 0);
+    if (__popc(chosen) < s.k && my_id < 0) {  // as many other lanes write the places left
+      rank = __popc(chosen) + __popc(~chosen & ((1u << lane) - 1u));
+      w = 0.0f;
+    }
+    if (rank < s.k) {
+      const int64_t at = t * s.k + rank;
+      if (in_buf(weights + at, 4, weights, out_bytes, &g_route_status) && in_buf(ids + at, 4, ids, out_bytes, &g_route_status)) {
+        weights[at] = w;
+        ids[at] = my_id;
+      }
+    }
+  }
+  if (lane == 0 && routed_here) atomicAdd(&routed_tokens, routed_here);
+  __syncwarp();
+  // the warps' sums side by side, then added up in warp order
+#pragma unroll
+  for (int i = 0; i < kW; ++i) own_x[owned_at<kW>(lane, i)] = acc[i];
+  __syncthreads();
+  for (int e = tid; e < s.E; e += 32 * kWarps) {
+    const int g_e = e / gr.size, j = e - g_e * gr.size;
+    const float* at = reinterpret_cast<const float*>(smem) + owned_at<kW>((g_e << gr.shift) + j / kW, j % kW);
+    float sum = 0.0f;
+#pragma unroll 8
+    for (int w = 0; w < kWarps; ++w) sum += at[w * kLane];
     sums[e] = sum;
   }
   __syncthreads();
@@ -645,34 +1008,54 @@ struct GroupsCall {
   cudaStream_t stream;
 };
 
-template <typename T, int kPer, int kV, bool kLogistic>
-int launch_groups(const GroupsCall& a) {
-  constexpr int kThreads = route_threads<kPer>(), kWarps = kThreads / 32;
-  const int blocks = route_blocks(a.s.tokens, kWarps, a.sms);
+// A forward kernel over blocks of so many warps, and the join where there is more than one.
+template <typename T, typename Kernel>
+int launch_choice(const GroupsCall& a, const Grouped& gr, Kernel* kernel, int warps, size_t smem, bool (&attr_done)[64]) {
+  const int blocks = route_blocks(a.s.tokens, warps, a.sms);
   float* part_p = reinterpret_cast<float*>(a.workspace);
   int32_t* part_c = reinterpret_cast<int32_t*>(part_p + static_cast<int64_t>(blocks) * a.s.E);
   int32_t* part_n = part_c + static_cast<int64_t>(blocks) * a.s.E;
   uint32_t* joined = reinterpret_cast<uint32_t*>(part_n + blocks);
   float* part_loss = reinterpret_cast<float*>(joined + 1);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ECUDA;
+  if (!attr_done[dev]) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 184 * 1024) != cudaSuccess) return MXQ_ECUDA;
+    attr_done[dev] = true;
+  }
+  const int rc = launch_pdl(kernel, static_cast<unsigned>(blocks), 32 * warps, smem, a.stream, static_cast<const T*>(a.logits), a.s, gr,
+                            a.bias, a.mask, a.weights, a.ids, part_p, part_c, part_n, joined, a.counts, a.loss, a.n);
+  if (rc != MXQ_OK || blocks == 1) return rc;
+  return launch_pdl(route_join_kernel, static_cast<unsigned>(ceil_div(a.s.E, 32)), 32 * kJoinWarps, 0, a.stream, a.s, blocks, part_p,
+                    part_c, part_n, joined, part_loss, a.counts, a.loss, a.n);
+}
+template <typename T, int kPer, int kV, bool kLogistic>
+int launch_groups(const GroupsCall& a) {
+  constexpr int kThreads = route_threads<kPer>(), kWarps = kThreads / 32;
   // the next number of floats that is a group's lanes' vectors past a multiple of 32 banks:
   // neighbouring groups' lanes then read neighbouring banks
   Grouped gr = a.gr;
   gr.pitch = gr.size + ((gr.lanes * kV - gr.size) % 32 + 32) % 32;
   const int rows = gr.groups > 1 ? gr.groups * gr.pitch : 0;
-  const size_t smem = static_cast<size_t>(kWarps) * ((rows > 32 * kPer ? rows : 32 * kPer) + 32 * kPer) * 4 + 32 * kPer * 4 + static_cast<size_t>(a.s.E) * 4;
-  const auto kernel = route_groups_kernel<T, kPer, kV, kLogistic, kThreads>;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MXQ_ECUDA;
+  const size_t smem = static_cast<size_t>(kWarps) * ((rows > 32 * kPer ? rows : 32 * kPer) + 32 * kPer) * 4 + 32 * kPer * 4 +
+                      static_cast<size_t>(a.s.E) * 4;
   static bool attr_done[64] = {};  // benign race: the same attribute set twice
-  if (!attr_done[dev]) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 184 * 1024) != cudaSuccess) return MXQ_ECUDA;
-    attr_done[dev] = true;
-  }
-  const int rc = launch_pdl(kernel, static_cast<unsigned>(blocks), kThreads, smem, a.stream, static_cast<const T*>(a.logits), a.s, gr,
-                            a.bias, a.mask, a.weights, a.ids, part_p, part_c, part_n, joined, a.counts, a.loss, a.n);
-  if (rc != MXQ_OK || blocks == 1) return rc;
-  return launch_pdl(route_join_kernel, static_cast<unsigned>(ceil_div(a.s.E, 32)), 32 * kJoinWarps, 0, a.stream, a.s, blocks, part_p,
-                    part_c, part_n, joined, part_loss, a.counts, a.loss, a.n);
+  return launch_choice<T>(a, gr, route_groups_kernel<T, kPer, kV, kLogistic, kThreads>, kWarps, smem, attr_done);
+}
+template <typename T, int kW, bool kVector>
+int launch_owned(const GroupsCall& a, int scores) {
+  const size_t smem = ((2 * 32 + 1) * 32 * kW + 32 * 32) * 4 + static_cast<size_t>(a.s.E) * 8;
+  static bool attr_done[2][64] = {};  // benign race: the same attribute set twice
+  return scores == MXQ_SCORES_SIGMOID ? launch_choice<T>(a, a.gr, route_owned_kernel<T, kW, kVector, true>, 32, smem, attr_done[0])
+                                      : launch_choice<T>(a, a.gr, route_owned_kernel<T, kW, kVector, false>, 32, smem, attr_done[1]);
+}
+// Vectors where every lane has all of its kW experts or none, at aligned places.
+template <typename T, int kW>
+int launch_owned_width(const GroupsCall& a, int scores, int align) {
+  constexpr int kBytes = kW * static_cast<int>(sizeof(T));
+  if constexpr (kW > 1)
+    if (a.gr.size % kW != 0 || align < (kBytes < 16 ? kBytes : 16)) return launch_owned<T, kW, false>(a, scores);
+  return launch_owned<T, kW, true>(a, scores);
 }
 template <typename T, int kPer, int kV, bool kLogistic>
 int launch_groups_backward(const GroupsCall& a) {
@@ -700,9 +1083,17 @@ int launch_grouped(const GroupsCall& a, int scores) {
   const int size = kBack ? a.s.E : a.gr.size;
   const bool v4 = align >= static_cast<int>(4 * sizeof(T)) && size % 4 == 0, v2 = align >= static_cast<int>(2 * sizeof(T)) && size % 2 == 0;
   const int E = a.s.E;
-  if (E <= 32) return launch_scores<T, 1, 1, kBack>(a, scores);
-  if (E <= 64) return v2 ? launch_scores<T, 2, 2, kBack>(a, scores) : launch_scores<T, 2, 1, kBack>(a, scores);
-  if (E <= 128) return v4 ? launch_scores<T, 4, 4, kBack>(a, scores) : launch_scores<T, 4, 1, kBack>(a, scores);
+  if constexpr (kBack) {
+    if (E <= 32) return launch_scores<T, 1, 1, true>(a, scores);
+    if (E <= 64) return v2 ? launch_scores<T, 2, 2, true>(a, scores) : launch_scores<T, 2, 1, true>(a, scores);
+    if (E <= 128) return v4 ? launch_scores<T, 4, 4, true>(a, scores) : launch_scores<T, 4, 1, true>(a, scores);
+  } else {  // by a lane's part of a group, which is at most 8 for up to 128 experts
+    const int64_t part = ceil_div(a.gr.size, a.gr.lanes);
+    if (part <= 1) return launch_owned_width<T, 1>(a, scores, align);
+    if (part <= 2) return launch_owned_width<T, 2>(a, scores, align);
+    if (part <= 4) return launch_owned_width<T, 4>(a, scores, align);
+    if (part <= 8) return launch_owned_width<T, 8>(a, scores, align);
+  }
   if (E <= 256) return v4 ? launch_scores<T, 8, 4, kBack>(a, scores) : launch_scores<T, 8, 1, kBack>(a, scores);
   if (E <= 512) return v4 ? launch_scores<T, 16, 4, kBack>(a, scores) : launch_scores<T, 16, 1, kBack>(a, scores);
   return v4 ? launch_scores<T, 32, 4, kBack>(a, scores) : launch_scores<T, 32, 1, kBack>(a, scores);

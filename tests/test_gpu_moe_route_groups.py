@@ -294,3 +294,34 @@ def test_no_tokens():
     r = mxq.moe_route_groups(x, 4, groups=8, best_groups=2)
     assert r.ids.shape == (0, 4) and not r.counts.any() and float(r.loss) == 0 and int(r.routed) == 0
     assert mxq.moe_route_groups_backward(x, r, r.weights).shape == (0, 64)
+
+
+@pytest.mark.parametrize("size", [2, 32])
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_large_biases_that_cancel_in_a_group(scores, size):
+    """A group's two largest are about +100 and -100 off: what fp32 loses of each is more than its sum's own rounding."""
+    E, T = 16 * size, 40000 // size
+    bias = torch.full((E,), -100.0)
+    bias[::size] = 100.0
+    x = torch.randn(T, E, generator=torch.Generator().manual_seed(8))
+    Case(T, E, 5, 16, 5, scores, "f32", bias=bias, x=x).check(exact=False)
+
+
+@pytest.mark.parametrize("T,E,groups,best", [(400, 64, 1, 1), (400, 64, 32, 20), (300, 200, 8, 5), (200, 510, 2, 1)])
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+def test_the_most_choices_of_a_token(scores, T, E, groups, best):
+    """32 of them, the next ones at some distance, near, and alike."""
+    g = torch.Generator().manual_seed(9)
+    x = torch.randn(T, E, generator=g)
+    Case(T, E, 32, groups, best, scores, "f32", x=x).check()
+    Case(T, E, 32, groups, best, scores, "bf16", bias="zero", x=x).check()
+    # Two groups with the same two scores and the same two biases, the other way round, have
+    # sums that are equal, and in 64 bits differ by their roundings: at most 4 of values
+    # below 2, 4 * 2^-53.  Rows whose choice of groups hangs on less are left out.
+    few = Case(T, E, 32, groups, best, scores, "f32", bias="few", x=torch.round(2 * x) / 2)
+    c = scores_of(few.x.double().cpu().numpy(), scores) + few.bias.double().cpu().numpy()
+    value = np.sort(np.sort(c.reshape(T, groups, -1), axis=2)[:, :, -2:].sum(2), axis=1)[:, ::-1]
+    if best < groups:
+        few.x = few.x[torch.from_numpy(value[:, best - 1] - value[:, best] > 2.0**-51).cuda()]
+        assert few.x.shape[0] > T // 2
+    few.check()

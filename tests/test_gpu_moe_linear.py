@@ -307,6 +307,17 @@ def test_slopes_at_the_ends():
         assert torch.isnan(dz[6])
 
 
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_slopes_of_large_values(name):
+    """1 above and 0 below, up to infinity: no power of z overflows on the way."""
+    sizes = [60.0, 70.0, 127.0, 130.0, 1e6, 1e12, 2e13, 1e19, 2e19, 1e30, 3e38, torch.inf]
+    for dtype in (F32, BF16):
+        z = torch.tensor(sizes + [1.0] * (128 - len(sizes)), device="cuda").to(dtype).expand(128, 128).contiguous()
+        for sign in (1, -1):
+            dz = mxq.moe_linear_backward(torch.ones_like(z), sign * z, activation=name)[0][:, :len(sizes)]
+            assert bool(((dz - (1 if sign > 0 else 0)).abs() <= 1e-20).all())
+
+
 @pytest.mark.parametrize("bad", [[128, 64, 256], [64, 128, 256], [-128, 128, 256], [128, 256, 640], [256, 128, 384]])
 def test_offs_that_are_no_ends_write_nothing(bad):
     p = Problem([1, 1, 2], 0, 128, 128)

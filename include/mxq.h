@@ -429,8 +429,9 @@ int mxq_moe_combine_backward(const void *dy, int dtype, int64_t tokens, int64_t 
  *     residual  [M, N] of the output's type, rows ldr apart, or NULL; may be y itself.
  *     y, z      [M, N] of type dtype, each rounded once from fp32; z may be NULL.
  *   mxq_moe_weight_gradient   dw[e, n, k] = sum over the rows m of group e of
- *               a[n, m] b[k, m], added to what dw holds with `accumulate`; a group
- *               without rows gives 0 (or leaves dw).
+ *               a[n, m] b[k, m], added to what dw holds with `accumulate` (in fp32; the
+ *               addition to an fp32 dw takes subnormal numbers for 0); a group without
+ *               rows gives 0 (or leaves dw).
  *     a, sa     q_col [N, M] and s_col [N*M/32] of the cast dz; b, sb of the cast x.
  *     dw        [G, N, K] of type dtype, rows ldd and matrices stride_d apart.
  *   mxq_moe_linear_backward   dz = dy act'(z) (rows behind the last group: 0) and

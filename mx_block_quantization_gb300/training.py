@@ -598,7 +598,8 @@ def moe_weight_gradient(a, sa, b, sb, offs=None, *, dtype=None, out=None, accumu
     """The weights' gradient [G, N, K] of :func:`moe_linear`: for each group the product
     dz^T x over its rows, from the column-wise bytes and scales of the cast dz (a [N, M],
     sa) and of the cast x (b [K, M], sb), both with these ``offs``; [N, K] without.  fp32
-    unless ``dtype`` says bf16.  With ``accumulate`` it is added to ``out``."""
+    unless ``dtype`` says bf16.  With ``accumulate`` it is added to ``out``, where fp32
+    numbers below 2^-126 count as 0."""
     dev = a.device
     lda = _e4m3(a, "a")
     N, M = a.shape

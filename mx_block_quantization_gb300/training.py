@@ -836,13 +836,15 @@ def adamw_step(params, grads, moments: Moments, step, *, lr, betas=(0.9, 0.999),
         ms, vs = (_flat(t, name, torch.uint8, (total // 32,), dev)
                   for t, name in ((moments.m_scale, "m_scale"), (moments.v_scale, "v_scale")))
     table, live = [], set()
-    for i, (p, g) in enumerate(zip(params, grads)):
+    for i, (p, g) in enumerate(zip(params, grads)):  # the checks of a tensor take longer than its share of a launch
         if g is None or sizes[i] == 0:
             continue
-        code, gcode = _code(p, "params"), _code(g, "grads")
-        if p.device != dev or g.device != dev or not dev.type == "cuda":
+        code, gcode = _CODES.get(p.dtype), _CODES.get(g.dtype)
+        if code is None or gcode is None:
+            _code(p, "params"), _code(g, "grads")
+        if p.device != dev or g.device != dev:
             raise ValueError("params and grads must be CUDA tensors of one device (no CPU path)")
-        if not p.is_contiguous() or not g.is_contiguous() or g.shape != p.shape:
+        if not (p.is_contiguous() and g.is_contiguous() and g.shape == p.shape):
             raise ValueError("params and grads must be contiguous and of one shape")
         at, copy = p.data_ptr(), 0
         if copies is not None and copies[i] is not None:

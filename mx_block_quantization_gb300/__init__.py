@@ -28,6 +28,10 @@ Operations (sources by page title):
   :func:`embedding` and their gradients, :func:`orthogonalize` (``training.py``) --
   the operators of a mixture-of-experts training step whose grouped rows the
   dual-axis cast takes.
+* :func:`moe_linear`, :func:`moe_weight_gradient`, :func:`moe_linear_backward` -- the
+  experts' products on the cast's bytes and their gradients;
+  :func:`moe_route_groups` and its gradient -- routing among groups of experts;
+  :func:`adamw_step`, :func:`adamw_moments` -- AdamW over many tensors.
 
 With MXQ_CHECKED=1 in the environment the binding loads libmxq_checked.so,
 the same kernels with every computed global access tested against its buffer.

@@ -349,7 +349,7 @@ int mxq_moe_route_backward(const void *logits, int dtype, int64_t tokens, int32_
  *   ids      int32 [tokens, k]: the chosen experts, largest s + bias first, ties to the
  *            lowest index.  The choice is that of 64-bit sums: near ties are computed so.
  *   weights  fp32 [tokens, k]: scale * s at the ids (renorm 0), or scale * s over the sum
- *            of the chosen s (renorm 1; 0 where that sum is 0).
+ *            of the chosen s (renorm 1; 0 where that sum is 0).  An s below 2^-126 is 0.
  *   loss     as there, with p = s / sum_e s_e (0 where that sum is 0).
  * workspace: of mxq_moe_route_workspace.
  *

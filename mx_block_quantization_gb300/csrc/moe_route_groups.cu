@@ -66,6 +66,13 @@ template <typename T, int kPer, bool kLogistic>
 __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int E, int k, int groups, int best, int size) {
   constexpr int kAtOnce = kPer < 4 ? kPer : 4;  // chains of the scores in flight
   const int lane = threadIdx.x & 31;
+  // a router that begins with zeros: all alike, the lowest ones (131071 such tokens with
+  // 256 experts: 1700 us without this)
+  const float x0 = widen(row[0]), b0 = bias != nullptr ? bias[0] : 0.0f;
+  bool alike = fabsf(x0) < CUDART_INF_F && fabsf(b0) < CUDART_INF_F;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) alike = alike && widen(row[e]) == x0 && (bias == nullptr || bias[e] == b0);
+  if (__all_sync(kAll, alike)) return lane < k ? lane : -1;
   double c[kPer];
   uint64_t key[kPer];
   float top = -CUDART_INF_F;

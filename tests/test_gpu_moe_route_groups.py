@@ -325,3 +325,25 @@ def test_the_most_choices_of_a_token(scores, T, E, groups, best):
         few.x = few.x[torch.from_numpy(value[:, best - 1] - value[:, best] > 2.0**-51).cuda()]
         assert few.x.shape[0] > T // 2
     few.check()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,best,k", [(64, 8, 4, 6), (64, 64 // 2, 5, 10), (200, 1, 1, 32), (510, 2, 1, 8), (1024, 32, 2, 32)])
+def test_rows_of_one_value(E, groups, best, k, scores, kind):
+    """Of zeros, of others with one bias for all, and with an expert left out, an infinite one, one that is not a number."""
+    x = torch.zeros(12, E)
+    x[1], x[2], x[3], x[4] = -3.5, 20.0, -90.0, 0.25
+    x[5, 0], x[6, E - 1], x[7, 1], x[8, E // 2] = -torch.inf, -torch.inf, 0.5, -0.0
+    x[9] = -torch.inf
+    # 1 / (1 + e^90) = 8.2e-40 is below 2^-126 = 1.2e-38, where a score is 0 and so are weights
+    # over such scores' sum: the choice is compared for that row, the rest without it
+    held = torch.tensor([t for t in range(12) if t != 3 or scores == "softmax"])
+    for bias in ("none", torch.full((E,), -0.75)):
+        Case(12, E, k, groups, best, scores, kind, bias=bias, x=x).check(exact=False)
+        Case(len(held), E, k, groups, best, scores, kind, bias=bias, x=x[held]).check()
+    if scores == "sigmoid":  # a row of its own with softmax has no score at all
+        x[10], x[11, 3] = torch.inf, torch.nan
+        Case(12, E, k, groups, best, scores, kind, bias="zero", x=x).check(exact=False)
+    Case(12, E, k, groups, best, scores, kind, bias=torch.full((E,), torch.inf), x=x).check(exact=False)
+    Case(12, E, k, groups, best, scores, kind, bias=torch.full((E,), -torch.inf), x=x).check(exact=False)

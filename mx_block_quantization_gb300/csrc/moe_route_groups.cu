@@ -144,15 +144,31 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
   return mine;
 }
 
-// How near two values may be in fp32 and still not be known to be in order: twice what a
-// value can be off by.  logistic: 2^-22 for the exponential's and the reciprocal's units in
-// the last place and the sum's rounding.  softmax: (kPer + 16) 2^-24 of the score for the
-// sum over a lane's values and the lanes, and its exponent's distance from the largest,
-// `below`, times 2^-24.  And 2^-24 of c for the addition of the bias.
+// What fp32 may be off by.  A logistic score: 2^-22, for the exponential's and the
+// reciprocal's units in the last place and the sum's rounding.  A softmax's score s, in
+// 2^-24 of it: 4 for its exponential and 2.25 of its distance `below` the largest logit, as
+// much for the sum's terms on their mean (14 at most with 1024 of them), kPer + 4 for their
+// additions, 3 for reciprocal and product.  And the addition of the bias 2^-24 of c, taken
+// twice.
 template <int kPer, bool kLogistic>
-__device__ __forceinline__ float doubt(float s, float below, float c) {
+__device__ __forceinline__ float off_by(float s, float below, float c) {
+  const float of_c = 0x1p-23f * fabsf(c);
+  return kLogistic ? 0x1p-22f + of_c : fmaf(s * 0x1p-24f, fmaf(2.25f, below, kPer + 25), of_c);
+}
+// How far above the next value one has to lie to be known to be above it and all others
+// behind: c is the larger one.  A softmax's scores are right for their size, and the others'
+// may be larger than its own, with biases below its: s = c - bias is at most c - least, and
+// at most the row's largest score, `cap`.  What is said above grows with s; it is taken for no
+// less than 2^-11 cap, where `below` is less than 8.  Biases up to kFarBias are not in `least`, so that
+// an expert that is left out by one does not count: their c are below -1 and not near one
+// from -1/2 on.
+constexpr float kFarBias = -2.0f;
+template <int kPer, bool kLogistic>
+__device__ __forceinline__ float doubt(float c, float cap, float least) {
   const float of_c = 0x1p-22f * fabsf(c);
-  return kLogistic ? 0x1p-21f + of_c : fmaf(s * 0x1p-22f, kPer + 16 + below, of_c);
+  if (kLogistic) return 0x1p-21f + of_c;
+  const float most = c >= -0.5f ? fmaxf(fminf(c - least, cap), 0x1p-11f * cap) : cap;
+  return fmaf(most, 0x1p-23f * (kPer + 25 + 18), of_c);
 }
 // The most that the two largest |c| of a group add up to, for scores up to `most`.
 __device__ __forceinline__ float group_bound(float most, float bias) { return 2.0f * (most + bias); }
@@ -178,30 +194,27 @@ __device__ __noinline__ int rank_exactly(float x, float b, int e, int n) {
   return lane < n ? before : kMaxK;
 }
 
-// The places of n candidates, one a lane, some nearer than fp32 can tell: equal ones go by
-// their index where logit and bias are alike, others by 64 bits.  few_c and few_xb: 32 of
-// the warp's.  Less than 0 where that takes the whole row (choose_exactly).
+// The places of n candidates, one a lane, some perhaps nearer than fp32 can tell: equal ones
+// go by their index where logit and bias are alike, and where two others are nearer than
+// they may be off by all go by 64 bits.  Less than 0 where that takes the whole row
+// (choose_exactly).
 template <int kPer, bool kLogistic>
-__device__ __noinline__ int settle(int e, float x, float b, float score, float below, int n, int k, float* few_c, float2* few_xb) {
+__device__ __noinline__ int settle(int e, float x, float b, float score, float below, int n, int k) {
   const int lane = threadIdx.x & 31;
-  const float c = lane < n ? score + b : -CUDART_INF_F;
+  const float c = lane < n ? score + b : -CUDART_INF_F, off = off_by<kPer, kLogistic>(score, below, c);
+  const float low = c - off, high = c + off;
   int before = 0;
+  bool clear = true;
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    const float other = __shfl_sync(kAll, c, i);
+    const float other = __shfl_sync(kAll, c, i), other_high = __shfl_sync(kAll, high, i);
+    const float other_x = __shfl_sync(kAll, x, i), other_b = __shfl_sync(kAll, b, i);
     const int o = __shfl_sync(kAll, e, i);
-    before += other > c || (other == c && o < e) ? 1 : 0;
+    const bool first = other > c || (other == c && o < e);
+    before += first ? 1 : 0;
+    clear = clear && (first || other_high < low || (other_x == x && other_b == b));
   }
-  __syncwarp();
-  if (lane < n) few_c[before] = c, few_xb[before] = make_float2(x, b);
-  __syncwarp();
-  bool clear = true;
-  if (lane < n && before < k && before + 1 < n) {
-    const float2 after = few_xb[before + 1];
-    clear = c - few_c[before + 1] > doubt<kPer, kLogistic>(score, below, c) || (x == after.x && b == after.y);
-  }
-  __syncwarp();
-  if (__all_sync(kAll, clear)) return lane < n ? before : kMaxK;
+  if (__all_sync(kAll, clear || lane >= n || before >= k)) return lane < n ? before : kMaxK;
   return kLogistic ? rank_exactly(x, b, e, n) : -1;
 }
 
@@ -265,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ int32_t routed_tokens;
   __shared__ int32_t few[kWarps][32];                // experts near the top, in any order
   __shared__ __align__(16) float few_c[kWarps][32];  // their c, then in order
-  __shared__ float2 few_xb[kWarps][32];              // in order, their logits and biases
   // the groups' rows while tokens are worked on; after that the warps' sums
   float* by_warp = reinterpret_cast<float*>(smem);                        // [warps, 32 * kPer]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -282,16 +294,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
   if (gridDim.x > 1) pdl_launch_dependents();  // the join's few blocks wait beside this one
   constexpr int kVectors = kPer / kV;
-  float acc[kPer], most_bias = 0.0f;
+  float acc[kPer], most_bias = 0.0f, least = CUDART_INF_F;
   int first_lane[kVectors], place[kVectors];  // of the vector's group, and in the groups' rows
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
   for (int e = lane; e < 32 * kPer; e += 32) {
     const float b = bias != nullptr && e < s.E ? read_at(bias, e, s.E, 0.0f, &g_route_status) : 0.0f;
     most_bias = fmaxf(most_bias, fabsf(b));
+    if (!kLogistic && e < s.E && b > kFarBias) least = fminf(least, b);
     if (warp == 0) sums[e] = b;
   }
   most_bias = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most_bias)));  // not negative: ordered as its bits
+  if (!kLogistic) least = key_value(__reduce_min_sync(kAll, order_key(least)));
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < kVectors; ++q) {
@@ -469,19 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           bool clear = true;
           if (lane < n && before < s.k && before + 1 < n)
-            clear = own_c - few_c[warp][before + 1] > doubt<kPer, kLogistic>(my_s, top - x_e, own_c);
-          if (!__all_sync(kAll, clear)) {  // clear all the same where both logit and bias are alike
-            if (lane < n) few_xb[warp][before] = make_float2(x_e, own_b);
-            __syncwarp();
-            if (!clear) {
-              const float2 after = few_xb[warp][before + 1];
-              clear = x_e == after.x && own_b == after.y;
-            }
-            certain = __all_sync(kAll, clear);
-            if (kLogistic && !certain) {
-              before = rank_exactly(x_e, own_b, e, n);
-              certain = true;
-            }
+            clear = own_c - few_c[warp][before + 1] > doubt<kPer, kLogistic>(own_c, inv, least);
+          if (!__all_sync(kAll, clear)) {
+            before = settle<kPer, kLogistic>(e, x_e, own_b, my_s, top - x_e, n, s.k);
+            certain = !__any_sync(kAll, before < 0);
           }
           if (certain && lane < n && before < s.k) {
             rank = before;
@@ -627,13 +632,13 @@ __device__ __forceinline__ float owned_cut(float v) { return kW > 1 ? fmaf(fabsf
 // expert, -1 where it has none; all -2 where it takes the whole row.
 template <int kW, bool kLogistic>
 __device__ __noinline__ int settle_owned(const uint32_t* lists, bool in, const float* own_x, const float* own_b, float top, float inv,
-                                         float most_bias, int k, int size, int lanes, int shift, float* few_c, float2* few_xb) {
+                                         float least, int k, int size, int lanes, int shift) {
   const int lane = threadIdx.x & 31;
   uint32_t head = in ? lists[lane] : 0u, kept = 0u;
   int from = 0, taken = 1, n = 0;
   const auto far = [&] {  // the last one from the k-th
     const float low = owned_value<kW>(__shfl_sync(kAll, kept, k - 1)), end = owned_value<kW>(__shfl_sync(kAll, kept, n - 1));
-    return low - end > 4.0f * (doubt<kW, kLogistic>(fabsf(low) + most_bias, 88.0f, low) + owned_cut<kW>(low));
+    return low - end > 4.0f * (doubt<kW, kLogistic>(low, inv, least) + owned_cut<kW>(low));
   };
   bool all = false;
   while (!all) {
@@ -649,7 +654,7 @@ __device__ __noinline__ int settle_owned(const uint32_t* lists, bool in, const f
   const int e = (from >> shift) * size + (from & (lanes - 1)) * kW + place;
   const float x = own_x[owned_at<kW>(from, place)], b = own_b[owned_at<kW>(from, place)];
   const float score = kLogistic ? logistic(x) : exp2_ftz((x - top) * kLog2E) * inv;
-  const int before = settle<kW, kLogistic>(e, x, b, score, top - x, n, k, few_c, few_xb);
+  const int before = settle<kW, kLogistic>(e, x, b, score, top - x, n, k);
   if (__any_sync(kAll, before < 0)) return -2;
   return lane < n && before < k ? before << 16 | e : -1;
 }
@@ -663,8 +668,6 @@ __global__ void __launch_bounds__(1024, 1)
   constexpr int kWarps = 32, kLane = 32 * kW, kU = kW < 4 ? kW : 4;
   __shared__ int32_t routed_tokens;
   __shared__ uint2 slots[kWarps][kMaxK + 1];  // the candidates' keys and lanes, largest first
-  __shared__ float few_c[kWarps][32];
-  __shared__ float2 few_xb[kWarps][32];
   float* own_x = reinterpret_cast<float*>(smem);          // [warps][kW of 32 lanes]: the token's logits; then the warps' sums
   uint32_t* lists = reinterpret_cast<uint32_t*>(own_x + kWarps * kLane);  // [warps][kW + 1, 32]: the lanes' keys, largest first, and 0
   float* own_b = reinterpret_cast<float*>(lists + kWarps * (kLane + 32)); // [kW of 32 lanes]: the biases
@@ -681,15 +684,17 @@ __global__ void __launch_bounds__(1024, 1)
   const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
   const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
   if (gridDim.x > 1) pdl_launch_dependents();  // the join's few blocks wait beside this one
-  float most_bias = 0.0f, acc[kW];
+  float most_bias = 0.0f, least = CUDART_INF_F, acc[kW];
 #pragma unroll
   for (int i = 0; i < kW; ++i) {
     acc[i] = 0.0f;
     const float b = bias != nullptr && i < there ? read_at(bias, e0 + i, s.E, 0.0f, &g_route_status) : 0.0f;
     if (warp == 0) own_b[owned_at<kW>(lane, i)] = b;
     most_bias = fmaxf(most_bias, fabsf(b));
+    if (!kLogistic && i < there && b > kFarBias) least = fminf(least, b);
   }
   most_bias = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most_bias)));  // not negative: ordered as its bits
+  if (!kLogistic) least = key_value(__reduce_min_sync(kAll, order_key(least)));
   __syncthreads();
   int routed_here = 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -802,12 +807,11 @@ __global__ void __launch_bounds__(1024, 1)
         my_s = kLogistic ? logistic(x_e) : exp2_ftz((x_e - top) * kLog2E) * inv;
         const float own_c = my_s + own_b[owned_at<kW>(from, place)];
         const bool clear = lane >= s.k || own.x == 0u || next == 0u ||
-                           own_c - owned_value<kW>(next) > doubt<kW, kLogistic>(my_s, top - x_e, own_c) + 2.0f * owned_cut<kW>(own_c);
+                           own_c - owned_value<kW>(next) > doubt<kW, kLogistic>(own_c, inv, least) + 2.0f * owned_cut<kW>(own_c);
         if (__all_sync(kAll, clear) && __reduce_add_sync(kAll, at - begin) == 128u * n) {
           if (lane < s.k && own.x != 0u) rank = lane, my_id = (from >> gr.shift) * gr.size + (from & (gr.lanes - 1)) * kW + place;
         } else if (n > 0) {
-          const int found = settle_owned<kW, kLogistic>(lists, in, own_x, own_b, top, inv, most_bias, s.k, gr.size, gr.lanes, gr.shift,
-                                                        few_c[warp], few_xb[warp]);
+          const int found = settle_owned<kW, kLogistic>(lists, in, own_x, own_b, top, inv, least, s.k, gr.size, gr.lanes, gr.shift);
           certain = found != -2;
           if (found >= 0) {
             rank = found >> 16, my_id = found & 0xFFFF;

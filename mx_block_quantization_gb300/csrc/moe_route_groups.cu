@@ -409,7 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           second = fmaxf(fmaxf(second, next), fminf(first, other));
           first = fmaxf(first, other);
         }
-        uint32_t left = order_key(second > -CUDART_INF_F ? first + second : first), last = 0u, chosen = 0u;
+        // the sum of two of the type's lowest values is a group's all the same
+        const float value = fmaxf(second > -CUDART_INF_F ? first + second : first, -FLT_MAX);
+        uint32_t left = first > -CUDART_INF_F ? order_key(value) : 0u, last = 0u, chosen = 0u;
 #pragma unroll 1
         for (int r = 0; r < gr.best; ++r) {
           const uint32_t most = __reduce_max_sync(kAll, left);
@@ -770,8 +772,8 @@ __global__ void __launch_bounds__(1024, 1)
           second = max(max(second, next), min(first, other));
           first = max(first, other);
         }
-        uint32_t left = order_key(owned_value<kW>(first) + (second != 0u ? owned_value<kW>(second) : 0.0f)), last = 0u;
-        if (first == 0u) left = 0u;
+        const float value = fmaxf(owned_value<kW>(first) + (second != 0u ? owned_value<kW>(second) : 0.0f), -FLT_MAX);
+        uint32_t left = first != 0u ? order_key(value) : 0u, last = 0u;
         in = false;
 #pragma unroll 1
         for (int r = 0; r < gr.best; ++r) {  // groups of like values at once

@@ -62,3 +62,27 @@ def test_a_large_score_that_its_bias_takes_back(E, at, between):
         assert keep.sum() > T // 2
         for k in (1, 2, 3):
             compare(x, bias, k, keep=keep)
+
+
+LOWEST = torch.finfo(torch.float32).min
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("E,groups,best,k", [(32, 4, 2, 10), (64, 4, 3, 20), (256, 8, 2, 32), (288, 8, 2, 32), (512, 32, 2, 20), (1024, 32, 2, 32)])
+def test_experts_left_out_by_the_lowest_bias(E, groups, best, k, scores):
+    """Groups whose experts all have a bias of the type's lowest value come last, and are
+    chosen where no others are left: the sum of two of them leaves fp32's range, not 64
+    bits' (the scores vanish in it there too, so equal ones go by their index)."""
+    x = torch.randn(30, E, generator=torch.Generator().manual_seed(11))
+    size = E // groups
+    for live in (1, best, groups):
+        bias = torch.zeros(E)
+        for group in range(groups):
+            if group >= live:
+                bias[group * size:(group + 1) * size] = LOWEST
+        compare(x, bias, k, groups, best, scores)
+        compare(x, bias.flip(0), k, groups, best, scores)
+    bias = torch.zeros(E)
+    bias[::2] = LOWEST
+    compare(x, bias, min(k, size), groups, best, scores)
+    compare(x, torch.full((E,), LOWEST), k, groups, best, scores)

@@ -152,7 +152,7 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
 // twice.
 template <int kPer, bool kLogistic>
 __device__ __forceinline__ float off_by(float s, float below, float c) {
-  const float of_c = 0x1p-23f * fabsf(c);
+  const float of_c = fminf(0x1p-23f * fabsf(c), FLT_MAX);  // an infinite c is exact
   return kLogistic ? 0x1p-22f + of_c : fmaf(s * 0x1p-24f, fmaf(2.25f, below, kPer + 25), of_c);
 }
 // How far above the next value one has to lie to be known to be above it and all others
@@ -161,23 +161,32 @@ __device__ __forceinline__ float off_by(float s, float below, float c) {
 // at most the row's largest score, `cap`.  What is said above grows with s; it is taken for no
 // less than 2^-11 cap, where `below` is less than 8.  Biases up to kFarBias are not in `least`, so that
 // an expert that is left out by one does not count: their c are below -1 and not near one
-// from -1/2 on.
+// from -1/2 on.  `cut` is added; an infinite c lies above every finite one.
 constexpr float kFarBias = -2.0f;
 template <int kPer, bool kLogistic>
-__device__ __forceinline__ float doubt(float c, float cap, float least) {
-  const float of_c = 0x1p-22f * fabsf(c);
-  if (kLogistic) return 0x1p-21f + of_c;
+__device__ __forceinline__ float doubt(float c, float cap, float least, float cut) {
+  const float of_c = fmaf(0x1p-22f, fabsf(c), cut);
+  if (kLogistic) return fminf(0x1p-21f + of_c, FLT_MAX);
   const float most = c >= -0.5f ? fmaxf(fminf(c - least, cap), 0x1p-11f * cap) : cap;
-  return fmaf(most, 0x1p-23f * (kPer + 25 + 18), of_c);
+  return fminf(fmaf(most, 0x1p-23f * (kPer + 25 + 18), of_c), FLT_MAX);
 }
-// The most that the two largest |c| of a group add up to, for scores up to `most`.
-__device__ __forceinline__ float group_bound(float most, float bias) { return 2.0f * (most + bias); }
-// How near two groups' values, sums of two c, may be: twice what is said above for the
-// scores (a softmax's s (kPer + 16 + below) is largest for the largest s, where below is
-// 0), and 2^-24 of the c for the additions of their biases and again for their sums.
+// The same for two groups' values, sums of two c, none of whose sizes add up to more than
+// `size`: two of a logistic's or of the row's largest score in each value, and 2^-24 of the c
+// for the additions of their biases and again for their sums.
 template <int kPer, bool kLogistic>
-__device__ __forceinline__ float group_doubt(float most, float bias) {
-  return fmaf(group_bound(most, bias), 0x1p-22f, kLogistic ? 0x1p-20f : most * (0x1p-21f * (kPer + 16)));
+__device__ __forceinline__ float group_doubt(float size, float cap) {
+  return fmaf(size, 0x1p-22f, kLogistic ? 0x1p-20f : cap * (0x1p-22f * (kPer + 25)));
+}
+// Whether the chosen groups are known to lie above the others where that does not say so,
+// as one group's large bias is no other's doubt: each value with what it may be off by
+// itself.  A lane has a group's value and the size of its c, `cut` more that the value may
+// lack; `there`: the group has an expert.
+template <int kPer, bool kLogistic>
+__device__ __noinline__ bool groups_clear(bool there, bool chosen, float value, float size, float cut, float cap) {
+  const float off = fabsf(value) < FLT_MAX ? fmaf(size, 0x1p-23f, kLogistic ? 0x1p-21f : cap * (0x1p-23f * (kPer + 25))) + cut : 0.0f;
+  const uint32_t low = __reduce_min_sync(kAll, there && chosen ? order_key(value - off) : ~0u);
+  const uint32_t high = __reduce_max_sync(kAll, there && !chosen ? order_key(value + off) : 0u);
+  return low > high;
 }
 
 // The place in 64 bits of each of n candidates, one a lane, with logistic scores.
@@ -294,17 +303,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
   if (gridDim.x > 1) pdl_launch_dependents();  // the join's few blocks wait beside this one
   constexpr int kVectors = kPer / kV;
-  float acc[kPer], most_bias = 0.0f, least = CUDART_INF_F;
+  float acc[kPer], least = CUDART_INF_F;
   int first_lane[kVectors], place[kVectors];  // of the vector's group, and in the groups' rows
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
   for (int e = lane; e < 32 * kPer; e += 32) {
     const float b = bias != nullptr && e < s.E ? read_at(bias, e, s.E, 0.0f, &g_route_status) : 0.0f;
-    most_bias = fmaxf(most_bias, fabsf(b));
     if (!kLogistic && e < s.E && b > kFarBias) least = fminf(least, b);
     if (warp == 0) sums[e] = b;
   }
-  most_bias = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most_bias)));  // not negative: ordered as its bits
   if (!kLogistic) least = key_value(__reduce_min_sync(kAll, order_key(least)));
   __syncthreads();
 #pragma unroll
@@ -422,7 +429,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           last = most;
         }
         const uint32_t next = __reduce_max_sync(kAll, left);
-        if (next != 0u) certain = key_value(last) - key_value(next) > group_doubt<kPer, kLogistic>(kLogistic ? 1.0f : inv, most_bias);
+        if (next != 0u) {
+          const float size = first > -CUDART_INF_F ? fabsf(first) + (second > -CUDART_INF_F ? fabsf(second) : 0.0f) : 0.0f;
+          const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));  // not negative: ordered as its bits
+          certain = key_value(last) - key_value(next) > group_doubt<kPer, kLogistic>(most, inv) ||
+                    groups_clear<kPer, kLogistic>(first > -CUDART_INF_F, chosen >> (g << gr.shift) & 1u, value, size, 0.0f, inv);
+        }
 #pragma unroll
         for (int q = 0; q < kVectors; ++q) {
           const bool in = chosen >> first_lane[q] & 1u;
@@ -485,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           bool clear = true;
           if (lane < n && before < s.k && before + 1 < n)
-            clear = own_c - few_c[warp][before + 1] > doubt<kPer, kLogistic>(own_c, inv, least);
+            clear = own_c - few_c[warp][before + 1] > doubt<kPer, kLogistic>(own_c, inv, least, 0.0f);
           if (!__all_sync(kAll, clear)) {
             before = settle<kPer, kLogistic>(e, x_e, own_b, my_s, top - x_e, n, s.k);
             certain = !__any_sync(kAll, before < 0);
@@ -640,7 +652,7 @@ __device__ __noinline__ int settle_owned(const uint32_t* lists, bool in, const f
   int from = 0, taken = 1, n = 0;
   const auto far = [&] {  // the last one from the k-th
     const float low = owned_value<kW>(__shfl_sync(kAll, kept, k - 1)), end = owned_value<kW>(__shfl_sync(kAll, kept, n - 1));
-    return low - end > 4.0f * (doubt<kW, kLogistic>(low, inv, least) + owned_cut<kW>(low));
+    return low - end > 4.0f * doubt<kW, kLogistic>(low, inv, least, owned_cut<kW>(low));
   };
   bool all = false;
   while (!all) {
@@ -686,16 +698,14 @@ __global__ void __launch_bounds__(1024, 1)
   const uint64_t in_bytes = (static_cast<uint64_t>(s.tokens - 1) * s.ld + s.E) * sizeof(T);
   const uint64_t out_bytes = static_cast<uint64_t>(s.tokens) * s.k * 4;
   if (gridDim.x > 1) pdl_launch_dependents();  // the join's few blocks wait beside this one
-  float most_bias = 0.0f, least = CUDART_INF_F, acc[kW];
+  float least = CUDART_INF_F, acc[kW];
 #pragma unroll
   for (int i = 0; i < kW; ++i) {
     acc[i] = 0.0f;
     const float b = bias != nullptr && i < there ? read_at(bias, e0 + i, s.E, 0.0f, &g_route_status) : 0.0f;
     if (warp == 0) own_b[owned_at<kW>(lane, i)] = b;
-    most_bias = fmaxf(most_bias, fabsf(b));
     if (!kLogistic && i < there && b > kFarBias) least = fminf(least, b);
   }
-  most_bias = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(most_bias)));  // not negative: ordered as its bits
   if (!kLogistic) least = key_value(__reduce_min_sync(kAll, order_key(least)));
   __syncthreads();
   int routed_here = 0;
@@ -772,7 +782,8 @@ __global__ void __launch_bounds__(1024, 1)
           second = max(max(second, next), min(first, other));
           first = max(first, other);
         }
-        const float value = fmaxf(owned_value<kW>(first) + (second != 0u ? owned_value<kW>(second) : 0.0f), -FLT_MAX);
+        const float of_first = owned_value<kW>(first), of_second = second != 0u ? owned_value<kW>(second) : 0.0f;
+        const float value = fmaxf(of_first + of_second, -FLT_MAX);
         uint32_t left = first != 0u ? order_key(value) : 0u, last = 0u;
         in = false;
 #pragma unroll 1
@@ -781,9 +792,12 @@ __global__ void __launch_bounds__(1024, 1)
           if (left == last) in = true, left = 0u;
         }
         const uint32_t next = __reduce_max_sync(kAll, left);
-        const float score = kLogistic ? 1.0f : inv;
-        if (next != 0u)
-          certain = key_value(last) - key_value(next) > group_doubt<kW, kLogistic>(score, most_bias) + owned_cut<kW>(group_bound(score, most_bias));
+        if (next != 0u) {
+          const float size = first != 0u ? fabsf(of_first) + fabsf(of_second) : 0.0f;
+          const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));  // not negative: ordered as its bits
+          certain = key_value(last) - key_value(next) > group_doubt<kW, kLogistic>(most, inv) + owned_cut<kW>(most) ||
+                    groups_clear<kW, kLogistic>(first != 0u, in, value, size, owned_cut<kW>(size), inv);
+        }
         if (__popc(__ballot_sync(kAll, in && first != 0u)) > gr.best << gr.shift) certain = false;
       }
       if (certain) {
@@ -809,7 +823,7 @@ __global__ void __launch_bounds__(1024, 1)
         my_s = kLogistic ? logistic(x_e) : exp2_ftz((x_e - top) * kLog2E) * inv;
         const float own_c = my_s + own_b[owned_at<kW>(from, place)];
         const bool clear = lane >= s.k || own.x == 0u || next == 0u ||
-                           own_c - owned_value<kW>(next) > doubt<kW, kLogistic>(own_c, inv, least) + 2.0f * owned_cut<kW>(own_c);
+                           own_c - owned_value<kW>(next) > doubt<kW, kLogistic>(own_c, inv, least, 2.0f * owned_cut<kW>(own_c));
         if (__all_sync(kAll, clear) && __reduce_add_sync(kAll, at - begin) == 128u * n) {
           if (lane < s.k && own.x != 0u) rank = lane, my_id = (from >> gr.shift) * gr.size + (from & (gr.lanes - 1)) * kW + place;
         } else if (n > 0) {

@@ -1,0 +1,58 @@
+"""moe_route_groups takes about as long whatever single biases are: a near tie is done again
+in 64 bits, and what makes every row look like one costs ten times the time of the call.  Times are compared with the same batch's of usual values
+in the same test, the shortest of several each; the margin is a factor of two.
+"""
+import math
+
+import pytest
+import torch
+
+import mx_block_quantization_gb300 as mxq
+from tests.gpu_util import require_gpu
+from tests.test_gpu_moe_route_groups import Case
+
+pytestmark = pytest.mark.gpu
+T, E = 131072, 256
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+    yield
+    torch.cuda.empty_cache()
+    assert mxq.device_status(clear=True) == 0
+
+
+def shortest(call):
+    """Microseconds of a call among eight of them, the best of six times."""
+    best = math.inf
+    for i in range(7):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        for _ in range(8):
+            call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 125 if i else math.inf)
+    return best
+
+
+def times(x, k, biases, **how):
+    return [shortest(lambda: mxq.moe_route_groups(x, k, bias=b, **how)) for b in biases]
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("e,groups,best", [(E, 8, 4), (E, 1, 1), (512, 8, 4)])
+def test_a_bias_that_leaves_an_expert_out_or_takes_it_always(e, groups, best, scores):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, e, generator=g, device="cuda") * 1.5
+    usual = torch.randn(e, generator=g, device="cuda") * 0.02
+    biases = [usual]
+    for value in (-math.inf, -1e9, torch.finfo(torch.float32).min, 1e9, math.inf, math.nan):
+        b = usual.clone()
+        b[77] = value
+        biases.append(b)
+    took = times(x, 8, biases, scores=scores, groups=groups, best_groups=best)
+    assert max(took) < 2 * took[0], took
+    for b in biases[1:]:
+        Case(300, e, 8, groups, best, scores, x=x[:300].cpu(), bias=b.cpu()).check(exact=False)

@@ -144,8 +144,9 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
   return mine;
 }
 
-// What fp32 may be off by.  A logistic score: 2^-22, for the exponential's and the
-// reciprocal's units in the last place and the sum's rounding.  A softmax's score s, in
+// What fp32 may be off by.  A logistic score s: 2^-22, for the exponential's and the
+// reciprocal's units in the last place and the sum's rounding; where s is small 2^-24 of it
+// times 7 and 1.25 of its logit's size, `below` 0, for the exponent.  A softmax's score, in
 // 2^-24 of it: 4 for its exponential and 2.25 of its distance `below` the largest logit, as
 // much for the sum's terms on their mean (14 at most with 1024 of them), kPer + 4 for their
 // additions, 3 for reciprocal and product.  And the addition of the bias 2^-24 of c, taken
@@ -153,22 +154,37 @@ __device__ __noinline__ int choose_exactly(const T* row, const float* bias, int 
 template <int kPer, bool kLogistic>
 __device__ __forceinline__ float off_by(float s, float below, float c) {
   const float of_c = fminf(0x1p-23f * fabsf(c), FLT_MAX);  // an infinite c is exact
-  return kLogistic ? 0x1p-22f + of_c : fmaf(s * 0x1p-24f, fmaf(2.25f, below, kPer + 25), of_c);
+  if (kLogistic) return fminf(s * 0x1p-24f * fmaf(1.25f, fmaxf(below, 0.0f), 7.0f), 0x1p-22f) + of_c;
+  return fmaf(s * 0x1p-24f, fmaf(2.25f, below, kPer + 25), of_c);
 }
-// How far above the next value one has to lie to be known to be above it and all others
-// behind: c is the larger one.  A softmax's scores are right for their size, and the others'
-// may be larger than its own, with biases below its: s = c - bias is at most c - least, and
-// at most the row's largest score, `cap`.  What is said above grows with s; it is taken for no
-// less than 2^-11 cap, where `below` is less than 8.  Biases up to kFarBias are not in `least`, so that
-// an expert that is left out by one does not count: their c are below -1 and not near one
-// from -1/2 on.  `cut` is added; an infinite c lies above every finite one.
+// Twice what any score may be off by whose c is not above this one.  It goes by the scores'
+// size: s = c - bias is at most c - least, and at most 1 or a softmax's largest, `cap`.  What is
+// said above grows with s; it is taken for no less than 2^-40, where a logistic's exponent
+// counts 35, or 2^-16 cap, where a softmax's counts 25.  Biases up to kFarBias are not in
+// `least`, so that an expert that is left out by one does not count: their c are below -1 and
+// not near one from -1/2 on.
 constexpr float kFarBias = -2.0f;
 template <int kPer, bool kLogistic>
+__device__ __forceinline__ float scores_doubt(float c, float cap, float least) {
+  if (kLogistic) cap = 1.0f;
+  const float most = c >= -0.5f ? fmaxf(fminf(c - least, cap), (kLogistic ? 0x1p-40f : 0x1p-16f) * cap) : cap;
+  return kLogistic ? fminf(most * (0x1p-23f * (7 + 35)), 0x1p-21f) : most * (0x1p-23f * (kPer + 25 + 25));
+}
+// How far above the next value one has to lie to be known to be above it and all others
+// behind, c the larger one: these may have larger scores than it, with biases below its.
+// `cut` is added; an infinite c lies above every finite one.
+template <int kPer, bool kLogistic>
 __device__ __forceinline__ float doubt(float c, float cap, float least, float cut) {
-  const float of_c = fmaf(0x1p-22f, fabsf(c), cut);
-  if (kLogistic) return fminf(0x1p-21f + of_c, FLT_MAX);
-  const float most = c >= -0.5f ? fmaxf(fminf(c - least, cap), 0x1p-11f * cap) : cap;
-  return fminf(fmaf(most, 0x1p-23f * (kPer + 25 + 18), of_c), FLT_MAX);
+  return fminf(fmaf(0x1p-22f, fabsf(c), scores_doubt<kPer, kLogistic>(c, cap, least)) + cut, FLT_MAX);
+}
+// The same for any scores of a logistic, which nearly always tells as much.
+__device__ __forceinline__ float any_doubt(float c, float cut) { return fminf(fmaf(0x1p-22f, fabsf(c), 0x1p-21f) + cut, FLT_MAX); }
+// Whether all lanes' c are known to be above what comes behind them, `gap` lower.
+template <int kPer, bool kLogistic>
+__device__ __forceinline__ bool all_clear(bool no_matter, float gap, float c, float cap, float least, float cut) {
+  if (!kLogistic) return __all_sync(kAll, no_matter || gap > doubt<kPer, false>(c, cap, least, cut));
+  const bool clear = no_matter || gap > any_doubt(c, cut);
+  return __all_sync(kAll, clear) || __all_sync(kAll, clear || gap > doubt<kPer, true>(c, cap, least, cut));
 }
 // The same for two groups' values, sums of two c, none of whose sizes add up to more than
 // `size`: two of a logistic's or of the row's largest score in each value, and 2^-24 of the c
@@ -178,12 +194,13 @@ __device__ __forceinline__ float group_doubt(float size, float cap) {
   return fmaf(size, 0x1p-22f, kLogistic ? 0x1p-20f : cap * (0x1p-22f * (kPer + 25)));
 }
 // Whether the chosen groups are known to lie above the others where that does not say so,
-// as one group's large bias is no other's doubt: each value with what it may be off by
-// itself.  A lane has a group's value and the size of its c, `cut` more that the value may
-// lack; `there`: the group has an expert.
+// as one group's large bias is no other's doubt, nor are scores larger than its own: each
+// value with what it may be off by itself.  A lane has a group's value, its largest c and
+// the size of its two, `cut` more that the value may lack; `there`: the group has an expert.
 template <int kPer, bool kLogistic>
-__device__ __noinline__ bool groups_clear(bool there, bool chosen, float value, float size, float cut, float cap) {
-  const float off = fabsf(value) < FLT_MAX ? fmaf(size, 0x1p-23f, kLogistic ? 0x1p-21f : cap * (0x1p-23f * (kPer + 25))) + cut : 0.0f;
+__device__ __noinline__ bool groups_clear(bool there, bool chosen, float value, float first, float size, float cut, float cap,
+                                          float least) {
+  const float off = fabsf(value) < FLT_MAX ? fmaf(size, 0x1p-23f, scores_doubt<kPer, kLogistic>(first, cap, least)) + cut : 0.0f;
   const uint32_t low = __reduce_min_sync(kAll, there && chosen ? order_key(value - off) : ~0u);
   const uint32_t high = __reduce_max_sync(kAll, there && !chosen ? order_key(value + off) : 0u);
   return low > high;
@@ -309,10 +326,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
   for (int e = lane; e < 32 * kPer; e += 32) {
     const float b = bias != nullptr && e < s.E ? read_at(bias, e, s.E, 0.0f, &g_route_status) : 0.0f;
-    if (!kLogistic && e < s.E && b > kFarBias) least = fminf(least, b);
+    if (e < s.E && b > kFarBias) least = fminf(least, b);
     if (warp == 0) sums[e] = b;
   }
-  if (!kLogistic) least = key_value(__reduce_min_sync(kAll, order_key(least)));
+  least = key_value(__reduce_min_sync(kAll, order_key(least)));
   __syncthreads();
 #pragma unroll
   for (int q = 0; q < kVectors; ++q) {
@@ -433,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float size = first > -CUDART_INF_F ? fabsf(first) + (second > -CUDART_INF_F ? fabsf(second) : 0.0f) : 0.0f;
           const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));  // not negative: ordered as its bits
           certain = key_value(last) - key_value(next) > group_doubt<kPer, kLogistic>(most, inv) ||
-                    groups_clear<kPer, kLogistic>(first > -CUDART_INF_F, chosen >> (g << gr.shift) & 1u, value, size, 0.0f, inv);
+                    groups_clear<kPer, kLogistic>(first > -CUDART_INF_F, chosen >> (g << gr.shift) & 1u, value, first, size, 0.0f, inv, least);
         }
 #pragma unroll
         for (int q = 0; q < kVectors; ++q) {
@@ -456,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (any && certain) {
         const float low = bar != 0u ? key_value(bar) : -FLT_MAX;
-        const float from = fmaxf(low - 0x1p-18f * (1.0f + fabsf(low)), -FLT_MAX);
+        const float from = fmaxf(low - 4.0f * doubt<kPer, kLogistic>(low, inv, least, 0.0f), -FLT_MAX);
         // those from there on side by side, the lanes' one behind the other
         int own_n = 0;
 #pragma unroll
@@ -495,10 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane < n) few_c[warp][before] = own_c;
           __syncwarp();
-          bool clear = true;
-          if (lane < n && before < s.k && before + 1 < n)
-            clear = own_c - few_c[warp][before + 1] > doubt<kPer, kLogistic>(own_c, inv, least, 0.0f);
-          if (!__all_sync(kAll, clear)) {
+          const bool no_matter = lane >= n || before >= s.k || before + 1 >= n;
+          const float gap = no_matter ? 0.0f : own_c - few_c[warp][before + 1];
+          if (!all_clear<kPer, kLogistic>(no_matter, gap, own_c, inv, least, 0.0f)) {
             before = settle<kPer, kLogistic>(e, x_e, own_b, my_s, top - x_e, n, s.k);
             certain = !__any_sync(kAll, before < 0);
           }
@@ -704,9 +720,9 @@ __global__ void __launch_bounds__(1024, 1)
     acc[i] = 0.0f;
     const float b = bias != nullptr && i < there ? read_at(bias, e0 + i, s.E, 0.0f, &g_route_status) : 0.0f;
     if (warp == 0) own_b[owned_at<kW>(lane, i)] = b;
-    if (!kLogistic && i < there && b > kFarBias) least = fminf(least, b);
+    if (i < there && b > kFarBias) least = fminf(least, b);
   }
-  if (!kLogistic) least = key_value(__reduce_min_sync(kAll, order_key(least)));
+  least = key_value(__reduce_min_sync(kAll, order_key(least)));
   __syncthreads();
   int routed_here = 0;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
@@ -796,7 +812,7 @@ __global__ void __launch_bounds__(1024, 1)
           const float size = first != 0u ? fabsf(of_first) + fabsf(of_second) : 0.0f;
           const float most = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));  // not negative: ordered as its bits
           certain = key_value(last) - key_value(next) > group_doubt<kW, kLogistic>(most, inv) + owned_cut<kW>(most) ||
-                    groups_clear<kW, kLogistic>(first != 0u, in, value, size, owned_cut<kW>(size), inv);
+                    groups_clear<kW, kLogistic>(first != 0u, in, value, of_first, size, owned_cut<kW>(size), inv, least);
         }
         if (__popc(__ballot_sync(kAll, in && first != 0u)) > gr.best << gr.shift) certain = false;
       }
@@ -822,9 +838,9 @@ __global__ void __launch_bounds__(1024, 1)
         const float x_e = own_x[owned_at<kW>(from, place)];
         my_s = kLogistic ? logistic(x_e) : exp2_ftz((x_e - top) * kLog2E) * inv;
         const float own_c = my_s + own_b[owned_at<kW>(from, place)];
-        const bool clear = lane >= s.k || own.x == 0u || next == 0u ||
-                           own_c - owned_value<kW>(next) > doubt<kW, kLogistic>(own_c, inv, least, 2.0f * owned_cut<kW>(own_c));
-        if (__all_sync(kAll, clear) && __reduce_add_sync(kAll, at - begin) == 128u * n) {
+        const bool clear = all_clear<kW, kLogistic>(lane >= s.k || own.x == 0u || next == 0u, own_c - owned_value<kW>(next), own_c, inv,
+                                                    least, 2.0f * owned_cut<kW>(own_c));
+        if (clear && __reduce_add_sync(kAll, at - begin) == 128u * n) {
           if (lane < s.k && own.x != 0u) rank = lane, my_id = (from >> gr.shift) * gr.size + (from & (gr.lanes - 1)) * kW + place;
         } else if (n > 0) {
           const int found = settle_owned<kW, kLogistic>(lists, in, own_x, own_b, top, inv, least, s.k, gr.size, gr.lanes, gr.shift);

@@ -86,3 +86,25 @@ def test_experts_left_out_by_the_lowest_bias(E, groups, best, k, scores):
     bias[::2] = LOWEST
     compare(x, bias, min(k, size), groups, best, scores)
     compare(x, torch.full((E,), LOWEST), k, groups, best, scores)
+
+
+@pytest.mark.parametrize("groups,best", [(1, 1), (8, 3)])
+@pytest.mark.parametrize("E", [32, 128, 256, 512])
+def test_small_scores_near_one_another(E, groups, best):
+    """Sigmoid scores of 1e-4 to 1e-11, logits a few units in the last place apart and equal
+    ones; without a bias, with one for all and with one that takes the scores' order back."""
+    g = torch.Generator().manual_seed(12)
+    for shift in (-9.0, -14.0, -19.0, -25.0):
+        at = shift - 0.25 * torch.randint(0, 4, (60, E), generator=g)
+        x = at + torch.randint(-3, 4, (60, E), generator=g) * 2.0**-20
+        s = torch.sigmoid(x[0].double())
+        for bias in (torch.zeros(E), torch.full((E,), 0.001), (s.max() - s).float()):
+            c = torch.sigmoid(x.double()) + bias.double()
+            # two scores and two biases the other way round have sums that are equal but for
+            # their roundings, as have groups of such pairs: rows without near sums are kept
+            if groups > 1:
+                value = torch.topk(c.view(60, groups, -1), 2, dim=2).values.sum(2).sort(1, descending=True).values
+                keep = value[:, best - 1] - value[:, best] > 2.0**-50 * value[:, 0].abs()
+            else:
+                keep = torch.ones(60, dtype=torch.bool)
+            compare(x, bias, 8, groups, best, "sigmoid", keep.numpy())

@@ -1,5 +1,6 @@
-"""moe_route_groups takes about as long whatever single biases are: a near tie is done again
-in 64 bits, and what makes every row look like one costs ten times the time of the call.  Times are compared with the same batch's of usual values
+"""moe_route_groups takes about as long whatever single biases are and however small the
+scores: a near tie is done again in 64 bits, and what makes every row look like one costs
+ten times the time of the call.  Times are compared with the same batch's of usual values
 in the same test, the shortest of several each; the margin is a factor of two.
 """
 import math
@@ -56,3 +57,19 @@ def test_a_bias_that_leaves_an_expert_out_or_takes_it_always(e, groups, best, sc
     assert max(took) < 2 * took[0], took
     for b in biases[1:]:
         Case(300, e, 8, groups, best, scores, x=x[:300].cpu(), bias=b.cpu()).check(exact=False)
+
+
+@pytest.mark.parametrize("bias", [None, 0.0, -0.01])
+@pytest.mark.parametrize("e,groups,best", [(E, 8, 4), (E, 1, 1), (512, 8, 4)])
+def test_small_scores(e, groups, best, bias):
+    """Sigmoid scores of 1e-6, and of 1e-9, are as far apart for their size as usual ones.  A
+    bias of all experts leaves them what fp32 has behind its size: with 0.01 1e-9 of them, so
+    that there only the larger ones are compared."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(T, e, generator=g, device="cuda") * 1.5
+    bias = None if bias is None else torch.full((e,), bias, device="cuda")
+    shifts = [0.0, -14.0, -20.0] if bias is None or not bias.any() else [0.0, -10.0]
+    took = [times(x + y, 8, [bias], scores="sigmoid", groups=groups, best_groups=best)[0] for y in shifts]
+    assert max(took) < 2 * took[0], took
+    for y in shifts[1:]:
+        Case(300, e, 8, groups, best, "sigmoid", x=x[:300].cpu() + y, bias=None if bias is None else bias.cpu()).check(exact=False)

@@ -502,6 +502,10 @@ int mxq_embedding_backward(const void *ids, int ids_bytes, int64_t tokens, const
  *   grad_scale  device memory, or NULL: 1.
  *   beta1, beta2 in [0, 1), eps >= 0.
  * No two outputs may overlap, nor an output and an input.
+ *
+ * mxq_adamw_check: the checks of a longer list (at most 2^24 entries), which takes several
+ * calls, before the first of them: types, sizes, places and overlaps among all of its
+ * buffers.  It launches nothing and needs no device.
  */
 #define MXQ_ADAMW_TENSORS 512
 typedef struct mxq_adamw_tensor {
@@ -516,6 +520,9 @@ int mxq_adamw(const mxq_adamw_tensor *tensors, int32_t count, int32_t bits, void
               const int64_t *step_at, double lr, const float *lr_at, double beta1, double beta2,
               double eps, double weight_decay, const float *grad_scale, uint64_t seed,
               cudaStream_t stream);
+int mxq_adamw_check(const mxq_adamw_tensor *tensors, int64_t count, int32_t bits, const void *m,
+                    const void *v, const uint8_t *m_scale, const uint8_t *v_scale, int64_t total,
+                    const int64_t *step_at, const float *lr_at, const float *grad_scale);
 
 /*
  * Newton-Schulz orthogonalisation of a momentum matrix, or of a stack of them:

@@ -141,6 +141,7 @@ def lib() -> ctypes.CDLL:
                 ("mxq_embedding_backward", ci, [vp, ci, i64, vp, ci, i64, i64, i64, i64, f32, vp, ci, i64, vp, i64, vp]),
                 ("mxq_adamw", ci, [vp, i32, i32, vp, vp, vp, vp, i64, i64, vp, f64, vp, f64, f64, f64, f64, vp, ctypes.c_uint64,
                                    vp]),
+                ("mxq_adamw_check", ci, [vp, i64, i32, vp, vp, vp, vp, i64, vp, vp, vp]),
                 ("mxq_orthogonalize_workspace", i64, [i64, i64, i64]),
                 ("mxq_orthogonalize", ci, [vp, ci, i64, i64, i64, i64, i64, i32, f32, f32, f32, f32, f32, vp, i64, i64,
                                            vp, i64, vp])):

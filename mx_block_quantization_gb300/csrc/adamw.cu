@@ -37,6 +37,8 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <memory>
+#include <new>
 
 #include "train_common.cuh"
 
@@ -583,29 +585,14 @@ int launch_adamw(const mxq_adamw_tensor* tensors, int32_t count, const Step& s, 
   return MXQ_OK;
 }
 
-}  // namespace
-
-namespace mxq {
-int adamw_status_read(unsigned int* out, bool clear) { return read_status_word(g_adamw_status, out, clear); }
-int adamw_watch(uint64_t address) { return watch_address(address); }
-}  // namespace mxq
-
-extern "C" int mxq_adamw(const mxq_adamw_tensor* tensors, int32_t count, int32_t bits, void* m, void* v, uint8_t* m_scale,
-                         uint8_t* v_scale, int64_t total, int64_t step, const int64_t* step_at, double lr, const float* lr_at,
-                         double beta1, double beta2, double eps, double weight_decay, const float* grad_scale, uint64_t seed,
-                         cudaStream_t stream) {
-  if (bits != 8 && bits != 32) return MXQ_EBADDTYPE;
-  if (count < 0 || count > MXQ_ADAMW_TENSORS || total < 0 || total > (int64_t{1} << 44) || total % kStartAlign != 0 ||
-      (!step_at && (step < 1 || step > INT32_MAX)) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) ||
-      !isfinite(eps) || !isfinite(weight_decay) || (!lr_at && !isfinite(lr)))
-    return MXQ_EBADSHAPE;
-  if (count == 0) return MXQ_OK;
-  if (!tensors) return MXQ_ENULL;
+// The buffers of a list of tensors: their types, sizes, places and overlaps.  `ranges` holds
+// 4 count + 6.  *used: tensors with elements.
+int check_buffers(const mxq_adamw_tensor* tensors, int32_t count, int32_t bits, const void* m, const void* v, const uint8_t* m_scale,
+                  const uint8_t* v_scale, int64_t total, const int64_t* step_at, const float* lr_at, const float* grad_scale, Marked* ranges,
+                  int32_t* used) {
   const int es = bits == 32 ? 4 : 1;
-  Marked ranges[4 * MXQ_ADAMW_TENSORS + 6];
   int n = 0;
-  int64_t chunks = 0;
-  int32_t used = 0;
+  *used = 0;
   for (int32_t i = 0; i < count; ++i) {
     const mxq_adamw_tensor& t = tensors[i];
     if ((t.dtype != MXQ_F32 && t.dtype != MXQ_BF16) || (t.grad_dtype != MXQ_F32 && t.grad_dtype != MXQ_BF16)) return MXQ_EBADDTYPE;
@@ -619,11 +606,9 @@ extern "C" int mxq_adamw(const mxq_adamw_tensor* tensors, int32_t count, int32_t
     ranges[n++] = {address_of(t.grad), static_cast<uint64_t>(t.n) * gs, false};
     ranges[n++] = {m ? address_of(m) + static_cast<uint64_t>(t.start) * es : 0,
                    static_cast<uint64_t>(ceil_div(t.n, kScaleBlock) * kScaleBlock) * es, true};
-    chunks += ceil_div(t.n, kChunk);
-    ++used;
+    ++*used;
   }
-  if (used == 0) return MXQ_OK;
-  if (chunks > INT32_MAX) return MXQ_EBADSHAPE;
+  if (*used == 0) return MXQ_OK;
   if (!m || !v || (bits == 8 && (!m_scale || !v_scale))) return MXQ_ENULL;
   if (!aligned_to(m, 16) || !aligned_to(v, 16) || !aligned_to(lr_at, 4) || !aligned_to(grad_scale, 4) || !aligned_to(step_at, 8))
     return MXQ_EALIGN;
@@ -633,7 +618,35 @@ extern "C" int mxq_adamw(const mxq_adamw_tensor* tensors, int32_t count, int32_t
   ranges[n++] = {address_of(lr_at), 4, false};
   ranges[n++] = {address_of(grad_scale), 4, false};
   ranges[n++] = {address_of(step_at), 8, false};
-  if (marked_overlap(ranges, n)) return MXQ_EOVERLAP;
+  return marked_overlap(ranges, n) ? MXQ_EOVERLAP : MXQ_OK;
+}
+bool total_ok(int64_t total) { return total >= 0 && total <= (int64_t{1} << 44) && total % kStartAlign == 0; }
+
+}  // namespace
+
+namespace mxq {
+int adamw_status_read(unsigned int* out, bool clear) { return read_status_word(g_adamw_status, out, clear); }
+int adamw_watch(uint64_t address) { return watch_address(address); }
+}  // namespace mxq
+
+extern "C" int mxq_adamw(const mxq_adamw_tensor* tensors, int32_t count, int32_t bits, void* m, void* v, uint8_t* m_scale,
+                         uint8_t* v_scale, int64_t total, int64_t step, const int64_t* step_at, double lr, const float* lr_at,
+                         double beta1, double beta2, double eps, double weight_decay, const float* grad_scale, uint64_t seed,
+                         cudaStream_t stream) {
+  if (bits != 8 && bits != 32) return MXQ_EBADDTYPE;
+  if (count < 0 || count > MXQ_ADAMW_TENSORS || !total_ok(total) || (!step_at && (step < 1 || step > INT32_MAX)) ||
+      !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) || !isfinite(eps) || !isfinite(weight_decay) ||
+      (!lr_at && !isfinite(lr)))
+    return MXQ_EBADSHAPE;
+  if (count == 0) return MXQ_OK;
+  if (!tensors) return MXQ_ENULL;
+  Marked ranges[4 * MXQ_ADAMW_TENSORS + 6];
+  int32_t used = 0;
+  const int rc = check_buffers(tensors, count, bits, m, v, m_scale, v_scale, total, step_at, lr_at, grad_scale, ranges, &used);
+  if (rc != MXQ_OK || used == 0) return rc;
+  int64_t chunks = 0;
+  for (int32_t i = 0; i < count; ++i) chunks += ceil_div(tensors[i].n, kChunk);
+  if (chunks > INT32_MAX) return MXQ_EBADSHAPE;
   Step s = {};
   s.m = m, s.v = v, s.ms = m_scale, s.vs = v_scale;
   s.total = total;
@@ -648,4 +661,18 @@ extern "C" int mxq_adamw(const mxq_adamw_tensor* tensors, int32_t count, int32_t
   const int sms = sm_count_current_device(nullptr);
   if (sms <= 0) return MXQ_ECUDA;
   return bits == 32 ? launch_adamw<32>(tensors, count, s, sms, stream) : launch_adamw<8>(tensors, count, s, sms, stream);
+}
+
+extern "C" int mxq_adamw_check(const mxq_adamw_tensor* tensors, int64_t count, int32_t bits, const void* m, const void* v,
+                               const uint8_t* m_scale, const uint8_t* v_scale, int64_t total, const int64_t* step_at, const float* lr_at,
+                               const float* grad_scale) {
+  if (bits != 8 && bits != 32) return MXQ_EBADDTYPE;
+  if (count < 0 || count > (1 << 24) || !total_ok(total)) return MXQ_EBADSHAPE;
+  if (count == 0) return MXQ_OK;
+  if (!tensors) return MXQ_ENULL;
+  const std::unique_ptr<Marked[]> ranges(new (std::nothrow) Marked[4 * count + 6]);
+  if (!ranges) return MXQ_EBADSHAPE;
+  int32_t used = 0;
+  return check_buffers(tensors, static_cast<int32_t>(count), bits, m, v, m_scale, v_scale, total, step_at, lr_at, grad_scale, ranges.get(),
+                       &used);
 }

@@ -816,7 +816,8 @@ def adamw_step(params, grads, moments: Moments, step, *, lr, betas=(0.9, 0.999),
     parameters are also rounded to.  ``step`` t counts from 1; ``step`` (int64) and ``lr``
     (fp32) may be tensors [] on the device, read as the step runs, so that a captured step
     can be replayed.  ``grad_scale``: an fp32 tensor [] that multiplies the gradients.
-    Moments in 8 bits are rounded at random by ``seed`` and the step."""
+    Moments in 8 bits are rounded at random by ``seed`` and the step.  A list that is refused
+    leaves everything as it was."""
     params, grads = list(params), list(grads)
     n = len(params)
     if len(grads) != n or (copies is not None and len(copies) != n):
@@ -864,11 +865,16 @@ def adamw_step(params, grads, moments: Moments, step, *, lr, betas=(0.9, 0.999),
         raise ValueError("step must count from 1")
     b1, b2 = betas
     where = _elsewhere(dev, stream)
+    L, count = lib(), len(table) // 6
+    table = (ctypes.c_int64 * len(table))(*table)
+    if count > _TENSORS:  # several launches: all is checked before the first
+        rc = L.mxq_adamw_check(table, count, bits, m, v, ms, vs, total, step_at, lr_at, grad_scale)
+        if rc != OK:
+            raise MxqError(rc, "mxq_adamw")
     with where if where is not None else nullcontext():
         handle = _stream(dev.index)
-        for at in range(0, len(table), 6 * _TENSORS):
-            part = table[at:at + 6 * _TENSORS]
-            rc = lib().mxq_adamw((ctypes.c_int64 * len(part))(*part), len(part) // 6, bits, m, v, ms, vs, total, step, step_at,
-                                 lr, lr_at, b1, b2, eps, weight_decay, grad_scale, seed, handle)
+        for at in range(0, count, _TENSORS):
+            rc = L.mxq_adamw(ctypes.byref(table, 48 * at), min(count - at, _TENSORS), bits, m, v, ms, vs, total, step, step_at,
+                             lr, lr_at, b1, b2, eps, weight_decay, grad_scale, seed, handle)
             if rc != OK:
                 raise MxqError(rc, "mxq_adamw")

@@ -817,7 +817,8 @@ def adamw_step(params, grads, moments: Moments, step, *, lr, betas=(0.9, 0.999),
     (fp32) may be tensors [] on the device, read as the step runs, so that a captured step
     can be replayed.  ``grad_scale``: an fp32 tensor [] that multiplies the gradients.
     Moments in 8 bits are rounded at random by ``seed`` and the step.  A list that is refused
-    leaves everything as it was."""
+    leaves everything as it was.  Parameters and copies count as modified in place for
+    autograd; the replay of a captured step is not seen by it."""
     params, grads = list(params), list(grads)
     n = len(params)
     if len(grads) != n or (copies is not None and len(copies) != n):
@@ -836,7 +837,7 @@ def adamw_step(params, grads, moments: Moments, step, *, lr, betas=(0.9, 0.999),
             raise ValueError("moments in 8 bits have scales")
         ms, vs = (_flat(t, name, torch.uint8, (total // 32,), dev)
                   for t, name in ((moments.m_scale, "m_scale"), (moments.v_scale, "v_scale")))
-    table, live = [], set()
+    table, live, written = [], set(), []
     for i, (p, g) in enumerate(zip(params, grads)):  # the checks of a tensor take longer than its share of a launch
         if g is None or sizes[i] == 0:
             continue
@@ -850,7 +851,9 @@ def adamw_step(params, grads, moments: Moments, step, *, lr, betas=(0.9, 0.999),
         at, copy = p.data_ptr(), 0
         if copies is not None and copies[i] is not None:
             copy = _flat(copies[i], "copies", torch.bfloat16, p.shape, dev)
+            written.append(copies[i])
         live.add(at)
+        written.append(p)
         table += (at, g.data_ptr(), copy, sizes[i], starts[i], code | gcode << 32)
     if len(live) * 6 != len(table):
         raise ValueError("params must be different tensors")
@@ -878,3 +881,5 @@ def adamw_step(params, grads, moments: Moments, step, *, lr, betas=(0.9, 0.999),
                              lr, lr_at, b1, b2, eps, weight_decay, grad_scale, seed, handle)
             if rc != OK:
                 raise MxqError(rc, "mxq_adamw")
+    # written through addresses: a backward pass of a graph that saved one of them has to see it
+    torch.autograd.graph.increment_version(written)

@@ -1,4 +1,4 @@
-"""adamw_step as a call: lists that take several launches."""
+"""adamw_step as a call: lists that take several launches, and what autograd is told."""
 import pytest
 import torch
 
@@ -42,3 +42,24 @@ def test_a_long_list_is_refused_before_anything_moves(fault, bits):
     assert e.value.code == mxq.EOVERLAP
     assert all(torch.equal(a, b) for a, b in zip(params, before[0]))
     assert all(b is None or torch.equal(a, b) for a, b in zip(moments, before[1]))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_graph_that_saved_a_parameter_is_told(bits):
+    """As after torch's own optimisers: a backward pass through values that the step has
+    changed is an error, not a gradient of the new ones."""
+    params = [t.requires_grad_() for t in tensors([100, 300, 200])]
+    copies = [p.detach().to(BF16) for p in params[:2]] + [None]
+    scale = torch.ones(300, device="cuda", requires_grad=True)
+    saved = (params[0] ** 2).sum(), (copies[1] * scale).sum(), (params[2] ** 2).sum()
+    moments = mxq.adamw_moments(params, bits)
+    grads = tensors([100, 300, 200], seed=1)
+    grads[2] = None
+    mxq.adamw_step(params, grads, moments, 1, copies=copies, **HOW)
+    for y in saved[:2]:
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    saved[2].backward()                 # no gradient: left as it is
+    assert torch.equal(params[2].grad, 2 * params[2].detach())
+    with torch.inference_mode():        # these have no versions
+        mxq.adamw_step([params[0] * 1.0], grads[:1], mxq.adamw_moments(params[:1], bits), 1, **HOW)

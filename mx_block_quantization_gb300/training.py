@@ -555,8 +555,9 @@ def moe_linear(q, s, w, sw, offs=None, *, bias=None, activation: Optional[str] =
 def moe_linear_backward(dy, z=None, offs=None, *, activation: Optional[str] = None, out=None, stream=None):
     """Gradients (dz [M, N], dbias fp32 [G, N], or [N] without offs) of what
     :func:`moe_linear` adds to the product: dz = dy act'(z) with the pre-activation z,
-    zero behind the last group, and its sum over each group.  Without an activation dz is
-    dy itself.  The residual's gradient is dy."""
+    zero behind the last group, and its sum over each group without the rows behind the
+    last one.  Without an activation dz is dy itself, with those rows as they are, unless
+    ``out`` has another tensor for it.  The residual's gradient is dy."""
     dev = dy.device
     dtype_code = _code(dy, "dy")
     ld = _matrix(dy, "dy")
@@ -583,12 +584,11 @@ def moe_linear_backward(dy, z=None, offs=None, *, activation: Optional[str] = No
         dbias = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
         dz, dbias = out
-        if not code and dz is not dy:
-            raise ValueError("without an activation dz is dy itself")
     ld_dz = _output(dz, "dz", (M, N), dy.dtype, dev)[0]
+    dz_p = dz.data_ptr() if code or dz is not dy else None
     db = _flat(dbias, "dbias", torch.float32, torch.Size(shape), dev)
     rc = L.mxq_moe_linear_backward(dy.data_ptr(), dtype_code, ld, z.data_ptr() if code else None, ldz, code, op, G, M, N,
-                                   dz.data_ptr() if code else None, ld_dz, db, wp, size, _stream(dev.index))
+                                   dz_p, ld_dz, db, wp, size, _stream(dev.index))
     if rc != OK:
         raise MxqError(rc, "mxq_moe_linear_backward")
     return dz, dbias

@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kBackThreads) epilogue_backward_kernel(const E
         const int64_t row = static_cast<int64_t>(block) * kBlock + r0 + q * ty;
         const bool in = live && r0 + q * ty < kBlock;
         const T* from = static_cast<const T*>(a.dy) + row * a.ld_dy + col;
-        dy[q] = load_if<T, kV>(from, in && in_buf(from, sizeof dy[q], a.dy, a.dy_bytes, &g_linear_status));
+        dy[q] = load_if_written<T, kV>(from, in && in_buf(from, sizeof dy[q], a.dy, a.dy_bytes, &g_linear_status));
         if (kAct != kNone) {
           const T* at = static_cast<const T*>(a.z) + row * a.ld_z + col;
           z[q] = load_if<T, kV>(at, in && in_buf(at, sizeof z[q], a.z, a.z_bytes, &g_linear_status));

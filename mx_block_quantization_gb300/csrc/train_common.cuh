@@ -55,49 +55,55 @@ __device__ __forceinline__ void write_at(T* a, int64_t i, int64_t n, T v, unsign
   if (in_array(a, i, n, status)) a[i] = v;
 }
 
-// Load of data that this launch does not write, not kept in L1; zero where `wanted`
-// is false.  The condition is the load's own predicate: as a branch around each
-// load it makes the loads wait for one another.
-template <typename T, int kN>
-__device__ __forceinline__ Vec<T, kN> load_if(const T* p, bool wanted) {
-  Vec<T, kN> v;
-  const uint32_t w = wanted ? 1u : 0u;
-  if constexpr (sizeof v == 16) {
-    uint4 q;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-        : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)
-        : "l"(p), "r"(w));
-    *reinterpret_cast<uint4*>(&v) = q;
-  } else if constexpr (sizeof v == 8) {
-    uint2 q;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];\n\t}"
-        : "=&r"(q.x), "=&r"(q.y)
-        : "l"(p), "r"(w));
-    *reinterpret_cast<uint2*>(&v) = q;
-  } else if constexpr (sizeof v == 4) {
-    uint32_t q;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.b32 %0, [%1];\n\t}"
-        : "=&r"(q)
-        : "l"(p), "r"(w));
-    *reinterpret_cast<uint32_t*>(&v) = q;
-  } else {
-    uint16_t q;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t"
-        "@p ld.global.nc.L1::no_allocate.b16 %0, [%1];\n\t}"
-        : "=&h"(q)
-        : "l"(p), "r"(w));
-    *reinterpret_cast<uint16_t*>(&v) = q;
+// Load of data, not kept in L1; zero where `wanted` is false.  The condition is the load's
+// own predicate: as a branch around each load it makes the loads wait for one another.
+// load_if is for data that this launch does not write, load_if_written for what it may
+// write in place: the cache that the first may use is not told of stores.
+#define MXQ_LOAD_IF(name, op)                                                                                          \
+  template <typename T, int kN>                                                                                        \
+  __device__ __forceinline__ Vec<T, kN> name(const T* p, bool wanted) {                                                \
+    Vec<T, kN> v;                                                                                                      \
+    const uint32_t w = wanted ? 1u : 0u;                                                                               \
+    if constexpr (sizeof v == 16) {                                                                                    \
+      uint4 q;                                                                                                         \
+      asm volatile(                                                                                                    \
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"                                                            \
+          "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"                                   \
+          "@p " op ".v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"                                                              \
+          : "=&r"(q.x), "=&r"(q.y), "=&r"(q.z), "=&r"(q.w)                                                             \
+          : "l"(p), "r"(w));                                                                                           \
+      *reinterpret_cast<uint4*>(&v) = q;                                                                               \
+    } else if constexpr (sizeof v == 8) {                                                                              \
+      uint2 q;                                                                                                         \
+      asm volatile(                                                                                                    \
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"                        \
+          "@p " op ".v2.b32 {%0, %1}, [%2];\n\t}"                                                                      \
+          : "=&r"(q.x), "=&r"(q.y)                                                                                     \
+          : "l"(p), "r"(w));                                                                                           \
+      *reinterpret_cast<uint2*>(&v) = q;                                                                               \
+    } else if constexpr (sizeof v == 4) {                                                                              \
+      uint32_t q;                                                                                                      \
+      asm volatile(                                                                                                    \
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t"                                          \
+          "@p " op ".b32 %0, [%1];\n\t}"                                                                               \
+          : "=&r"(q)                                                                                                   \
+          : "l"(p), "r"(w));                                                                                           \
+      *reinterpret_cast<uint32_t*>(&v) = q;                                                                            \
+    } else {                                                                                                           \
+      uint16_t q;                                                                                                      \
+      asm volatile(                                                                                                    \
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b16 %0, 0;\n\t"                                          \
+          "@p " op ".b16 %0, [%1];\n\t}"                                                                               \
+          : "=&h"(q)                                                                                                   \
+          : "l"(p), "r"(w));                                                                                           \
+      *reinterpret_cast<uint16_t*>(&v) = q;                                                                            \
+    }                                                                                                                  \
+    return v;                                                                                                          \
   }
-  return v;
-}
+MXQ_LOAD_IF(load_if, "ld.global.nc.L1::no_allocate")
+MXQ_LOAD_IF(load_if_written, "ld.global.L1::no_allocate")
+#undef MXQ_LOAD_IF
+
 template <typename T, int kN>
 __device__ __forceinline__ Vec<T, kN> load_once(const T* p) {
   return load_if<T, kN>(p, true);

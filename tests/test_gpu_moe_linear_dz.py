@@ -43,3 +43,23 @@ def test_rows_behind_the_last_group_without_an_activation(blocks, tail, N, dtype
     with pytest.raises(mxq.MxqError) as e:
         mxq.moe_linear_backward(room[:, :N], offs=offs, out=(room[:, 2:N + 2], torch.empty_like(dbias)))
     assert e.value.code == mxq.EOVERLAP
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("activation", [None, "relu", "silu", "gelu"])
+@pytest.mark.parametrize("pad", [0, 1, 8])
+def test_in_place_of_dy(activation, dtype, pad):
+    """dz over dy, with many blocks of the grid side by side in a row: the bits of a call
+    with buffers of their own at the same pitch."""
+    blocks, N = [9, 0, 30, 1], 1152
+    M, offs = 128 * (sum(blocks) + 3), ends_of(blocks).cuda()
+    both = torch.empty(2, M, N + pad, dtype=dtype, device="cuda")
+    both[0, :, :N] = normal((M, N), 1, dtype=dtype)
+    both[1, :, :N] = normal((M, N), 2, 2.0, dtype=dtype)
+    dy, z = both[0, :, :N], both[1, :, :N]
+    out = torch.empty_like(both[0])[:, :N], torch.empty(4, N, device="cuda")
+    dz, dbias = mxq.moe_linear_backward(dy, z, offs, activation=activation, out=out)
+    over = dy[:]  # another tensor of the same memory
+    for _ in range(2 if activation is None else 1):  # without an activation again and again
+        got, again = mxq.moe_linear_backward(dy, z, offs, activation=activation, out=(over, torch.empty_like(dbias)))
+        assert torch.equal(got, dz) and torch.equal(again, dbias)

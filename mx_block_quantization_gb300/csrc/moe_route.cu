@@ -661,7 +661,7 @@ int check_route_shape(int dtype, int64_t tokens, int32_t experts, int32_t k, int
 }  // namespace
 
 namespace mxq {
-int route_softmax_status_read(unsigned int* out, bool clear) {
+int route_status_read(unsigned int* out, bool clear) {
   return read_status_word(g_route_status, out, clear);
 }
 int route_watch(uint64_t address) { return watch_address(address); }

@@ -31,24 +31,6 @@ int embedding_watch(uint64_t address);  // embedding.cu
 int ortho_watch(uint64_t address);      // orthogonalize.cu
 int linear_watch(uint64_t address);     // moe_linear.cu
 int adamw_watch(uint64_t address);      // adamw.cu
-
-int route_softmax_status_read(unsigned int* out, bool clear);  // moe_route.cu
-int route_groups_status_read(unsigned int* out, bool clear);   // moe_route_groups.cu
-int linear_status_read(unsigned int* out, bool clear);         // moe_linear.cu
-int adamw_status_read(unsigned int* out, bool clear);          // adamw.cu
-
-// The words of these files together, under the one name that mxq_device_status reads for
-// them: the profile of the cast goes with its source file, which holds that function.
-int route_status_read(unsigned int* out, bool clear) {
-  *out = 0;
-  for (auto* read : {route_softmax_status_read, route_groups_status_read, linear_status_read, adamw_status_read}) {
-    unsigned int w = 0;
-    const int rc = read(&w, clear);
-    if (rc != MXQ_OK) return rc;
-    *out |= w;
-  }
-  return MXQ_OK;
-}
 }  // namespace mxq
 
 extern "C" int mxq_selftest_watch(const void *address) {

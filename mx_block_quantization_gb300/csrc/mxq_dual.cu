@@ -765,10 +765,13 @@ int compose_status_read(unsigned int* out, bool clear);  // mxq_compose.cu
 int cols_status_read(unsigned int* out, bool clear);     // mx_cols_tma.cu
 int packed_status_read(unsigned int* out, bool clear);   // mx_packed.cu
 int mma_status_read(unsigned int* out, bool clear);      // mxq_mma_check.cu
-int route_status_read(unsigned int* out, bool clear);      // moe_route.cu
-int exchange_status_read(unsigned int* out, bool clear);   // moe_exchange.cu
-int embedding_status_read(unsigned int* out, bool clear);  // embedding.cu
-int ortho_status_read(unsigned int* out, bool clear);      // orthogonalize.cu
+int route_status_read(unsigned int* out, bool clear);         // moe_route.cu
+int route_groups_status_read(unsigned int* out, bool clear);  // moe_route_groups.cu
+int exchange_status_read(unsigned int* out, bool clear);      // moe_exchange.cu
+int linear_status_read(unsigned int* out, bool clear);        // moe_linear.cu
+int embedding_status_read(unsigned int* out, bool clear);     // embedding.cu
+int ortho_status_read(unsigned int* out, bool clear);         // orthogonalize.cu
+int adamw_status_read(unsigned int* out, bool clear);         // adamw.cu
 }
 
 // The device status word is the OR of the per-file words of the kernels.
@@ -794,8 +797,8 @@ extern "C" int mxq_device_status(uint32_t* out, int clear) {
   rc = mxq::mma_status_read(&g, clear != 0);
   if (rc != MXQ_OK) return rc;
   v |= w | c | t | k | g;
-  for (auto* read : {mxq::route_status_read, mxq::exchange_status_read, mxq::embedding_status_read,
-                     mxq::ortho_status_read}) {
+  for (auto* read : {mxq::route_status_read, mxq::route_groups_status_read, mxq::exchange_status_read, mxq::linear_status_read,
+                     mxq::embedding_status_read, mxq::ortho_status_read, mxq::adamw_status_read}) {
     rc = read(&g, clear != 0);
     if (rc != MXQ_OK) return rc;
     v |= g;

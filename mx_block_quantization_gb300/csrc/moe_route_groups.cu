@@ -465,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t mine = order_key(most);
       // the k-th largest lane maximum, equal ones counted once; 0 when there are fewer
       uint32_t bar = __reduce_max_sync(kAll, mine);
+      const uint32_t first_key = bar;
       const bool any = bar != 0u;
 #pragma unroll 4
       for (int j = 1; j < s.k; ++j) {
@@ -472,19 +473,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar = __reduce_max_sync(kAll, mine);
       }
       if (any && certain) {
-        const float low = bar != 0u ? key_value(bar) : -FLT_MAX;
-        const float from = fmaxf(low - 4.0f * doubt<kPer, kLogistic>(low, inv, least, 0.0f), -FLT_MAX);
-        // those from there on side by side, the lanes' one behind the other
-        int own_n = 0;
+        float from;
+        int own_n, upto, n;
+        const auto gather = [&](float low) {  // those from there on side by side, the lanes' one behind the other
+          from = fmaxf(low - 4.0f * doubt<kPer, kLogistic>(low, inv, least, 0.0f), -FLT_MAX);
+          own_n = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) own_n += c[i] >= from ? 1 : 0;
-        int upto = own_n;
+          for (int i = 0; i < kPer; ++i) own_n += c[i] >= from ? 1 : 0;
+          upto = own_n;
 #pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-          const int other = __shfl_up_sync(kAll, upto, d);
-          if (lane >= d) upto += other;
+          for (int d = 1; d < 32; d *= 2) {
+            const int other = __shfl_up_sync(kAll, upto, d);
+            if (lane >= d) upto += other;
+          }
+          n = __shfl_sync(kAll, upto, 31);
+        };
+        gather(bar != 0u ? key_value(bar) : -FLT_MAX);
+        if (n > 32) {  // lanes with several of the largest, as when k is near 32: from the k-th of all on, by halving
+          uint32_t below = bar, above = first_key + 1u;
+          int count = n;
+#pragma unroll 1
+          while (count != s.k && above - below > 1u) {
+            const uint32_t mid = below + (above - below) / 2u;
+            int own = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) own += c[i] >= key_value(mid) ? 1 : 0;
+            own = __reduce_add_sync(kAll, own);
+            if (own >= s.k) below = mid, count = own;
+            else above = mid;
+          }
+          gather(key_value(max(below, order_key(-FLT_MAX))));
         }
-        const int n = __shfl_sync(kAll, upto, 31);
         if (n <= 32) {
           uint32_t at = smem_u32(&few[warp][upto - own_n]);
 #pragma unroll

@@ -73,3 +73,17 @@ def test_small_scores(e, groups, best, bias):
     assert max(took) < 2 * took[0], took
     for y in shifts[1:]:
         Case(300, e, 8, groups, best, "sigmoid", x=x[:300].cpu() + y, bias=None if bias is None else bias.cpu()).check(exact=False)
+
+
+@pytest.mark.parametrize("scores", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("e,groups,best", [(250, 5, 3), (512, 1, 1), (512, 8, 4), (1000, 1, 1)])
+def test_the_most_choices(e, groups, best, scores):
+    """32 experts a token take four times as many rounds as 8, and the search for the 32nd."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, e, generator=g, device="cuda") * 1.5
+    bias = torch.randn(e, generator=g, device="cuda") * 0.02
+    how = dict(scores=scores, groups=groups, best_groups=best)
+    took = [times(x, k, [bias], **how)[0] for k in (8, 20, 32)]
+    assert max(took) < 4 * took[0], took
+    for k in (20, 32):
+        Case(300, e, k, groups, best, scores, x=x[:300].cpu(), bias=bias.cpu()).check(exact=False)

@@ -493,9 +493,11 @@ int mxq_embedding_backward(const void *ids, int ids_bytes, int64_t tokens, const
  *             Nothing is done for n == 0.  A bf16 p is rounded to nearest.
  *   bits      32: m and v fp32 [total].  8: m and the root of v as E4M3 [total] with E8M0
  *             scales m_scale and v_scale [total/32], one for 32 elements by the cast's
- *             rule; rounded at random from (seed, t, place) so that the mean is exact,
- *             a root that is not 0 never to 0; a block with a value that is not finite
- *             becomes NaN.  All bytes of a tensor's last 32 are written, 0 behind its
+ *             rule; rounded at random from (seed, t, place), m and the root with their
+ *             exact value as mean (v, the square, gains the roundings' variance, some
+ *             percent), a root that is not 0 never to 0 (elements below 2^-17 of the
+ *             largest of their 32 take smaller steps); a block with a value that is not
+ *             finite becomes NaN.  All bytes of a tensor's last 32 are written, 0 behind its
  *             end.  total is a multiple of 128; m and v 16-byte aligned.
  *   t         *step_at (device memory) or, with step_at NULL, step; at least 1.
  *   lr        *lr_at (device memory) or, with lr_at NULL, lr.

@@ -15,8 +15,12 @@
 // its rule for the scale: m, and the root of v, whose exponents span half of v's.  A step
 // changes v by (1 - b2) of it, far less than half a step of E4M3, so rounding to nearest
 // would never let it fall; both are rounded at random instead, up with the probability of
-// what lies above the value below, so that their mean is the exact value's.  A root that
-// is not 0 is never rounded to 0: m over eps would be no step that the gradients ask for.
+// what lies above the value below, so that the mean of m and of the root is the exact one's.
+// v is the root's square, and gains the variance of its roundings: with normal gradients it
+// is 2.5% too high on the mean for b2 0.95 and 4.2% for 0.999, single elements 0.2 to 3.6 of
+// the exact one.  A root that is not 0 is never rounded to 0, as m over eps would be no step
+// that the gradients ask for: elements 2^-17 of their block's largest and below have the
+// smallest root of the block, and steps as much smaller as theirs would be.
 // The random bits are a mixing of the element's place, the step and the seed (two rounds
 // of shift, exclusive or and product with the fractional digits of the roots of 2 and 3),
 // 16 of them for each moment: the same call gives the same bits.

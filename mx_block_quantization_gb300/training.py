@@ -816,7 +816,9 @@ def adamw_step(params, grads, moments: Moments, step, *, lr, betas=(0.9, 0.999),
     parameters are also rounded to.  ``step`` t counts from 1; ``step`` (int64) and ``lr``
     (fp32) may be tensors [] on the device, read as the step runs, so that a captured step
     can be replayed.  ``grad_scale``: an fp32 tensor [] that multiplies the gradients.
-    Moments in 8 bits are rounded at random by ``seed`` and the step.  A list that is refused
+    Moments in 8 bits are rounded at random by ``seed`` and the step: m and the root of v
+    are right on the mean, v is 2% to 5% high, and elements far below the largest of their
+    32 take smaller steps.  A list that is refused
     leaves everything as it was.  Parameters and copies count as modified in place for
     autograd; the replay of a captured step is not seen by it."""
     params, grads = list(params), list(grads)

@@ -616,8 +616,8 @@ def mxfp8_scaled_mm(a, sa, b, sb, *, out=None, stream=None):
 
 _TRAINING = ("Routing", "MoePlan", "moe_route", "moe_route_backward",
              "moe_route_groups", "moe_route_groups_backward", "moe_rows", "moe_plan", "moe_dispatch",
-             "moe_combine", "moe_combine_backward", "moe_linear", "moe_linear_backward", "moe_weight_gradient", "embedding", "embedding_backward", "orthogonalize",
-             "Moments", "adamw_moments", "adamw_step")
+             "moe_combine", "moe_combine_backward", "moe_linear", "moe_linear_backward", "moe_weight_gradient",
+             "embedding", "embedding_backward", "orthogonalize", "Moments", "adamw_moments", "adamw_step")
 
 
 def __getattr__(name):

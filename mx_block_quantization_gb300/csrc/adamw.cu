@@ -34,7 +34,9 @@
 // in 32 bits (28 bytes an element, the copy rate would be 1138), bound by DRAM with its
 // reads and writes mixed; 811 us and 5.5 TB/s with 8 bits (16.1 bytes an element, 655),
 // bound by instruction issue: 78 an element, half of them on the integer pipe, most of them
-// for the random bits (10) and the two encodings (22).
+// for the random bits (10) and the two encodings (22).  A tensor whose addresses are no
+// multiples of 16 bytes (the copy's of 8) goes by loads of single elements without the ring:
+// 60M parameters 306 to 332 us in place of 265, in 8 bits 306 in place of 167.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <math_constants.h>

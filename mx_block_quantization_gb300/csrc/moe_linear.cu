@@ -35,11 +35,19 @@
 // time (no difference).  Every look at a barrier takes shared memory's bandwidth from the
 // operands: waits that are suspended, by one lane of a warp, are worth 31 us of 683.
 //
-// 128 routed rows to 64 experts of 7168 x 2048, one block of rows each: 166 us, 6.1 TB/s,
-// the weights' bytes.  Weights' gradient, 24 x [1408, 2176] fp32 onto what is there from
-// 40009 rows: 148 us, 5.0 TB/s, bound by L2's additions: a kernel of nothing else does
-// 4.95 TB/s of reads and writes.  With the addend loaded into registers 174, loaded a chunk
-// ahead no less.  64 x [2048, 7168] from 57344 rows: 1508, 790 without the addend.
+// 128 routed rows to 64 experts of 7168 x 2048: 165 us for the weights of the 51 experts
+// that have rows there, a block of 128 each, 854 MB in all, 5.2 TB/s.  The rows' gradient, 61440
+// rows of width 2048 to 7168 with the weights' column-wise cast: 693 us, 2.60 PFLOP/s,
+// where the forward product takes 611.
+//
+// Weights' gradient, 24 x [1408, 2176] fp32 onto what is there from 40009 rows: 148 us, 5.0
+// TB/s, bound by its epilogue of single additions in L2: a kernel of nothing but these does
+// 4.95 TB/s of reads and writes.  (Additions of 16 bytes and bulk ones are 10 to 15% faster
+// by themselves; here, where rows had to be brought together for them, nothing was gained.)
+// With the addend loaded into registers 174, loaded a chunk ahead no less.  Without an
+// addend 120 to 128, where the products' 13 stages a tile are as long as the tile's stores; bf16
+// 126, and 142 onto what is there.  64 x [2048, 7168] from 57344 rows: 1508, 790 without the
+// addend; from 61440 to bf16 1148 and 760.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -491,6 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 // A block takes 128 rows, which lie in one group, and columns of one vector a thread: the
 // rows' sums of dz are its part of dbias, added up over the group's blocks in order by the
 // second kernel.  57344 x 4096 silu in bf16: 250 us with them, 6.05 TB/s, bound by DRAM.
+// Rows that do not all begin at 16 bytes go by single elements: 431 us at a pitch of 4097,
+// fp32 of half the width 269 in place of 220.
 constexpr int kBackThreads = 256;
 
 struct Epilogue {

@@ -13,20 +13,26 @@
 //   softmax   p (h - sum p h)  with  h = g + c.
 //
 // The choice is that of 64-bit arithmetic: c is computed in fp32, where it is off by a few
-// 2^-23, and wherever two values that the choice hangs on lie nearer than that (the last
-// of the chosen groups and the first of the others, neighbours among the chosen experts
-// and the first of the others) the token is done again in 64 bits (choose_exactly).
-// Experts with the same logit and the same bias are equal and go by their index at once.
+// 2^-23, and wherever two values that the choice hangs on lie nearer than that (the chosen
+// groups and the others, neighbours among the chosen experts and the first of the others)
+// they are compared again: by their own errors, which are small for small scores (settle,
+// groups_clear), the candidates in 64 bits (rank_exactly), and at last the whole row in 64
+// bits (choose_exactly).  Experts with the same logit and the same bias are equal and go by
+// their index at once.  131071 tokens of 256 experts in 8 groups take 113 us; with logits
+// around -20 118, with one bias of -inf or -1e9 112, of 1e9 or inf 120; if all of them
+// went by 64 bits, 1895.  That is left for rows whose scores vanish beside a bias of all
+// experts: logits around -20 with biases of -0.01.
 //
 // One warp owns a token, a lane keeps some of its logits in registers, and the next
 // token's are loaded ahead, as in moe_route.cu.  Up to eight experts of one group a lane:
 // route_owned_kernel; else (more than 256 experts, or groups that fill their lanes badly)
 // route_groups_kernel.  Both are bound by the instructions they issue, at three quarters
-// of the issue slots: 131071 tokens, 256 experts in 8 groups, fp32, takes 115 us forward
-// (about 610 instructions a token; the logits' bytes alone take 20) and 52 backward
+// of the issue slots: 131071 tokens, 256 experts in 8 groups, fp32, takes 113 us forward
+// (about 615 instructions a token; the logits' bytes alone take 20) and 52 backward
 // (40 for the bytes of logits and gradient); 10007 tokens, 150 experts in 5 groups,
 // bf16, softmax, 25 us, and some 10 more where a single token has to be done again in 64
-// bits, backward 13.
+// bits, backward 13.  More than 256 experts: 131071 x 512 in 8 groups, k 8, 206 and 99 us,
+// 65536 x 1024 in 32 groups 269 and 107.
 #include "moe_route_common.cuh"
 
 namespace {
@@ -598,9 +604,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // heads and moves one lane on.  A key's lowest bits give way to the expert's place in its
 // lane, lower places first, and what they held is added to the doubt.
 // A group's best is known without a pass through shared memory and a candidate without a
-// pass over all: 610 instructions a token in place of 860 with the kernel above, 115 us in
-// place of 124 (131071 tokens, 256 experts in 8 groups), and 25 to 35 in place of 38
-// (10007 tokens, 150 experts in 5 groups, softmax).
+// pass over all: 615 instructions a token in place of 860 with the kernel above.  131071
+// tokens by this kernel and by that: 16 experts 47 and 54 us, 64 in 8 groups 74 and 95, 64
+// without groups, softmax, 62 and 74, 128 in 8 groups 83 and 108, 150 bf16 in 5 groups,
+// softmax, 128 and 165, 256 in 8 groups 114 and 132, in 32 groups 126 and 156, bf16 without
+// groups, softmax, 93 and 102.
 template <int kW>
 __device__ __forceinline__ void sort_down(uint32_t (&k)[kW]) {
   const auto order = [&](int a, int b) {

@@ -1,9 +1,12 @@
 """Operators of a mixture-of-experts training step around the MXFP8 cast.
 
-Routing with its balance loss (:func:`moe_route`), the exchange of rows with the
-128-row expert groups that :func:`quantize_2d_dual` takes (:func:`moe_plan`,
-:func:`moe_dispatch`, :func:`moe_combine`), the embedding table
-(:func:`embedding`) and their gradients, each a call of its own.  The functions
+Routing with its balance loss (:func:`moe_route`, :func:`moe_route_groups`), the
+exchange of rows with the 128-row expert groups that :func:`quantize_2d_dual` takes
+(:func:`moe_plan`, :func:`moe_dispatch`, :func:`moe_combine`), the experts' products on
+what it gives (:func:`moe_linear`, :func:`moe_weight_gradient`,
+:func:`moe_linear_backward`), the embedding table (:func:`embedding`) and their
+gradients, each a call of its own, and what moves the parameters
+(:func:`orthogonalize`, :func:`adamw_step`).  The functions
 marshal torch CUDA tensors into the C ABI of ``include/mxq.h``, which states
 each operation; there is no CPU path.
 

@@ -108,3 +108,66 @@ def test_small_scores_near_one_another(E, groups, best):
             else:
                 keep = torch.ones(60, dtype=torch.bool)
             compare(x, bias, 8, groups, best, "sigmoid", keep.numpy())
+
+
+def choose_all(x, bias, k, groups, best, scores):
+    """ids of all rows at once on the device in 64 bits, and which rows' choice does not hang
+    on less than 2^-46 of values of a size of 1, or 2^-46 of them: scores here and in the
+    kernel's 64-bit pass are right to some 2^-51."""
+    T, E = x.shape
+    wide = x.double()
+    c = (torch.sigmoid(wide) if scores == "sigmoid" else torch.softmax(wide, 1)) + bias.double()
+    held = torch.ones(T, dtype=torch.bool, device=x.device)
+
+    def apart(high, low):  # or one of them is not there
+        return (high - low > 2.0**-46 * high.abs().clamp(min=1.0)) | (low == -torch.inf)
+    if best < groups:
+        top = torch.sort(c.view(T, groups, E // groups), dim=2, descending=True).values[:, :, :2]
+        two = torch.where(top > -torch.inf, top, 0.0)
+        value = torch.where(top[:, :, 0] > -torch.inf, two.sum(2), -torch.inf)
+        order = torch.sort(value, dim=1, descending=True, stable=True)
+        size = two.abs().sum(2).gather(1, order.indices[:, best - 1:best + 1]).amax(1).clamp(min=1.0)
+        held &= (order.values[:, best - 1] - order.values[:, best] > 2.0**-46 * size) | (order.values[:, best] == -torch.inf)
+        chosen = torch.zeros(T, groups, dtype=torch.bool, device=x.device).scatter_(1, order.indices[:, :best], True)
+        c = torch.where(chosen.repeat_interleave(E // groups, 1), c, -torch.inf)
+    order = torch.sort(c, dim=1, descending=True, stable=True)
+    at, v = order.indices[:, :k + 1], order.values[:, :k + 1]
+    by_x, by_b = x.gather(1, at), bias[at]
+    same = (by_x[:, 1:] == by_x[:, :-1]) & (by_b[:, 1:] == by_b[:, :-1])
+    held &= (same | apart(v[:, :-1], v[:, 1:])).all(1)
+    return torch.where(order.values[:, :k] > -torch.inf, order.indices[:, :k], -1).int(), held
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_random_routers(seed):
+    """Logits at any place and of any spread, equal, near, and with biases that take scores
+    back; biases of any size, and some that leave an expert out or take it always."""
+    import random
+    rng, g = random.Random(seed), torch.Generator(device="cuda").manual_seed(seed)
+    normal = lambda *shape: torch.randn(*shape, generator=g, device="cuda")  # noqa: E731
+    for _ in range(150):
+        groups, size = rng.choice([1, 1, 2, 3, 5, 8, 8, 16, 17, 32]), rng.choice([1, 2, 3, 7, 8, 16, 31, 32, 50, 64, 128])
+        E, T, scores = groups * size, rng.choice([1, 64, 300]), rng.choice(["sigmoid", "softmax"])
+        if E > 1024:
+            continue
+        best = rng.randint(1, groups)
+        k = min(rng.choice([1, 2, 6, 8, 8, 16, 24, 32]), best * size)
+        x = normal(T, E) * rng.choice([0.01, 0.5, 1.5, 4, 10]) + rng.choice([0, 0, -5, -9, -14, -20, -30, 12, 20])
+        bias = normal(E) * rng.choice([0, 0.001, 0.02, 0.1, 1, 50, 1e4, 1e8])
+        kind = rng.choice(["any", "few", "near", "taken back", "taken back", "bf16"])
+        if kind == "few":
+            x = torch.round(2 * x) / 2
+        elif kind == "bf16":
+            x = x.bfloat16()
+        elif kind != "any":
+            x = x[:1] + torch.randint(-30, 31, (T, E), generator=g, device="cuda") * 2.0**-rng.choice([14, 18, 20, 22])
+        if kind == "taken back":
+            s = torch.sigmoid(x[0].double()) if scores == "sigmoid" else torch.softmax(x[0].double(), 0)
+            bias = (rng.choice([0.0, 0.01, 0.5, -1, 3]) - s).float()
+        for value in (-1e9, 1e9, LOWEST, -torch.inf):
+            if rng.random() < 0.12:
+                bias[rng.randrange(E)] = value
+        want, held = choose_all(x.float(), bias, k, groups, best, scores)
+        got = mxq.moe_route_groups(x, k, bias=bias, scores=scores, groups=groups, best_groups=best).ids
+        wrong = (got != want).any(1) & held
+        assert not wrong.any(), (kind, E, groups, best, k, scores, int(wrong.sum()), got[wrong][0].tolist(), want[wrong][0].tolist())
